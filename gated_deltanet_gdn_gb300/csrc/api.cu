@@ -1,5 +1,6 @@
 // C ABI of the gated delta rule library: argument validation, buffer layouts and
 // dispatch to the kernels. Declared in include/gdn.h.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -18,20 +19,6 @@ __device__ unsigned g_device_error;
 constexpr int MAX_DEVICES = 64;
 unsigned* g_err_ptr[MAX_DEVICES];
 std::mutex g_err_mutex;
-
-// Device address of the error word on the current device (resolved once per device,
-// with that device current).
-unsigned* device_error_word() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return nullptr;
-  std::lock_guard<std::mutex> lock(g_err_mutex);
-  if (!g_err_ptr[dev]) {
-    void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_device_error) != cudaSuccess) return nullptr;
-    g_err_ptr[dev] = static_cast<unsigned*>(p);
-  }
-  return g_err_ptr[dev];
-}
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -176,9 +163,37 @@ const char* kKernelNames[K_COUNT] = {"chunk_prep_kernel",    "chunk_scan_fwd_ker
                                      "replay_decode_kernel", "replay_state_kernel", "chunk_dqa_kernel",
                                      "chunk_bwd_tc_kernel", "chunk_prep_tc_kernel",
                                      "chunk_bwd_sync_zero_kernel", "chunk_merge128_kernel",
-                                     "chunk_mid128_kernel"};
+                                     "chunk_mid128_kernel", "block_norm_fwd_kernel", "block_norm_bwd_kernel",
+                                     "block_norm_wgrad_kernel", "kv_append_kernel", "paged_attn_kernel",
+                                     "paged_attn_join_kernel"};
 
 }  // namespace
+
+// Device address of the error word on the current device (resolved once per device,
+// with that device current).
+unsigned* device_error_word() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return nullptr;
+  std::lock_guard<std::mutex> lock(g_err_mutex);
+  if (!g_err_ptr[dev]) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_device_error) != cudaSuccess) return nullptr;
+    g_err_ptr[dev] = static_cast<unsigned*>(p);
+  }
+  return g_err_ptr[dev];
+}
+
+int device_sm_count() {
+  static std::atomic<int> known[MAX_DEVICES];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
 
 void prof_mark(KernelId id, cudaStream_t s, bool begin) {
   if (!g_prof_on) return;
@@ -412,10 +427,10 @@ const char* gdn_status_string(int s) {
   switch (s) {
     case GDN_OK: return "ok";
     case GDN_ERR_INVALID_ARG: return "invalid argument (NULL or misaligned pointer, bad size or flag)";
-    case GDN_ERR_UNSUPPORTED: return "unsupported configuration (Dk, Dv in {64, 128}; dtype bf16 or fp32)";
+    case GDN_ERR_UNSUPPORTED: return "unsupported configuration (Dk, Dv or head width in {64, 128}; dtype bf16 or fp32; pages of a multiple of 16 tokens; normalised width up to 8192)";
     case GDN_ERR_SHAPE: return "T must be a multiple of 64 on the chunked path";
     case GDN_ERR_CUDA: return "CUDA launch or runtime error";
-    case GDN_ERR_INTERNAL: return "a kernel reported an error (a bounded wait timed out, or a replay fill count out of range)";
+    case GDN_ERR_INTERNAL: return "a kernel reported an error (a bounded wait timed out, a replay fill count out of range, or a length, page or position outside a paged cache)";
     case GDN_ERR_SCRATCH_LIMIT: return "problem needs more residual scratch than the static GDN_NOALLOC_SCRATCH_BYTES array";
     default: return "unknown status";
   }

@@ -232,6 +232,56 @@ struct ReplayStateArgs {
   unsigned* err;
 };
 
+// Norms around a block with its gate and residual scale (block_norm.cu): R rows of G
+// groups of C elements, R * G < 2^31, C <= NORM_MAX_WIDTH. Input strides in elements, row
+// then group; outputs contiguous. Optional parts are NULL.
+constexpr int NORM_MAX_WIDTH = 8192;
+constexpr int NORM_BWD_PARTS = 304;  // most CTAs of the backward: two per SM of 152
+struct NormArgs {
+  int R, G, C, bf16, sigmoid;
+  float eps;
+  const void *x, *gate, *residual, *w_post, *res_scale, *w_pre, *dh, *dy;
+  long long x_rs, x_gs, gate_rs, gate_gs, res_rs, res_gs, dh_rs, dh_gs, dy_rs, dy_gs;
+  float* stats;  // [R*G][2]: r1, r2
+  void *h, *y;
+  void *dx, *dgate, *dresidual, *dw_post, *dres_scale, *dw_pre;
+  float* partial;  // [NORM_BWD_PARTS][3][C]
+};
+
+// Paged key/value cache and the new tokens of B sequences (kv_append.cu, paged_attn.cu).
+// Token t of sequence b (cu[b] <= t < cu[b+1]) has position lens[b] - (cu[b+1] - cu[b]) +
+// (t - cu[b]). Strides in elements. Cache element (page, head, row, channel).
+struct PagedArgs {
+  int N, B, Hq, Hk, D, page_size, num_pages, max_pages, bf16;
+  const int *page_table, *cu, *lens;
+  long long pt_stride;
+  void *kc, *vc;
+  long long k_ps, k_hs, k_rs, v_ps, v_hs, v_rs;
+  unsigned* err;
+};
+struct AppendArgs {
+  PagedArgs p;
+  const void *q, *k, *v;
+  void* q_out;
+  long long q_ts, q_hs, kn_ts, kn_hs, vn_ts, vn_hs, qo_ts, qo_hs;
+  const float *cos, *sin;  // [positions][rot / 2]
+  int positions, rot, pairs;
+};
+struct AttnArgs {
+  PagedArgs p;
+  const void* q;
+  void* out;
+  float* lse;  // [N][Hq] or NULL
+  long long q_ts, q_hs, o_ts, o_hs;
+  float scale;
+  int max_q, max_kv;  // the caller's bounds: they choose the variant, never the result
+  float* ws;
+};
+// Bit of the device error word set by the paged kernels: a length beyond the page table, a
+// page outside the cache, or a position beyond the rotation table.
+constexpr unsigned ERR_PAGE = 4u;
+constexpr int ATTN_MAX_CTAS = 160;  // most CTAs of paged_attn_kernel (one per SM)
+
 // Kernel identifiers for the optional per-launch timing (gdn_profile_* in the C ABI).
 enum KernelId {
   K_PREP = 0,      // chunk_prep_kernel
@@ -255,10 +305,20 @@ enum KernelId {
   K_BWD_SYNC = 18,      // chunk_bwd_sync_zero_kernel: zeroes the fused backward's counters
   K_MERGE = 19,         // chunk_merge128_kernel: two 64-token blocks -> one 128-token chunk
   K_MID = 20,           // chunk_mid128_kernel: the 64-token blocks' dU, dS1, states and U
-  K_COUNT = 21
+  K_NORM_FWD = 21,      // block_norm_fwd_kernel
+  K_NORM_BWD = 22,      // block_norm_bwd_kernel
+  K_NORM_WGRAD = 23,    // block_norm_wgrad_kernel: adds the backward's partial weight gradients
+  K_KV_APPEND = 24,     // kv_append_kernel
+  K_ATTN = 25,          // paged_attn_kernel (mma.sync)
+  K_ATTN_JOIN = 26,     // paged_attn_join_kernel: joins the parts of split rows
+  K_COUNT = 27
 };
 // Records a CUDA event on s before (begin = true) or after a launch when timing is on.
 void prof_mark(KernelId id, cudaStream_t s, bool begin);
+// Device address of the error word on the current device (NULL if it cannot be resolved).
+unsigned* device_error_word();
+// SMs of the current device (0 if it cannot be read).
+int device_sm_count();
 
 // Each returns a cudaError_t from the launches (cudaSuccess when all were accepted).
 cudaError_t launch_chunk_fwd(const ChunkFwdArgs& a, cudaStream_t s);
@@ -298,5 +358,11 @@ cudaError_t launch_l2norm_bwd(void* dq, void* dk, const void* qn, const void* kn
 // and the fold of a buffer into a full state.
 cudaError_t launch_replay_decode(const ReplayArgs& a, cudaStream_t s);
 cudaError_t launch_replay_state(const ReplayStateArgs& a, cudaStream_t s);
+// Block norms (block_norm.cu). vec: widths, strides and pointers allow 16-byte accesses.
+cudaError_t launch_block_norm(const NormArgs& a, bool vec, bool bwd, cudaStream_t s);
+// Paged cache (kv_append.cu, paged_attn.cu).
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_paged_attn(const AttnArgs& a, cudaStream_t s);
+size_t paged_attn_workspace(const AttnArgs& a);  // bytes of AttnArgs::ws
 
 }  // namespace gdn

@@ -1,0 +1,503 @@
+// Attention of new tokens over a paged key/value cache, for few query rows per KV head
+// (single tokens, drafts) and for fp32.
+//
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - m),  j <= the token's position
+//
+// One pass over the keys with the running maximum m and sum (fp32, base 2). Every key and
+// value is used for 16 query rows, so HBM bounds it: 4 D bytes per key in bf16 against
+// 64 D flop. What matters is a deep, even stream of loads:
+//  * the keys of all items are cut into units of 16 (inside one page, page sizes being
+//    multiples of 16) and numbered through; each CTA takes an equal run of them, whatever
+//    the lengths of the sequences, and its warps take every WARPS-th unit of the run;
+//  * each warp streams its units through a ring of its own (cp.async, 16 bytes a lane)
+//    that runs ahead across item boundaries, with no barrier between warps;
+//  * at an item's end the warps' (m, sum, o) are merged through shared memory. An item
+//    that a CTA holds whole is written at once; the parts of one cut between CTAs go to
+//    the workspace and a second kernel joins them in the order of the CTAs.
+// The products run on mma.sync: a 16-row tile would leave seven eighths of a 128-row
+// tcgen05 tile empty, and the tensor rate is not what bounds this kernel. In bf16 the
+// probabilities are rounded to bf16 for the second product (their sum is not); fp32 uses
+// the three-term TF32 split for both.
+#include "paged_attn.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int ROWS = 16, UNIT = 16;
+
+template <class T, int D>
+struct Lay {
+  static constexpr int WARPS = sizeof(T) == 2 ? 8 : 4;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int TILE = UNIT * D * (int)sizeof(T);  // bytes of one K or V unit
+  static constexpr int STAGES = 3;
+  static constexpr int Q = 0;                              // [16][D] T, swizzled
+  static constexpr int RING = ROWS * D * (int)sizeof(T);
+  static constexpr int MCOLS = 32;                         // columns merged at a time
+  static constexpr int MERGE = RING + WARPS * STAGES * 2 * TILE;
+  static constexpr int ML = MERGE + WARPS * ROWS * MCOLS * 4;  // float m[WARPS][16], l[WARPS][16]
+  static constexpr int BYTES = ML + 2 * WARPS * ROWS * 4;
+};
+
+// Units of (sequence, KV head): sum over its items of the 16-key units their last row
+// sees, at least one each (an item without keys still writes its zeros).
+__device__ __forceinline__ int item_units(const Seq& s, int G, int item) {
+  int last = (item + 1) * ROWS - 1;
+  const int rows = s.n * G;
+  if (last >= rows) last = rows - 1;
+  const int limit = s.len - s.n + last / G;
+  return limit < 0 ? 1 : limit / UNIT + 1;
+}
+__device__ __forceinline__ int seq_items(const Seq& s, int G) { return (s.n * G + ROWS - 1) / ROWS; }
+__device__ __forceinline__ long long seq_units(const Seq& s, int G) {
+  long long u = 0;
+  for (int i = 0, n = seq_items(s, G); i < n; ++i) u += item_units(s, G, i);
+  return u;
+}
+
+struct Item {
+  int b, h, i;           // sequence, KV head, item of the head
+  Seq s;
+  long long start, end;  // its units, numbered through all items
+};
+
+// The item holding unit f, for one warp (all lanes). total: every unit. f < total.
+__device__ __forceinline__ long long total_units(const PagedArgs& p, int G, int lane, bool report) {
+  long long t = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    const Seq s = load_seq(p, b, report);
+    t += seq_units(s, G) * p.Hk;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+  return t;
+}
+__device__ __forceinline__ void locate(const PagedArgs& p, int G, int lane, long long f, Item& it) {
+  long long base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    long long u = 0;
+    if (b < p.B) u = seq_units(load_seq(p, b, false), G) * p.Hk;
+    long long inc = u;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += o;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + inc > f);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      base += __shfl_sync(0xffffffffu, inc - u, l);
+      it.b = b0 + l;
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  it.s = load_seq(p, it.b, false);
+  const long long per = seq_units(it.s, G);
+  long long rem = f - base;
+  it.h = (int)(rem / per);
+  rem -= it.h * per;
+  it.i = 0;
+  long long at = 0;
+  int u = item_units(it.s, G, 0);
+  while (at + u <= rem) {
+    at += u;
+    u = item_units(it.s, G, ++it.i);
+  }
+  it.start = f - rem + at;
+  it.end = it.start + u;
+}
+// The next item in the numbering (not called past the last).
+__device__ __forceinline__ void next_item(const PagedArgs& p, int G, Item& it) {
+  if (++it.i >= seq_items(it.s, G)) {
+    it.i = 0;
+    if (++it.h >= p.Hk) {
+      it.h = 0;
+      do {
+        ++it.b;
+        it.s = load_seq(p, it.b, false);
+      } while (it.s.n == 0 && it.b + 1 < p.B);
+    }
+  }
+  it.start = it.end;
+  it.end += item_units(it.s, G, it.i);
+}
+
+// CTA c of n takes the units [cut(c), cut(c + 1)).
+__device__ __forceinline__ long long cut(long long total, int n, int c) { return total * c / n; }
+// CTAs that take part: enough units for each of their warps to have one.
+__device__ __forceinline__ int active_ctas(long long total, int grid, int warps) {
+  const long long most = (total + warps - 1) / warps;
+  return most < grid ? (int)most : grid;
+}
+
+// Two-slot partial of a CTA in the workspace: o [16][D] relative to m, then m [16], l [16].
+template <int D>
+__device__ __forceinline__ float* part_slot(float* ws, int cta, int second) {
+  return ws + (size_t)(2 * cta + second) * (ROWS * D + 2 * ROWS);
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  typedef Lay<T, D> L;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align1024(smem_raw);
+  const PagedArgs& p = a.p;
+  const int G = p.Hq / p.Hk;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  Tile<T, ROWS, D> Qs{reinterpret_cast<T*>(sm + L::Q)};
+  uint8_t* ring = sm + L::RING + warp * L::STAGES * 2 * L::TILE;
+  float* merge = reinterpret_cast<float*>(sm + L::MERGE);
+  float* sml = reinterpret_cast<float*>(sm + L::ML);
+
+  const long long total = total_units(p, G, lane, blockIdx.x == 0 && warp == 0);
+  const int ncta = active_ctas(total, gridDim.x, L::WARPS);
+  if ((int)blockIdx.x >= ncta) return;
+  const long long lo = cut(total, ncta, blockIdx.x), hi = cut(total, ncta, blockIdx.x + 1);
+  Item cur;
+  locate(p, G, lane, lo, cur);
+  Item ahead = cur;  // the loads' item
+  long long nextf = lo + warp;  // the next unit to load
+  int st_load = 0;
+
+  auto load_unit = [&]() {
+    if (nextf < hi) {
+      while (nextf >= ahead.end) next_item(p, G, ahead);
+      const int key0 = (int)(nextf - ahead.start) * UNIT;
+      if (key0 < ahead.s.len) {
+        const int page = load_page(p, ahead.b, key0);
+        const int row0 = key0 % p.page_size;
+        const T* kp = static_cast<const T*>(p.kc) + page * p.k_ps + ahead.h * p.k_hs + row0 * p.k_rs;
+        const T* vp = static_cast<const T*>(p.vc) + page * p.v_ps + ahead.h * p.v_hs + row0 * p.v_rs;
+        constexpr int V = 16 / (int)sizeof(T), CH = D / V;  // 16-byte chunks of a row
+        Tile<T, UNIT, D> Kt{reinterpret_cast<T*>(ring + st_load * 2 * L::TILE)};
+        Tile<T, UNIT, D> Vt{reinterpret_cast<T*>(ring + (st_load * 2 + 1) * L::TILE)};
+#pragma unroll
+        for (int q = 0; q < UNIT * CH / 32; ++q) {
+          const int r = (q * 32 + lane) / CH, c = (q * 32 + lane) % CH * V;
+          cp_async16(Kt.ptr(r, c), kp + r * p.k_rs + c);
+        }
+#pragma unroll
+        for (int q = 0; q < UNIT * CH / 32; ++q) {
+          const int r = (q * 32 + lane) / CH, c = (q * 32 + lane) % CH * V;
+          cp_async16(Vt.ptr(r, c), vp + r * p.v_rs + c);
+        }
+      }
+    }
+    cp_async_commit();
+    nextf += L::WARPS;
+    st_load = st_load + 1 == L::STAGES ? 0 : st_load + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < L::STAGES - 1; ++i) load_unit();
+
+  int st = 0;
+  long long f = lo + warp;  // the next unit to use
+  const float c = a.scale * LOG2E;
+  while (true) {
+    const int row0 = cur.i * ROWS, rows = min(ROWS, cur.s.n * G - row0);
+    // the item's queries (rows past the end are zero)
+    __syncthreads();
+    {
+      constexpr int V = 16 / (int)sizeof(T), CH = D / V;
+      for (int q = tid; q < ROWS * CH; q += L::THREADS) {
+        const int r = q / CH, col = q % CH * V;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows) {
+          const int qr = row0 + r, tok = cur.s.first + qr / G, head = cur.h * G + qr % G;
+          v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + tok * a.q_ts + head * a.q_hs + col);
+        }
+        *reinterpret_cast<uint4*>(Qs.ptr(r, col)) = v;
+      }
+    }
+    __syncthreads();
+    uint32_t qf[sizeof(T) == 2 ? D / 16 : 1][4];
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) load_a(qf[ks], aview<false>(Qs), 0, ks * 16, lane);
+    }
+    // last key each of this thread's two rows sees
+    const int p0 = cur.s.len - cur.s.n;
+    int lim[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) lim[e] = g + 8 * e < rows ? p0 + (row0 + g + 8 * e) / G : -1;
+    const int lim_min = p0 + row0 / G;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[D / 8][4];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+
+    const long long end = cur.end < hi ? cur.end : hi;
+    for (; f < end; f += L::WARPS) {
+      load_unit();
+      cp_async_wait<L::STAGES - 1>();
+      __syncwarp();
+      const int key0 = (int)(f - cur.start) * UNIT;
+      Tile<T, UNIT, D> Kt{reinterpret_cast<T*>(ring + st * 2 * L::TILE)};
+      Tile<T, UNIT, D> Vt{reinterpret_cast<T*>(ring + (st * 2 + 1) * L::TILE)};
+      st = st + 1 == L::STAGES ? 0 : st + 1;
+      if (key0 + UNIT > cur.s.len) {  // rows of the page past the length hold anything: 0 * NaN is not 0
+        constexpr int V = 16 / (int)sizeof(T), CH = D / V;
+        const int keep = max(cur.s.len - key0, 0);
+        for (int q = lane; q < (UNIT - keep) * CH; q += 32)
+          *reinterpret_cast<uint4*>(Vt.ptr(keep + q / CH, q % CH * V)) = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
+      }
+      float s[1][2][4];
+      zero<1, 2>(s);
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t b[4];
+          load_b2(b, bview<false>(Kt), 0, ks * 16, lane);
+          mma_bf16(s[0][0], qf[ks], b);
+          mma_bf16(s[0][1], qf[ks], b + 2);
+        }
+      } else {
+        warp_gemm_tf32x3<1, 2>(s, aview<false>(Qs), bview<false>(Kt), 0, 0, 0, D, lane);
+      }
+      // scores in base 2; hidden keys are -inf
+      const bool mask = key0 + UNIT - 1 > lim_min;
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[0][j][e] * c;
+          if (mask && key0 + j * 8 + frag_col(lane, e) > lim[e >> 1]) x = -INFINITY;
+          s[0][j][e] = x;
+          top[e >> 1] = fmaxf(top[e >> 1], x);
+        }
+      float ref[2];
+      bool moved = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+        moved |= top[e] > m[e];
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+        float fac[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float nm = fmaxf(m[e], top[e]);
+          fac[e] = m[e] == nm ? 1.f : exp2f(m[e] - nm);  // m = -inf: 0
+          m[e] = nm;
+          l[e] *= fac[e];
+        }
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][e] *= fac[e >> 1];
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) ref[e] = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[0][j][e] = exp2f(s[0][j][e] - ref[e >> 1]);
+          l[e >> 1] += s[0][j][e];
+        }
+      // the score fragment is the second product's A fragment
+      if constexpr (sizeof(T) == 2) {
+        uint32_t pa[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(s[0][q >> 1][(q & 1) * 2], s[0][q >> 1][(q & 1) * 2 + 1]);
+          pa[q] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+#pragma unroll
+        for (int n0 = 0; n0 < D; n0 += 16) {
+          uint32_t b[4];
+          load_b2(b, bview<true>(Vt), n0, 0, lane);
+          mma_bf16(o[n0 / 8], pa, b);
+          mma_bf16(o[n0 / 8 + 1], pa, b + 2);
+        }
+      } else {
+        // keys 2t and 2t + 1 of each eight stand at k = t and t + 4, in both operands
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t ah[4], al[4];
+          tf32_split(s[0][j][0], ah[0], al[0]);
+          tf32_split(s[0][j][2], ah[1], al[1]);
+          tf32_split(s[0][j][1], ah[2], al[2]);
+          tf32_split(s[0][j][3], ah[3], al[3]);
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            uint32_t bh[2], bl[2];
+            tf32_split(Vt.at(j * 8 + 2 * t, n * 8 + g), bh[0], bl[0]);
+            tf32_split(Vt.at(j * 8 + 2 * t + 1, n * 8 + g), bh[1], bl[1]);
+            mma_tf32(o[n], al, bh);
+            mma_tf32(o[n], ah, bl);
+            mma_tf32(o[n], ah, bh);
+          }
+        }
+      }
+      __syncwarp();  // the stage is loaded again by other lanes
+    }
+    // merge the warps
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+      if (t == 0) {
+        sml[warp * ROWS + g + 8 * e] = m[e];
+        sml[(L::WARPS + warp) * ROWS + g + 8 * e] = l[e];
+      }
+    }
+    __syncthreads();
+    const bool whole = cur.start >= lo && cur.end <= hi;
+    float* part = part_slot<D>(a.ws, blockIdx.x, cur.start < lo ? 0 : 1);
+    float fac[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float M = -INFINITY;
+      for (int w = 0; w < L::WARPS; ++w) M = fmaxf(M, sml[w * ROWS + g + 8 * e]);
+      fac[e] = m[e] == -INFINITY ? 0.f : exp2f(m[e] - M);
+    }
+#pragma unroll
+    for (int c0 = 0; c0 < D; c0 += L::MCOLS) {
+#pragma unroll
+      for (int j = 0; j < L::MCOLS / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          float2* d = reinterpret_cast<float2*>(merge + ((size_t)warp * ROWS + g + 4 * e) * L::MCOLS + j * 8 + 2 * t);
+          *d = make_float2(o[c0 / 8 + j][e] * fac[e >> 1], o[c0 / 8 + j][e + 1] * fac[e >> 1]);
+        }
+      __syncthreads();
+      for (int q = tid; q < rows * L::MCOLS; q += L::THREADS) {
+        const int r = q / L::MCOLS, col = q % L::MCOLS;
+        float sum = 0.f, M = -INFINITY, lt = 0.f;
+#pragma unroll
+        for (int w = 0; w < L::WARPS; ++w) {
+          sum += merge[(w * ROWS + r) * L::MCOLS + col];
+          M = fmaxf(M, sml[w * ROWS + r]);
+        }
+#pragma unroll
+        for (int w = 0; w < L::WARPS; ++w)
+          if (sml[w * ROWS + r] != -INFINITY) lt += sml[(L::WARPS + w) * ROWS + r] * exp2f(sml[w * ROWS + r] - M);
+        if (whole) {
+          const int qr = row0 + r, tok = cur.s.first + qr / G, head = cur.h * G + qr % G;
+          const float inv = M == -INFINITY ? 0.f : 1.f / lt;
+          static_cast<T*>(a.out)[tok * a.o_ts + head * a.o_hs + c0 + col] = from_f32<T>(sum * inv);
+          if (a.lse && c0 + col == 0)
+            a.lse[(size_t)tok * p.Hq + head] = M == -INFINITY ? -INFINITY : (M + log2f(lt)) * LN2;
+        } else {
+          part[r * D + c0 + col] = sum;
+          if (c0 + col == 0) {
+            part[ROWS * D + r] = M;
+            part[ROWS * D + ROWS + r] = lt;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (cur.end >= hi) break;
+    next_item(p, G, cur);
+  }
+  cp_async_wait<0>();
+}
+
+// Joins an item's parts, one CTA of D threads per item: o = sum_c o_c 2^(m_c - m) over the
+// CTAs that share it, in their order.
+template <class T, int D>
+__global__ void __launch_bounds__(D) paged_attn_join_kernel(AttnArgs a, int grid) {
+  pdl_wait();
+  const PagedArgs& p = a.p;
+  const int G = p.Hq / p.Hk, lane = threadIdx.x & 31;
+  const long long total = total_units(p, G, lane, false);
+  const int ncta = active_ctas(total, grid, Lay<T, D>::WARPS);
+  // item blockIdx.x of all
+  long long idx = blockIdx.x, base = 0;
+  Item it;
+  it.b = -1;
+  for (int b = 0; b < p.B; ++b) {
+    const Seq s = load_seq(p, b, false);
+    const long long n = (long long)seq_items(s, G) * p.Hk;
+    if (idx < n) {
+      it.b = b;
+      it.s = s;
+      break;
+    }
+    idx -= n;
+    base += seq_units(s, G) * p.Hk;
+  }
+  if (it.b < 0) return;
+  const int per = seq_items(it.s, G);
+  it.h = (int)(idx / per);
+  it.i = (int)(idx % per);
+  base += seq_units(it.s, G) * it.h;
+  for (int i = 0; i < it.i; ++i) base += item_units(it.s, G, i);
+  it.start = base;
+  it.end = base + item_units(it.s, G, it.i);
+  // the CTA whose run holds unit f
+  auto holder = [&](long long f) {
+    int c = (int)(f * ncta / total);
+    while (c + 1 < ncta && cut(total, ncta, c + 1) <= f) ++c;
+    while (c > 0 && cut(total, ncta, c) > f) --c;
+    return c;
+  };
+  const int c0 = holder(it.start), c1 = holder(it.end - 1);
+  if (c0 == c1) return;
+  const int row0 = it.i * ROWS, rows = min(ROWS, it.s.n * G - row0);
+  for (int r = 0; r < rows; ++r) {
+    float M = -INFINITY;
+    for (int q = c0; q <= c1; ++q) M = fmaxf(M, part_slot<D>(a.ws, q, q == c0)[ROWS * D + r]);
+    float sum = 0.f, lt = 0.f;
+    for (int q = c0; q <= c1; ++q) {
+      const float* part = part_slot<D>(a.ws, q, q == c0);
+      const float m = part[ROWS * D + r];
+      if (m == -INFINITY) continue;
+      const float w = exp2f(m - M);
+      sum += part[r * D + threadIdx.x] * w;
+      lt += part[ROWS * D + ROWS + r] * w;
+    }
+    const int qr = row0 + r, tok = it.s.first + qr / G, head = it.h * G + qr % G;
+    const float inv = M == -INFINITY ? 0.f : 1.f / lt;
+    static_cast<T*>(a.out)[tok * a.o_ts + head * a.o_hs + threadIdx.x] = from_f32<T>(sum * inv);
+    if (a.lse && threadIdx.x == 0)
+      a.lse[(size_t)tok * p.Hq + head] = M == -INFINITY ? -INFINITY : (M + log2f(lt)) * LN2;
+  }
+}
+
+template <class T, int D>
+cudaError_t run(const AttnArgs& a, cudaStream_t s) {
+  typedef Lay<T, D> L;
+  const int bytes = L::BYTES + 1024;
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  const int nsm = device_sm_count();
+  if (nsm < 1) return cudaErrorInvalidDevice;
+  const int grid = nsm < ATTN_MAX_CTAS ? nsm : ATTN_MAX_CTAS;
+  prof_mark(K_ATTN, s, true);
+  e = launch_pdl(paged_attn_kernel<T, D>, dim3(grid), dim3(L::THREADS), bytes, s, a);
+  prof_mark(K_ATTN, s, false);
+  if (e != cudaSuccess) return e;
+  const int G = a.p.Hq / a.p.Hk;
+  // an upper bound: full items, and one that is not full per sequence with new tokens
+  const long long rows = (long long)a.p.N * G, seqs = a.p.B < a.p.N ? a.p.B : a.p.N;
+  const long long items = (rows / ROWS + seqs) * a.p.Hk;
+  prof_mark(K_ATTN_JOIN, s, true);
+  e = launch_pdl(paged_attn_join_kernel<T, D>, dim3((unsigned)items), dim3(D), 0, s, a, grid);
+  prof_mark(K_ATTN_JOIN, s, false);
+  return e;
+}
+
+}  // namespace
+
+size_t paged_attn_workspace(const AttnArgs& a) {
+  return (size_t)2 * ATTN_MAX_CTAS * (ROWS * a.p.D + 2 * ROWS) * sizeof(float);
+}
+
+cudaError_t launch_paged_attn(const AttnArgs& a, cudaStream_t s) {
+  if (a.p.bf16) return a.p.D == 64 ? run<bf16, 64>(a, s) : run<bf16, 128>(a, s);
+  return a.p.D == 64 ? run<float, 64>(a, s) : run<float, 128>(a, s);
+}
+
+}  // namespace gdn

@@ -282,6 +282,140 @@ int gdn_replay_decode(const gdn_dims* dims, int L, const void* q, const void* k,
 int gdn_replay_state(const gdn_dims* dims, int L, const float* ckpt, const void* buffer,
                      const int* fill, float* h_out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the rule in a hybrid stack: softmax attention layers over
+ * a paged key/value cache, and the norms around every block.
+ *
+ * Paged cache. Keys and values of B sequences lie in pages of page_size tokens:
+ * element (page, head, row, channel) of the key cache is at k + page *
+ * k_page_stride + head * k_head_stride + row * k_row_stride + channel, the value
+ * cache likewise (strides in elements, so either order of heads and rows fits,
+ * and both caches may be slices of one allocation). page_table row b lists
+ * sequence b's pages in order; entries past its length are not read.
+ *
+ * New tokens are packed: sequence b's are rows cu_seqlens[b] .. cu_seqlens[b+1]
+ * - 1 of the token tensors (cu_seqlens[0] = 0; a sequence may have none).
+ * kv_lens[b] counts the cached tokens WITH the new ones, so new token i of n has
+ * position kv_lens[b] - n + i, and the same arrays serve the append and the
+ * attention after it. A token with a negative position (kv_lens[b] < n) is not
+ * kept, and sees no key: its attention row is zero (lse -infinity). Rows from
+ * cu_seqlens[B] on are padding: nothing is read or written for them.
+ *
+ * Token tensors are [N, heads, D] with any token and head strides (in elements,
+ * 0 or more); channels are contiguous. Pointers are 16-byte aligned and every
+ * stride is a multiple of 16 bytes. The integer arrays are device memory and
+ * are read by the kernels only: a captured graph replays with new lengths. A
+ * length beyond max_pages * page_size, a listed page outside [0, num_pages) or a
+ * position beyond the rotation table sets bit 4 of the device error word; the
+ * token is then not stored, or the length or page is clamped for reading.
+ * Errors: GDN_ERR_INVALID_ARG as above and for bad strides, Hq not a multiple of
+ * Hk, bad rot or scale not finite and positive; GDN_ERR_UNSUPPORTED for D not 64
+ * or 128, page_size not a multiple of 16, an unknown dtype, or N * Hq above
+ * 2^31 - 1. */
+typedef struct {
+  int N, B;    /* new tokens (rows of q, k, v), sequences */
+  int Hq, Hk;  /* query heads, key/value heads: query head h reads head h / (Hq / Hk) */
+  int D;       /* head width: 64 or 128 */
+  int page_size, num_pages;
+  int max_pages; /* entries of a page_table row */
+  int dtype;     /* gdn_dtype of tokens and cache */
+  int flags;     /* GDN_FLAG_ROPE_PAIRS */
+} gdn_paged_dims;
+typedef struct {
+  void *k, *v;
+  long long k_page_stride, k_head_stride, k_row_stride;
+  long long v_page_stride, v_head_stride, v_row_stride;
+  const int* page_table; /* [B] rows of max_pages, page_table_stride apart */
+  long long page_table_stride;
+  const int* cu_seqlens; /* [B + 1] */
+  const int* kv_lens;    /* [B] */
+} gdn_paged_cache;
+typedef struct {
+  void* p; /* read only, for inputs */
+  long long token_stride, head_stride;
+} gdn_tokens;
+
+/* The rotation takes channels (2i, 2i + 1) as pair i instead of (i, i + rot/2). */
+#define GDN_FLAG_ROPE_PAIRS 16
+
+/* Stores the new tokens' k and v in their pages, and turns k by its position on
+ * the way: pair i of the first rot channels, (a, b), becomes (a cos - b sin,
+ * b cos + a sin) with cos = cos_table[position][i], likewise sin (float32 tables
+ * [positions, rot/2]; rot a multiple of 16 up to D, 0 = no rotation, tables
+ * NULL). With q not NULL, q (Hq heads) is turned alike into q_out, which may be q
+ * itself. The arithmetic is float32, rounded once. Each value is read and
+ * written once. */
+int gdn_kv_append(const gdn_paged_dims* dims, const gdn_paged_cache* cache, const gdn_tokens* k,
+                  const gdn_tokens* v, const gdn_tokens* q, const gdn_tokens* q_out,
+                  const float* cos_table, const float* sin_table, int positions, int rot,
+                  void* stream);
+
+/* Causal attention of the new tokens over the cache, their own keys included
+ * (append them first): out = sum_j softmax_j(scale q . k_j) v_j over the keys j
+ * up to the token's position; one new token per sequence (decode), a draft, a
+ * chunk and a whole prompt are the same call. Scores, maxima, sums and outputs
+ * accumulate in float32; with bf16 the probabilities are rounded to bf16 for the
+ * product with v. lse (NULL or [N, Hq] float32): log sum_j exp(scale q . k_j).
+ * Cached rows past a sequence's length may hold anything, NaN included. A
+ * non-finite value in a visible row reaches the outputs of every row that
+ * sees it and may reach rows of the same sequence that stand before it.
+ * max_q and max_kv bound the new tokens and the length of any one sequence
+ * (0 < max_q <= N, 0 < max_kv): they choose the kernel and its split, never the
+ * result. workspace: gdn_paged_attn_workspace_bytes(dims, max_q, max_kv) bytes,
+ * 256-byte aligned, no initialisation needed, not shared by calls that overlap. */
+size_t gdn_paged_attn_workspace_bytes(const gdn_paged_dims* dims, int max_q, int max_kv);
+int gdn_paged_attn(const gdn_paged_dims* dims, const gdn_paged_cache* cache, const gdn_tokens* q,
+                   float scale, int max_q, int max_kv, const gdn_tokens* out, float* lse,
+                   void* workspace, void* stream);
+
+/* Norms after and before a block, with its gate and residual scale. Per row of C
+ * elements (R rows of G groups, each group normalised by itself), every part
+ * optional (NULL) except x:
+ *     n = x / sqrt(mean(x^2) + eps) * w_post        n = x without w_post
+ *     m = n * act(gate)                             silu, or sigmoid by flag
+ *     h = residual + res_scale * m
+ *     y = h / sqrt(mean(h^2) + eps) * w_pre         only with w_pre
+ * With x the output of the rule per head (G = H, C = Dv), w_post and gate this is
+ * the gated output norm; with G = 1, all parts, the step between two blocks.
+ * Arithmetic is float32; y is formed from h before h is rounded.
+ *   x, gate, residual, dh, dy   [R, G, C], any row and group strides (elements)
+ *   w_post, res_scale, w_pre    [C]
+ *   h, y, dx, dgate, dresidual  [R, G, C] contiguous
+ *   stats                       [R, G, 2] float32, written by the forward for the
+ *                               backward: the two inverse norms (1 where absent)
+ * All but stats have dims.dtype. Any C up to 8192 (else GDN_ERR_UNSUPPORTED);
+ * multiples of 16 bytes in C, strides and pointers take the wide loads. R * G up
+ * to 2^31 - 1. eps finite and not negative.
+ * The backward takes the forward's inputs and stats, dh (NULL = zeros) and dy
+ * (with w_pre), and writes every gradient that is not NULL in grads; gradients of
+ * absent parts must be NULL. The weight gradients are summed in float32 in a
+ * fixed order. workspace: gdn_block_norm_workspace_bytes(dims), 256-byte
+ * aligned. */
+#define GDN_FLAG_GATE_SIGMOID 32
+typedef struct {
+  int R, G, C;
+  int dtype;
+  int flags; /* GDN_FLAG_GATE_SIGMOID */
+  float eps;
+} gdn_norm_dims;
+typedef struct {
+  const void* p;
+  long long row_stride, group_stride;
+} gdn_rows;
+typedef struct {
+  gdn_rows x, gate, residual;
+  const void *w_post, *res_scale, *w_pre;
+} gdn_norm_parts;
+typedef struct {
+  void *dx, *dgate, *dresidual, *dw_post, *dres_scale, *dw_pre;
+} gdn_norm_grads;
+int gdn_block_norm_fwd(const gdn_norm_dims* dims, const gdn_norm_parts* parts, void* h, void* y,
+                       float* stats, void* stream);
+size_t gdn_block_norm_workspace_bytes(const gdn_norm_dims* dims);
+int gdn_block_norm_bwd(const gdn_norm_dims* dims, const gdn_norm_parts* parts, const float* stats,
+                       const gdn_rows* dh, const gdn_rows* dy, const gdn_norm_grads* grads,
+                       void* workspace, void* stream);
+
 /* Self-test of the failure path: launches a one-thread kernel that first waits,
  * with the library's cross-CTA counter wait (the one the forward's output CTAs use
  * on the scan), for a counter nothing raises, and gives up after max_tries polls
@@ -300,7 +434,9 @@ int gdn_selftest_wait_timeout(unsigned max_tries, unsigned long long* cycles, vo
 
 /* Reads and clears the library's device error word on the current device
  * (bits, OR-ed: 1 = a kernel gave up waiting for one of its own asynchronous
- * copies; 2 = a replay fill count was outside [0, L]).
+ * copies; 2 = a replay fill count was outside [0, L]; 4 = a paged call met a
+ * length beyond its page table, a page outside the cache, or a position beyond
+ * the rotation table).
  * Synchronises the device. Returns GDN_OK when the word was zero,
  * GDN_ERR_INTERNAL when it was not, GDN_ERR_CUDA if the read failed. */
 int gdn_check_device_error(void);
@@ -330,7 +466,10 @@ int gdn_version(void);
  * with Dk = Dv = 128; when B * H is below the SM count the same launch also runs
  * the reverse scan, which then replaces 9 too), 17 chunk preparation on tcgen05
  * tensor cores (replaces 0 for bf16 operands with Dk = Dv = 128), 18 the zeroing
- * of that single backward launch's counters; gdn_kernel_name(id) names them
+ * of that single backward launch's counters, 19 the merge of 64-token blocks and
+ * 20 the mid-block records (GDN_FLAG_CHUNK128 only), 21 block norms forward,
+ * 22 backward and 23 the sums of its weight gradients, 24 paged cache append,
+ * 25 paged attention and 26 the join of its split rows; gdn_kernel_name(id) names them
  * ("" for an unknown id). Not part of the paper's method: instrumentation. */
 int gdn_profile_enable(int on);
 int gdn_profile_read(double* ms, int* launches, int n);
