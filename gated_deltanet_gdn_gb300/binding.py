@@ -41,7 +41,7 @@ EXPORTED = ("gdn_chunk_residual_bytes", "gdn_chunk_bwd_workspace_bytes", "gdn_ch
             "gdn_replay_state", "gdn_selftest_wait_timeout", "gdn_kv_append",
             "gdn_paged_attn_workspace_bytes", "gdn_paged_attn", "gdn_block_norm_fwd",
             "gdn_block_norm_workspace_bytes", "gdn_block_norm_bwd")
-KERNEL_COUNT = 27
+KERNEL_COUNT = 29
 GDN_REPLAY_MAX_TOKENS = 8
 
 

@@ -165,7 +165,7 @@ const char* kKernelNames[K_COUNT] = {"chunk_prep_kernel",    "chunk_scan_fwd_ker
                                      "chunk_bwd_sync_zero_kernel", "chunk_merge128_kernel",
                                      "chunk_mid128_kernel", "block_norm_fwd_kernel", "block_norm_bwd_kernel",
                                      "block_norm_wgrad_kernel", "kv_append_kernel", "paged_attn_kernel",
-                                     "paged_attn_join_kernel"};
+                                     "paged_attn_join_kernel", "paged_attn_tc_kernel", "paged_attn_tc_join_kernel"};
 
 }  // namespace
 

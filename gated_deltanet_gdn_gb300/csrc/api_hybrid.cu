@@ -27,7 +27,7 @@ int check_paged(const gdn_paged_dims* d) {
   if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
   if (d->D != 64 && d->D != 128) return GDN_ERR_UNSUPPORTED;
   if (d->page_size % 16 != 0) return GDN_ERR_UNSUPPORTED;
-  if ((long long)d->N * d->Hq > INT_MAX) return GDN_ERR_UNSUPPORTED;
+  if ((long long)d->N * d->Hq > (1 << 30)) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 bool has_work(const gdn_paged_dims* d) { return d->N > 0 && d->B > 0; }

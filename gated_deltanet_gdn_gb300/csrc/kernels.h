@@ -280,7 +280,8 @@ struct AttnArgs {
 // Bit of the device error word set by the paged kernels: a length beyond the page table, a
 // page outside the cache, or a position beyond the rotation table.
 constexpr unsigned ERR_PAGE = 4u;
-constexpr int ATTN_MAX_CTAS = 160;  // most CTAs of paged_attn_kernel (one per SM)
+constexpr int ATTN_MAX_CTAS = 160;   // most CTAs of paged_attn_kernel (one per SM)
+constexpr int TC_SPLIT_ITEMS = 608;  // most parts of a split paged_attn_tc_kernel call
 
 // Kernel identifiers for the optional per-launch timing (gdn_profile_* in the C ABI).
 enum KernelId {
@@ -311,7 +312,9 @@ enum KernelId {
   K_KV_APPEND = 24,     // kv_append_kernel
   K_ATTN = 25,          // paged_attn_kernel (mma.sync)
   K_ATTN_JOIN = 26,     // paged_attn_join_kernel: joins the parts of split rows
-  K_COUNT = 27
+  K_ATTN_TC = 27,       // paged_attn_tc_kernel (tcgen05)
+  K_ATTN_TC_JOIN = 28,  // paged_attn_tc_join_kernel
+  K_COUNT = 29
 };
 // Records a CUDA event on s before (begin = true) or after a launch when timing is on.
 void prof_mark(KernelId id, cudaStream_t s, bool begin);
@@ -364,5 +367,11 @@ cudaError_t launch_block_norm(const NormArgs& a, bool vec, bool bwd, cudaStream_
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_paged_attn(const AttnArgs& a, cudaStream_t s);
 size_t paged_attn_workspace(const AttnArgs& a);  // bytes of AttnArgs::ws
+// The tcgen05 kernel (paged_attn_tc.cu): bf16 with more query rows per KV head than the
+// mma.sync kernel takes at a time. done: false when the cache's strides do not fit a tensor
+// map and nothing was launched.
+bool paged_attn_tc_applies(const AttnArgs& a);
+size_t paged_attn_tc_workspace(const AttnArgs& a);
+cudaError_t launch_paged_attn_tc(const AttnArgs& a, cudaStream_t s, bool* done);
 
 }  // namespace gdn

@@ -259,7 +259,18 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
           mma_bf16(s[0][1], qf[ks], b + 2);
         }
       } else {
-        warp_gemm_tf32x3<1, 2>(s, aview<false>(Qs), bview<false>(Kt), 0, 0, 0, D, lane);
+        // each step of eight channels starts from zero and is added in fp32: the tensor core's own
+        // accumulation truncates, which over D channels costs a digit
+#pragma unroll
+        for (int k0 = 0; k0 < D; k0 += 8) {
+          float x[1][2][4];
+          zero<1, 2>(x);
+          warp_gemm_tf32x3<1, 2>(x, aview<false>(Qs), bview<false>(Kt), 0, 0, k0, k0 + 8, lane);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[0][j][e] += x[0][j][e];
+        }
       }
       // scores in base 2; hidden keys are -inf
       const bool mask = key0 + UNIT - 1 > lim_min;
@@ -321,22 +332,28 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
         }
       } else {
         // keys 2t and 2t + 1 of each eight stand at k = t and t + 4, in both operands
+        uint32_t ah[2][4], al[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          uint32_t ah[4], al[4];
-          tf32_split(s[0][j][0], ah[0], al[0]);
-          tf32_split(s[0][j][2], ah[1], al[1]);
-          tf32_split(s[0][j][1], ah[2], al[2]);
-          tf32_split(s[0][j][3], ah[3], al[3]);
+          tf32_split(s[0][j][0], ah[j][0], al[j][0]);
+          tf32_split(s[0][j][2], ah[j][1], al[j][1]);
+          tf32_split(s[0][j][1], ah[j][2], al[j][2]);
+          tf32_split(s[0][j][3], ah[j][3], al[j][3]);
+        }
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
+        for (int n = 0; n < D / 8; ++n) {
+          float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
             uint32_t bh[2], bl[2];
             tf32_split(Vt.at(j * 8 + 2 * t, n * 8 + g), bh[0], bl[0]);
             tf32_split(Vt.at(j * 8 + 2 * t + 1, n * 8 + g), bh[1], bl[1]);
-            mma_tf32(o[n], al, bh);
-            mma_tf32(o[n], ah, bl);
-            mma_tf32(o[n], ah, bh);
+            mma_tf32(x, al[j], bh);
+            mma_tf32(x, ah[j], bl);
+            mma_tf32(x, ah[j], bh);
           }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][e] += x[e];
         }
       }
       __syncwarp();  // the stage is loaded again by other lanes
@@ -492,10 +509,17 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attn_workspace(const AttnArgs& a) {
-  return (size_t)2 * ATTN_MAX_CTAS * (ROWS * a.p.D + 2 * ROWS) * sizeof(float);
+  const size_t own = (size_t)2 * ATTN_MAX_CTAS * (ROWS * a.p.D + 2 * ROWS) * sizeof(float);
+  const size_t tc = paged_attn_tc_applies(a) ? paged_attn_tc_workspace(a) : 0;
+  return own > tc ? own : tc;
 }
 
 cudaError_t launch_paged_attn(const AttnArgs& a, cudaStream_t s) {
+  if (paged_attn_tc_applies(a)) {
+    bool done = false;
+    const cudaError_t e = launch_paged_attn_tc(a, s, &done);
+    if (done || e != cudaSuccess) return e;
+  }
   if (a.p.bf16) return a.p.D == 64 ? run<bf16, 64>(a, s) : run<bf16, 128>(a, s);
   return a.p.D == 64 ? run<float, 64>(a, s) : run<float, 128>(a, s);
 }

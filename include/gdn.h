@@ -311,7 +311,7 @@ int gdn_replay_state(const gdn_dims* dims, int L, const float* ckpt, const void*
  * Errors: GDN_ERR_INVALID_ARG as above and for bad strides, Hq not a multiple of
  * Hk, bad rot or scale not finite and positive; GDN_ERR_UNSUPPORTED for D not 64
  * or 128, page_size not a multiple of 16, an unknown dtype, or N * Hq above
- * 2^31 - 1. */
+ * 2^30. */
 typedef struct {
   int N, B;    /* new tokens (rows of q, k, v), sequences */
   int Hq, Hk;  /* query heads, key/value heads: query head h reads head h / (Hq / Hk) */
@@ -469,7 +469,8 @@ int gdn_version(void);
  * of that single backward launch's counters, 19 the merge of 64-token blocks and
  * 20 the mid-block records (GDN_FLAG_CHUNK128 only), 21 block norms forward,
  * 22 backward and 23 the sums of its weight gradients, 24 paged cache append,
- * 25 paged attention and 26 the join of its split rows; gdn_kernel_name(id) names them
+ * 25 paged attention of few rows and 26 the join of its parts, 27 paged attention on
+ * tcgen05 tensor cores and 28 the join of its parts; gdn_kernel_name(id) names them
  * ("" for an unknown id). Not part of the paper's method: instrumentation. */
 int gdn_profile_enable(int on);
 int gdn_profile_read(double* ms, int* launches, int n);
