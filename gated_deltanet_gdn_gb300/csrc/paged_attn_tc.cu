@@ -32,8 +32,8 @@ constexpr int ROWS = 256, HALF = 128, KT = 128;  // query rows of an item, of a 
 constexpr int THREADS = 384;  // three warpgroups: two of softmax, and one with the two warps below
 constexpr int MMA_WARP = 8, LOAD_WARP = 9;
 // Registers a thread, moved from the third warpgroup to the softmax (which holds 128 scores):
-// the launch has 168 each, 2 * 208 + 88 = 3 * 168.
-constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
+// the launch has 168 each, 2 * 224 + 56 = 3 * 168.
+constexpr int SOFTMAX_REGS = 224, OTHER_REGS = 56;
 constexpr float RESCALE = 8.f;  // growth of the maximum (base 2) that rescales O
 
 template <int N>
@@ -61,13 +61,36 @@ struct TcLay {
   static constexpr int P_STEP = D == 128 ? 128 : 64;     // between the two tiles' P
 };
 
-// D[tmem] (+)= A[tmem] * B[smem]; issued by one thread. A: 16-bit pairs in 32-bit columns.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// Four MMAs along K (64 channels of Q and K, or 64 keys of P and V), called by a whole warp
+// and issued by the lane that elect.sync names, the same one every time. The descriptors'
+// steps are added inside: kept outside, the compiler holds every step of every tile in
+// registers, and the warp spends more time on them than the tensor cores on the products.
+__device__ __forceinline__ void umma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, q;\n .reg .b64 x, y;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n setp.eq.b32 p, 0, 0;\n"
+      " add.s64 x, %1, 2;\n add.s64 y, %2, 2;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n"
+      " add.s64 x, %1, 4;\n add.s64 y, %2, 4;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n"
+      " add.s64 x, %1, 6;\n add.s64 y, %2, 6;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A[tmem]: 16-bit pairs in 32-bit columns; B MN-major, 2048 bytes a step.
+__device__ __forceinline__ void umma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b32 x;\n .reg .b64 y;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n setp.eq.b32 p, 0, 0;\n"
+      " add.u32 x, %1, 8;\n add.s64 y, %2, 128;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n"
+      " add.u32 x, %1, 16;\n add.s64 y, %2, 256;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n"
+      " add.u32 x, %1, 24;\n add.s64 y, %2, 384;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// umma_commit by the elected lane.
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
@@ -189,11 +212,37 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* sm = align1024(smem_raw);
   const PagedArgs& p = a.p;
   const int G = p.Hq / p.Hk;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   TcItem it;
   if (!find_item(p, G, lane, blockIdx.x / splits, blockIdx.x % splits, splits, it)) return;
   if (p.err && warp == 0 && lane == 0 && p.lens[it.b] > (long long)p.max_pages * p.page_size) atomicOr(p.err, ERR_PAGE);
   if ((int)(blockIdx.x % splits) >= it.splits) return;
+
+  if (warp < MMA_WARP && it.need[warp >> 2] > 0) {
+    // The queries of a row tile, rows past the end zero: a thread takes 16 bytes of every
+    // STEP-th row, all in flight at once (cp.async), while the CTA sets itself up.
+    constexpr int CH = D / 8, STEP = HALF / CH;
+    const int w = warp >> 2, r = tid & (HALF - 1), col = r % CH * 8;
+    Tile<bf16, HALF, D> Qs{reinterpret_cast<bf16*>(sm + L::Q + w * HALF * D * 2)};
+    int row = r / CH, g = it.row0 + w * HALF + row, tok = it.s.first + g / G, sub = g % G;
+    const int dt = STEP / G, ds = STEP % G;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (w * HALF + row < it.rows)
+        cp_async16(Qs.ptr(row, col),
+                   static_cast<const bf16*>(a.q) + tok * a.q_ts + (long long)(it.h * G + sub) * a.q_hs + col);
+      else
+        *reinterpret_cast<uint4*>(Qs.ptr(row, col)) = make_uint4(0u, 0u, 0u, 0u);
+      row += STEP;
+      tok += dt;
+      sub += ds;
+      if (sub >= G) {
+        sub -= G;
+        ++tok;
+      }
+    }
+    cp_async_commit();
+  }
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
   uint64_t *full = bars, *empty = bars + L::SLOTS, *qbar = bars + 2 * L::SLOTS, *sbar = qbar + 2, *pbar = sbar + 2,
@@ -227,18 +276,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int row = w * HALF + r;                   // row of the item
     Tile<bf16, HALF, D> Qs{reinterpret_cast<bf16*>(sm + L::Q + w * HALF * D * 2)};
     const int need = it.need[w];
-    if (need > 0) {
-      constexpr int CH = D / 8;
-#pragma unroll 4
-      for (int i = 0; i < CH; ++i) {
-        const int q = i * HALF + r, qr = w * HALF + q / CH, col = q % CH * 8;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (qr < it.rows) {
-          const int g = it.row0 + qr, tok = it.s.first + g / G, head = it.h * G + g % G;
-          v = *reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) + tok * a.q_ts + head * a.q_hs + col);
-        }
-        *reinterpret_cast<uint4*>(Qs.ptr(q / CH, col)) = v;
-      }
+    if (need > 0) {  // the queries, on their way since before the barrier
+      cp_async_wait<0>();
       fence_proxy_async();
       mbar_arrive(&qbar[w]);
     }
@@ -324,11 +363,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
     }
     const bool live = row < it.rows;
-    const int g = it.row0 + row, tok = it.s.first + g / G, head = it.h * G + g % G;
     const bool none = need == 0 || m == -INFINITY;
     if (it.splits == 1) {
+      // Through shared memory (the tile's queries are done with), so that a warp stores whole
+      // rows: a row per lane would touch 32 lines with every store.
       const float inv = none ? 0.f : 1.f / l;
-      bf16* dst = static_cast<bf16*>(a.out) + (live ? tok * a.o_ts + head * a.o_hs : 0);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         uint32_t o[32];
@@ -336,22 +375,33 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_ld32_nowait(to + 32 * i, o);
           tmem_wait_ld();
         }
-        if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t u[4];
+        for (int e = 0; e < 32; e += 8) {
+          uint32_t u[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float v0 = none ? 0.f : __uint_as_float(o[e + 2 * x]) * inv;
-              const float v1 = none ? 0.f : __uint_as_float(o[e + 2 * x + 1]) * inv;
-              const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
-              u[x] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(dst + 32 * i + e) = make_uint4(u[0], u[1], u[2], u[3]);
+          for (int x = 0; x < 4; ++x) {
+            const float v0 = none ? 0.f : __uint_as_float(o[e + 2 * x]) * inv;
+            const float v1 = none ? 0.f : __uint_as_float(o[e + 2 * x + 1]) * inv;
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
+            u[x] = *reinterpret_cast<const uint32_t*>(&h);
           }
+          *reinterpret_cast<uint4*>(Qs.ptr(r, 32 * i + e)) = make_uint4(u[0], u[1], u[2], u[3]);
         }
       }
-      if (live && a.lse) a.lse[(size_t)tok * p.Hq + head] = none ? -INFINITY : (m + log2f(l)) * LN2;
+      if (live && a.lse) {
+        const int g = it.row0 + row;
+        a.lse[(size_t)(it.s.first + g / G) * p.Hq + it.h * G + g % G] = none ? -INFINITY : (m + log2f(l)) * LN2;
+      }
+      __syncwarp();
+      constexpr int CH = D / 8, STEP = 32 / CH;  // rows of one store
+#pragma unroll 4
+      for (int i = 0; i < CH; ++i) {
+        const int rr = (warp & 3) * 32 + i * STEP + lane / CH, col = lane % CH * 8, g = it.row0 + w * HALF + rr;
+        if (w * HALF + rr < it.rows)
+          *reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + (it.s.first + g / G) * a.o_ts +
+                                    (long long)(it.h * G + g % G) * a.o_hs + col) =
+              *reinterpret_cast<const uint4*>(Qs.ptr(rr, col));
+      }
     } else {
       float* part = tc_part<D>(a.ws, blockIdx.x);
       if (live) {
@@ -377,8 +427,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   if (warp == MMA_WARP) {
     // ---------------------------------------------------------------- products
-    const uint32_t id_s = umma_idesc_bf16(HALF, KT), id_o = umma_idesc_bf16(HALF, D, false, true);
+    constexpr uint32_t id_s = umma_idesc_bf16(HALF, KT), id_o = umma_idesc_bf16(HALF, D, false, true);
     constexpr int PANEL = KT * 128;
+    // warp-uniform by construction, and known to be to the compiler
+    const int need[2] = {__shfl_sync(0xffffffffu, it.need[0], 0), __shfl_sync(0xffffffffu, it.need[1], 0)};
+    const int tiles = max(need[0], need[1]), keys = __shfl_sync(0xffffffffu, it.s.len - it.t0 * KT, 0);
+    const uint32_t acc = __shfl_sync(0xffffffffu, tm, 0);
+    const uint64_t dq = desc_kmajor(sm + L::Q), dring = desc_kmajor(sm + L::RING),
+                   dvring = desc_mnmajor(sm + L::RING, PANEL);
     int slot = 0;
     uint32_t phase = 0;
     auto next_slot = [&]() {
@@ -387,76 +443,64 @@ __global__ void __launch_bounds__(THREADS, 1)
         phase ^= 1;
       }
     };
-    auto scores = [&](int w, const void* ktile) {
-      if (lane == 0) {
-        const uint64_t dq = desc_kmajor(sm + L::Q + w * HALF * D * 2), dk = desc_kmajor(ktile);
+    auto scores = [&](int w, int kslot) {
+      const uint64_t q = dq + (uint64_t)(w * (HALF * D * 2 / 16)), k = dring + (uint64_t)(kslot * (L::SLOT / 16));
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          umma_bf16(tm + L::S + w * 128, kstep_kmajor(dq, ks, PANEL), kstep_kmajor(dk, ks, PANEL), id_s, ks > 0);
-        umma_commit(&sbar[w]);
-      }
-      __syncwarp();
+      for (int h = 0; h < D / 64; ++h)
+        umma4_ss(acc + L::S + w * 128, q + h * (PANEL / 16), k + h * (PANEL / 16), id_s, h > 0);
+      commit_elected(&sbar[w]);
     };
     for (int w = 0; w < 2; ++w)
-      if (it.need[w] > 0) mbar_wait(&qbar[w], 0, p.err);
+      if (need[w] > 0) mbar_wait(&qbar[w], 0, p.err);
     tc_fence_after();
-    if (n > 0) {
+    if (tiles > 0) {
       mbar_wait(&full[slot], phase, p.err);
       for (int w = 0; w < 2; ++w)
-        if (it.need[w] > 0) scores(w, sm + L::RING + slot * L::SLOT);
-      if (lane == 0) umma_commit(&empty[slot]);
+        if (need[w] > 0) scores(w, slot);
+      commit_elected(&empty[slot]);
       next_slot();
     }
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; j < tiles; ++j) {
       const int vslot = slot;
-      uint8_t* vt = sm + L::RING + vslot * L::SLOT;
       mbar_wait(&full[vslot], phase, p.err);
       next_slot();
       const int kslot = slot;
       const uint32_t kphase = phase;
-      const bool more = j + 1 < n;
+      const bool more = j + 1 < tiles;
       if (more) next_slot();
-      const int keep = it.s.len - (it.t0 + j) * KT;
+      const int keep = keys - j * KT;
       if (keep < KT) {  // rows past the length hold anything: 0 * NaN is not 0
-        Tile<bf16, KT, D> Vs{reinterpret_cast<bf16*>(vt)};
+        Tile<bf16, KT, D> Vs{reinterpret_cast<bf16*>(sm + L::RING + vslot * L::SLOT)};
         for (int q = lane; q < (KT - keep) * (D / 8); q += 32)
           *reinterpret_cast<uint4*>(Vs.ptr(keep + q / (D / 8), q % (D / 8) * 8)) = make_uint4(0u, 0u, 0u, 0u);
         fence_proxy_async();
         __syncwarp();
       }
       bool kready = false;
+#pragma unroll
       for (int w = 0; w < 2; ++w) {
-        if (j < it.need[w]) {
+        if (j < need[w]) {
           mbar_wait(&pbar[w], j & 1, p.err);
           tc_fence_after();
-          if (lane == 0) {
-            const uint64_t dv = desc_mnmajor(vt, PANEL);
+          const uint64_t v = dvring + (uint64_t)(vslot * (L::SLOT / 16));
 #pragma unroll
-            for (int ks = 0; ks < KT / 16; ++ks)
-              umma_bf16_ts(tm + L::O + w * D, tm + L::P + w * L::P_STEP + 8 * ks, kstep_mnmajor(dv, ks), id_o,
-                           (j > 0 || ks > 0) ? 1u : 0u);
-            umma_commit(&obar[w]);
-          }
-          __syncwarp();
+          for (int h = 0; h < 2; ++h)
+            umma4_ts(acc + L::O + w * D, acc + L::P + w * L::P_STEP + 32 * h, v + h * 512, id_o, (j > 0 || h > 0) ? 1u : 0u);
+          commit_elected(&obar[w]);
         }
-        if (j + 1 < it.need[w]) {
+        if (j + 1 < need[w]) {
           if (!kready) {
             mbar_wait(&full[kslot], kphase, p.err);
             kready = true;
           }
-          scores(w, sm + L::RING + kslot * L::SLOT);
+          scores(w, kslot);
         }
       }
-      if (lane == 0) {
-        umma_commit(&empty[vslot]);
-        if (more) umma_commit(&empty[kslot]);
-      }
+      commit_elected(&empty[vslot]);
+      if (more) commit_elected(&empty[kslot]);
     }
-    if (lane == 0) {
-      umma_commit(drained);
-      mbar_drain(drained, 0);
-    }
-    __syncwarp();
+    commit_elected(drained);
+    mbar_drain(drained, 0);
     tc_fence_before();
   } else if (warp == LOAD_WARP) {
     // ---------------------------------------------------------------- key and value tiles
