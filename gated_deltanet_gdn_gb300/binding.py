@@ -1,4 +1,5 @@
-"""ctypes binding of libgdn.so (include/gdn.h). Argument marshalling only.
+"""Binding of libgdn.so (include/gdn.h). Argument marshalling only: by ctypes, and compiled
+(csrc/binding_ext.cpp) for the calls that a decoding step makes in every layer.
 
 Every step of the computation runs in the library's CUDA kernels; PyTorch only
 allocates device memory and supplies the current CUDA stream. There is no CPU
@@ -7,6 +8,7 @@ or framework fallback: if the library cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from typing import Dict, Optional, Tuple
@@ -95,6 +97,7 @@ class GdnError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+_ext = None
 
 
 def load(build_if_needed: bool = True) -> ctypes.CDLL:
@@ -159,6 +162,20 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
             lib.gdn_block_norm_bwd.restype = i
             _lib = lib
     return _lib
+
+
+def _compiled():
+    """The compiled argument marshalling of the paged cache and block norm calls (csrc/binding_ext.cpp)."""
+    global _ext
+    load()
+    with _lock:
+        if _ext is None:
+            spec = importlib.util.spec_from_file_location("_gdn_ext", _build.EXT_PATH)
+            ext = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(ext)
+            ext.set_error(GdnError)
+            _ext = ext
+    return _ext
 
 
 def lib_path() -> str:
@@ -359,73 +376,17 @@ def gdn_replay_state(ckpt, buffer, fill, L: int, *, h_out=None) -> torch.Tensor:
     return h_out
 
 
-def _invalid(name: str, msg: str):
-    raise GdnError(name, GDN_ERR_INVALID_ARG, msg)
-
-
-def _on_device(t: torch.Tensor, dev: torch.device, name: str):
-    if not t.is_cuda or t.device != dev:
-        _invalid(name, f"{name} must be a CUDA tensor on {dev}")
-
-
-def _launch(dev: torch.device, fn, *args) -> int:
-    """fn(*args, stream) on dev's current stream, with dev current."""
-    if dev.index == torch.cuda.current_device():
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    with torch.cuda.device(dev):
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _steps(t: torch.Tensor, n: int):
-    """The first n strides of t, 0 for dimensions of one element (their strides mean nothing)."""
-    return [0 if a == 1 else s for a, s in zip(t.shape[:n], t.stride()[:n])]
-
-
-def _tokens(t: torch.Tensor, shape, dtype, dev, name: str) -> GdnTokens:
-    """A [N, heads, D] tensor with contiguous channels, as the C struct."""
-    if t.dim() != 3 or tuple(t.shape) != tuple(shape):
-        _invalid(name, f"{name} must be {list(shape)}, got {list(t.shape)}")
-    _on_device(t, dev, name)
-    if t.dtype != dtype:
-        _invalid(name, f"{name} must be {dtype} like the cache")
-    if t.stride(2) != 1 and t.numel() > 0:
-        _invalid(name, f"{name} must have contiguous channels")
-    return GdnTokens(t.data_ptr(), *_steps(t, 2))
-
-
-def _ints(t: torch.Tensor, shape, dev, name: str):
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
-        _invalid(name, f"{name} must be int32 {list(shape)}, got {t.dtype} {list(t.shape)}")
-    _on_device(t, dev, name)
-    if t.numel() > 1 and t.stride(-1) != 1:
-        _invalid(name, f"{name} must have contiguous rows")
-
-
-def _paged(tokens: torch.Tensor, Hq: int, k_cache, v_cache, page_table, cu_seqlens, kv_lens, flags: int = 0):
-    """(dims, cache) of the paged calls; k_cache, v_cache [pages, heads, page size, D], any strides."""
-    dev = k_cache.device
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dim() != 4 or t.shape != k_cache.shape or t.dtype != k_cache.dtype:
-            _invalid(name, f"{name} must be [pages, heads, page size, D], both caches alike")
-        _on_device(t, dev, name)
-        if t.stride(3) != 1 and t.numel() > 0:
-            _invalid(name, f"{name} must have contiguous channels")
+def make_paged_dims(q: torch.Tensor, k_cache: torch.Tensor, page_table: torch.Tensor, flags: int = 0) -> GdnPagedDims:
+    """dims of a paged call from q [N, Hq, D], k_cache [pages, Hk, page size, D] and page_table [B, pages]."""
     pages, Hk, page_size, D = k_cache.shape
-    B = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
-    if page_table.dim() != 2:
-        _invalid("page_table", "page_table must be [sequences, pages per sequence]")
-    _ints(kv_lens, (B,), dev, "kv_lens")
-    _ints(cu_seqlens, (B + 1,), dev, "cu_seqlens")
-    _ints(page_table, (B, page_table.shape[1]), dev, "page_table")
-    dims = GdnPagedDims(tokens.shape[0], B, Hq, Hk, D, page_size, pages, page_table.shape[1],
+    return GdnPagedDims(q.shape[0], page_table.shape[0], q.shape[1], Hk, D, page_size, pages, page_table.shape[1],
                         _dtype_code(k_cache.dtype), int(flags))
-    cache = GdnPagedCache(k_cache.data_ptr(), v_cache.data_ptr(), *_steps(k_cache, 3), *_steps(v_cache, 3),
-                          page_table.data_ptr(), page_table.stride(0), cu_seqlens.data_ptr(), kv_lens.data_ptr())
-    return dims, cache
+
+
+def make_norm_dims(x: torch.Tensor, eps: float = 1e-6, flags: int = 0) -> GdnNormDims:
+    """dims of a block norm call from x [rows, C] or [rows..., groups, C]."""
+    C, G = x.shape[-1], (1 if x.dim() == 2 else x.shape[-2])
+    return GdnNormDims(x.numel() // max(C * G, 1), max(G, 1), C, _dtype_code(x.dtype), int(flags), float(eps))
 
 
 def gdn_kv_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, q=None, q_out=None, cos=None,
@@ -433,33 +394,12 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, q=
     """Store packed new tokens' k, v [N, Hk, D] in the paged cache [pages, Hk, page size, D], in place;
     with cos, sin (fp32 [positions, rot / 2]) k is rotated by its position, and so is q [N, Hq, D].
     kv_lens counts the new tokens. Returns the rotated q (q_out, which may be q), or None without q."""
-    dev, dt = k_cache.device, k_cache.dtype
-    Hq = k_cache.shape[1] if q is None or q.dim() != 3 else q.shape[1]
-    dims, cache = _paged(k, Hq, k_cache, v_cache, page_table, cu_seqlens, kv_lens, flags)
-    shape = (dims.N, dims.Hk, dims.D)
-    ks, vs = _tokens(k, shape, dt, dev, "k"), _tokens(v, shape, dt, dev, "v")
-    qs = qo = None
-    if q is not None:
-        qs = _tokens(q, (dims.N, Hq, dims.D), dt, dev, "q")
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dt, device=dev)
-        qo = _tokens(q_out, q.shape, dt, dev, "q_out")
-    positions = rot = 0
-    if (cos is None) != (sin is None):
-        _invalid("cos", "cos and sin go together")
-    if cos is not None:
-        for name, t in (("cos", cos), ("sin", sin)):
-            if t.dim() != 2 or t.shape != cos.shape or t.dtype != torch.float32 or not t.is_contiguous():
-                _invalid(name, f"{name} must be a contiguous float32 [positions, rot / 2] table")
-            _on_device(t, dev, name)
-        positions, rot = cos.shape[0], 2 * cos.shape[1]
-    st = _launch(dev, load().gdn_kv_append, dims, cache, ks, vs, qs, qo, _addr(cos), _addr(sin), positions, rot)
-    _check("gdn_kv_append", st)
-    return None if q is None else q_out
+    return (_ext or _compiled()).kv_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, q, q_out, cos,
+                                           sin, flags)
 
 
 def gdn_paged_attn_workspace_bytes(dims: GdnPagedDims, max_q: int, max_kv: int) -> int:
-    return int(load().gdn_paged_attn_workspace_bytes(dims, int(max_q), int(max_kv)))
+    return int(load().gdn_paged_attn_workspace_bytes(ctypes.byref(dims), int(max_q), int(max_kv)))
 
 
 def gdn_paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, scale: Optional[float] = None, *,
@@ -469,122 +409,28 @@ def gdn_paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, scale: 
     appended to. max_q, max_kv: the caller's bounds on new tokens and length of one sequence (they
     choose the kernel and its split; without them the largest possible are taken). lse: optional fp32
     [N, Hq] output, the log of each row's softmax sum. Returns out [N, Hq, D]."""
-    dev, dt = k_cache.device, k_cache.dtype
-    if q.dim() != 3:
-        _invalid("q", "q must be [N, heads, D]")
-    dims, cache = _paged(q, q.shape[1], k_cache, v_cache, page_table, cu_seqlens, kv_lens)
-    qs = _tokens(q, (dims.N, dims.Hq, dims.D), dt, dev, "q")
-    if scale is None:
-        scale = dims.D ** -0.5
-    if out is None:
-        out = torch.empty(q.shape, dtype=dt, device=dev)
-    os_ = _tokens(out, q.shape, dt, dev, "out")
-    if lse is not None:
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (dims.N, dims.Hq) or not lse.is_contiguous():
-            _invalid("lse", "lse must be a contiguous float32 [N, Hq]")
-        _on_device(lse, dev, "lse")
-    if max_q is None:
-        max_q = max(dims.N, 1)
-    if max_kv is None:
-        max_kv = max(min(dims.max_pages * dims.page_size, 2 ** 31 - 1), 1)
-    lib = load()
-    need = lib.gdn_paged_attn_workspace_bytes(dims, int(max_q), int(max_kv))
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    else:
-        _on_device(workspace, dev, "workspace")
-        if workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
-            _invalid("workspace", f"workspace must be contiguous and hold {need} bytes")
-    st = _launch(dev, lib.gdn_paged_attn, dims, cache, qs, float(scale), int(max_q), int(max_kv), os_, _addr(lse),
-                 workspace.data_ptr())
-    _check("gdn_paged_attn", st)
-    return out
-
-
-def _rows(t: Optional[torch.Tensor], like: torch.Tensor, name: str) -> GdnRows:
-    """A tensor of x's shape as rows [R, G, C] with contiguous channels (a 2-D tensor has G = 1)."""
-    if t is None:
-        return GdnRows(None, 0, 0)
-    if t.shape != like.shape or t.dtype != like.dtype:
-        _invalid(name, f"{name} must be {like.dtype} {list(like.shape)}, got {t.dtype} {list(t.shape)}")
-    _on_device(t, like.device, name)
-    if t.numel() == 0:
-        return GdnRows(t.data_ptr(), 0, 0)
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
-        _invalid(name, f"{name} must have contiguous channels")
-    if t.dim() == 2:
-        return GdnRows(t.data_ptr(), _steps(t, 1)[0], 0)
-    if t.dim() > 3:
-        try:
-            t = t.view(-1, t.shape[-2], t.shape[-1])
-        except RuntimeError:
-            _invalid(name, f"the leading dimensions of {name} must fold into one")
-    return GdnRows(t.data_ptr(), *_steps(t, 2))
-
-
-def _norm_parts(x, gate, residual, w_post, res_scale, w_pre, eps, flags):
-    if x.dim() < 2:
-        _invalid("x", "x must be [rows, C] or [rows..., groups, C]")
-    C, G = x.shape[-1], (1 if x.dim() == 2 else x.shape[-2])
-    R = x.numel() // (C * G) if x.numel() else 0
-    for name, w in (("w_post", w_post), ("res_scale", res_scale), ("w_pre", w_pre)):
-        if w is None:
-            continue
-        if tuple(w.shape) != (C,) or w.dtype != x.dtype or not w.is_contiguous():
-            _invalid(name, f"{name} must be a contiguous {x.dtype} [{C}]")
-        _on_device(w, x.device, name)
-    dims = GdnNormDims(R, max(G, 1), C, _dtype_code(x.dtype), int(flags), float(eps))
-    parts = GdnNormParts(_rows(x, x, "x"), _rows(gate, x, "gate"), _rows(residual, x, "residual"), _addr(w_post),
-                         _addr(res_scale), _addr(w_pre))
-    return dims, parts
+    return (_ext or _compiled()).paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, scale, max_q,
+                                            max_kv, out, lse, workspace)
 
 
 def gdn_block_norm_fwd(x, *, gate=None, residual=None, w_post=None, res_scale=None, w_pre=None, eps: float = 1e-6,
                        flags: int = 0):
     """h = residual + res_scale * (norm(x) * w_post * act(gate)) and y = norm(h) * w_pre, every part
     optional; the norm is over the last dimension. Returns (h, y or None, stats)."""
-    dims, parts = _norm_parts(x, gate, residual, w_post, res_scale, w_pre, eps, flags)
-    dev = x.device
-    _on_device(x, dev, "x")
-    h = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if w_pre is not None else None
-    stats = torch.empty((dims.R, dims.G, 2), dtype=torch.float32, device=dev)
-    st = _launch(dev, load().gdn_block_norm_fwd, dims, parts, h.data_ptr(), _addr(y), stats.data_ptr())
-    _check("gdn_block_norm_fwd", st)
-    return h, y, stats
+    return (_ext or _compiled()).block_norm_fwd(x, gate, residual, w_post, res_scale, w_pre, eps, flags)
 
 
 def gdn_block_norm_workspace_bytes(dims: GdnNormDims) -> int:
-    return int(load().gdn_block_norm_workspace_bytes(dims))
+    return int(load().gdn_block_norm_workspace_bytes(ctypes.byref(dims)))
 
 
 def gdn_block_norm_bwd(x, stats, dh, dy=None, *, gate=None, residual=None, w_post=None, res_scale=None, w_pre=None,
                        eps: float = 1e-6, flags: int = 0, workspace=None) -> Dict[str, Optional[torch.Tensor]]:
     """Gradients of gdn_block_norm_fwd from dh (or None) and dy (with w_pre): dx, dgate, dresidual,
     dw_post, dres_scale, dw_pre in the inputs' dtype, None for absent parts."""
-    dims, parts = _norm_parts(x, gate, residual, w_post, res_scale, w_pre, eps, flags)
-    dev = x.device
-    _on_device(x, dev, "x")
-    if stats.dtype != torch.float32 or tuple(stats.shape) != (dims.R, dims.G, 2) or not stats.is_contiguous():
-        _invalid("stats", "stats must be the forward's")
-    _on_device(stats, dev, "stats")
-    rh, ry = _rows(dh, x, "dh"), _rows(dy, x, "dy")
-    given = dict(dx=x, dgate=gate, dresidual=residual, dw_post=w_post, dres_scale=res_scale, dw_pre=w_pre)
-    new = torch.zeros if dims.R == 0 else torch.empty  # no rows: nothing is launched, the sums are zero
-    grads = {n: None if t is None else new(t.shape, dtype=t.dtype, device=dev) for n, t in given.items()}
-    lib = load()
-    need = lib.gdn_block_norm_workspace_bytes(dims)
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    else:
-        _on_device(workspace, dev, "workspace")
-        if workspace.numel() * workspace.element_size() < need or not workspace.is_contiguous():
-            _invalid("workspace", f"workspace must be contiguous and hold {need} bytes")
-    st = _launch(dev, lib.gdn_block_norm_bwd, dims, parts, stats.data_ptr(), rh if dh is not None else None,
-                 ry if dy is not None else None, GdnNormGrads(*(_addr(t) for t in grads.values())),
-                 workspace.data_ptr())
-    _check("gdn_block_norm_bwd", st)
-    return grads
+    grads = (_ext or _compiled()).block_norm_bwd(x, stats, dh, dy, gate, residual, w_post, res_scale, w_pre, eps,
+                                                 flags, workspace)
+    return dict(zip(("dx", "dgate", "dresidual", "dw_post", "dres_scale", "dw_pre"), grads))
 
 
 def gdn_selftest_wait_timeout(max_tries: int = 1024, device: Optional[torch.device] = None,
