@@ -186,12 +186,14 @@ int gdn_block_norm_fwd(const gdn_norm_dims* d, const gdn_norm_parts* parts, void
   if (!aligned(h, 16) || !aligned(y, 16)) wide = false;
   NormArgs a = norm_args(d, parts);
   a.h = h; a.y = y; a.stats = stats;
+  a.err = device_error_word();
+  if (!a.err) return GDN_ERR_CUDA;
   return launch_status(launch_block_norm(a, wide, false, static_cast<cudaStream_t>(stream)));
 }
 
 size_t gdn_block_norm_workspace_bytes(const gdn_norm_dims* d) {
   if (check_norm(d) != GDN_OK || d->R == 0) return 0;
-  return (size_t)NORM_BWD_PARTS * 3 * d->C * sizeof(float);
+  return (size_t)norm_bwd_parts(d->C) * 3 * d->C * sizeof(float);
 }
 
 int gdn_block_norm_bwd(const gdn_norm_dims* d, const gdn_norm_parts* parts, const float* stats, const gdn_rows* dh,
@@ -229,6 +231,8 @@ int gdn_block_norm_bwd(const gdn_norm_dims* d, const gdn_norm_parts* parts, cons
   a.dx = grads->dx; a.dgate = grads->dgate; a.dresidual = grads->dresidual;
   a.dw_post = grads->dw_post; a.dres_scale = grads->dres_scale; a.dw_pre = grads->dw_pre;
   a.partial = static_cast<float*>(workspace);
+  a.err = device_error_word();
+  if (!a.err) return GDN_ERR_CUDA;
   return launch_status(launch_block_norm(a, wide, true, static_cast<cudaStream_t>(stream)));
 }
 

@@ -236,7 +236,13 @@ struct ReplayStateArgs {
 // groups of C elements, R * G < 2^31, C <= NORM_MAX_WIDTH. Input strides in elements, row
 // then group; outputs contiguous. Optional parts are NULL.
 constexpr int NORM_MAX_WIDTH = 8192;
-constexpr int NORM_BWD_PARTS = 304;  // most CTAs of the backward: two per SM of 152
+constexpr int NORM_CTAS_PER_SM = 8;
+// Most CTAs of the backward (rows of partial weight gradients): several per SM of 152 for
+// narrow rows, one for wide ones.
+inline int norm_bwd_parts(int C) {
+  const int per_sm = 6144 / C;
+  return 152 * (per_sm < 1 ? 1 : per_sm > NORM_CTAS_PER_SM ? NORM_CTAS_PER_SM : per_sm);
+}
 struct NormArgs {
   int R, G, C, bf16, sigmoid;
   float eps;
@@ -245,7 +251,8 @@ struct NormArgs {
   float* stats;  // [R*G][2]: r1, r2
   void *h, *y;
   void *dx, *dgate, *dresidual, *dw_post, *dres_scale, *dw_pre;
-  float* partial;  // [NORM_BWD_PARTS][3][C]
+  float* partial;  // [norm_bwd_parts(C)][3][C]
+  unsigned* err;
 };
 
 // Paged key/value cache and the new tokens of B sequences (kv_append.cu, paged_attn.cu).
