@@ -16,8 +16,8 @@
 // Every input is read once. Three forms, by the width of a row:
 //  * narrow rows (up to 32 vectors of 16 bytes; the norm of a head): a part of a warp per
 //    row, reductions by shuffle, the next row's vectors loaded while this one's are used;
-//  * wide rows: persistent CTAs, one row at a time with 16 bytes of it per thread, the
-//    inputs of the next rows on their way through a ring in shared memory (bulk copies);
+//  * wide rows: persistent CTAs, one row at a time, the inputs of the next rows on their
+//    way through a ring in shared memory (bulk copies by a warp of their own);
 //  * rows whose width, strides or pointers do not allow 16-byte accesses: element by
 //    element, a CTA (or a warp) per row.
 // The sums over rows of the weight gradients stay in the registers of the threads that own
@@ -456,50 +456,98 @@ __global__ void __launch_bounds__(SUB ? SUB_THREADS : NORM_THREADS_MAX, HEAD ? 3
 }
 
 // ---------------------------------------------------------------- wide rows
-// Sum over the CTA of one value per thread. buf: 32 floats; successive sums alternate between
-// two of them, so that a barrier lies between the reads of one and its next writes.
-__device__ __forceinline__ float cta_sum(float v, float* buf) {
+// Packed fp32 pairs: one instruction does the fp32 operation on both halves, each rounded
+// as the scalar one. The wide kernels are close to the issue rate, which this halves for
+// most of their arithmetic.
+typedef uint64_t f2;
+__device__ __forceinline__ f2 pk(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpk(f2 r, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r)); }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// 16 bytes as pairs, and back (one rounding).
+__device__ __forceinline__ void pairs_of(const uint4& u, f2 (&x)[4], const bf16*) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int w = 0, nw = blockDim.x >> 5; w < nw; w += 4) {  // unused slots hold zeros
-    const float4 b = *reinterpret_cast<const float4*>(buf + w);
-    s += (b.x + b.y) + (b.z + b.w);
+  for (int i = 0; i < 4; ++i) x[i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void pairs_of(const uint4& u, f2 (&x)[2], const float*) {
+  x[0] = pk(__uint_as_float(u.x), __uint_as_float(u.y));
+  x[1] = pk(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ uint4 rounded(const f2 (&x)[4], const bf16*) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpk(x[i], lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  return s;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 rounded(const f2 (&x)[2], const float*) {
+  float a, b, c, d;
+  unpk(x[0], a, b);
+  unpk(x[1], c, d);
+  return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+}
+// act(g) and act'(g) of a pair, as `activation`.
+__device__ __forceinline__ void activation2(f2 g, int sigmoid, f2& a, f2& d) {
+  if (!sigmoid) {
+    const f2 one = pk(1.f, 1.f);
+    float t0, t1;
+    unpk(mul2(g, pk(-1.4426950408889634f, -1.4426950408889634f)), t0, t1);
+    unpk(add2(pk(ex2_approx(t0), ex2_approx(t1)), one), t0, t1);
+    const f2 s = pk(rcp_approx(t0), rcp_approx(t1));
+    a = mul2(g, s);
+    d = mul2(s, fma2(g, fma2(s, pk(-1.f, -1.f), one), one));
+  } else {
+    float g2[2], a2[2], d2[2];
+    unpk(g, g2[0], g2[1]);
+    activation<2>(g2, 1, a2, d2);
+    a = pk(a2[0], a2[1]);
+    d = pk(d2[0], d2[1]);
+  }
 }
 
 constexpr int MAX_STAGES = 8;
 struct StreamShared {
   float buf[2][32];
-  uint64_t bar[MAX_STAGES];
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES];
 };
 constexpr int STREAM_HEAD = 512;  // bytes of StreamShared before the ring
 static_assert(sizeof(StreamShared) <= STREAM_HEAD, "barriers and sums before the ring");
 
-// The ring of a persistent CTA: stage s holds the inputs of one row, `tensors` rows of
-// `bytes` each. Thread 0 issues; a stage is filled again after the first barrier of the row
-// after the one that used it, which every thread reaches with that one behind it.
-struct Ring {
-  uint8_t* base;
-  uint64_t* bar;
-  const char* src[5];
-  long long rs[5], gs[5];  // bytes
-  int tensors, stages;
-  uint32_t bytes;
-  __device__ __forceinline__ void load(unsigned row, unsigned G, int stage) const {
-    mbar_arrive_expect_tx(&bar[stage], (uint32_t)tensors * bytes);
-    const long long r = row / G, g = row % G;
-    for (int t = 0; t < tensors; ++t)
-      bulk_g2s(base + ((size_t)stage * tensors + t) * bytes, src[t] + r * rs[t] + g * gs[t], bytes, &bar[stage]);
-  }
-};
-
-template <class T, int NV, int MAXT, bool BWD>
-__global__ void __launch_bounds__(MAXT, BWD || MAXT > 384 ? 1 : 2) block_norm_stream_kernel(NormArgs a, int stages) {
-  constexpr int VEC = 16 / (int)sizeof(T);
+// A persistent CTA: one warp (the last) fills a ring of `stages` rows, each the row's
+// vectors of up to five inputs (bulk copies); the others take a row at a time, NV vectors
+// of 16 bytes of it per thread. Two sums over the row each way, a barrier each.
+//
+// SPLIT: the backward of the widest rows, whose column sums and row values take more
+// registers than an equal share: the workers are whole warpgroups and take some of the
+// filling warpgroup's (384 of them: 3 * 160 + 32 = 4 * 128; 512: 4 * 112 + 32 = 5 * 96).
+constexpr int SPLIT_LOW = 32;
+constexpr int split_high(int maxt) { return maxt == 384 ? 160 : 112; }
+template <class T, int NV, int MAXT, bool BWD, bool SPLIT>
+__global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ? 1 : 2)
+    block_norm_stream_kernel(NormArgs a, int stages) {
+  constexpr int VEC = 16 / (int)sizeof(T), NP = VEC / 2;
   pdl_wait();
   extern __shared__ __align__(128) uint8_t smem[];
   StreamShared* sh = reinterpret_cast<StreamShared*>(smem);
@@ -510,276 +558,303 @@ __global__ void __launch_bounds__(MAXT, BWD || MAXT > 384 ? 1 : 2) block_norm_st
   const int tr = a.residual && (!BWD || pre) ? nt++ : 0;
   const int th = BWD && a.dh ? nt++ : 0;
   const int ty = BWD && pre ? nt++ : 0;
-  Ring ring;
+  const int workers = blockDim.x - (SPLIT ? 128 : 32);
+  const uint32_t bytes = (uint32_t)a.C * sizeof(T);
+  const uint32_t ring = STREAM_HEAD + (BWD ? 3 * bytes : 0);  // offset of the ring
+  const unsigned rows = (unsigned)a.R * (unsigned)a.G, grid = gridDim.x;
+  const T* kind = nullptr;  // names the type for the packing functions
+  for (int i = threadIdx.x; i < 64; i += blockDim.x) (&sh->buf[0][0])[i] = 0.f;
   if (threadIdx.x == 0) {
-    ring.base = smem + STREAM_HEAD;
-    ring.bar = sh->bar;
-    ring.tensors = nt;
-    ring.stages = stages;
-    ring.bytes = (uint32_t)a.C * sizeof(T);
-    auto put = [&](int t, const void* p, long long rs, long long gs) {
-      ring.src[t] = static_cast<const char*>(p);
-      ring.rs[t] = rs * (long long)sizeof(T);
-      ring.gs[t] = gs * (long long)sizeof(T);
-    };
-    put(0, a.x, a.x_rs, a.x_gs);
-    if (tg) put(tg, a.gate, a.gate_rs, a.gate_gs);
-    if (tr) put(tr, a.residual, a.res_rs, a.res_gs);
-    if (th) put(th, a.dh, a.dh_rs, a.dh_gs);
-    if (ty) put(ty, a.dy, a.dy_rs, a.dy_gs);
-    for (int i = 0; i < stages; ++i) mbar_init(&sh->bar[i], 1);
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], workers / 32);
+    }
     fence_mbar_init();
   }
-  for (int i = threadIdx.x; i < 64; i += blockDim.x) (&sh->buf[0][0])[i] = 0.f;
   __syncthreads();
-  const unsigned rows = (unsigned)a.R * (unsigned)a.G, G = a.G, grid = gridDim.x;
-  if (threadIdx.x == 0)
-    for (int i = 0; i < stages; ++i)
-      if (blockIdx.x + (size_t)i * grid < rows) ring.load(blockIdx.x + i * grid, G, i);
 
-  // this thread's columns, and their weights
-  const int col0 = threadIdx.x * VEC, cstep = blockDim.x * VEC;
-  Raw<T, VEC> w1[NV], w2[NV], ws[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = col0 + i * cstep;
-    w1[i].clear(); w2[i].clear(); ws[i].clear();
-    if (c < a.C) {
-      if (post) w1[i].load(static_cast<const T*>(a.w_post) + c);
-      if (pre) w2[i].load(static_cast<const T*>(a.w_pre) + c);
-      if (scaled) ws[i].load(static_cast<const T*>(a.res_scale) + c);
+  if ((int)threadIdx.x >= workers) {
+    if constexpr (SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SPLIT_LOW));
+    if ((int)threadIdx.x == workers) {
+      int stage = 0, loads = 0;
+      for (size_t row = blockIdx.x; row < rows; row += grid, ++loads) {
+        if (loads >= stages) mbar_wait(&sh->empty[stage], (uint32_t)(loads / stages - 1) & 1u, a.err);
+        mbar_arrive_expect_tx(&sh->full[stage], (uint32_t)nt * bytes);
+        uint8_t* dst = smem + ring + (size_t)stage * nt * bytes;
+        const long long r = (unsigned)row / (unsigned)a.G, g = (unsigned)row % (unsigned)a.G;
+        auto copy = [&](int t, const void* p, long long rs, long long gs) {
+          bulk_g2s(dst + (size_t)t * bytes, static_cast<const T*>(p) + r * rs + g * gs, bytes, &sh->full[stage]);
+        };
+        copy(0, a.x, a.x_rs, a.x_gs);
+        if (tg) copy(tg, a.gate, a.gate_rs, a.gate_gs);
+        if (tr) copy(tr, a.residual, a.res_rs, a.res_gs);
+        if (th) copy(th, a.dh, a.dh_rs, a.dh_gs);
+        if (ty) copy(ty, a.dy, a.dy_rs, a.dy_gs);
+        if (++stage == stages) stage = 0;
+      }
+      drain_ring(sh->full, stages, loads);
     }
+    return;
   }
-  float sw1[NV][VEC], sw2[NV][VEC], ssc[NV][VEC];  // backward: sums over this CTA's rows
-  if (BWD) {
+
+  if constexpr (SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(split_high(MAXT)));
+
+  // Sum over the workers. Successive sums alternate between two buffers, so that a barrier
+  // lies between the reads of one and its next writes; slots of absent warps hold zeros.
+  int flip = 0;
+  auto total = [&](f2 v2) {
+    float v, hi;
+    unpk(v2, v, hi);
+    v += hi;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    float* buf = sh->buf[flip ^= 1];
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    asm volatile("bar.sync 1, %0;" ::"r"(workers) : "memory");
+    float s = 0.f;
+    for (int w = 0; w < workers / 32; w += 4) {
+      const float4 b = *reinterpret_cast<const float4*>(buf + w);
+      s += (b.x + b.y) + (b.z + b.w);
+    }
+    return s;
+  };
+  // this thread's columns, and their weights: in registers, or in the backward (whose sums
+  // take them) in shared memory before the ring, each thread its own
+  const int col0 = threadIdx.x * VEC, cstep = workers * VEC;
+  uint4 wreg[BWD ? 1 : 3][NV];
+  const void* const wsrc[3] = {a.w_post, a.w_pre, a.res_scale};
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) sw1[i][e] = sw2[i][e] = ssc[i][e] = 0.f;
-  }
+  for (int t = 0; t < 3; ++t)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = col0 + i * cstep;
+      uint4 u = make_uint4(0u, 0u, 0u, 0u);
+      if (c < a.C && wsrc[t]) u = *reinterpret_cast<const uint4*>(static_cast<const T*>(wsrc[t]) + c);
+      if constexpr (!BWD) wreg[t][i] = u;
+      else if (c < a.C) *reinterpret_cast<uint4*>(smem + STREAM_HEAD + (size_t)t * bytes + c * sizeof(T)) = u;
+    }
+  enum { POST = 0, PRE = 1, SCALE = 2 };
+  auto weight = [&](int t, int i, int c, f2 (&w)[NP]) {
+    if constexpr (!BWD) pairs_of(wreg[t][i], w, kind);
+    else pairs_of(*reinterpret_cast<const uint4*>(smem + STREAM_HEAD + (size_t)t * bytes + c * sizeof(T)), w, kind);
+  };
+  const f2 zero2 = pk(0.f, 0.f);
+  f2 sw1[NV][NP], sw2[NV][NP], ssc[NV][NP];  // backward: sums over this CTA's rows
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < NP; ++e) sw1[i][e] = sw2[i][e] = ssc[i][e] = zero2;
   const float invC = 1.f / (float)a.C;
-  int stage = 0, flip = 0;
+  int stage = 0;
   uint32_t phase = 0;
-  bool first = true;
   float2 st_next = make_float2(1.f, 1.f);
   if (BWD && blockIdx.x < rows) st_next = *reinterpret_cast<const float2*>(a.stats + 2 * (size_t)blockIdx.x);
   for (size_t row = blockIdx.x; row < rows; row += grid) {
-    const int used = stage;  // this row's stage
-    bool refill = !first;
-    first = false;
-    auto after_barrier = [&]() {
-      if (refill && threadIdx.x == 0) {
-        const size_t next = row + (size_t)(stages - 1) * grid;
-        if (next < rows) ring.load((unsigned)next, G, used == 0 ? stages - 1 : used - 1);
-      }
-      refill = false;
-    };
     const float2 st = st_next;
     if (BWD && row + grid < rows) st_next = *reinterpret_cast<const float2*>(a.stats + 2 * (row + grid));
-    // with one stage the row's data cannot be on its way yet; with no sums there is no other barrier
-    if (stages == 1 || !(post || pre)) {
-      __syncthreads();
-      after_barrier();
-    }
-    mbar_wait(&sh->bar[stage], phase, a.err);
-    const uint8_t* in = smem + STREAM_HEAD + (size_t)stage * nt * a.C * sizeof(T);
-    if (++stage == stages) {
-      stage = 0;
-      phase ^= 1;
-    }
-    auto fetch = [&](int t, int c, float (&v)[VEC]) {
-      Raw<T, VEC> r;
-      r.load(reinterpret_cast<const T*>(in + (size_t)t * a.C * sizeof(T)) + c);
-      r.get(v);
+    mbar_wait(&sh->full[stage], phase, a.err);
+    const uint8_t* in = smem + ring + (size_t)stage * nt * bytes;
+    auto fetch = [&](int t, int c, f2 (&v)[NP]) {
+      pairs_of(*reinterpret_cast<const uint4*>(in + (size_t)t * bytes + c * sizeof(T)), v, kind);
+    };
+    auto release = [&]() {  // the warp has read its part of the stage
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&sh->empty[stage]);
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1;
+      }
     };
     if constexpr (!BWD) {
       float r1 = 1.f, r2 = 1.f;
       if (post) {
-        float ss = 0.f;
+        f2 ss = zero2;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = col0 + i * cstep;
           if (c >= a.C) continue;
-          float x[VEC];
+          f2 x[NP];
           fetch(0, c, x);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) ss = fmaf(x[e], x[e], ss);
+          for (int e = 0; e < NP; ++e) ss = fma2(x[e], x[e], ss);
         }
-        r1 = rsqrtf(cta_sum(ss, sh->buf[flip ^= 1]) * invC + a.eps);
-        after_barrier();
+        r1 = rsqrtf(total(ss) * invC + a.eps);
       }
-      float h[NV][VEC], hh = 0.f;
+      const f2 r1p = pk(r1, r1);
+      f2 h[NV][NP], hh = zero2;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = col0 + i * cstep;
         if (c >= a.C) continue;
-        float w[VEC];
+        f2 w[NP];
         fetch(0, c, h[i]);
         if (post) {
-          w1[i].get(w);
+          weight(POST, i, c, w);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) h[i][e] *= r1 * w[e];
+          for (int e = 0; e < NP; ++e) h[i][e] = mul2(mul2(h[i][e], r1p), w[e]);
         }
         if (gated) {
-          float ac[VEC], ad[VEC];
           fetch(tg, c, w);
-          activation<VEC>(w, a.sigmoid, ac, ad);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) h[i][e] *= ac[e];
+          for (int e = 0; e < NP; ++e) {
+            f2 ac, ad;
+            activation2(w[e], a.sigmoid, ac, ad);
+            h[i][e] = mul2(h[i][e], ac);
+          }
         }
         if (scaled) {
-          ws[i].get(w);
+          weight(SCALE, i, c, w);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) h[i][e] *= w[e];
+          for (int e = 0; e < NP; ++e) h[i][e] = mul2(h[i][e], w[e]);
         }
         if (tr) {
           fetch(tr, c, w);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) h[i][e] += w[e];
+          for (int e = 0; e < NP; ++e) h[i][e] = add2(h[i][e], w[e]);
         }
-        Raw<T, VEC> raw;
-        raw.set(h[i]);
-        raw.store(static_cast<T*>(a.h) + row * a.C + c);
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.h) + row * a.C + c) = rounded(h[i], kind);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) hh = fmaf(h[i][e], h[i][e], hh);
+        for (int e = 0; e < NP; ++e) hh = fma2(h[i][e], h[i][e], hh);
       }
+      release();
       if (pre) {
-        r2 = rsqrtf(cta_sum(hh, sh->buf[flip ^= 1]) * invC + a.eps);
-        after_barrier();
+        r2 = rsqrtf(total(hh) * invC + a.eps);
+        const f2 r2p = pk(r2, r2);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = col0 + i * cstep;
           if (c >= a.C) continue;
-          float w[VEC];
-          w2[i].get(w);
+          f2 w[NP];
+          weight(PRE, i, c, w);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) w[e] *= h[i][e] * r2;
-          Raw<T, VEC> raw;
-          raw.set(w);
-          raw.store(static_cast<T*>(a.y) + row * a.C + c);
+          for (int e = 0; e < NP; ++e) w[e] = mul2(mul2(h[i][e], r2p), w[e]);
+          *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * a.C + c) = rounded(w, kind);
         }
       }
       if (threadIdx.x == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(r1, r2);
     } else {
       const float r1 = post ? st.x : 1.f, r2 = pre ? st.y : 1.f;
-      float h[NV][VEC], ac[NV][VEC], nd[NV][VEC];  // h, act(gate), n act'(gate)
-      float c2 = 0.f, s2 = 0.f;
+      const f2 r1p = pk(r1, r1), r2p = pk(r2, r2);
+      f2 h[NV][NP], ac[NV][NP], nd[NV][NP];  // h, act(gate), n act'(gate)
+      f2 s2 = zero2;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = col0 + i * cstep;
         if (c >= a.C) continue;
-        float n[VEC], w[VEC];
+        f2 n[NP], w[NP];
         fetch(0, c, n);
         if (post) {
-          w1[i].get(w);
+          weight(POST, i, c, w);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) n[e] *= r1 * w[e];
+          for (int e = 0; e < NP; ++e) n[e] = mul2(mul2(n[e], r1p), w[e]);
         }
         if (gated) {
           fetch(tg, c, w);
-          activation<VEC>(w, a.sigmoid, ac[i], nd[i]);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) nd[i][e] *= n[e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            ac[i][e] = 1.f;
-            nd[i][e] = 0.f;
+          for (int e = 0; e < NP; ++e) {
+            f2 ad;
+            activation2(w[e], a.sigmoid, ac[i][e], ad);
+            nd[i][e] = mul2(n[e], ad);
+            n[e] = mul2(n[e], ac[i][e]);  // m
           }
         }
         if (ty) {
-          float dy[VEC];
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) h[i][e] = n[e] * ac[i][e];
+          f2 dy[NP];
           if (scaled) {
-            ws[i].get(w);
+            weight(SCALE, i, c, w);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) h[i][e] *= w[e];
+            for (int e = 0; e < NP; ++e) n[e] = mul2(n[e], w[e]);
           }
           if (tr) {
             fetch(tr, c, w);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) h[i][e] += w[e];
+            for (int e = 0; e < NP; ++e) n[e] = add2(n[e], w[e]);
           }
           fetch(ty, c, dy);
-          w2[i].get(w);
+          weight(PRE, i, c, w);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            s2 = fmaf(dy[e] * w[e], h[i][e], s2);
-            sw2[i][e] = fmaf(dy[e] * r2, h[i][e], sw2[i][e]);
+          for (int e = 0; e < NP; ++e) {
+            h[i][e] = n[e];
+            s2 = fma2(mul2(dy[e], w[e]), n[e], s2);
+            sw2[i][e] = fma2(mul2(dy[e], r2p), n[e], sw2[i][e]);
           }
         }
       }
+      f2 c2 = zero2;
       if (ty) {
-        c2 = cta_sum(s2, sh->buf[flip ^= 1]) * invC * r2 * r2;
-        after_barrier();
+        const float t = -total(s2) * invC * r2 * r2 * r2;
+        c2 = pk(t, t);
       }
-      float s1 = 0.f;
+      f2 s1 = zero2;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = col0 + i * cstep;
         if (c >= a.C) continue;
-        float D[VEC], x[VEC], w[VEC];
+        f2 D[NP], x[NP], w[NP];
+        if (th) {
+          fetch(th, c, D);
+        } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) D[e] = 0.f;
-        if (th) fetch(th, c, D);
+          for (int e = 0; e < NP; ++e) D[e] = zero2;
+        }
         if (ty) {
-          float dy[VEC];
+          f2 dy[NP];
           fetch(ty, c, dy);
-          w2[i].get(w);
+          weight(PRE, i, c, w);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) D[e] += r2 * (dy[e] * w[e] - h[i][e] * c2);
+          for (int e = 0; e < NP; ++e) D[e] = fma2(h[i][e], c2, fma2(mul2(dy[e], w[e]), r2p, D[e]));
         }
-        Raw<T, VEC> raw;
-        if (a.dresidual) {
-          raw.set(D);
-          raw.store(static_cast<T*>(a.dresidual) + row * a.C + c);
-        }
+        if (a.dresidual) *reinterpret_cast<uint4*>(static_cast<T*>(a.dresidual) + row * a.C + c) = rounded(D, kind);
         fetch(0, c, x);
         if (scaled) {
-          w1[i].get(w);
+          if (post) weight(POST, i, c, w);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            ssc[i][e] = fmaf(D[e] * ac[i][e], post ? x[e] * (r1 * w[e]) : x[e], ssc[i][e]);
-          ws[i].get(w);
+          for (int e = 0; e < NP; ++e) {
+            f2 m = post ? mul2(mul2(x[e], r1p), w[e]) : x[e];
+            if (gated) m = mul2(m, ac[i][e]);
+            ssc[i][e] = fma2(D[e], m, ssc[i][e]);
+          }
+          weight(SCALE, i, c, w);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) D[e] *= w[e];
+          for (int e = 0; e < NP; ++e) D[e] = mul2(D[e], w[e]);
         }
-        if (a.dgate) {
+        if (gated) {
+          if (a.dgate) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) w[e] = D[e] * nd[i][e];
-          raw.set(w);
-          raw.store(static_cast<T*>(a.dgate) + row * a.C + c);
+            for (int e = 0; e < NP; ++e) w[e] = mul2(D[e], nd[i][e]);
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.dgate) + row * a.C + c) = rounded(w, kind);
+          }
+#pragma unroll
+          for (int e = 0; e < NP; ++e) D[e] = mul2(D[e], ac[i][e]);
         }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) h[i][e] = D[e] * ac[i][e];  // now dn, then u
         if (post) {
-          w1[i].get(w);
+          weight(POST, i, c, w);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            sw1[i][e] = fmaf(h[i][e], x[e] * r1, sw1[i][e]);
-            h[i][e] *= w[e];
-            s1 = fmaf(h[i][e], x[e], s1);
+          for (int e = 0; e < NP; ++e) {
+            sw1[i][e] = fma2(D[e], mul2(x[e], r1p), sw1[i][e]);
+            D[e] = mul2(D[e], w[e]);
+            s1 = fma2(D[e], x[e], s1);
           }
         }
+#pragma unroll
+        for (int e = 0; e < NP; ++e) h[i][e] = D[e];  // now u
       }
-      float c1 = 0.f;
+      f2 c1 = zero2;
       if (post) {
-        c1 = cta_sum(s1, sh->buf[flip ^= 1]) * invC * r1 * r1;
-        after_barrier();
+        const float t = -total(s1) * invC * r1 * r1 * r1;
+        c1 = pk(t, t);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = col0 + i * cstep;
         if (c >= a.C) continue;
-        float x[VEC];
+        f2 x[NP];
         fetch(0, c, x);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x[e] = r1 * (h[i][e] - x[e] * c1);
-        Raw<T, VEC> raw;
-        raw.set(x);
-        raw.store(static_cast<T*>(a.dx) + row * a.C + c);
+        for (int e = 0; e < NP; ++e) x[e] = fma2(x[e], c1, mul2(h[i][e], r1p));
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.C + c) = rounded(x, kind);
       }
+      release();
     }
   }
   if constexpr (BWD) {
@@ -789,16 +864,13 @@ __global__ void __launch_bounds__(MAXT, BWD || MAXT > 384 ? 1 : 2) block_norm_st
       const int c = col0 + i * cstep;
       if (c >= a.C) continue;
 #pragma unroll
-      for (int e = 0; e < VEC; e += 4) {
-        if (a.dw_post) *reinterpret_cast<float4*>(part + c + e) = make_float4(sw1[i][e], sw1[i][e + 1], sw1[i][e + 2], sw1[i][e + 3]);
-        if (a.dw_pre) *reinterpret_cast<float4*>(part + a.C + c + e) = make_float4(sw2[i][e], sw2[i][e + 1], sw2[i][e + 2], sw2[i][e + 3]);
-        if (a.dres_scale) *reinterpret_cast<float4*>(part + 2 * a.C + c + e) = make_float4(ssc[i][e], ssc[i][e + 1], ssc[i][e + 2], ssc[i][e + 3]);
+      for (int e = 0; e < NP; ++e) {
+        if (a.dw_post) *reinterpret_cast<f2*>(part + c + 2 * e) = sw1[i][e];
+        if (a.dw_pre) *reinterpret_cast<f2*>(part + a.C + c + 2 * e) = sw2[i][e];
+        if (a.dres_scale) *reinterpret_cast<f2*>(part + 2 * a.C + c + 2 * e) = ssc[i][e];
       }
     }
   }
-  if (threadIdx.x == 0)  // after a failed wait copies may still be on their way
-    for (int i = 0; i < stages; ++i)
-      if (blockIdx.x + (size_t)i * grid < rows) mbar_drain(&sh->bar[i], (uint32_t)(((rows - 1 - blockIdx.x) / grid - i) / stages) & 1u);
 }
 
 // Adds the CTAs' partial rows: 32 columns per CTA, 32 threads per column over the rows (a
@@ -845,23 +917,28 @@ cudaError_t run_narrow(const NormArgs& a, bool bwd, int* parts, cudaStream_t s) 
   return head ? run<T, V, 1, SUB, true>(a, SUB_THREADS, bwd, parts, s) : run<T, V, 1, SUB, false>(a, SUB_THREADS, bwd, parts, s);
 }
 
-// Wide rows: persistent CTAs of `threads`, as many per SM as leave each a ring of two
-// stages or more and the SM its registers; the ring takes the rest of the shared memory.
-template <class T, int NV, int MAXT, bool BWD>
-cudaError_t run_stream(const NormArgs& a, int threads, int* parts, cudaStream_t s) {
+// Wide rows: persistent CTAs, as many per SM as leave each a ring of two stages or more and
+// the SM its registers; the ring takes the rest of the shared memory. *fits: whether one
+// stage does.
+template <class T, int NV, int MAXT, bool BWD, bool SPLIT>
+cudaError_t run_stream(const NormArgs& a, int* parts, bool* fits, cudaStream_t s) {
   const int nsm = device_sm_count();
   if (nsm < 1) return cudaErrorInvalidDevice;
+  constexpr int VEC = 16 / (int)sizeof(T), STEP = SPLIT ? 128 : 32, BUDGET = 226 * 1024;
+  const int workers = ((a.C / VEC + NV - 1) / NV + STEP - 1) / STEP * STEP;
   const bool pre = a.w_pre != nullptr;
   const int tensors = 1 + (a.gate != nullptr) + (a.residual && (!BWD || pre)) + (BWD && a.dh) + (BWD && pre);
-  const int stage = tensors * a.C * (int)sizeof(T), budget = 216 * 1024;
-  int per_sm = (BWD ? 384 : 768) / threads;
+  const int row = a.C * (int)sizeof(T), stage = tensors * row, head = STREAM_HEAD + (BWD ? 3 * row : 0);
+  *fits = head + stage <= BUDGET;
+  if (!*fits) return cudaSuccess;
+  int per_sm = (BWD ? 384 : 768) / workers;
   if (per_sm < 1) per_sm = 1;
   if (per_sm > NORM_CTAS_PER_SM) per_sm = NORM_CTAS_PER_SM;
-  while (per_sm > 1 && budget / per_sm < 2 * stage + STREAM_HEAD) --per_sm;
-  int stages = (budget / per_sm - STREAM_HEAD) / stage;
-  stages = stages < 1 ? 1 : stages > MAX_STAGES ? MAX_STAGES : stages;
-  const int bytes = STREAM_HEAD + stages * stage;
-  auto kern = block_norm_stream_kernel<T, NV, MAXT, BWD>;
+  while (per_sm > 1 && BUDGET / per_sm - 1024 < 2 * stage + head) --per_sm;  // 1 KB of each CTA is the system's
+  int stages = (BUDGET / per_sm - (per_sm > 1 ? 1024 : 0) - head) / stage;
+  if (stages > MAX_STAGES) stages = MAX_STAGES;
+  const int bytes = head + stages * stage;
+  auto kern = block_norm_stream_kernel<T, NV, MAXT, BWD, SPLIT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   long long grid = (long long)a.R * a.G;
@@ -869,13 +946,9 @@ cudaError_t run_stream(const NormArgs& a, int threads, int* parts, cudaStream_t 
   if (BWD && grid > norm_bwd_parts(a.C)) grid = norm_bwd_parts(a.C);
   if (BWD) *parts = (int)grid;
   prof_mark(BWD ? K_NORM_BWD : K_NORM_FWD, s, true);
-  e = launch_pdl(kern, dim3((unsigned)grid), dim3(threads), bytes, s, a, stages);
+  e = launch_pdl(kern, dim3((unsigned)grid), dim3(workers + (SPLIT ? 128 : 32)), bytes, s, a, stages);
   prof_mark(BWD ? K_NORM_BWD : K_NORM_FWD, s, false);
   return e;
-}
-template <class T, int NV, int MAXT>
-cudaError_t run_stream(const NormArgs& a, int threads, bool bwd, int* parts, cudaStream_t s) {
-  return bwd ? run_stream<T, NV, MAXT, true>(a, threads, parts, s) : run_stream<T, NV, MAXT, false>(a, threads, parts, s);
 }
 
 template <class T>
@@ -886,15 +959,24 @@ cudaError_t pick(const NormArgs& a, bool vec, bool bwd, int* parts, cudaStream_t
     if (n <= 8) return run_narrow<T, 8>(a, bwd, parts, s);
     if (n <= 16) return run_narrow<T, 16>(a, bwd, parts, s);
     if (n <= 32) return run_narrow<T, 32>(a, bwd, parts, s);
-    // two vectors per thread (four of fp32 in the widest rows): as many columns' sums as the
-    // backward's registers hold without spilling at 384 threads
-    if (n <= 768) return run_stream<T, 2, 384>(a, ((n + 1) / 2 + 31) / 32 * 32, bwd, parts, s);
-    if constexpr (sizeof(T) == 2) {
-      return run_stream<T, 2, 512>(a, ((n + 1) / 2 + 31) / 32 * 32, bwd, parts, s);
+    bool fits = false;
+    cudaError_t e = cudaSuccess;
+    if (!bwd) {
+      if (n <= 768) e = run_stream<T, 2, 384, false, false>(a, parts, &fits, s);
+      else if (n <= 1024) e = run_stream<T, 2, 512, false, false>(a, parts, &fits, s);
+      else if constexpr (sizeof(T) == 4) e = run_stream<T, 4, 512, false, false>(a, parts, &fits, s);
+    } else if constexpr (sizeof(T) == 2) {
+      // eight columns' sums per thread, or sixteen with the registers split
+      if (n <= 384) e = run_stream<T, 1, 384, true, false>(a, parts, &fits, s);
+      else if (n <= 768) e = run_stream<T, 2, 384, true, true>(a, parts, &fits, s);
+      else e = run_stream<T, 2, 512, true, true>(a, parts, &fits, s);
     } else {
-      if (n <= 1536) return run_stream<T, 4, 384>(a, ((n + 3) / 4 + 31) / 32 * 32, bwd, parts, s);
-      return run_stream<T, 4, 512>(a, ((n + 3) / 4 + 31) / 32 * 32, bwd, parts, s);
+      if (n <= 768) e = run_stream<T, 2, 384, true, false>(a, parts, &fits, s);
+      else if (n <= 1536) e = run_stream<T, 4, 384, true, true>(a, parts, &fits, s);
+      else e = run_stream<T, 4, 512, true, true>(a, parts, &fits, s);
     }
+    if (e != cudaSuccess || fits) return e;
+    // the inputs of one fp32 row above 28 KB, all parts present, exceed the shared memory
   }
   if (a.C <= 128) return run<T, 1, 4, 32, false>(a, SUB_THREADS, bwd, parts, s);
   if (a.C <= 2048) return run<T, 1, 4, 0, false>(a, ((a.C + 3) / 4 + 31) / 32 * 32, bwd, parts, s);
