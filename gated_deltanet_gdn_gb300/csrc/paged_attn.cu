@@ -27,7 +27,8 @@ constexpr int ROWS = 16, UNIT = 16;
 
 template <class T, int D>
 struct Lay {
-  static constexpr int WARPS = sizeof(T) == 2 ? 8 : 4;
+  // as many warps as the rings of three stages leave room for
+  static constexpr int WARPS = D * sizeof(T) <= 256 ? 8 : 4;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int TILE = UNIT * D * (int)sizeof(T);  // bytes of one K or V unit
   static constexpr int STAGES = 3;
@@ -36,11 +37,12 @@ struct Lay {
   static constexpr int MCOLS = 32;                         // columns merged at a time
   static constexpr int MERGE = RING + WARPS * STAGES * 2 * TILE;
   static constexpr int ML = MERGE + WARPS * ROWS * MCOLS * 4;  // float m[WARPS][16], l[WARPS][16]
-  static constexpr int BYTES = ML + 2 * WARPS * ROWS * 4;
+  static constexpr int TOT = ML + 2 * WARPS * ROWS * 4;        // float m[16], l[16] of the CTA
+  static constexpr int BYTES = TOT + 2 * ROWS * 4;
 };
 
-// Units of (sequence, KV head): sum over its items of the 16-key units their last row
-// sees, at least one each (an item without keys still writes its zeros).
+// Units of an item: the 16-key units its last row sees, at least one (an item without keys
+// still writes its zeros).
 __device__ __forceinline__ int item_units(const Seq& s, int G, int item) {
   int last = (item + 1) * ROWS - 1;
   const int rows = s.n * G;
@@ -49,9 +51,36 @@ __device__ __forceinline__ int item_units(const Seq& s, int G, int item) {
   return limit < 0 ? 1 : limit / UNIT + 1;
 }
 __device__ __forceinline__ int seq_items(const Seq& s, int G) { return (s.n * G + ROWS - 1) / ROWS; }
-__device__ __forceinline__ long long seq_units(const Seq& s, int G) {
+
+__device__ __forceinline__ long long warp_sum(long long t) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+  return t;
+}
+__device__ __forceinline__ long long warp_scan(long long t, int lane) {  // inclusive
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, t, off);
+    if (lane >= off) t += o;
+  }
+  return t;
+}
+// Units of one KV head of the sequences b0 + lane, each in its lane: by itself where all
+// have one or two items (single tokens, drafts), else the warp over each one's items.
+__device__ __forceinline__ long long lane_units(const Seq& s, int G, int lane) {
+  const int n = seq_items(s, G);
   long long u = 0;
-  for (int i = 0, n = seq_items(s, G); i < n; ++i) u += item_units(s, G, i);
+  if (!__any_sync(0xffffffffu, n > 2)) {
+    for (int i = 0; i < n; ++i) u += item_units(s, G, i);
+    return u;
+  }
+  for (int l = 0; l < 32; ++l) {
+    const Seq q{__shfl_sync(0xffffffffu, s.n, l), 0, __shfl_sync(0xffffffffu, s.len, l)};
+    long long t = 0;
+    for (int i = lane, m = seq_items(q, G); i < m; i += 32) t += item_units(q, G, i);
+    t = warp_sum(t);
+    if (lane == l) u = t;
+  }
   return u;
 }
 
@@ -61,52 +90,49 @@ struct Item {
   long long start, end;  // its units, numbered through all items
 };
 
-// The item holding unit f, for one warp (all lanes). total: every unit. f < total.
+// Every unit of the call (one warp, all lanes).
 __device__ __forceinline__ long long total_units(const PagedArgs& p, int G, int lane, bool report) {
   long long t = 0;
-  for (int b = lane; b < p.B; b += 32) {
-    const Seq s = load_seq(p, b, report);
-    t += seq_units(s, G) * p.Hk;
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-  return t;
-}
-__device__ __forceinline__ void locate(const PagedArgs& p, int G, int lane, long long f, Item& it) {
-  long long base = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    long long u = 0;
-    if (b < p.B) u = seq_units(load_seq(p, b, false), G) * p.Hk;
-    long long inc = u;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += o;
-    }
+    t += lane_units(b < p.B ? load_seq(p, b, report) : Seq{0, 0, 0}, G, lane);
+  }
+  return warp_sum(t) * p.Hk;
+}
+// The item holding unit f < total (one warp, all lanes).
+__device__ __forceinline__ void locate(const PagedArgs& p, int G, int lane, long long f, Item& it) {
+  long long base = 0, per = 1;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    const Seq s = b < p.B ? load_seq(p, b, false) : Seq{0, 0, 0};
+    const long long u = lane_units(s, G, lane), inc = warp_scan(u * p.Hk, lane);
     const unsigned hit = __ballot_sync(0xffffffffu, base + inc > f);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      base += __shfl_sync(0xffffffffu, inc - u, l);
+      base += __shfl_sync(0xffffffffu, inc - u * p.Hk, l);
+      per = __shfl_sync(0xffffffffu, u, l);
       it.b = b0 + l;
+      it.s = Seq{__shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.first, l), __shfl_sync(0xffffffffu, s.len, l)};
       break;
     }
     base += __shfl_sync(0xffffffffu, inc, 31);
   }
-  it.s = load_seq(p, it.b, false);
-  const long long per = seq_units(it.s, G);
-  long long rem = f - base;
-  it.h = (int)(rem / per);
-  rem -= it.h * per;
-  it.i = 0;
-  long long at = 0;
-  int u = item_units(it.s, G, 0);
-  while (at + u <= rem) {
-    at += u;
-    u = item_units(it.s, G, ++it.i);
+  it.h = (int)((f - base) / per);
+  base += it.h * per;
+  const int n = seq_items(it.s, G);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int u = i0 + lane < n ? item_units(it.s, G, i0 + lane) : 0;
+    const long long inc = warp_scan(u, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, base + inc > f);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      it.i = i0 + l;
+      it.end = base + __shfl_sync(0xffffffffu, inc, l);
+      it.start = it.end - __shfl_sync(0xffffffffu, u, l);
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
   }
-  it.start = f - rem + at;
-  it.end = it.start + u;
 }
 // The next item in the numbering (not called past the last).
 __device__ __forceinline__ void next_item(const PagedArgs& p, int G, Item& it) {
@@ -132,10 +158,20 @@ __device__ __forceinline__ int active_ctas(long long total, int grid, int warps)
   return most < grid ? (int)most : grid;
 }
 
-// Two-slot partial of a CTA in the workspace: o [16][D] relative to m, then m [16], l [16].
+// The parts of a CTA in the workspace: slot 0 for an item that began in an earlier CTA,
+// slot 1 for one that begins here and goes on. o [16][D] relative to m, then m [16], l [16].
 template <int D>
 __device__ __forceinline__ float* part_slot(float* ws, int cta, int second) {
   return ws + (size_t)(2 * cta + second) * (ROWS * D + 2 * ROWS);
+}
+// What the join needs of CTA c's slot 1: how many CTAs after it hold the rest (0: no such
+// item), the item's first row and rows, the sequence's first token and the KV head.
+struct PartHead {
+  int more, row0, rows, first, h, pad[3];
+};
+template <int D>
+__device__ __forceinline__ PartHead* part_heads(float* ws) {
+  return reinterpret_cast<PartHead*>(part_slot<D>(ws, ATTN_MAX_CTAS, 0));
 }
 
 template <class T, int D>
@@ -152,10 +188,15 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
   uint8_t* ring = sm + L::RING + warp * L::STAGES * 2 * L::TILE;
   float* merge = reinterpret_cast<float*>(sm + L::MERGE);
   float* sml = reinterpret_cast<float*>(sm + L::ML);
+  float* tot = reinterpret_cast<float*>(sm + L::TOT);
 
   const long long total = total_units(p, G, lane, blockIdx.x == 0 && warp == 0);
   const int ncta = active_ctas(total, gridDim.x, L::WARPS);
-  if ((int)blockIdx.x >= ncta) return;
+  PartHead* head = part_heads<D>(a.ws) + blockIdx.x;
+  if ((int)blockIdx.x >= ncta) {
+    if (tid == 0) head->more = 0;
+    return;
+  }
   const long long lo = cut(total, ncta, blockIdx.x), hi = cut(total, ncta, blockIdx.x + 1);
   Item cur;
   locate(p, G, lane, lo, cur);
@@ -371,6 +412,25 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
     __syncthreads();
     const bool whole = cur.start >= lo && cur.end <= hi;
     float* part = part_slot<D>(a.ws, blockIdx.x, cur.start < lo ? 0 : 1);
+    if (tid < ROWS) {
+      float M = -INFINITY, lt = 0.f;
+#pragma unroll
+      for (int w = 0; w < L::WARPS; ++w) M = fmaxf(M, sml[w * ROWS + tid]);
+#pragma unroll
+      for (int w = 0; w < L::WARPS; ++w)
+        if (sml[w * ROWS + tid] != -INFINITY) lt += sml[(L::WARPS + w) * ROWS + tid] * exp2f(sml[w * ROWS + tid] - M);
+      tot[tid] = M;
+      tot[ROWS + tid] = lt;
+      if (tid < rows) {
+        if (!whole) {
+          part[ROWS * D + tid] = M;
+          part[ROWS * D + ROWS + tid] = lt;
+        } else if (a.lse) {
+          const int qr = row0 + tid;
+          a.lse[(size_t)(cur.s.first + qr / G) * p.Hq + cur.h * G + qr % G] = M == -INFINITY ? -INFINITY : (M + log2f(lt)) * LN2;
+        }
+      }
+    }
     float fac[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -388,99 +448,74 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
           *d = make_float2(o[c0 / 8 + j][e] * fac[e >> 1], o[c0 / 8 + j][e + 1] * fac[e >> 1]);
         }
       __syncthreads();
-      for (int q = tid; q < rows * L::MCOLS; q += L::THREADS) {
-        const int r = q / L::MCOLS, col = q % L::MCOLS;
-        float sum = 0.f, M = -INFINITY, lt = 0.f;
+      for (int q = tid; q < rows * (L::MCOLS / 4); q += L::THREADS) {
+        const int r = q / (L::MCOLS / 4), col = q % (L::MCOLS / 4) * 4;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < L::WARPS; ++w) {
-          sum += merge[(w * ROWS + r) * L::MCOLS + col];
-          M = fmaxf(M, sml[w * ROWS + r]);
+          const float4 v = *reinterpret_cast<const float4*>(merge + (w * ROWS + r) * L::MCOLS + col);
+          sum[0] += v.x; sum[1] += v.y; sum[2] += v.z; sum[3] += v.w;
         }
-#pragma unroll
-        for (int w = 0; w < L::WARPS; ++w)
-          if (sml[w * ROWS + r] != -INFINITY) lt += sml[(L::WARPS + w) * ROWS + r] * exp2f(sml[w * ROWS + r] - M);
         if (whole) {
-          const int qr = row0 + r, tok = cur.s.first + qr / G, head = cur.h * G + qr % G;
-          const float inv = M == -INFINITY ? 0.f : 1.f / lt;
-          static_cast<T*>(a.out)[tok * a.o_ts + head * a.o_hs + c0 + col] = from_f32<T>(sum * inv);
-          if (a.lse && c0 + col == 0)
-            a.lse[(size_t)tok * p.Hq + head] = M == -INFINITY ? -INFINITY : (M + log2f(lt)) * LN2;
+          const int qr = row0 + r, tok = cur.s.first + qr / G, head_ = cur.h * G + qr % G;
+          const float inv = tot[r] == -INFINITY ? 0.f : 1.f / tot[ROWS + r];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] *= inv;
+          st4(static_cast<T*>(a.out) + tok * a.o_ts + head_ * a.o_hs + c0 + col, sum);
         } else {
-          part[r * D + c0 + col] = sum;
-          if (c0 + col == 0) {
-            part[ROWS * D + r] = M;
-            part[ROWS * D + ROWS + r] = lt;
-          }
+          st4(part + r * D + c0 + col, sum);
         }
       }
       __syncthreads();
     }
-    if (cur.end >= hi) break;
+    if (cur.end >= hi) {
+      if (tid == 0) {
+        int more = 0;
+        if (cur.start >= lo && cur.end > hi) {  // the CTA that holds the item's last unit
+          int q = (int)((cur.end - 1) * ncta / total);
+          while (q + 1 < ncta && cut(total, ncta, q + 1) <= cur.end - 1) ++q;
+          while (cut(total, ncta, q) > cur.end - 1) --q;
+          more = q - blockIdx.x;
+        }
+        *head = PartHead{more, row0, rows, cur.s.first, cur.h, {0, 0, 0}};
+      }
+      break;
+    }
     next_item(p, G, cur);
   }
   cp_async_wait<0>();
 }
 
-// Joins an item's parts, one CTA of D threads per item: o = sum_c o_c 2^(m_c - m) over the
-// CTAs that share it, in their order.
+// Joins the parts of the item that begins in CTA blockIdx.x and goes on in the next ones:
+// o = sum_c o_c 2^(m_c - m), in the order of the CTAs. A thread per row and four columns.
 template <class T, int D>
-__global__ void __launch_bounds__(D) paged_attn_join_kernel(AttnArgs a, int grid) {
+__global__ void __launch_bounds__(ROWS * D / 4) paged_attn_join_kernel(AttnArgs a) {
   pdl_wait();
-  const PagedArgs& p = a.p;
-  const int G = p.Hq / p.Hk, lane = threadIdx.x & 31;
-  const long long total = total_units(p, G, lane, false);
-  const int ncta = active_ctas(total, grid, Lay<T, D>::WARPS);
-  // item blockIdx.x of all
-  long long idx = blockIdx.x, base = 0;
-  Item it;
-  it.b = -1;
-  for (int b = 0; b < p.B; ++b) {
-    const Seq s = load_seq(p, b, false);
-    const long long n = (long long)seq_items(s, G) * p.Hk;
-    if (idx < n) {
-      it.b = b;
-      it.s = s;
-      break;
-    }
-    idx -= n;
-    base += seq_units(s, G) * p.Hk;
-  }
-  if (it.b < 0) return;
-  const int per = seq_items(it.s, G);
-  it.h = (int)(idx / per);
-  it.i = (int)(idx % per);
-  base += seq_units(it.s, G) * it.h;
-  for (int i = 0; i < it.i; ++i) base += item_units(it.s, G, i);
-  it.start = base;
-  it.end = base + item_units(it.s, G, it.i);
-  // the CTA whose run holds unit f
-  auto holder = [&](long long f) {
-    int c = (int)(f * ncta / total);
-    while (c + 1 < ncta && cut(total, ncta, c + 1) <= f) ++c;
-    while (c > 0 && cut(total, ncta, c) > f) --c;
-    return c;
+  const int c = blockIdx.x;
+  const PartHead h = part_heads<D>(a.ws)[c];
+  const int r = threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;
+  if (h.more == 0 || r >= h.rows) return;
+  constexpr size_t STEP = 2 * (ROWS * D + 2 * ROWS);  // from one CTA's slot to the next CTA's
+  const float *first = part_slot<D>(a.ws, c, 1), *rest = part_slot<D>(a.ws, c + 1, 0);
+  float M = first[ROWS * D + r];
+#pragma unroll 8
+  for (int q = 0; q < h.more; ++q) M = fmaxf(M, rest[q * STEP + ROWS * D + r]);
+  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+  auto add = [&](const float* part) {
+    const float m = part[ROWS * D + r], w = m == -INFINITY ? 0.f : exp2f(m - M);
+    const float4 v = *reinterpret_cast<const float4*>(part + r * D + col);
+    o[0] += v.x * w; o[1] += v.y * w; o[2] += v.z * w; o[3] += v.w * w;
+    l += part[ROWS * D + ROWS + r] * w;
   };
-  const int c0 = holder(it.start), c1 = holder(it.end - 1);
-  if (c0 == c1) return;
-  const int row0 = it.i * ROWS, rows = min(ROWS, it.s.n * G - row0);
-  for (int r = 0; r < rows; ++r) {
-    float M = -INFINITY;
-    for (int q = c0; q <= c1; ++q) M = fmaxf(M, part_slot<D>(a.ws, q, q == c0)[ROWS * D + r]);
-    float sum = 0.f, lt = 0.f;
-    for (int q = c0; q <= c1; ++q) {
-      const float* part = part_slot<D>(a.ws, q, q == c0);
-      const float m = part[ROWS * D + r];
-      if (m == -INFINITY) continue;
-      const float w = exp2f(m - M);
-      sum += part[r * D + threadIdx.x] * w;
-      lt += part[ROWS * D + ROWS + r] * w;
-    }
-    const int qr = row0 + r, tok = it.s.first + qr / G, head = it.h * G + qr % G;
-    const float inv = M == -INFINITY ? 0.f : 1.f / lt;
-    static_cast<T*>(a.out)[tok * a.o_ts + head * a.o_hs + threadIdx.x] = from_f32<T>(sum * inv);
-    if (a.lse && threadIdx.x == 0)
-      a.lse[(size_t)tok * p.Hq + head] = M == -INFINITY ? -INFINITY : (M + log2f(lt)) * LN2;
-  }
+  add(first);
+#pragma unroll 8
+  for (int q = 0; q < h.more; ++q) add(rest + q * STEP);
+  const int G = a.p.Hq / a.p.Hk, qr = h.row0 + r, tok = h.first + qr / G, head = h.h * G + qr % G;
+  const float inv = M == -INFINITY ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] *= inv;
+  st4(static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + col, o);
+  if (a.lse && col == 0) a.lse[(size_t)tok * a.p.Hq + head] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * LN2;
 }
 
 template <class T, int D>
@@ -496,12 +531,8 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
   e = launch_pdl(paged_attn_kernel<T, D>, dim3(grid), dim3(L::THREADS), bytes, s, a);
   prof_mark(K_ATTN, s, false);
   if (e != cudaSuccess) return e;
-  const int G = a.p.Hq / a.p.Hk;
-  // an upper bound: full items, and one that is not full per sequence with new tokens
-  const long long rows = (long long)a.p.N * G, seqs = a.p.B < a.p.N ? a.p.B : a.p.N;
-  const long long items = (rows / ROWS + seqs) * a.p.Hk;
   prof_mark(K_ATTN_JOIN, s, true);
-  e = launch_pdl(paged_attn_join_kernel<T, D>, dim3((unsigned)items), dim3(D), 0, s, a, grid);
+  e = launch_pdl(paged_attn_join_kernel<T, D>, dim3(grid), dim3(ROWS * D / 4), 0, s, a);
   prof_mark(K_ATTN_JOIN, s, false);
   return e;
 }
@@ -509,7 +540,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attn_workspace(const AttnArgs& a) {
-  const size_t own = (size_t)2 * ATTN_MAX_CTAS * (ROWS * a.p.D + 2 * ROWS) * sizeof(float);
+  const size_t own = (size_t)2 * ATTN_MAX_CTAS * (ROWS * a.p.D + 2 * ROWS) * sizeof(float) + ATTN_MAX_CTAS * sizeof(PartHead);
   const size_t tc = paged_attn_tc_applies(a) ? paged_attn_tc_workspace(a) : 0;
   return own > tc ? own : tc;
 }
