@@ -144,6 +144,7 @@ template <class T, int VEC, int NV, int SUB, bool HEAD>
 __global__ void __launch_bounds__(SUB ? SUB_THREADS : NORM_THREADS_MAX)
     block_norm_fwd_kernel(NormArgs a) {
   pdl_wait();
+  pdl_trigger();
   __shared__ __align__(16) float buf[2][32];
   const Place<SUB> at;
   const T *wpost = static_cast<const T*>(a.w_post), *rscale = HEAD ? nullptr : static_cast<const T*>(a.res_scale),
@@ -252,6 +253,7 @@ template <class T, int VEC, int NV, int SUB, bool HEAD>
 __global__ void __launch_bounds__(SUB ? SUB_THREADS : NORM_THREADS_MAX, HEAD ? 3 : 1)
     block_norm_bwd_kernel(NormArgs a) {
   pdl_wait();
+  pdl_trigger();
   __shared__ __align__(16) float buf[2][32];
   const Place<SUB> at;
   const T *gate = static_cast<const T*>(a.gate), *res = HEAD ? nullptr : static_cast<const T*>(a.residual),
@@ -549,6 +551,7 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
     block_norm_stream_kernel(NormArgs a, int stages) {
   constexpr int VEC = 16 / (int)sizeof(T), NP = VEC / 2;
   pdl_wait();
+  pdl_trigger();
   extern __shared__ __align__(128) uint8_t smem[];
   StreamShared* sh = reinterpret_cast<StreamShared*>(smem);
   const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr, gated = a.gate != nullptr, scaled = a.res_scale != nullptr;
@@ -879,6 +882,7 @@ constexpr int WG_LANES = 32;
 template <class T>
 __global__ void __launch_bounds__(32 * WG_LANES) block_norm_wgrad_kernel(NormArgs a, int parts) {
   pdl_wait();
+  pdl_trigger();
   __shared__ float s[WG_LANES][33];
   T* out = static_cast<T*>(blockIdx.y == 0 ? a.dw_post : blockIdx.y == 1 ? a.dw_pre : a.dres_scale);
   if (!out) return;

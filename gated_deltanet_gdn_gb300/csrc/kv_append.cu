@@ -36,6 +36,7 @@ __device__ __forceinline__ uint4 pack(const float (&x)[16 / sizeof(T)]) {
 template <class T, int D>
 __global__ void __launch_bounds__(THREADS) kv_append_kernel(AppendArgs a) {
   pdl_wait();
+  pdl_trigger();
   constexpr int V = 16 / (int)sizeof(T), UNITS = D / (2 * V), SLOTS = THREADS / UNITS;
   const PagedArgs& p = a.p;
   const int nq = a.q ? p.Hq : 0, rows = nq + 2 * p.Hk;

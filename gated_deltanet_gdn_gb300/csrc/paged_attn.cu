@@ -34,9 +34,9 @@ struct Lay {
   static constexpr int STAGES = 3;
   static constexpr int Q = 0;                              // [16][D] T, swizzled
   static constexpr int RING = ROWS * D * (int)sizeof(T);
-  static constexpr int MCOLS = 32;                         // columns merged at a time
+  static constexpr int MROWS = 4096 / (WARPS * D);         // rows merged at a time
   static constexpr int MERGE = RING + WARPS * STAGES * 2 * TILE;
-  static constexpr int ML = MERGE + WARPS * ROWS * MCOLS * 4;  // float m[WARPS][16], l[WARPS][16]
+  static constexpr int ML = MERGE + WARPS * MROWS * D * 4;  // float m[WARPS][16], l[WARPS][16]
   static constexpr int TOT = ML + 2 * WARPS * ROWS * 4;        // float m[16], l[16] of the CTA
   static constexpr int BYTES = TOT + 2 * ROWS * 4;
 };
@@ -90,32 +90,34 @@ struct Item {
   long long start, end;  // its units, numbered through all items
 };
 
-// Every unit of the call (one warp, all lanes).
-__device__ __forceinline__ long long total_units(const PagedArgs& p, int G, int lane, bool report) {
-  long long t = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    t += lane_units(b < p.B ? load_seq(p, b, report) : Seq{0, 0, 0}, G, lane);
-  }
-  return warp_sum(t) * p.Hk;
+// The units of 32 sequences b0 + lane over all KV heads, and their running sum.
+struct Chunk {
+  Seq s;
+  long long u, inc;
+};
+__device__ __forceinline__ Chunk load_chunk(const PagedArgs& p, int G, int lane, int b0, bool report) {
+  Chunk c;
+  c.s = b0 + lane < p.B ? load_seq(p, b0 + lane, report) : Seq{0, 0, 0};
+  c.u = lane_units(c.s, G, lane);
+  c.inc = warp_scan(c.u * p.Hk, lane);
+  return c;
 }
-// The item holding unit f < total (one warp, all lanes).
-__device__ __forceinline__ void locate(const PagedArgs& p, int G, int lane, long long f, Item& it) {
+// The item holding unit f < total (one warp, all lanes). c: the first chunk.
+__device__ __forceinline__ void locate(const PagedArgs& p, int G, int lane, long long f, Chunk c, Item& it) {
   long long base = 0, per = 1;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    const Seq s = b < p.B ? load_seq(p, b, false) : Seq{0, 0, 0};
-    const long long u = lane_units(s, G, lane), inc = warp_scan(u * p.Hk, lane);
-    const unsigned hit = __ballot_sync(0xffffffffu, base + inc > f);
+    if (b0 > 0) c = load_chunk(p, G, lane, b0, false);
+    const unsigned hit = __ballot_sync(0xffffffffu, base + c.inc > f);
     if (hit) {
       const int l = __ffs(hit) - 1;
-      base += __shfl_sync(0xffffffffu, inc - u * p.Hk, l);
-      per = __shfl_sync(0xffffffffu, u, l);
+      base += __shfl_sync(0xffffffffu, c.inc - c.u * p.Hk, l);
+      per = __shfl_sync(0xffffffffu, c.u, l);
       it.b = b0 + l;
-      it.s = Seq{__shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.first, l), __shfl_sync(0xffffffffu, s.len, l)};
+      it.s = Seq{__shfl_sync(0xffffffffu, c.s.n, l), __shfl_sync(0xffffffffu, c.s.first, l),
+                 __shfl_sync(0xffffffffu, c.s.len, l)};
       break;
     }
-    base += __shfl_sync(0xffffffffu, inc, 31);
+    base += __shfl_sync(0xffffffffu, c.inc, 31);
   }
   it.h = (int)((f - base) / per);
   base += it.h * per;
@@ -190,7 +192,11 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
   float* sml = reinterpret_cast<float*>(sm + L::ML);
   float* tot = reinterpret_cast<float*>(sm + L::TOT);
 
-  const long long total = total_units(p, G, lane, blockIdx.x == 0 && warp == 0);
+  const bool report = blockIdx.x == 0 && warp == 0;
+  const Chunk chunk = load_chunk(p, G, lane, 0, report);
+  long long total = __shfl_sync(0xffffffffu, chunk.inc, 31);
+  for (int b0 = 32; b0 < p.B; b0 += 32)
+    total += __shfl_sync(0xffffffffu, load_chunk(p, G, lane, b0, report).inc, 31);
   const int ncta = active_ctas(total, gridDim.x, L::WARPS);
   PartHead* head = part_heads<D>(a.ws) + blockIdx.x;
   if ((int)blockIdx.x >= ncta) {
@@ -199,62 +205,84 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
   }
   const long long lo = cut(total, ncta, blockIdx.x), hi = cut(total, ncta, blockIdx.x + 1);
   Item cur;
-  locate(p, G, lane, lo, cur);
-  Item ahead = cur;  // the loads' item
-  long long nextf = lo + warp;  // the next unit to load
-  int st_load = 0;
-
-  auto load_unit = [&]() {
+  locate(p, G, lane, lo, chunk, cur);
+  // The loads run ahead of the item in work. A unit's page is looked up one unit before its
+  // loads are issued, so that they do not wait for it.
+  Item ahead = cur;
+  long long nextf = lo + warp;  // the next unit to look up
+  struct Ref {
+    int page, row0, h;  // page < 0: nothing to load
+  };
+  auto look_up = [&]() {
+    Ref r{-1, 0, 0};
     if (nextf < hi) {
       while (nextf >= ahead.end) next_item(p, G, ahead);
       const int key0 = (int)(nextf - ahead.start) * UNIT;
-      if (key0 < ahead.s.len) {
-        const int page = load_page(p, ahead.b, key0);
-        const int row0 = key0 % p.page_size;
-        const T* kp = static_cast<const T*>(p.kc) + page * p.k_ps + ahead.h * p.k_hs + row0 * p.k_rs;
-        const T* vp = static_cast<const T*>(p.vc) + page * p.v_ps + ahead.h * p.v_hs + row0 * p.v_rs;
-        constexpr int V = 16 / (int)sizeof(T), CH = D / V;  // 16-byte chunks of a row
-        Tile<T, UNIT, D> Kt{reinterpret_cast<T*>(ring + st_load * 2 * L::TILE)};
-        Tile<T, UNIT, D> Vt{reinterpret_cast<T*>(ring + (st_load * 2 + 1) * L::TILE)};
+      if (key0 < ahead.s.len) r = Ref{load_page(p, ahead.b, key0), key0 % p.page_size, ahead.h};
+    }
+    nextf += L::WARPS;
+    return r;
+  };
+  int st_load = 0;
+  auto load_unit = [&](const Ref& u) {
+    if (u.page >= 0) {
+      const T* kp = static_cast<const T*>(p.kc) + u.page * p.k_ps + u.h * p.k_hs + u.row0 * p.k_rs;
+      const T* vp = static_cast<const T*>(p.vc) + u.page * p.v_ps + u.h * p.v_hs + u.row0 * p.v_rs;
+      constexpr int V = 16 / (int)sizeof(T), CH = D / V;  // 16-byte chunks of a row
+      Tile<T, UNIT, D> Kt{reinterpret_cast<T*>(ring + st_load * 2 * L::TILE)};
+      Tile<T, UNIT, D> Vt{reinterpret_cast<T*>(ring + (st_load * 2 + 1) * L::TILE)};
 #pragma unroll
-        for (int q = 0; q < UNIT * CH / 32; ++q) {
-          const int r = (q * 32 + lane) / CH, c = (q * 32 + lane) % CH * V;
-          cp_async16(Kt.ptr(r, c), kp + r * p.k_rs + c);
-        }
+      for (int q = 0; q < UNIT * CH / 32; ++q) {
+        const int r = (q * 32 + lane) / CH, c = (q * 32 + lane) % CH * V;
+        cp_async16(Kt.ptr(r, c), kp + r * p.k_rs + c);
+      }
 #pragma unroll
-        for (int q = 0; q < UNIT * CH / 32; ++q) {
-          const int r = (q * 32 + lane) / CH, c = (q * 32 + lane) % CH * V;
-          cp_async16(Vt.ptr(r, c), vp + r * p.v_rs + c);
-        }
+      for (int q = 0; q < UNIT * CH / 32; ++q) {
+        const int r = (q * 32 + lane) / CH, c = (q * 32 + lane) % CH * V;
+        cp_async16(Vt.ptr(r, c), vp + r * p.v_rs + c);
       }
     }
     cp_async_commit();
-    nextf += L::WARPS;
     st_load = st_load + 1 == L::STAGES ? 0 : st_load + 1;
   };
+  // the queries of an item, this thread's 16-byte pieces (rows past the end are zero)
+  constexpr int QV = 16 / (int)sizeof(T), QCH = D / QV, QN = (ROWS * QCH + L::THREADS - 1) / L::THREADS;
+  uint4 qr[QN];
+  auto load_q = [&](const Item& it) {
 #pragma unroll
-  for (int i = 0; i < L::STAGES - 1; ++i) load_unit();
+    for (int i = 0; i < QN; ++i) {
+      const int q = tid + i * L::THREADS, r = it.i * ROWS + q / QCH;
+      qr[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (q < ROWS * QCH && r < it.s.n * G)
+        qr[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (it.s.first + r / G) * a.q_ts +
+                                                (long long)(it.h * G + r % G) * a.q_hs + q % QCH * QV);
+    }
+  };
+  auto store_q = [&]() {
+#pragma unroll
+    for (int i = 0; i < QN; ++i) {
+      const int q = tid + i * L::THREADS;
+      if (q < ROWS * QCH) *reinterpret_cast<uint4*>(Qs.ptr(q / QCH, q % QCH * QV)) = qr[i];
+    }
+  };
+  load_q(cur);
+  Ref ref;
+  {
+    Ref first[L::STAGES - 1];
+#pragma unroll
+    for (int i = 0; i < L::STAGES - 1; ++i) first[i] = look_up();
+    ref = look_up();
+#pragma unroll
+    for (int i = 0; i < L::STAGES - 1; ++i) load_unit(first[i]);
+  }
+  store_q();
 
   int st = 0;
   long long f = lo + warp;  // the next unit to use
   const float c = a.scale * LOG2E;
   while (true) {
     const int row0 = cur.i * ROWS, rows = min(ROWS, cur.s.n * G - row0);
-    // the item's queries (rows past the end are zero)
-    __syncthreads();
-    {
-      constexpr int V = 16 / (int)sizeof(T), CH = D / V;
-      for (int q = tid; q < ROWS * CH; q += L::THREADS) {
-        const int r = q / CH, col = q % CH * V;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) {
-          const int qr = row0 + r, tok = cur.s.first + qr / G, head = cur.h * G + qr % G;
-          v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + tok * a.q_ts + head * a.q_hs + col);
-        }
-        *reinterpret_cast<uint4*>(Qs.ptr(r, col)) = v;
-      }
-    }
-    __syncthreads();
+    __syncthreads();  // the item's queries are in place
     uint32_t qf[sizeof(T) == 2 ? D / 16 : 1][4];
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
@@ -275,7 +303,8 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
 
     const long long end = cur.end < hi ? cur.end : hi;
     for (; f < end; f += L::WARPS) {
-      load_unit();
+      load_unit(ref);
+      ref = look_up();
       cp_async_wait<L::STAGES - 1>();
       __syncwarp();
       const int key0 = (int)(f - cur.start) * UNIT;
@@ -399,7 +428,13 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
       }
       __syncwarp();  // the stage is loaded again by other lanes
     }
-    // merge the warps
+    // the next item's queries are on their way while the warps are merged
+    const bool more = cur.end < hi;
+    Item nxt = cur;
+    if (more) {
+      next_item(p, G, nxt);
+      load_q(nxt);
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -438,22 +473,25 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
       for (int w = 0; w < L::WARPS; ++w) M = fmaxf(M, sml[w * ROWS + g + 8 * e]);
       fac[e] = m[e] == -INFINITY ? 0.f : exp2f(m[e] - M);
     }
+    for (int r0 = 0; r0 < rows; r0 += L::MROWS) {
 #pragma unroll
-    for (int c0 = 0; c0 < D; c0 += L::MCOLS) {
+      for (int e = 0; e < 2; ++e) {
+        const int r = g + 8 * e - r0;
+        if (r >= 0 && r < L::MROWS) {
+          float* d = merge + ((size_t)warp * L::MROWS + r) * D + 2 * t;
 #pragma unroll
-      for (int j = 0; j < L::MCOLS / 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          float2* d = reinterpret_cast<float2*>(merge + ((size_t)warp * ROWS + g + 4 * e) * L::MCOLS + j * 8 + 2 * t);
-          *d = make_float2(o[c0 / 8 + j][e] * fac[e >> 1], o[c0 / 8 + j][e + 1] * fac[e >> 1]);
+          for (int j = 0; j < D / 8; ++j)
+            *reinterpret_cast<float2*>(d + j * 8) = make_float2(o[j][2 * e] * fac[e], o[j][2 * e + 1] * fac[e]);
         }
+      }
       __syncthreads();
-      for (int q = tid; q < rows * (L::MCOLS / 4); q += L::THREADS) {
-        const int r = q / (L::MCOLS / 4), col = q % (L::MCOLS / 4) * 4;
+      for (int q = tid; q < L::MROWS * (D / 4); q += L::THREADS) {
+        const int r = r0 + q / (D / 4), col = q % (D / 4) * 4;
+        if (r >= rows) continue;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < L::WARPS; ++w) {
-          const float4 v = *reinterpret_cast<const float4*>(merge + (w * ROWS + r) * L::MCOLS + col);
+          const float4 v = *reinterpret_cast<const float4*>(merge + (w * L::MROWS + r - r0) * D + col);
           sum[0] += v.x; sum[1] += v.y; sum[2] += v.z; sum[3] += v.w;
         }
         if (whole) {
@@ -461,14 +499,14 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
           const float inv = tot[r] == -INFINITY ? 0.f : 1.f / tot[ROWS + r];
 #pragma unroll
           for (int e = 0; e < 4; ++e) sum[e] *= inv;
-          st4(static_cast<T*>(a.out) + tok * a.o_ts + head_ * a.o_hs + c0 + col, sum);
+          st4(static_cast<T*>(a.out) + tok * a.o_ts + head_ * a.o_hs + col, sum);
         } else {
-          st4(part + r * D + c0 + col, sum);
+          st4(part + r * D + col, sum);
         }
       }
       __syncthreads();
     }
-    if (cur.end >= hi) {
+    if (!more) {
       if (tid == 0) {
         int more = 0;
         if (cur.start >= lo && cur.end > hi) {  // the CTA that holds the item's last unit
@@ -481,7 +519,8 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
       }
       break;
     }
-    next_item(p, G, cur);
+    cur = nxt;
+    store_q();
   }
   cp_async_wait<0>();
 }
@@ -491,6 +530,7 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
 template <class T, int D>
 __global__ void __launch_bounds__(ROWS * D / 4) paged_attn_join_kernel(AttnArgs a) {
   pdl_wait();
+  pdl_trigger();
   const int c = blockIdx.x;
   const PartHead h = part_heads<D>(a.ws)[c];
   const int r = threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;
