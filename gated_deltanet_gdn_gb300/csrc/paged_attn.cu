@@ -119,7 +119,7 @@ __device__ __forceinline__ void locate(const PagedArgs& p, int G, int lane, long
     }
     base += __shfl_sync(0xffffffffu, c.inc, 31);
   }
-  it.h = (int)((f - base) / per);
+  it.h = (f - base) >> 32 ? (int)((f - base) / per) : (int)((uint32_t)(f - base) / (uint32_t)per);
   base += it.h * per;
   const int n = seq_items(it.s, G);
   for (int i0 = 0; i0 < n; i0 += 32) {
@@ -152,8 +152,11 @@ __device__ __forceinline__ void next_item(const PagedArgs& p, int G, Item& it) {
   it.end += item_units(it.s, G, it.i);
 }
 
-// CTA c of n takes the units [cut(c), cut(c + 1)).
-__device__ __forceinline__ long long cut(long long total, int n, int c) { return total * c / n; }
+// CTA c of n takes the units [cut(c), cut(c + 1)); 32-bit division where it will do.
+__device__ __forceinline__ long long cut(long long total, int n, int c) {
+  const long long x = total * c;
+  return x >> 32 ? x / n : (long long)((uint32_t)x / (uint32_t)n);
+}
 // CTAs that take part: enough units for each of their warps to have one.
 __device__ __forceinline__ int active_ctas(long long total, int grid, int warps) {
   const long long most = (total + warps - 1) / warps;
@@ -211,23 +214,24 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
   Item ahead = cur;
   long long nextf = lo + warp;  // the next unit to look up
   struct Ref {
-    int page, row0, h;  // page < 0: nothing to load
+    int entry, row0, h;  // h < 0: nothing to load
   };
   auto look_up = [&]() {
-    Ref r{-1, 0, 0};
+    Ref r{0, 0, -1};
     if (nextf < hi) {
       while (nextf >= ahead.end) next_item(p, G, ahead);
       const int key0 = (int)(nextf - ahead.start) * UNIT;
-      if (key0 < ahead.s.len) r = Ref{load_page(p, ahead.b, key0), key0 % p.page_size, ahead.h};
+      if (key0 < ahead.s.len) r = Ref{page_entry(p, ahead.b, key0), key0 % p.page_size, ahead.h};
     }
     nextf += L::WARPS;
     return r;
   };
   int st_load = 0;
   auto load_unit = [&](const Ref& u) {
-    if (u.page >= 0) {
-      const T* kp = static_cast<const T*>(p.kc) + u.page * p.k_ps + u.h * p.k_hs + u.row0 * p.k_rs;
-      const T* vp = static_cast<const T*>(p.vc) + u.page * p.v_ps + u.h * p.v_hs + u.row0 * p.v_rs;
+    if (u.h >= 0) {
+      const long long page = checked_page(p, u.entry);
+      const T* kp = static_cast<const T*>(p.kc) + page * p.k_ps + u.h * p.k_hs + u.row0 * p.k_rs;
+      const T* vp = static_cast<const T*>(p.vc) + page * p.v_ps + u.h * p.v_hs + u.row0 * p.v_rs;
       constexpr int V = 16 / (int)sizeof(T), CH = D / V;  // 16-byte chunks of a row
       Tile<T, UNIT, D> Kt{reinterpret_cast<T*>(ring + st_load * 2 * L::TILE)};
       Tile<T, UNIT, D> Vt{reinterpret_cast<T*>(ring + (st_load * 2 + 1) * L::TILE)};
@@ -532,24 +536,41 @@ __global__ void __launch_bounds__(ROWS * D / 4) paged_attn_join_kernel(AttnArgs 
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x;
-  const PartHead h = part_heads<D>(a.ws)[c];
   const int r = threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;
-  if (h.more == 0 || r >= h.rows) return;
   constexpr size_t STEP = 2 * (ROWS * D + 2 * ROWS);  // from one CTA's slot to the next CTA's
+  constexpr int BATCH = 8;
   const float *first = part_slot<D>(a.ws, c, 1), *rest = part_slot<D>(a.ws, c + 1, 0);
-  float M = first[ROWS * D + r];
-#pragma unroll 8
-  for (int q = 0; q < h.more; ++q) M = fmaxf(M, rest[q * STEP + ROWS * D + r]);
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-  auto add = [&](const float* part) {
-    const float m = part[ROWS * D + r], w = m == -INFINITY ? 0.f : exp2f(m - M);
-    const float4 v = *reinterpret_cast<const float4*>(part + r * D + col);
-    o[0] += v.x * w; o[1] += v.y * w; o[2] += v.z * w; o[3] += v.w * w;
-    l += part[ROWS * D + ROWS + r] * w;
-  };
-  add(first);
-#pragma unroll 8
-  for (int q = 0; q < h.more; ++q) add(rest + q * STEP);
+  float M = -INFINITY, o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+  const PartHead h = part_heads<D>(a.ws)[c];
+  if (h.more == 0 || r >= h.rows) return;
+  for (int q0 = 0; q0 <= h.more; q0 += BATCH) {  // parts in batches, all of a batch's loads in flight
+    float m[BATCH], s[BATCH];
+    float4 v[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int q = q0 + i;  // part 0 is this CTA's
+      const float* part = q == 0 ? first : rest + (size_t)(min(q, h.more) - 1) * STEP;
+      m[i] = part[ROWS * D + r];
+      s[i] = part[ROWS * D + ROWS + r];
+      v[i] = *reinterpret_cast<const float4*>(part + r * D + col);
+    }
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (q0 + i <= h.more) top = fmaxf(top, m[i]);
+    const float f = M == -INFINITY ? 0.f : exp2f(M - top);
+    M = top;
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] *= f;
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (q0 + i <= h.more && m[i] != -INFINITY) {
+        const float w = exp2f(m[i] - M);
+        o[0] += v[i].x * w; o[1] += v[i].y * w; o[2] += v[i].z * w; o[3] += v[i].w * w;
+        l += s[i] * w;
+      }
+  }
   const int G = a.p.Hq / a.p.Hk, qr = h.row0 + r, tok = h.first + qr / G, head = h.h * G + qr % G;
   const float inv = M == -INFINITY ? 0.f : 1.f / l;
 #pragma unroll

@@ -37,9 +37,12 @@ __device__ __forceinline__ Seq load_seq(const PagedArgs& p, int b, bool report) 
   if (s.len < 0) s.len = 0;
   return s;
 }
-// Page of key `key` of sequence b, clamped into the cache.
-__device__ __forceinline__ int load_page(const PagedArgs& p, int b, int key) {
-  int page = p.page_table[b * p.pt_stride + key / p.page_size];
+// The page table's entry for key `key` of sequence b, and the entry clamped into the cache
+// (apart, so that the check does not wait for the load where it is issued).
+__device__ __forceinline__ int page_entry(const PagedArgs& p, int b, int key) {
+  return p.page_table[b * p.pt_stride + key / p.page_size];
+}
+__device__ __forceinline__ int checked_page(const PagedArgs& p, int page) {
   if (page < 0 || page >= p.num_pages) {
     if (p.err) atomicOr(p.err, ERR_PAGE);
     page = 0;

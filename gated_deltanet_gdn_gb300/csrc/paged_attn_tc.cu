@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       int page = 0, prow = 0;
       if (lane < have) {
         const int key = key0 + lane * box_rows;
-        page = load_page(p, it.b, key);
+        page = checked_page(p, page_entry(p, it.b, key));
         prow = key % p.page_size;
       }
 #pragma unroll
