@@ -287,8 +287,6 @@ struct AttnArgs {
 // Bit of the device error word set by the paged kernels: a length beyond the page table, a
 // page outside the cache, or a position beyond the rotation table.
 constexpr unsigned ERR_PAGE = 4u;
-constexpr int ATTN_MAX_CTAS = 160;   // most CTAs of paged_attn_kernel (one per SM)
-constexpr int TC_SPLIT_ITEMS = 608;  // most parts of a split paged_attn_tc_kernel call
 
 // Kernel identifiers for the optional per-launch timing (gdn_profile_* in the C ABI).
 enum KernelId {

@@ -41,143 +41,7 @@ struct Lay {
   static constexpr int BYTES = TOT + 2 * ROWS * 4;
 };
 
-// Units of an item: the 16-key units its last row sees, at least one (an item without keys
-// still writes its zeros).
-__device__ __forceinline__ int item_units(const Seq& s, int G, int item) {
-  int last = (item + 1) * ROWS - 1;
-  const int rows = s.n * G;
-  if (last >= rows) last = rows - 1;
-  const int limit = s.len - s.n + last / G;
-  return limit < 0 ? 1 : limit / UNIT + 1;
-}
-__device__ __forceinline__ int seq_items(const Seq& s, int G) { return (s.n * G + ROWS - 1) / ROWS; }
-
-__device__ __forceinline__ long long warp_sum(long long t) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-  return t;
-}
-__device__ __forceinline__ long long warp_scan(long long t, int lane) {  // inclusive
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, t, off);
-    if (lane >= off) t += o;
-  }
-  return t;
-}
-// Units of one KV head of the sequences b0 + lane, each in its lane: by itself where all
-// have one or two items (single tokens, drafts), else the warp over each one's items.
-__device__ __forceinline__ long long lane_units(const Seq& s, int G, int lane) {
-  const int n = seq_items(s, G);
-  long long u = 0;
-  if (!__any_sync(0xffffffffu, n > 2)) {
-    for (int i = 0; i < n; ++i) u += item_units(s, G, i);
-    return u;
-  }
-  for (int l = 0; l < 32; ++l) {
-    const Seq q{__shfl_sync(0xffffffffu, s.n, l), 0, __shfl_sync(0xffffffffu, s.len, l)};
-    long long t = 0;
-    for (int i = lane, m = seq_items(q, G); i < m; i += 32) t += item_units(q, G, i);
-    t = warp_sum(t);
-    if (lane == l) u = t;
-  }
-  return u;
-}
-
-struct Item {
-  int b, h, i;           // sequence, KV head, item of the head
-  Seq s;
-  long long start, end;  // its units, numbered through all items
-};
-
-// The units of 32 sequences b0 + lane over all KV heads, and their running sum.
-struct Chunk {
-  Seq s;
-  long long u, inc;
-};
-__device__ __forceinline__ Chunk load_chunk(const PagedArgs& p, int G, int lane, int b0, bool report) {
-  Chunk c;
-  c.s = b0 + lane < p.B ? load_seq(p, b0 + lane, report) : Seq{0, 0, 0};
-  c.u = lane_units(c.s, G, lane);
-  c.inc = warp_scan(c.u * p.Hk, lane);
-  return c;
-}
-// The item holding unit f < total (one warp, all lanes). c: the first chunk.
-__device__ __forceinline__ void locate(const PagedArgs& p, int G, int lane, long long f, Chunk c, Item& it) {
-  long long base = 0, per = 1;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    if (b0 > 0) c = load_chunk(p, G, lane, b0, false);
-    const unsigned hit = __ballot_sync(0xffffffffu, base + c.inc > f);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      base += __shfl_sync(0xffffffffu, c.inc - c.u * p.Hk, l);
-      per = __shfl_sync(0xffffffffu, c.u, l);
-      it.b = b0 + l;
-      it.s = Seq{__shfl_sync(0xffffffffu, c.s.n, l), __shfl_sync(0xffffffffu, c.s.first, l),
-                 __shfl_sync(0xffffffffu, c.s.len, l)};
-      break;
-    }
-    base += __shfl_sync(0xffffffffu, c.inc, 31);
-  }
-  it.h = (f - base) >> 32 ? (int)((f - base) / per) : (int)((uint32_t)(f - base) / (uint32_t)per);
-  base += it.h * per;
-  const int n = seq_items(it.s, G);
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int u = i0 + lane < n ? item_units(it.s, G, i0 + lane) : 0;
-    const long long inc = warp_scan(u, lane);
-    const unsigned hit = __ballot_sync(0xffffffffu, base + inc > f);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      it.i = i0 + l;
-      it.end = base + __shfl_sync(0xffffffffu, inc, l);
-      it.start = it.end - __shfl_sync(0xffffffffu, u, l);
-      break;
-    }
-    base += __shfl_sync(0xffffffffu, inc, 31);
-  }
-}
-// The next item in the numbering (not called past the last).
-__device__ __forceinline__ void next_item(const PagedArgs& p, int G, Item& it) {
-  if (++it.i >= seq_items(it.s, G)) {
-    it.i = 0;
-    if (++it.h >= p.Hk) {
-      it.h = 0;
-      do {
-        ++it.b;
-        it.s = load_seq(p, it.b, false);
-      } while (it.s.n == 0 && it.b + 1 < p.B);
-    }
-  }
-  it.start = it.end;
-  it.end += item_units(it.s, G, it.i);
-}
-
-// CTA c of n takes the units [cut(c), cut(c + 1)); 32-bit division where it will do.
-__device__ __forceinline__ long long cut(long long total, int n, int c) {
-  const long long x = total * c;
-  return x >> 32 ? x / n : (long long)((uint32_t)x / (uint32_t)n);
-}
-// CTAs that take part: enough units for each of their warps to have one.
-__device__ __forceinline__ int active_ctas(long long total, int grid, int warps) {
-  const long long most = (total + warps - 1) / warps;
-  return most < grid ? (int)most : grid;
-}
-
-// The parts of a CTA in the workspace: slot 0 for an item that began in an earlier CTA,
-// slot 1 for one that begins here and goes on. o [16][D] relative to m, then m [16], l [16].
-template <int D>
-__device__ __forceinline__ float* part_slot(float* ws, int cta, int second) {
-  return ws + (size_t)(2 * cta + second) * (ROWS * D + 2 * ROWS);
-}
-// What the join needs of CTA c's slot 1: how many CTAs after it hold the rest (0: no such
-// item), the item's first row and rows, the sequence's first token and the KV head.
-struct PartHead {
-  int more, row0, rows, first, h, pad[3];
-};
-template <int D>
-__device__ __forceinline__ PartHead* part_heads(float* ws) {
-  return reinterpret_cast<PartHead*>(part_slot<D>(ws, ATTN_MAX_CTAS, 0));
-}
+typedef Numbering<ROWS, UNIT, 0> Num;
 
 template <class T, int D>
 __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnArgs a) {
@@ -195,20 +59,14 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
   float* sml = reinterpret_cast<float*>(sm + L::ML);
   float* tot = reinterpret_cast<float*>(sm + L::TOT);
 
-  const bool report = blockIdx.x == 0 && warp == 0;
-  const Chunk chunk = load_chunk(p, G, lane, 0, report);
-  long long total = __shfl_sync(0xffffffffu, chunk.inc, 31);
-  for (int b0 = 32; b0 < p.B; b0 += 32)
-    total += __shfl_sync(0xffffffffu, load_chunk(p, G, lane, b0, report).inc, 31);
-  const int ncta = active_ctas(total, gridDim.x, L::WARPS);
-  PartHead* head = part_heads<D>(a.ws) + blockIdx.x;
-  if ((int)blockIdx.x >= ncta) {
+  PartHead* head = part_heads<ROWS, D>(a.ws, gridDim.x) + blockIdx.x;
+  Num::Run run;
+  if (!Num::plan(p, G, lane, blockIdx.x, gridDim.x, L::WARPS, run)) {
     if (tid == 0) head->more = 0;
     return;
   }
-  const long long lo = cut(total, ncta, blockIdx.x), hi = cut(total, ncta, blockIdx.x + 1);
-  Item cur;
-  locate(p, G, lane, lo, chunk, cur);
+  const long long lo = run.lo, hi = run.hi;
+  Item cur = run.first;
   // The loads run ahead of the item in work. A unit's page is looked up one unit before its
   // loads are issued, so that they do not wait for it.
   Item ahead = cur;
@@ -219,7 +77,7 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
   auto look_up = [&]() {
     Ref r{0, 0, -1};
     if (nextf < hi) {
-      while (nextf >= ahead.end) next_item(p, G, ahead);
+      while (nextf >= ahead.end) Num::next_item(p, G, ahead);
       const int key0 = (int)(nextf - ahead.start) * UNIT;
       if (key0 < ahead.s.len) r = Ref{page_entry(p, ahead.b, key0), key0 % p.page_size, ahead.h};
     }
@@ -436,7 +294,7 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
     const bool more = cur.end < hi;
     Item nxt = cur;
     if (more) {
-      next_item(p, G, nxt);
+      Num::next_item(p, G, nxt);
       load_q(nxt);
     }
 #pragma unroll
@@ -450,7 +308,7 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
     }
     __syncthreads();
     const bool whole = cur.start >= lo && cur.end <= hi;
-    float* part = part_slot<D>(a.ws, blockIdx.x, cur.start < lo ? 0 : 1);
+    float* part = Parts<ROWS, D>::slot(a.ws, blockIdx.x, cur.start < lo ? 0 : 1);
     if (tid < ROWS) {
       float M = -INFINITY, lt = 0.f;
 #pragma unroll
@@ -513,12 +371,7 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
     if (!more) {
       if (tid == 0) {
         int more = 0;
-        if (cur.start >= lo && cur.end > hi) {  // the CTA that holds the item's last unit
-          int q = (int)((cur.end - 1) * ncta / total);
-          while (q + 1 < ncta && cut(total, ncta, q + 1) <= cur.end - 1) ++q;
-          while (cut(total, ncta, q) > cur.end - 1) --q;
-          more = q - blockIdx.x;
-        }
+        if (cur.start >= lo && cur.end > hi) more = holder(run.total, run.ncta, cur.end - 1) - blockIdx.x;
         *head = PartHead{more, row0, rows, cur.s.first, cur.h, {0, 0, 0}};
       }
       break;
@@ -537,11 +390,11 @@ __global__ void __launch_bounds__(ROWS * D / 4) paged_attn_join_kernel(AttnArgs 
   pdl_trigger();
   const int c = blockIdx.x;
   const int r = threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;
-  constexpr size_t STEP = 2 * (ROWS * D + 2 * ROWS);  // from one CTA's slot to the next CTA's
+  constexpr size_t STEP = 2 * Parts<ROWS, D>::SLOT;  // from one CTA's slot to the next CTA's
   constexpr int BATCH = 8;
-  const float *first = part_slot<D>(a.ws, c, 1), *rest = part_slot<D>(a.ws, c + 1, 0);
+  const float *first = Parts<ROWS, D>::slot(a.ws, c, 1), *rest = Parts<ROWS, D>::slot(a.ws, c + 1, 0);
   float M = -INFINITY, o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-  const PartHead h = part_heads<D>(a.ws)[c];
+  const PartHead h = part_heads<ROWS, D>(a.ws, gridDim.x)[c];
   if (h.more == 0 || r >= h.rows) return;
   for (int q0 = 0; q0 <= h.more; q0 += BATCH) {  // parts in batches, all of a batch's loads in flight
     float m[BATCH], s[BATCH];
@@ -585,9 +438,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
   const int bytes = L::BYTES + 1024;
   cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  const int nsm = device_sm_count();
-  if (nsm < 1) return cudaErrorInvalidDevice;
-  const int grid = nsm < ATTN_MAX_CTAS ? nsm : ATTN_MAX_CTAS;
+  const int grid = launch_ctas(a, ROWS, UNIT, L::WARPS);
   prof_mark(K_ATTN, s, true);
   e = launch_pdl(paged_attn_kernel<T, D>, dim3(grid), dim3(L::THREADS), bytes, s, a);
   prof_mark(K_ATTN, s, false);
@@ -601,7 +452,8 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attn_workspace(const AttnArgs& a) {
-  const size_t own = (size_t)2 * ATTN_MAX_CTAS * (ROWS * a.p.D + 2 * ROWS) * sizeof(float) + ATTN_MAX_CTAS * sizeof(PartHead);
+  const int warps = a.p.D * (a.p.bf16 ? 2 : 4) <= 256 ? 8 : 4, grid = launch_ctas(a, ROWS, UNIT, warps);
+  const size_t own = a.p.D == 64 ? Parts<ROWS, 64>::bytes(grid) : Parts<ROWS, 128>::bytes(grid);
   const size_t tc = paged_attn_tc_applies(a) ? paged_attn_tc_workspace(a) : 0;
   return own > tc ? own : tc;
 }

@@ -9,16 +9,20 @@
 // tiles (the sums stay exact: P, its sum and O refer to the same maximum).
 //
 // Two warpgroups of softmax threads (one row tile each, a thread per row), and in a third
-// one warp that issues every MMA and one that feeds a ring of key and value tiles by TMA, a box
-// per run of rows inside one page. The tensor pipe works on one row tile's products while
-// the other tile's softmax runs:
+// one warp that issues every MMA, one that feeds a ring of key and value tiles by TMA (a
+// box per run of rows inside one page), and one per row tile that brings its queries. The
+// tensor pipe works on one row tile's products while the other tile's softmax runs:
 //   ... PV0(j) QK0(j+1) | PV1(j) QK1(j+1) | PV0(j+1) ...
 // P takes the first half of its tile's S columns at D = 128 (MMAs of one shape execute in
 // issue order, so QK(j+1) cannot overtake the PV(j) that reads P); at D = 64 it has columns
 // of its own.
 //
-// Few items are split over the keys (a fixed number of splits per call, equal runs of
-// tiles per item); the parts go to the workspace and a second kernel joins them in order.
+// One persistent CTA per SM takes an equal run of the call's (item, key tile) units, so
+// neither ragged lengths, nor the causal triangle, nor fewer items than SMs leave SMs idle.
+// Every role walks the run by itself: the next item's keys and queries are on their way,
+// and its first product done, while this item's output is written. An item that a CTA
+// holds whole is written at once; at the ends of a CTA's run the parts go to the workspace
+// and a second kernel joins them in the order of the CTAs.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -29,11 +33,11 @@ namespace gdn {
 namespace {
 
 constexpr int ROWS = 256, HALF = 128, KT = 128;  // query rows of an item, of a tile; keys of a tile
-constexpr int THREADS = 384;  // three warpgroups: two of softmax, and one with the two warps below
-constexpr int MMA_WARP = 8, LOAD_WARP = 9;
+constexpr int THREADS = 384;  // three warpgroups: two of softmax, and one of the warps below
+constexpr int MMA_WARP = 8, LOAD_WARP = 9, QLOAD_WARP = 10;  // queries: 10 and 11
 // Registers a thread, moved from the third warpgroup to the softmax (which holds 128 scores):
-// the launch has 168 each, 2 * 224 + 56 = 3 * 168.
-constexpr int SOFTMAX_REGS = 224, OTHER_REGS = 56;
+// the launch has 168 each, 2 * 216 + 72 = 3 * 168.
+constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
 constexpr float RESCALE = 8.f;  // growth of the maximum (base 2) that rescales O
 
 template <int N>
@@ -48,13 +52,16 @@ __device__ __forceinline__ void fewer_registers() {
 template <int D>
 struct TcLay {
   static constexpr int SLOT = KT * D * 2;                // one K or V tile
-  static constexpr int SLOTS = D == 128 ? 5 : 8;
+  static constexpr int SLOTS = D == 128 ? 4 : 8;
   static constexpr int Q = 0;                            // two [128][D] tiles
   static constexpr int RING = 2 * HALF * D * 2;
-  static constexpr int BAR = RING + SLOTS * SLOT;
-  // barriers: full[SLOTS], empty[SLOTS], q[2], s[2], p[2], o[2], drained
-  static constexpr int NBAR = 2 * SLOTS + 9;
-  static constexpr int TSLOT = BAR + NBAR * 8;
+  static constexpr int OUT = RING + SLOTS * SLOT;        // two [128][64] tiles on their way out
+  static constexpr int BAR = OUT + 2 * HALF * 64 * 2;
+  // barriers: full[SLOTS], empty[SLOTS], then q, qfree, s, o [2] each, p [2][2] (row tile,
+  // half of the keys), drained
+  static constexpr int NBAR = 2 * SLOTS + 13;
+  static constexpr int RUN = BAR + (NBAR + 1) / 2 * 16;
+  static constexpr int TSLOT = RUN + 128;
   static constexpr int BYTES = TSLOT + 16;
   // tensor memory columns
   static constexpr int S = 0, O = 256, P = D == 128 ? 0 : 256 + 2 * D;
@@ -136,74 +143,35 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// An item of one CTA: rows row0 .. row0 + rows - 1 of (sequence, KV head), key tiles
-// [t0, t1) of the item's `tiles`, and the tiles each row half needs.
-struct TcItem {
-  int b, h, row0, rows, p0;
-  Seq s;
-  int tiles, t0, t1, splits, need[2];
-};
+// An item's start and end take a CTA about as long as OVER key tiles.
+constexpr int OVER = 3;
+typedef Numbering<ROWS, KT, OVER> Num;
+constexpr int MIN_UNITS = OVER + 2;  // units that make a CTA take part
 
-__device__ __forceinline__ int tile_count(const Seq& s, int G, int last_row) {
-  const int limit = s.len - s.n + last_row / G;
-  return limit < 0 ? 0 : limit / KT + 1;
-}
-// Item `idx` (one warp, all lanes). Sequences and the items of a sequence are numbered from
-// the last, the one with the most keys first, and the KV heads of a run of rows side by
-// side. False when there are fewer items.
-__device__ __forceinline__ bool find_item(const PagedArgs& p, int G, int lane, int idx, int split, int splits, TcItem& it) {
-  int run = idx / p.Hk;
-  it.h = idx % p.Hk;
-  it.b = -1;
-  for (int b0 = p.B - 1; b0 >= 0; b0 -= 32) {
-    const int b = b0 - lane;
-    const Seq s = b >= 0 ? load_seq(p, b, false) : Seq{0, 0, 0};
-    const int n = (s.n * G + ROWS - 1) / ROWS;
-    int inc = n;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, off);
-      if (lane >= off) inc += o;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, inc > run);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      const int before = __shfl_sync(0xffffffffu, inc - n, l), count = __shfl_sync(0xffffffffu, n, l);
-      it.b = b0 - l;
-      it.s.n = __shfl_sync(0xffffffffu, s.n, l);
-      it.s.first = __shfl_sync(0xffffffffu, s.first, l);
-      it.s.len = __shfl_sync(0xffffffffu, s.len, l);
-      it.row0 = (count - 1 - (run - before)) * ROWS;
-      break;
-    }
-    run -= __shfl_sync(0xffffffffu, inc, 31);
-  }
-  if (it.b < 0) return false;
-  it.rows = min(ROWS, it.s.n * G - it.row0);
-  it.p0 = it.s.len - it.s.n;
-  it.tiles = tile_count(it.s, G, it.row0 + it.rows - 1);
-  const int per = max((it.tiles + splits - 1) / splits, 1);
-  it.splits = max((it.tiles + per - 1) / per, 1);
-  it.t0 = min(split * per, it.tiles);
-  it.t1 = min(it.t0 + per, it.tiles);
+// What a CTA does of one item: key tiles from t0 on, `need` of them for each row tile (none
+// when its run ends before the item's keys, or the rows see none).
+struct Segment {
+  int row0, rows, p0, t0, need[2];
+};
+__device__ __forceinline__ Segment segment(const Item& it, int G, long long lo, long long hi) {
+  Segment g;
+  g.row0 = it.i * ROWS;
+  g.rows = min(ROWS, it.s.n * G - g.row0);
+  g.p0 = it.s.len - it.s.n;
+  g.t0 = max((int)(lo > it.start ? lo - it.start : 0) - OVER, 0);
+  const int t1 = (int)((hi < it.end ? hi : it.end) - it.start) - OVER;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const int last = min(it.rows, (w + 1) * HALF) - 1;
-    const int t = last >= w * HALF ? tile_count(it.s, G, it.row0 + last) : 0;
-    it.need[w] = max(min(t, it.t1) - it.t0, 0);
+    const int last = min(g.rows, (w + 1) * HALF) - 1;
+    const int t = last >= w * HALF ? key_blocks<KT>(it.s, G, g.row0 + last) : 0;
+    g.need[w] = max(min(t, t1) - g.t0, 0);
   }
-  return true;
-}
-
-// Part of item-split c: o [256][D] relative to m, then m [256] (base 2), l [256].
-template <int D>
-__device__ __forceinline__ float* tc_part(float* ws, size_t c) {
-  return ws + c * (ROWS * (D + 2));
+  return g;
 }
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
-    paged_attn_tc_kernel(AttnArgs a, int splits, int box_rows, const __grid_constant__ CUtensorMap k_map,
+    paged_attn_tc_kernel(AttnArgs a, int box_rows, const __grid_constant__ CUtensorMap k_map,
                          const __grid_constant__ CUtensorMap v_map) {
   pdl_wait();
   pdl_trigger();
@@ -213,215 +181,207 @@ __global__ void __launch_bounds__(THREADS, 1)
   const PagedArgs& p = a.p;
   const int G = p.Hq / p.Hk;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  TcItem it;
-  if (!find_item(p, G, lane, blockIdx.x / splits, blockIdx.x % splits, splits, it)) return;
-  if (p.err && warp == 0 && lane == 0 && p.lens[it.b] > (long long)p.max_pages * p.page_size) atomicOr(p.err, ERR_PAGE);
-  if ((int)(blockIdx.x % splits) >= it.splits) return;
-
-  if (warp < MMA_WARP && it.need[warp >> 2] > 0) {
-    // The queries of a row tile, rows past the end zero: a thread takes 16 bytes of every
-    // STEP-th row, all in flight at once (cp.async), while the CTA sets itself up.
-    constexpr int CH = D / 8, STEP = HALF / CH;
-    const int w = warp >> 2, r = tid & (HALF - 1), col = r % CH * 8;
-    Tile<bf16, HALF, D> Qs{reinterpret_cast<bf16*>(sm + L::Q + w * HALF * D * 2)};
-    int row = r / CH, g = it.row0 + w * HALF + row, tok = it.s.first + g / G, sub = g % G;
-    const int dt = STEP / G, ds = STEP % G;
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      if (w * HALF + row < it.rows)
-        cp_async16(Qs.ptr(row, col),
-                   static_cast<const bf16*>(a.q) + tok * a.q_ts + (long long)(it.h * G + sub) * a.q_hs + col);
-      else
-        *reinterpret_cast<uint4*>(Qs.ptr(row, col)) = make_uint4(0u, 0u, 0u, 0u);
-      row += STEP;
-      tok += dt;
-      sub += ds;
-      if (sub >= G) {
-        sub -= G;
-        ++tok;
-      }
-    }
-    cp_async_commit();
-  }
-
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
-  uint64_t *full = bars, *empty = bars + L::SLOTS, *qbar = bars + 2 * L::SLOTS, *sbar = qbar + 2, *pbar = sbar + 2,
-           *obar = pbar + 2, *drained = obar + 2;
+  uint64_t *full = bars, *empty = bars + L::SLOTS, *qbar = bars + 2 * L::SLOTS, *qfree = qbar + 2, *sbar = qfree + 2,
+           *obar = sbar + 2, *pbar = obar + 2, *drained = pbar + 4;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::TSLOT);
-  if (tid == 0) {
-    for (int i = 0; i < 2 * L::SLOTS; ++i) mbar_init(&bars[i], 1);
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&qbar[w], HALF);
-      mbar_init(&sbar[w], 1);
-      mbar_init(&pbar[w], HALF);
-      mbar_init(&obar[w], 1);
-    }
-    mbar_init(drained, 1);
-    fence_mbar_init();
-  }
-  if (warp == MMA_WARP) {
+  // one warp finds the CTA's run of units while others set up
+  Num::Run* run = reinterpret_cast<Num::Run*>(sm + L::RUN);
+  if (warp == 0) {
+    Num::Run r;
+    if (!Num::plan(p, G, lane, blockIdx.x, gridDim.x, MIN_UNITS, r)) r.lo = r.hi = 0;
+    if (lane == 0) *run = r;
+  } else if (warp == MMA_WARP) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
+  } else if (tid == 32) {
+    for (int i = 0; i < L::NBAR; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&pbar[i], HALF);
+    fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *tslot;
-  const int n = max(it.need[0], it.need[1]);  // key tiles of this CTA
+  const long long lo = run->lo, hi = run->hi;
+  PartHead* head = part_heads<ROWS, D>(a.ws, gridDim.x) + blockIdx.x;
+  if (lo == hi) {  // no share
+    if (tid == 0) head->more = 0;
+    if (warp == MMA_WARP) tmem_dealloc(tm, 512);
+    return;
+  }
+  Item it = run->first;
 
   if (warp < MMA_WARP) {
     // ---------------------------------------------------------------- softmax
     more_registers<SOFTMAX_REGS>();
     const int w = warp >> 2, r = tid & (HALF - 1);  // row tile, row of it
     const int row = w * HALF + r;                   // row of the item
-    Tile<bf16, HALF, D> Qs{reinterpret_cast<bf16*>(sm + L::Q + w * HALF * D * 2)};
-    const int need = it.need[w];
-    if (need > 0) {  // the queries, on their way since before the barrier
-      cp_async_wait<0>();
-      fence_proxy_async();
-      mbar_arrive(&qbar[w]);
-    }
-    const int lim = row < it.rows ? it.p0 + (it.row0 + row) / G : -1;
-    const int lim_min = it.p0 + (it.row0 + w * HALF) / G;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's quarter of tensor memory
     const uint32_t ts = tm + lanes + L::S + w * 128, tp = tm + lanes + L::P + w * L::P_STEP, to = tm + lanes + L::O + w * D;
     const float c = a.scale * LOG2E;
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < need; ++j) {
-      mbar_wait(&sbar[w], j & 1, p.err);
-      tc_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32_nowait(ts + 32 * i, s[i]);
-      tmem_wait_ld();
-      const int key0 = (it.t0 + j) * KT;
-      if (key0 + KT - 1 > lim_min) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (key0 + 32 * i + e > lim) s[i][e] = 0xff800000u;
-      }
-      float top[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        top[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-        for (int e = 1; e < 32; ++e) top[i] = fmaxf(top[i], __uint_as_float(s[i][e]));
-      }
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-      const bool grow = mx > m + RESCALE;  // also the first finite maximum
-      if (j == 0) {
-        m = mx;
-      } else if (__any_sync(0xffffffffu, grow)) {
-        const float nm = grow ? mx : m;
-        const float f = grow ? ex2(m - nm) : 1.f;  // m = -inf: 0
-        m = nm;
-        l *= f;
-        mbar_wait(&obar[w], (j - 1) & 1, p.err);  // the last PV has completed
+    uint32_t k = 0;  // key tiles of this row tile so far: the parity of its barriers
+    while (true) {
+      const Segment g = segment(it, G, lo, hi);
+      const int need = g.need[w];
+      const int lim = row < g.rows ? g.p0 + (g.row0 + row) / G : -1;
+      const int lim_min = g.p0 + (g.row0 + w * HALF) / G;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < need; ++j, ++k) {
+        mbar_wait(&sbar[w], k & 1, p.err);
         tc_fence_after();
+        uint32_t s[4][32];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          uint32_t o[32];
-          tmem_ld32_nowait(to + 32 * i, o);
-          tmem_wait_ld();
-          float v[32];
+        for (int i = 0; i < 4; ++i) tmem_ld32_nowait(ts + 32 * i, s[i]);
+        tmem_wait_ld();
+        const int key0 = (g.t0 + j) * KT;
+        if (key0 + KT - 1 > lim_min) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f;
-          tmem_st32(to + 32 * i, v);
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (key0 + 32 * i + e > lim) s[i][e] = 0xff800000u;
+        }
+        float top[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          top[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) top[i] = fmaxf(top[i], __uint_as_float(s[i][e]));
+        }
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+        const bool grow = mx > m + RESCALE;  // also the first finite maximum
+        if (j == 0) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, grow)) {
+          const float nm = grow ? mx : m;
+          const float f = grow ? ex2(m - nm) : 1.f;  // m = -inf: 0
+          m = nm;
+          l *= f;
+          mbar_wait(&obar[w], (k - 1) & 1, p.err);  // the last PV has completed
+          tc_fence_after();
+#pragma unroll 1
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t o[16];
+            tmem_ld16_nowait(to + 16 * i, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(to + 16 * i, o);
+          }
+          tmem_wait_st();
+        }
+        const float ref = m == -INFINITY ? 0.f : -m;
+        const uint64_t c2 = pair(c, c), r2 = pair(ref, ref);
+        uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            unpair(fma2(pair(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1])), c2, r2), x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            sum[e & 1] = add2(sum[e & 1], pair(x0, x1));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x0, x1);
+            o[e] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          tmem_st16(tp + 16 * i, o);
         }
         tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&pbar[w]);
+        float s0, s1;
+        unpair(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
       }
-      const float ref = m == -INFINITY ? 0.f : -m;
-      const uint64_t c2 = pair(c, c), r2 = pair(ref, ref);
-      uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t o[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float x0, x1;
-          unpair(fma2(pair(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1])), c2, r2), x0, x1);
-          x0 = ex2(x0);
-          x1 = ex2(x1);
-          sum[e & 1] = add2(sum[e & 1], pair(x0, x1));
-          const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
-          o[e] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        tmem_st16(tp + 16 * i, o);
+      // the tile's output, or its part
+      if (need > 0) {
+        mbar_wait(&obar[w], (k - 1) & 1, p.err);
+        tc_fence_after();
       }
-      float s0, s1;
-      unpair(add2(sum[0], sum[1]), s0, s1);
-      l += s0 + s1;
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&pbar[w]);
-    }
-    // the tile's output, or its part
-    if (need > 0) {
-      mbar_wait(&obar[w], (need - 1) & 1, p.err);
-      tc_fence_after();
-    }
-    const bool live = row < it.rows;
-    const bool none = need == 0 || m == -INFINITY;
-    if (it.splits == 1) {
-      // Through shared memory (the tile's queries are done with), so that a warp stores whole
-      // rows: a row per lane would touch 32 lines with every store.
-      const float inv = none ? 0.f : 1.f / l;
+      const bool live = row < g.rows, whole = it.start >= lo && it.end <= hi;
+      const bool none = need == 0 || m == -INFINITY;
+      if (whole) {
+        // Through shared memory, 64 columns at a time and each warp its own rows, so that a
+        // store covers whole lines: a row per lane would touch 32 of them.
+        Tile<bf16, 32, 64> Os{reinterpret_cast<bf16*>(sm + L::OUT) + warp * 32 * 64};
+        const float inv = none ? 0.f : 1.f / l;
+        const int q0 = g.row0 + warp * 32 + lane / 8, sub0 = q0 % G;  // the first row this lane stores
+        const long long wrap = a.o_ts - G * a.o_hs, skip = (4 / G) * a.o_ts + (4 % G) * a.o_hs;
+        const int left = g.rows - warp * 32 - lane / 8;
+        bf16* const dst0 = static_cast<bf16*>(a.out) + (it.s.first + q0 / G) * a.o_ts + ((long long)it.h * G + sub0) * a.o_hs +
+                           lane % 8 * 8;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t o[32];
-        if (need > 0) {
-          tmem_ld32_nowait(to + 32 * i, o);
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint32_t u[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float v0 = none ? 0.f : __uint_as_float(o[e + 2 * x]) * inv;
-            const float v1 = none ? 0.f : __uint_as_float(o[e + 2 * x + 1]) * inv;
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
-            u[x] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int c0 = 0; c0 < D; c0 += 64) {
+          uint32_t o[2][32];
+          if (need > 0) {
+            tmem_ld32_nowait(to + c0, o[0]);
+            tmem_ld32_nowait(to + c0 + 32, o[1]);
+            tmem_wait_ld();
           }
-          *reinterpret_cast<uint4*>(Qs.ptr(r, 32 * i + e)) = make_uint4(u[0], u[1], u[2], u[3]);
+#pragma unroll
+          for (int e = 0; e < 64; e += 8) {
+            uint32_t u[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int y = e + 2 * x;
+              const float v0 = none ? 0.f : __uint_as_float(o[y / 32][y % 32]) * inv;
+              const float v1 = none ? 0.f : __uint_as_float(o[y / 32][y % 32 + 1]) * inv;
+              const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
+              u[x] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            *reinterpret_cast<uint4*>(Os.ptr(lane, e)) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+          __syncwarp();
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(Os.ptr(i * 4 + lane / 8, lane % 8 * 8));
+          bf16* dst = dst0 + c0;
+          int sub = sub0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // every fourth row
+            if (4 * i < left) *reinterpret_cast<uint4*>(dst) = v[i];
+            dst += skip;
+            sub += 4 % G;
+            if (sub >= G) {
+              sub -= G;
+              dst += wrap;
+            }
+          }
+          __syncwarp();
         }
-      }
-      if (live && a.lse) {
-        const int g = it.row0 + row;
-        a.lse[(size_t)(it.s.first + g / G) * p.Hq + it.h * G + g % G] = none ? -INFINITY : (m + log2f(l)) * LN2;
-      }
-      __syncwarp();
-      constexpr int CH = D / 8, STEP = 32 / CH;  // rows of one store
-#pragma unroll 4
-      for (int i = 0; i < CH; ++i) {
-        const int rr = (warp & 3) * 32 + i * STEP + lane / CH, col = lane % CH * 8, g = it.row0 + w * HALF + rr;
-        if (w * HALF + rr < it.rows)
-          *reinterpret_cast<uint4*>(static_cast<bf16*>(a.out) + (it.s.first + g / G) * a.o_ts +
-                                    (long long)(it.h * G + g % G) * a.o_hs + col) =
-              *reinterpret_cast<const uint4*>(Qs.ptr(rr, col));
-      }
-    } else {
-      float* part = tc_part<D>(a.ws, blockIdx.x);
-      if (live) {
+        if (live && a.lse) {
+          const int q = g.row0 + row;
+          a.lse[(size_t)(it.s.first + q / G) * p.Hq + it.h * G + q % G] = none ? -INFINITY : (m + log2f(l)) * LN2;
+        }
+      } else {
+        // part: four columns of all rows side by side, so that a warp's store is one run
+        float* part = Parts<ROWS, D>::slot(a.ws, blockIdx.x, it.start < lo ? 0 : 1);
         part[ROWS * D + row] = none ? -INFINITY : m;
         part[ROWS * D + ROWS + row] = l;
-      }
-      if (need > 0) {
+        if (need > 0) {
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          uint32_t o[32];
-          tmem_ld32_nowait(to + 32 * i, o);
-          tmem_wait_ld();
-          if (live)
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            tmem_ld32_nowait(to + 32 * i, o);
+            tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(part + (size_t)row * D + 32 * i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              *reinterpret_cast<uint4*>(part + ((8 * i + e / 4) * ROWS + row) * 4) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
         }
       }
+      tc_fence_before();
+      if (it.end >= hi) {
+        if (tid == 0)
+          *head = PartHead{it.start >= lo && it.end > hi ? holder(run->total, run->ncta, it.end - 1) - (int)blockIdx.x : 0,
+                           g.row0, g.rows, it.s.first, it.h, {0, 0, 0}};
+        break;
+      }
+      Num::next_item(p, G, it);
     }
-    tc_fence_before();
   } else {
     fewer_registers<OTHER_REGS>();
   }
@@ -429,75 +389,86 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---------------------------------------------------------------- products
     constexpr uint32_t id_s = umma_idesc_bf16(HALF, KT), id_o = umma_idesc_bf16(HALF, D, false, true);
     constexpr int PANEL = KT * 128;
-    // warp-uniform by construction, and known to be to the compiler
-    const int need[2] = {__shfl_sync(0xffffffffu, it.need[0], 0), __shfl_sync(0xffffffffu, it.need[1], 0)};
-    const int tiles = max(need[0], need[1]), keys = __shfl_sync(0xffffffffu, it.s.len - it.t0 * KT, 0);
     const uint32_t acc = __shfl_sync(0xffffffffu, tm, 0);
     const uint64_t dq = desc_kmajor(sm + L::Q), dring = desc_kmajor(sm + L::RING),
                    dvring = desc_mnmajor(sm + L::RING, PANEL);
     int slot = 0;
-    uint32_t phase = 0;
+    uint32_t phase = 0, np = 0;     // np: bit w is the parity of the next P of row tile w
+    uint32_t nq = 0;                // likewise of its next queries
     auto next_slot = [&]() {
       if (++slot == L::SLOTS) {
         slot = 0;
         phase ^= 1;
       }
     };
-    auto scores = [&](int w, int kslot) {
-      const uint64_t q = dq + (uint64_t)(w * (HALF * D * 2 / 16)), k = dring + (uint64_t)(kslot * (L::SLOT / 16));
+    while (true) {
+      const Segment g = segment(it, G, lo, hi);
+      // warp-uniform by construction, and known to be to the compiler
+      const int need[2] = {__shfl_sync(0xffffffffu, g.need[0], 0), __shfl_sync(0xffffffffu, g.need[1], 0)};
+      const int tiles = max(need[0], need[1]), keys = __shfl_sync(0xffffffffu, it.s.len - g.t0 * KT, 0);
+      auto scores = [&](int w, int kslot, bool last) {
+        const uint64_t q = dq + (uint64_t)(w * (HALF * D * 2 / 16)), k = dring + (uint64_t)(kslot * (L::SLOT / 16));
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h)
-        umma4_ss(acc + L::S + w * 128, q + h * (PANEL / 16), k + h * (PANEL / 16), id_s, h > 0);
-      commit_elected(&sbar[w]);
-    };
-    for (int w = 0; w < 2; ++w)
-      if (need[w] > 0) mbar_wait(&qbar[w], 0, p.err);
-    tc_fence_after();
-    if (tiles > 0) {
-      mbar_wait(&full[slot], phase, p.err);
-      for (int w = 0; w < 2; ++w)
-        if (need[w] > 0) scores(w, slot);
-      commit_elected(&empty[slot]);
-      next_slot();
-    }
-    for (int j = 0; j < tiles; ++j) {
-      const int vslot = slot;
-      mbar_wait(&full[vslot], phase, p.err);
-      next_slot();
-      const int kslot = slot;
-      const uint32_t kphase = phase;
-      const bool more = j + 1 < tiles;
-      if (more) next_slot();
-      const int keep = keys - j * KT;
-      if (keep < KT) {  // rows past the length hold anything: 0 * NaN is not 0
-        Tile<bf16, KT, D> Vs{reinterpret_cast<bf16*>(sm + L::RING + vslot * L::SLOT)};
-        for (int q = lane; q < (KT - keep) * (D / 8); q += 32)
-          *reinterpret_cast<uint4*>(Vs.ptr(keep + q / (D / 8), q % (D / 8) * 8)) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async();
-        __syncwarp();
-      }
-      bool kready = false;
+        for (int h = 0; h < D / 64; ++h)
+          umma4_ss(acc + L::S + w * 128, q + h * (PANEL / 16), k + h * (PANEL / 16), id_s, h > 0);
+        commit_elected(&sbar[w]);
+        if (last) commit_elected(&qfree[w]);  // the item's queries are done with
+      };
+      if (tiles > 0) {
+        mbar_wait(&full[slot], phase, p.err);
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (j < need[w]) {
-          mbar_wait(&pbar[w], j & 1, p.err);
-          tc_fence_after();
-          const uint64_t v = dvring + (uint64_t)(vslot * (L::SLOT / 16));
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            umma4_ts(acc + L::O + w * D, acc + L::P + w * L::P_STEP + 32 * h, v + h * 512, id_o, (j > 0 || h > 0) ? 1u : 0u);
-          commit_elected(&obar[w]);
-        }
-        if (j + 1 < need[w]) {
-          if (!kready) {
-            mbar_wait(&full[kslot], kphase, p.err);
-            kready = true;
+        for (int w = 0; w < 2; ++w)
+          if (need[w] > 0) {
+            mbar_wait(&qbar[w], nq >> w & 1, p.err);
+            nq ^= 1u << w;
+            tc_fence_after();
+            scores(w, slot, need[w] == 1);
           }
-          scores(w, kslot);
-        }
+        commit_elected(&empty[slot]);
+        next_slot();
       }
-      commit_elected(&empty[vslot]);
-      if (more) commit_elected(&empty[kslot]);
+      for (int j = 0; j < tiles; ++j) {
+        const int vslot = slot;
+        mbar_wait(&full[vslot], phase, p.err);
+        next_slot();
+        const int kslot = slot;
+        const uint32_t kphase = phase;
+        const bool more = j + 1 < tiles;
+        if (more) next_slot();
+        const int keep = keys - j * KT;
+        if (keep < KT) {  // rows past the length hold anything: 0 * NaN is not 0
+          Tile<bf16, KT, D> Vs{reinterpret_cast<bf16*>(sm + L::RING + vslot * L::SLOT)};
+          for (int q = lane; q < (KT - keep) * (D / 8); q += 32)
+            *reinterpret_cast<uint4*>(Vs.ptr(keep + q / (D / 8), q % (D / 8) * 8)) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async();
+          __syncwarp();
+        }
+        bool kready = false;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (j < need[w]) {
+            mbar_wait(&pbar[w], np >> w & 1, p.err);
+            tc_fence_after();
+            const uint64_t v = dvring + (uint64_t)(vslot * (L::SLOT / 16));
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              umma4_ts(acc + L::O + w * D, acc + L::P + w * L::P_STEP + 32 * h, v + h * 512, id_o, (j > 0 || h > 0) ? 1u : 0u);
+            np ^= 1u << w;
+            commit_elected(&obar[w]);
+          }
+          if (j + 1 < need[w]) {
+            if (!kready) {
+              mbar_wait(&full[kslot], kphase, p.err);
+              kready = true;
+            }
+            scores(w, kslot, j + 2 == need[w]);
+          }
+        }
+        commit_elected(&empty[vslot]);
+        if (more) commit_elected(&empty[kslot]);
+      }
+      if (it.end >= hi) break;
+      Num::next_item(p, G, it);
     }
     commit_elected(drained);
     mbar_drain(drained, 0);
@@ -506,94 +477,143 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---------------------------------------------------------------- key and value tiles
     const int pieces = KT / box_rows;
     constexpr int PANELS = D / 64;
-    int slot = 0, uses = 0;  // uses: loads issued
-    for (int j = 0; j < n; ++j) {
-      const int key0 = (it.t0 + j) * KT;
-      const int have = min(pieces, (it.s.len - key0 + box_rows - 1) / box_rows);  // pieces with cached rows
-      int page = 0, prow = 0;
-      if (lane < have) {
-        const int key = key0 + lane * box_rows;
-        page = checked_page(p, page_entry(p, it.b, key));
-        prow = key % p.page_size;
-      }
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (uses >= L::SLOTS) mbar_wait(&empty[slot], ((uses / L::SLOTS) - 1) & 1, p.err);
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(have * box_rows * D * 2));
-        __syncwarp();
+    int slot = 0, uses = 0;  // uses: loads issued, kept small below
+    uint32_t ephase = 1;     // parity that a slot's last release completes
+    while (true) {
+      const Segment g = segment(it, G, lo, hi);
+      const int n = max(g.need[0], g.need[1]);
+      for (int j = 0; j < n; ++j) {
+        const int key0 = (g.t0 + j) * KT;
+        const int have = min(pieces, (it.s.len - key0 + box_rows - 1) / box_rows);  // pieces with cached rows
+        int page = 0, prow = 0;
         if (lane < have) {
-          uint8_t* dst = sm + L::RING + slot * L::SLOT + lane * box_rows * 128;
-#pragma unroll
-          for (int c = 0; c < PANELS; ++c)
-            tma_load_4d(dst + c * KT * 128, kv ? &v_map : &k_map, 64 * c, prow, it.h, page, &full[slot]);
+          const int key = key0 + lane * box_rows;
+          page = checked_page(p, page_entry(p, it.b, key));
+          prow = key % p.page_size;
         }
-        ++uses;
-        if (++slot == L::SLOTS) slot = 0;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          if (uses >= L::SLOTS) mbar_wait(&empty[slot], ephase, p.err);
+          else ++uses;
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(have * box_rows * D * 2));
+          __syncwarp();
+          if (lane < have) {
+            uint8_t* dst = sm + L::RING + slot * L::SLOT + lane * box_rows * 128;
+#pragma unroll
+            for (int c = 0; c < PANELS; ++c)
+              tma_load_4d(dst + c * KT * 128, kv ? &v_map : &k_map, 64 * c, prow, it.h, page, &full[slot]);
+          }
+          if (++slot == L::SLOTS) {
+            slot = 0;
+            ephase ^= 1;
+          }
+        }
       }
+      if (it.end >= hi) break;
+      Num::next_item(p, G, it);
     }
-    if (lane == 0) drain_ring(full, L::SLOTS, uses);
+    // after a failed wait loads may still be on their way: the last one of every slot used
+    if (lane == 0)
+      for (int i = 0; i < uses; ++i) mbar_drain(&full[i], i < slot ? ephase ^ 1 : ephase);
     __syncwarp();
+  } else if (warp >= QLOAD_WARP) {
+    // ---------------------------------------------------------------- queries of a row tile
+    // All rows of the tile in flight at once (cp.async), rows past the end zero.
+    // A lane takes the same 16 bytes of every STEP-th row: their swizzled places repeat
+    // every eight rows, and the global address is stepped (G query heads a token).
+    constexpr int CH = D / 8, STEP = 32 / CH, TURN = 8 / STEP;
+    const int w = warp - QLOAD_WARP, col = lane % CH * 8;
+    Tile<bf16, HALF, D> Qs{reinterpret_cast<bf16*>(sm + L::Q + w * HALF * D * 2)};
+    uint32_t place[TURN];
+#pragma unroll
+    for (int i = 0; i < TURN; ++i) place[i] = smem_u32(Qs.ptr(lane / CH + i * STEP, col));
+    const long long wrap = a.q_ts - G * a.q_hs, skip = (STEP / G) * a.q_ts + (STEP % G) * a.q_hs;
+    uint32_t loads = 0;
+    while (true) {
+      const Segment g = segment(it, G, lo, hi);
+      if (g.need[w] > 0) {
+        const int q = g.row0 + w * HALF + lane / CH, left = g.rows - w * HALF - lane / CH;
+        int sub = q % G;
+        const bf16* src = static_cast<const bf16*>(a.q) + (it.s.first + q / G) * a.q_ts + ((long long)it.h * G + sub) * a.q_hs + col;
+        if (loads > 0) mbar_wait(&qfree[w], (loads - 1) & 1, p.err);
+        ++loads;
+#pragma unroll 2
+        for (int b = 0; b < HALF / 8; ++b) {
+#pragma unroll
+          for (int i = 0; i < TURN; ++i) {
+            const uint32_t to = place[i] + b * 1024;
+            if (b * 8 + i * STEP < left)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(src) : "memory");
+            else
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(to), "r"(0) : "memory");
+            src += skip;
+            sub += STEP % G;
+            if (sub >= G) {
+              sub -= G;
+              src += wrap;
+            }
+          }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qbar[w]);
+      }
+      if (it.end >= hi) break;
+      Num::next_item(p, G, it);
+    }
   }
   __syncthreads();
   tc_fence_after();
   if (warp == MMA_WARP) tmem_dealloc(tm, 512);
 }
 
-// Joins the parts of the split items: eight rows per CTA, a thread per four columns.
-constexpr int JOIN_ROWS = 8;
+// Joins the parts of the item that begins in CTA blockIdx.x and goes on in the next ones,
+// in the order of the CTAs: 32 rows per CTA (a row per lane), the columns over the warps.
+constexpr int JOIN_WARPS = 8;
 template <int D>
-__global__ void __launch_bounds__(JOIN_ROWS * D / 4) paged_attn_tc_join_kernel(AttnArgs a, int splits) {
+__global__ void __launch_bounds__(32 * JOIN_WARPS) paged_attn_tc_join_kernel(AttnArgs a) {
   pdl_wait();
-  const PagedArgs& p = a.p;
-  const int G = p.Hq / p.Hk, lane = threadIdx.x & 31;
-  TcItem it;
-  if (!find_item(p, G, lane, blockIdx.x, 0, splits, it) || it.splits == 1) return;
-  const int row = blockIdx.y * JOIN_ROWS + threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;
-  if (row >= it.rows) return;
-  const float* first = tc_part<D>(a.ws, (size_t)blockIdx.x * splits);
-  constexpr size_t STEP = ROWS * (D + 2);
-  float M = -INFINITY;
-  for (int s = 0; s < it.splits; ++s) M = fmaxf(M, first[s * STEP + ROWS * D + row]);
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-  for (int s = 0; s < it.splits; ++s) {
-    const float m = first[s * STEP + ROWS * D + row];
-    if (m == -INFINITY) continue;
-    const float f = ex2(m - M);
-    const float4 v = *reinterpret_cast<const float4*>(first + s * STEP + (size_t)row * D + col);
-    o[0] += v.x * f; o[1] += v.y * f; o[2] += v.z * f; o[3] += v.w * f;
-    l += first[s * STEP + ROWS * D + ROWS + row] * f;
-  }
-  const int g = it.row0 + row, tok = it.s.first + g / G, head = it.h * G + g % G;
-  const float inv = M == -INFINITY ? 0.f : 1.f / l;
+  pdl_trigger();
+  const int c = blockIdx.x, row = blockIdx.y * 32 + (threadIdx.x & 31), c40 = threadIdx.x >> 5;
+  const PartHead h = part_heads<ROWS, D>(a.ws, gridDim.x)[c];
+  if (h.more == 0 || row >= h.rows) return;
+  constexpr size_t STEP = 2 * Parts<ROWS, D>::SLOT;  // from one CTA's slot to the next CTA's
+  constexpr int N = D / 4 / JOIN_WARPS;              // vectors of four columns per thread
+  const float *first = Parts<ROWS, D>::slot(a.ws, c, 1), *rest = Parts<ROWS, D>::slot(a.ws, c + 1, 0);
+  float M = first[ROWS * D + row];
+#pragma unroll 8
+  for (int q = 0; q < h.more; ++q) M = fmaxf(M, rest[q * STEP + ROWS * D + row]);
+  float4 o[N];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] *= inv;
-  st4(static_cast<bf16*>(a.out) + tok * a.o_ts + head * a.o_hs + col, o);
-  if (a.lse && col == 0) a.lse[(size_t)tok * p.Hq + head] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * LN2;
-}
-
-// Most items a call can have: full ones, and one that is not full per sequence.
-long long item_bound(const AttnArgs& a) {
-  const long long G = a.p.Hq / a.p.Hk, rows = (long long)a.p.N * G, seqs = a.p.B < a.p.N ? a.p.B : a.p.N;
-  return (rows / ROWS + seqs) * a.p.Hk;
-}
-// Splits per item: the fewest SM-waves of key tiles, with a few tiles' time for an item's
-// start and end, and for reading the parts again.
-int split_count(const AttnArgs& a, int nsm) {
-  const long long G = a.p.Hq / a.p.Hk;
-  const long long per_seq = ((a.max_q < a.p.N ? a.max_q : a.p.N) * G + ROWS - 1) / ROWS;
-  long long items = per_seq * a.p.B * a.p.Hk;
-  if (item_bound(a) < items) items = item_bound(a);
-  const long long tiles = ((long long)a.max_kv + KT - 1) / KT;
-  long long best = 1, cost = 0;
-  for (long long ns = 1; ns <= 64 && (ns == 1 || (items * ns <= TC_SPLIT_ITEMS && 2 * ns <= tiles)); ++ns) {
-    const long long waves = (items * ns + nsm - 1) / nsm;
-    const long long c = waves * ((tiles + ns - 1) / ns + 4) + (ns > 1 ? 4 + ns / 4 : 0);
-    if (ns == 1 || c < cost) {
-      best = ns;
-      cost = c;
+  for (int i = 0; i < N; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  const float* part = first;
+#pragma unroll 4
+  for (int q = 0; q <= h.more; ++q) {
+    const float m = part[ROWS * D + row];
+    const bool some = m != -INFINITY;  // a part without keys has no o
+    const float f = some ? ex2(m - M) : 0.f;
+    l += some ? part[ROWS * D + ROWS + row] * f : 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(part + ((size_t)(c40 + i * JOIN_WARPS) * ROWS + row) * 4);
+      if (some) {
+        o[i].x += v.x * f; o[i].y += v.y * f; o[i].z += v.z * f; o[i].w += v.w * f;
+      }
     }
+    part = rest + q * STEP;
   }
-  return (int)best;
+  const int G = a.p.Hq / a.p.Hk, q = h.row0 + row, tok = h.first + q / G, head = h.h * G + q % G;
+  const float inv = M == -INFINITY ? 0.f : 1.f / l;
+  bf16* dst = static_cast<bf16*>(a.out) + tok * a.o_ts + head * a.o_hs;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float v[4] = {o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv};
+    st4(dst + (c40 + i * JOIN_WARPS) * 4, v);
+  }
+  if (a.lse && c40 == 0) a.lse[(size_t)tok * a.p.Hq + head] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * LN2;
 }
 
 // [pages][heads][rows][D] bf16 with the cache's strides; box: 64 channels of `box` rows.
@@ -611,18 +631,17 @@ bool cache_map(CUtensorMap* map, void* base, const PagedArgs& p, long long ps, l
 }
 
 template <int D>
-cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int box, int nsm, cudaStream_t s) {
+cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int box, cudaStream_t s) {
   const int bytes = TcLay<D>::BYTES + 1024;
   cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  const int splits = split_count(a, nsm);
-  const long long items = item_bound(a);
+  const int grid = launch_ctas(a, ROWS, KT, MIN_UNITS);
   prof_mark(K_ATTN_TC, s, true);
-  e = launch_pdl(paged_attn_tc_kernel<D>, dim3((unsigned)(items * splits)), dim3(THREADS), bytes, s, a, splits, box, km, vm);
+  e = launch_pdl(paged_attn_tc_kernel<D>, dim3(grid), dim3(THREADS), bytes, s, a, box, km, vm);
   prof_mark(K_ATTN_TC, s, false);
-  if (e != cudaSuccess || splits == 1) return e;
+  if (e != cudaSuccess) return e;
   prof_mark(K_ATTN_TC_JOIN, s, true);
-  e = launch_pdl(paged_attn_tc_join_kernel<D>, dim3((unsigned)items, ROWS / JOIN_ROWS), dim3(JOIN_ROWS * D / 4), 0, s, a, splits);
+  e = launch_pdl(paged_attn_tc_join_kernel<D>, dim3(grid, ROWS / 32), dim3(32 * JOIN_WARPS), 0, s, a);
   prof_mark(K_ATTN_TC_JOIN, s, false);
   return e;
 }
@@ -635,15 +654,12 @@ bool paged_attn_tc_applies(const AttnArgs& a) {
 }
 
 size_t paged_attn_tc_workspace(const AttnArgs& a) {
-  const int nsm = device_sm_count();
-  const int splits = split_count(a, nsm > 0 ? nsm : 152);
-  return splits == 1 ? 0 : (size_t)item_bound(a) * splits * ROWS * (a.p.D + 2) * sizeof(float);
+  const int grid = launch_ctas(a, ROWS, KT, MIN_UNITS);
+  return a.p.D == 64 ? Parts<ROWS, 64>::bytes(grid) : Parts<ROWS, 128>::bytes(grid);
 }
 
 cudaError_t launch_paged_attn_tc(const AttnArgs& a, cudaStream_t s, bool* done) {
   *done = false;
-  const int nsm = device_sm_count();
-  if (nsm < 1) return cudaErrorInvalidDevice;
   int box = KT;  // rows of a box: a run inside one page and inside one tile
   while (a.p.page_size % box != 0) box >>= 1;
   CUtensorMap km{}, vm{};
@@ -651,7 +667,7 @@ cudaError_t launch_paged_attn_tc(const AttnArgs& a, cudaStream_t s, bool* done) 
       !cache_map(&vm, a.p.vc, a.p, a.p.v_ps, a.p.v_hs, a.p.v_rs, box))
     return cudaSuccess;  // strides that a tensor map cannot hold: the caller takes the other kernel
   *done = true;
-  return a.p.D == 64 ? run<64>(a, km, vm, box, nsm, s) : run<128>(a, km, vm, box, nsm, s);
+  return a.p.D == 64 ? run<64>(a, km, vm, box, s) : run<128>(a, km, vm, box, s);
 }
 
 }  // namespace gdn
