@@ -207,6 +207,38 @@ struct Numbering {
     locate(p, G, lane, r.lo, c, r.first);
     return true;
   }
+  // Item `idx` as a run of its own: the KV heads of a run of rows side by side, the items of
+  // a sequence from its last, the one with the most keys, and the sequences likewise. False
+  // when there are fewer items.
+  static __device__ __forceinline__ bool pick(const PagedArgs& p, int G, int lane, int idx, Run& r) {
+    int i = idx / p.Hk;
+    Item& it = r.first;
+    it.h = idx % p.Hk;
+    for (int b0 = p.B - 1; b0 >= 0; b0 -= 32) {
+      const int b = b0 - lane;
+      const Seq s = b >= 0 ? load_seq(p, b, idx == 0) : Seq{0, 0, 0};
+      const int n = seq_items(s, G);
+      int inc = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += o;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, inc > i);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        it.b = b0 - l;
+        it.s = Seq{__shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.first, l), __shfl_sync(0xffffffffu, s.len, l)};
+        it.i = __shfl_sync(0xffffffffu, inc, l) - 1 - i;
+        it.start = r.lo = 0;
+        it.end = r.hi = r.total = item_units(it.s, G, it.i);
+        r.ncta = 1;
+        return true;
+      }
+      i -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return false;
+  }
   // CTAs that take part: enough units for each to have `least`.
   static __device__ __forceinline__ int active_ctas(long long total, int grid, int least) {
     const long long most = (total + least - 1) / least;
@@ -223,14 +255,18 @@ struct Parts {
   static __device__ __forceinline__ float* slot(float* ws, int cta, int second) { return ws + (size_t)(2 * cta + second) * SLOT; }
   static size_t bytes(int ctas) { return (2 * SLOT * sizeof(float) + 32) * (size_t)ctas; }
 };
+// Most items that a call can have: full ones, and one that is not full per sequence.
+inline long long most_items(const AttnArgs& a, int rows) {
+  const long long G = a.p.Hq / a.p.Hk, seqs = a.p.B < a.p.N ? a.p.B : a.p.N;
+  return ((long long)a.p.N * G / rows + seqs) * a.p.Hk;
+}
 // CTAs of a launch: one per SM, or as many as the work can occupy by the caller's bounds on
 // new tokens and length (which limit only this).
 inline int launch_ctas(const AttnArgs& a, int rows, int unit, int least) {
   const int nsm = device_sm_count() > 0 ? device_sm_count() : 152;
   const long long G = a.p.Hq / a.p.Hk, seqs = a.p.B < a.p.N ? a.p.B : a.p.N;
-  const long long per_seq = ((long long)(a.max_q < a.p.N ? a.max_q : a.p.N) * G + rows - 1) / rows * seqs;
-  const long long packed = (long long)a.p.N * G / rows + seqs;  // full items, and one that is not per sequence
-  const long long items = (per_seq < packed ? per_seq : packed) * a.p.Hk;
+  const long long per_seq = ((long long)(a.max_q < a.p.N ? a.max_q : a.p.N) * G + rows - 1) / rows * seqs * a.p.Hk;
+  const long long most = most_items(a, rows), items = per_seq < most ? per_seq : most;
   const long long per_item = ((long long)a.max_kv + unit - 1) / unit;
   if (items >= (long long)nsm * least || per_item >= (long long)nsm * least) return nsm;
   const long long want = (items * per_item + least - 1) / least;

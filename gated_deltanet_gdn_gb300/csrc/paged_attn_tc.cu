@@ -9,20 +9,25 @@
 // tiles (the sums stay exact: P, its sum and O refer to the same maximum).
 //
 // Two warpgroups of softmax threads (one row tile each, a thread per row), and in a third
-// one warp that issues every MMA, one that feeds a ring of key and value tiles by TMA (a
-// box per run of rows inside one page), and one per row tile that brings its queries. The
-// tensor pipe works on one row tile's products while the other tile's softmax runs:
+// one warp that issues every MMA, two that feed a ring of key and value tiles by TMA (a box
+// per run of rows inside one page; with pages of 16 one warp's issue would be the bound),
+// and one that brings the queries (the first item's are the softmax warps'). The tensor
+// pipe works on one row tile's products while the other tile's softmax runs:
 //   ... PV0(j) QK0(j+1) | PV1(j) QK1(j+1) | PV0(j+1) ...
 // P takes the first half of its tile's S columns at D = 128 (MMAs of one shape execute in
 // issue order, so QK(j+1) cannot overtake the PV(j) that reads P); at D = 64 it has columns
 // of its own.
 //
-// One persistent CTA per SM takes an equal run of the call's (item, key tile) units, so
-// neither ragged lengths, nor the causal triangle, nor fewer items than SMs leave SMs idle.
-// Every role walks the run by itself: the next item's keys and queries are on their way,
-// and its first product done, while this item's output is written. An item that a CTA
-// holds whole is written at once; at the ends of a CTA's run the parts go to the workspace
-// and a second kernel joins them in the order of the CTAs.
+// Two schedules, one body:
+//  * few items: one persistent CTA per SM takes an equal run of the call's (item, key tile)
+//    units, so neither ragged lengths, nor the causal triangle, nor fewer items than SMs
+//    leave SMs idle. Every role walks the run by itself, so that the next item's keys and
+//    queries are on their way, and its first product done, while this item's output is
+//    written. An item that a CTA holds whole is written at once; at the ends of a CTA's run
+//    the parts go to the workspace and a second kernel joins them in the order of the CTAs.
+//  * many items (two or more per SM): a CTA per item, the longest first and the KV heads of
+//    a run of rows side by side. The CTAs that run at the same time then read the same keys
+//    at the same time, which the L2 serves once.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -34,7 +39,7 @@ namespace {
 
 constexpr int ROWS = 256, HALF = 128, KT = 128;  // query rows of an item, of a tile; keys of a tile
 constexpr int THREADS = 384;  // three warpgroups: two of softmax, and one of the warps below
-constexpr int MMA_WARP = 8, LOAD_WARP = 9, QLOAD_WARP = 10;  // queries: 10 and 11
+constexpr int MMA_WARP = 8, KEY_WARP = 9, VALUE_WARP = 10, QUERY_WARP = 11;
 // Registers a thread, moved from the third warpgroup to the softmax (which holds 128 scores):
 // the launch has 168 each, 2 * 216 + 72 = 3 * 168.
 constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
@@ -55,14 +60,16 @@ struct TcLay {
   static constexpr int SLOTS = D == 128 ? 4 : 8;
   static constexpr int Q = 0;                            // two [128][D] tiles
   static constexpr int RING = 2 * HALF * D * 2;
-  static constexpr int OUT = RING + SLOTS * SLOT;        // two [128][64] tiles on their way out
-  static constexpr int BAR = OUT + 2 * HALF * 64 * 2;
+  static constexpr int OUT = RING + SLOTS * SLOT;        // two fp32 [128][32] stages of a merge
+  static constexpr int ML = OUT + HALF * 32 * 4;         // m, l of both row tiles, before the second stage's use
+  static constexpr int BAR = OUT + 2 * HALF * 32 * 4;
   // barriers: full[SLOTS], empty[SLOTS], then q, qfree, s, o [2] each, p [2][2] (row tile,
   // half of the keys), drained
   static constexpr int NBAR = 2 * SLOTS + 13;
   static constexpr int RUN = BAR + (NBAR + 1) / 2 * 16;
   static constexpr int TSLOT = RUN + 128;
   static constexpr int BYTES = TSLOT + 16;
+  static_assert(BYTES + 1024 <= 227 * 1024, "one CTA per SM");
   // tensor memory columns
   static constexpr int S = 0, O = 256, P = D == 128 ? 0 : 256 + 2 * D;
   static constexpr int P_STEP = D == 128 ? 128 : 64;     // between the two tiles' P
@@ -143,15 +150,35 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// 32 bytes of a row: one store of whole sectors, or two of 16 bytes where rows are only
+// aligned to those.
+__device__ __forceinline__ void store32(bf16* dst, const uint32_t (&u)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                 "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
+    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+  }
+}
+
 // An item's start and end take a CTA about as long as OVER key tiles.
 constexpr int OVER = 3;
 typedef Numbering<ROWS, KT, OVER> Num;
-constexpr int MIN_UNITS = OVER + 2;  // units that make a CTA take part
+constexpr int MIN_UNITS = 3;  // units that make a CTA take part
 
 // What a CTA does of one item: key tiles from t0 on, `need` of them for each row tile (none
-// when its run ends before the item's keys, or the rows see none).
+// when its run ends before the item's keys, or the rows see none). An item of one row tile
+// ("alone") has its rows in both, with the even key tiles for the first and the odd ones for
+// the second; the two are merged at the end.
 struct Segment {
   int row0, rows, p0, t0, need[2];
+  bool alone;
+  // the first row of row tile w in the item, and its j-th key tile
+  __device__ __forceinline__ int base(int w) const { return alone ? 0 : w * HALF; }
+  __device__ __forceinline__ int tile(int w, int j) const { return t0 + (alone ? 2 * j + w : j); }
+  __device__ __forceinline__ int tiles() const { return alone ? need[0] + need[1] : max(need[0], need[1]); }
 };
 __device__ __forceinline__ Segment segment(const Item& it, int G, long long lo, long long hi) {
   Segment g;
@@ -166,12 +193,54 @@ __device__ __forceinline__ Segment segment(const Item& it, int G, long long lo, 
     const int t = last >= w * HALF ? key_blocks<KT>(it.s, G, g.row0 + last) : 0;
     g.need[w] = max(min(t, t1) - g.t0, 0);
   }
+  g.alone = g.rows <= HALF;
+  if (g.alone) {
+    g.need[1] = g.need[0] >> 1;
+    g.need[0] -= g.need[1];
+  }
   return g;
+}
+
+// The queries of row tile w into its shared memory by COUNT threads, `t` the caller's
+// number: 16 bytes of every STEP-th row each, all in flight at once (cp.async), rows past the
+// end zero. The swizzled places repeat every eight rows, and the global address is stepped
+// (G query heads a token). Ends with the data visible to the tensor cores.
+template <int D, int COUNT>
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, const Segment& g, int G, int w, int t, bf16* tile) {
+  constexpr int CH = D / 8, STEP = COUNT / CH, TURN = STEP < 8 ? 8 / STEP : 1;
+  Tile<bf16, HALF, D> Qs{tile};
+  const int row = t / CH, col = t % CH * 8, q = g.row0 + g.base(w) + row, left = g.rows - g.base(w) - row;
+  uint32_t place[TURN];
+#pragma unroll
+  for (int i = 0; i < TURN; ++i) place[i] = smem_u32(Qs.ptr(row + i * STEP, col));
+  const long long wrap = a.q_ts - G * a.q_hs, skip = (STEP / G) * a.q_ts + (STEP % G) * a.q_hs;
+  int sub = q % G;
+  const bf16* src = static_cast<const bf16*>(a.q) + (it.s.first + q / G) * a.q_ts + ((long long)it.h * G + sub) * a.q_hs + col;
+#pragma unroll 2
+  for (int b = 0; b < HALF / (STEP * TURN); ++b) {
+#pragma unroll
+    for (int i = 0; i < TURN; ++i) {
+      const uint32_t to = place[i] + b * (STEP * TURN * 128);
+      if ((b * TURN + i) * STEP < left)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(src) : "memory");
+      else
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(to), "r"(0) : "memory");
+      src += skip;
+      sub += STEP % G;
+      if (sub >= G) {
+        sub -= G;
+        src += wrap;
+      }
+    }
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  fence_proxy_async();
 }
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
-    paged_attn_tc_kernel(AttnArgs a, int box_rows, const __grid_constant__ CUtensorMap k_map,
+    paged_attn_tc_kernel(AttnArgs a, int box_rows, int whole_items, const __grid_constant__ CUtensorMap k_map,
                          const __grid_constant__ CUtensorMap v_map) {
   pdl_wait();
   pdl_trigger();
@@ -189,7 +258,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   Num::Run* run = reinterpret_cast<Num::Run*>(sm + L::RUN);
   if (warp == 0) {
     Num::Run r;
-    if (!Num::plan(p, G, lane, blockIdx.x, gridDim.x, MIN_UNITS, r)) r.lo = r.hi = 0;
+    const bool some = whole_items ? Num::pick(p, G, lane, blockIdx.x, r)
+                                  : Num::plan(p, G, lane, blockIdx.x, gridDim.x, MIN_UNITS, r);
+    if (!some) r.lo = r.hi = 0;
     if (lane == 0) *run = r;
   } else if (warp == MMA_WARP) {
     tmem_alloc(tslot, 512);
@@ -206,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const long long lo = run->lo, hi = run->hi;
   PartHead* head = part_heads<ROWS, D>(a.ws, gridDim.x) + blockIdx.x;
   if (lo == hi) {  // no share
-    if (tid == 0) head->more = 0;
+    if (tid == 0 && !whole_items) head->more = 0;
     if (warp == MMA_WARP) tmem_dealloc(tm, 512);
     return;
   }
@@ -216,16 +287,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---------------------------------------------------------------- softmax
     more_registers<SOFTMAX_REGS>();
     const int w = warp >> 2, r = tid & (HALF - 1);  // row tile, row of it
-    const int row = w * HALF + r;                   // row of the item
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's quarter of tensor memory
     const uint32_t ts = tm + lanes + L::S + w * 128, tp = tm + lanes + L::P + w * L::P_STEP, to = tm + lanes + L::O + w * D;
     const float c = a.scale * LOG2E;
+    {
+      const Segment g = segment(it, G, lo, hi);
+      if ((w ? g.need[1] : g.need[0]) > 0) {
+        load_queries<D, HALF>(a, it, g, G, w, r, reinterpret_cast<bf16*>(sm + L::Q + w * HALF * D * 2));
+        asm volatile("bar.sync %0, 128;" ::"r"(2 + w) : "memory");
+        if (r == 0) mbar_arrive(&qbar[w]);
+      }
+    }
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | (a.o_ts * 2) | (a.o_hs * 2)) & 31) == 0;
     uint32_t k = 0;  // key tiles of this row tile so far: the parity of its barriers
     while (true) {
       const Segment g = segment(it, G, lo, hi);
-      const int need = g.need[w];
+      const int need = w ? g.need[1] : g.need[0];
+      const int row = g.base(w) + r;  // row of the item
       const int lim = row < g.rows ? g.p0 + (g.row0 + row) / G : -1;
-      const int lim_min = g.p0 + (g.row0 + w * HALF) / G;
+      const int lim_min = g.p0 + (g.row0 + g.base(w)) / G;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < need; ++j, ++k) {
         mbar_wait(&sbar[w], k & 1, p.err);
@@ -234,7 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) tmem_ld32_nowait(ts + 32 * i, s[i]);
         tmem_wait_ld();
-        const int key0 = (g.t0 + j) * KT;
+        const int key0 = g.tile(w, j) * KT;
         if (key0 + KT - 1 > lim_min) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -301,67 +381,91 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_wait(&obar[w], (k - 1) & 1, p.err);
         tc_fence_after();
       }
-      const bool live = row < g.rows, whole = it.start >= lo && it.end <= hi;
-      const bool none = need == 0 || m == -INFINITY;
-      if (whole) {
-        // Through shared memory, 64 columns at a time and each warp its own rows, so that a
-        // store covers whole lines: a row per lane would touch 32 of them.
-        Tile<bf16, 32, 64> Os{reinterpret_cast<bf16*>(sm + L::OUT) + warp * 32 * 64};
-        const float inv = none ? 0.f : 1.f / l;
-        const int q0 = g.row0 + warp * 32 + lane / 8, sub0 = q0 % G;  // the first row this lane stores
-        const long long wrap = a.o_ts - G * a.o_hs, skip = (4 / G) * a.o_ts + (4 % G) * a.o_hs;
-        const int left = g.rows - warp * 32 - lane / 8;
-        bf16* const dst0 = static_cast<bf16*>(a.out) + (it.s.first + q0 / G) * a.o_ts + ((long long)it.h * G + sub0) * a.o_hs +
-                           lane % 8 * 8;
+      const bool whole = it.start >= lo && it.end <= hi;
+      bool live = row < g.rows, none = need == 0 || m == -INFINITY;
+      if (g.alone) {
+        if (g.need[1] > 0) {
+          // merge the second row tile into the first, 32 columns at a time through shared memory
+          float* ml = reinterpret_cast<float*>(sm + L::ML);
+          float* stage = reinterpret_cast<float*>(sm + L::OUT);
+          ml[w * HALF + r] = m;
+          ml[(2 + w) * HALF + r] = l;
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          const float om = ml[(1 - w) * HALF + r], M = fmaxf(m, om);
+          const float f = m == -INFINITY ? 0.f : ex2(m - M), of = om == -INFINITY ? 0.f : ex2(om - M);
+          l = l * f + ml[(3 - w) * HALF + r] * of;
+          m = M;
+          none = M == -INFINITY;
 #pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 64) {
-          uint32_t o[2][32];
+          for (int i = 0; i < D / 32; ++i) {
+            float* at = stage + (i & 1) * HALF * 32 + r * 32;  // chunks of four columns, swizzled by row
+            uint32_t o[32];
+            tmem_ld32_nowait(to + 32 * i, o);
+            tmem_wait_ld();
+            if (w == 1) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(at + (((e >> 2) ^ (r & 7)) << 2)) =
+                    make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f, __uint_as_float(o[e + 2]) * f,
+                                __uint_as_float(o[e + 3]) * f);
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (w == 0) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(at + (((e >> 2) ^ (r & 7)) << 2));
+                o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), f, x.x));
+                o[e + 1] = __float_as_uint(fmaf(__uint_as_float(o[e + 1]), f, x.y));
+                o[e + 2] = __float_as_uint(fmaf(__uint_as_float(o[e + 2]), f, x.z));
+                o[e + 3] = __float_as_uint(fmaf(__uint_as_float(o[e + 3]), f, x.w));
+              }
+              tmem_st16(to + 32 * i, *reinterpret_cast<const uint32_t(*)[16]>(&o[0]));
+              tmem_st16(to + 32 * i + 16, *reinterpret_cast<const uint32_t(*)[16]>(&o[16]));
+            }
+          }
+          tmem_wait_st();
+          asm volatile("bar.sync 1, 256;" ::: "memory");  // the stages are free for the next merge
+        }
+        live = live && w == 0;  // the first row tile writes
+      }
+      if (whole) {
+        const float inv = none ? 0.f : 1.f / l;
+        const int q = g.row0 + row, tok = it.s.first + q / G, head_q = it.h * G + q % G;
+        bf16* dst = static_cast<bf16*>(a.out) + (live ? tok * a.o_ts + head_q * a.o_hs : 0);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
           if (need > 0) {
-            tmem_ld32_nowait(to + c0, o[0]);
-            tmem_ld32_nowait(to + c0 + 32, o[1]);
+            tmem_ld32_nowait(to + 32 * i, o);
             tmem_wait_ld();
           }
+          if (live) {
 #pragma unroll
-          for (int e = 0; e < 64; e += 8) {
-            uint32_t u[4];
+            for (int e = 0; e < 32; e += 16) {
+              uint32_t u[8];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int y = e + 2 * x;
-              const float v0 = none ? 0.f : __uint_as_float(o[y / 32][y % 32]) * inv;
-              const float v1 = none ? 0.f : __uint_as_float(o[y / 32][y % 32 + 1]) * inv;
-              const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
-              u[x] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(Os.ptr(lane, e)) = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-          __syncwarp();
-          uint4 v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(Os.ptr(i * 4 + lane / 8, lane % 8 * 8));
-          bf16* dst = dst0 + c0;
-          int sub = sub0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {  // every fourth row
-            if (4 * i < left) *reinterpret_cast<uint4*>(dst) = v[i];
-            dst += skip;
-            sub += 4 % G;
-            if (sub >= G) {
-              sub -= G;
-              dst += wrap;
+              for (int x = 0; x < 8; ++x) {
+                const float v0 = none ? 0.f : __uint_as_float(o[e + 2 * x]) * inv;
+                const float v1 = none ? 0.f : __uint_as_float(o[e + 2 * x + 1]) * inv;
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v0, v1);
+                u[x] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              store32(dst + 32 * i + e, u, wide);
             }
           }
-          __syncwarp();
         }
-        if (live && a.lse) {
-          const int q = g.row0 + row;
-          a.lse[(size_t)(it.s.first + q / G) * p.Hq + it.h * G + q % G] = none ? -INFINITY : (m + log2f(l)) * LN2;
+        if (live) {
+          if (a.lse) a.lse[(size_t)tok * p.Hq + head_q] = none ? -INFINITY : (m + log2f(l)) * LN2;
         }
       } else {
         // part: four columns of all rows side by side, so that a warp's store is one run
         float* part = Parts<ROWS, D>::slot(a.ws, blockIdx.x, it.start < lo ? 0 : 1);
-        part[ROWS * D + row] = none ? -INFINITY : m;
-        part[ROWS * D + ROWS + row] = l;
-        if (need > 0) {
+        const bool mine = !g.alone || w == 0;
+        if (mine) {
+          part[ROWS * D + row] = none ? -INFINITY : m;
+          part[ROWS * D + ROWS + row] = l;
+        }
+        if (need > 0 && mine) {
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             uint32_t o[32];
@@ -375,7 +479,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       tc_fence_before();
       if (it.end >= hi) {
-        if (tid == 0)
+        if (tid == 0 && !whole_items)
           *head = PartHead{it.start >= lo && it.end > hi ? holder(run->total, run->ncta, it.end - 1) - (int)blockIdx.x : 0,
                            g.row0, g.rows, it.s.first, it.h, {0, 0, 0}};
         break;
@@ -405,7 +509,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Segment g = segment(it, G, lo, hi);
       // warp-uniform by construction, and known to be to the compiler
       const int need[2] = {__shfl_sync(0xffffffffu, g.need[0], 0), __shfl_sync(0xffffffffu, g.need[1], 0)};
-      const int tiles = max(need[0], need[1]), keys = __shfl_sync(0xffffffffu, it.s.len - g.t0 * KT, 0);
+      const bool alone = __shfl_sync(0xffffffffu, (int)g.alone, 0) != 0;
+      const int tiles = __shfl_sync(0xffffffffu, g.tiles(), 0), keys = __shfl_sync(0xffffffffu, it.s.len - g.t0 * KT, 0);
       auto scores = [&](int w, int kslot, bool last) {
         const uint64_t q = dq + (uint64_t)(w * (HALF * D * 2 / 16)), k = dring + (uint64_t)(kslot * (L::SLOT / 16));
 #pragma unroll
@@ -414,11 +519,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         commit_elected(&sbar[w]);
         if (last) commit_elected(&qfree[w]);  // the item's queries are done with
       };
-      if (tiles > 0) {
+      // the first scores of each row tile: of one key tile, or of the first two
+      const int ahead = alone ? 2 : 1;
+      for (int i = 0; i < ahead && i < tiles; ++i) {
         mbar_wait(&full[slot], phase, p.err);
 #pragma unroll
         for (int w = 0; w < 2; ++w)
-          if (need[w] > 0) {
+          if (alone ? w == i : need[w] > 0) {
             mbar_wait(&qbar[w], nq >> w & 1, p.err);
             nq ^= 1u << w;
             tc_fence_after();
@@ -427,15 +534,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         commit_elected(&empty[slot]);
         next_slot();
       }
-      for (int j = 0; j < tiles; ++j) {
+      for (int i = 0; i < tiles; ++i) {
         const int vslot = slot;
         mbar_wait(&full[vslot], phase, p.err);
         next_slot();
         const int kslot = slot;
         const uint32_t kphase = phase;
-        const bool more = j + 1 < tiles;
+        const bool more = i + ahead < tiles;
         if (more) next_slot();
-        const int keep = keys - j * KT;
+        const int keep = keys - i * KT;
         if (keep < KT) {  // rows past the length hold anything: 0 * NaN is not 0
           Tile<bf16, KT, D> Vs{reinterpret_cast<bf16*>(sm + L::RING + vslot * L::SLOT)};
           for (int q = lane; q < (KT - keep) * (D / 8); q += 32)
@@ -446,7 +553,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool kready = false;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          if (j < need[w]) {
+          const int j = alone ? i >> 1 : i;  // the row tile's own count
+          if (alone ? (i & 1) == w : i < need[w]) {
             mbar_wait(&pbar[w], np >> w & 1, p.err);
             tc_fence_after();
             const uint64_t v = dvring + (uint64_t)(vslot * (L::SLOT / 16));
@@ -455,13 +563,13 @@ __global__ void __launch_bounds__(THREADS, 1)
               umma4_ts(acc + L::O + w * D, acc + L::P + w * L::P_STEP + 32 * h, v + h * 512, id_o, (j > 0 || h > 0) ? 1u : 0u);
             np ^= 1u << w;
             commit_elected(&obar[w]);
-          }
-          if (j + 1 < need[w]) {
-            if (!kready) {
-              mbar_wait(&full[kslot], kphase, p.err);
-              kready = true;
+            if (j + 1 < need[w]) {
+              if (!kready) {
+                mbar_wait(&full[kslot], kphase, p.err);
+                kready = true;
+              }
+              scores(w, kslot, j + 2 == need[w]);
             }
-            scores(w, kslot, j + 2 == need[w]);
           }
         }
         commit_elected(&empty[vslot]);
@@ -473,93 +581,66 @@ __global__ void __launch_bounds__(THREADS, 1)
     commit_elected(drained);
     mbar_drain(drained, 0);
     tc_fence_before();
-  } else if (warp == LOAD_WARP) {
+  } else if (warp == KEY_WARP || warp == VALUE_WARP) {
     // ---------------------------------------------------------------- key and value tiles
+    // The tiles of an item stand in the ring in the order in which the products take them:
+    // `ahead` key tiles, then a value tile and the next key tile in turn.
+    const bool value = warp == VALUE_WARP;
+    const CUtensorMap* map = value ? &v_map : &k_map;
     const int pieces = KT / box_rows;
     constexpr int PANELS = D / 64;
-    int slot = 0, uses = 0;  // uses: loads issued, kept small below
-    uint32_t ephase = 1;     // parity that a slot's last release completes
+    uint32_t base = 0;  // tiles of the items before
     while (true) {
       const Segment g = segment(it, G, lo, hi);
-      const int n = max(g.need[0], g.need[1]);
-      for (int j = 0; j < n; ++j) {
-        const int key0 = (g.t0 + j) * KT;
+      const int n = g.tiles(), ahead = g.alone ? 2 : 1;
+      // this lane's piece of a tile: its entry of the page table, read one tile ahead
+      const auto look_up = [&](int tile) {
+        const int key = (g.t0 + tile) * KT + lane * box_rows;
+        return tile < n && lane < pieces && key < it.s.len ? page_entry(p, it.b, key) : 0;
+      };
+      int coming = look_up(0);
+      for (int i = 0; i < n; ++i) {
+        const uint32_t at = base + (value ? i + min(n, i + ahead) : i < ahead ? i : 2 * i + 1 - ahead);
+        const int slot = at % L::SLOTS;
+        const uint32_t use = at / L::SLOTS;
+        const int page = checked_page(p, coming), key0 = (g.t0 + i) * KT;
+        coming = look_up(i + 1);
         const int have = min(pieces, (it.s.len - key0 + box_rows - 1) / box_rows);  // pieces with cached rows
-        int page = 0, prow = 0;
+        const int prow = (key0 + lane * box_rows) % p.page_size;
+        if (use > 0) mbar_wait(&empty[slot], (use - 1) & 1, p.err);
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(have * box_rows * D * 2));
+        __syncwarp();
         if (lane < have) {
-          const int key = key0 + lane * box_rows;
-          page = checked_page(p, page_entry(p, it.b, key));
-          prow = key % p.page_size;
-        }
+          uint8_t* dst = sm + L::RING + slot * L::SLOT + lane * box_rows * 128;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          if (uses >= L::SLOTS) mbar_wait(&empty[slot], ephase, p.err);
-          else ++uses;
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(have * box_rows * D * 2));
-          __syncwarp();
-          if (lane < have) {
-            uint8_t* dst = sm + L::RING + slot * L::SLOT + lane * box_rows * 128;
-#pragma unroll
-            for (int c = 0; c < PANELS; ++c)
-              tma_load_4d(dst + c * KT * 128, kv ? &v_map : &k_map, 64 * c, prow, it.h, page, &full[slot]);
-          }
-          if (++slot == L::SLOTS) {
-            slot = 0;
-            ephase ^= 1;
-          }
+          for (int c = 0; c < PANELS; ++c) tma_load_4d(dst + c * KT * 128, map, 64 * c, prow, it.h, page, &full[slot]);
         }
       }
+      base += 2 * n;
       if (it.end >= hi) break;
       Num::next_item(p, G, it);
     }
     // after a failed wait loads may still be on their way: the last one of every slot used
-    if (lane == 0)
-      for (int i = 0; i < uses; ++i) mbar_drain(&full[i], i < slot ? ephase ^ 1 : ephase);
+    if (lane == 0 && !value)
+      for (uint32_t at = base > L::SLOTS ? base - L::SLOTS : 0; at < base; ++at)
+        mbar_drain(&full[at % L::SLOTS], at / L::SLOTS & 1);
     __syncwarp();
-  } else if (warp >= QLOAD_WARP) {
-    // ---------------------------------------------------------------- queries of a row tile
-    // All rows of the tile in flight at once (cp.async), rows past the end zero.
-    // A lane takes the same 16 bytes of every STEP-th row: their swizzled places repeat
-    // every eight rows, and the global address is stepped (G query heads a token).
-    constexpr int CH = D / 8, STEP = 32 / CH, TURN = 8 / STEP;
-    const int w = warp - QLOAD_WARP, col = lane % CH * 8;
-    Tile<bf16, HALF, D> Qs{reinterpret_cast<bf16*>(sm + L::Q + w * HALF * D * 2)};
-    uint32_t place[TURN];
-#pragma unroll
-    for (int i = 0; i < TURN; ++i) place[i] = smem_u32(Qs.ptr(lane / CH + i * STEP, col));
-    const long long wrap = a.q_ts - G * a.q_hs, skip = (STEP / G) * a.q_ts + (STEP % G) * a.q_hs;
-    uint32_t loads = 0;
-    while (true) {
+  } else if (warp == QUERY_WARP) {
+    // ---------------------------------------------------------------- queries, after the first item's
+    uint32_t loads[2] = {0, 0};
+    for (bool first = true;; first = false) {
       const Segment g = segment(it, G, lo, hi);
-      if (g.need[w] > 0) {
-        const int q = g.row0 + w * HALF + lane / CH, left = g.rows - w * HALF - lane / CH;
-        int sub = q % G;
-        const bf16* src = static_cast<const bf16*>(a.q) + (it.s.first + q / G) * a.q_ts + ((long long)it.h * G + sub) * a.q_hs + col;
-        if (loads > 0) mbar_wait(&qfree[w], (loads - 1) & 1, p.err);
-        ++loads;
-#pragma unroll 2
-        for (int b = 0; b < HALF / 8; ++b) {
 #pragma unroll
-          for (int i = 0; i < TURN; ++i) {
-            const uint32_t to = place[i] + b * 1024;
-            if (b * 8 + i * STEP < left)
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(src) : "memory");
-            else
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(to), "r"(0) : "memory");
-            src += skip;
-            sub += STEP % G;
-            if (sub >= G) {
-              sub -= G;
-              src += wrap;
-            }
+      for (int w = 0; w < 2; ++w)
+        if (g.need[w] > 0) {
+          if (!first) {
+            if (loads[w] > 0) mbar_wait(&qfree[w], (loads[w] - 1) & 1, p.err);
+            load_queries<D, 32>(a, it, g, G, w, lane, reinterpret_cast<bf16*>(sm + L::Q + w * HALF * D * 2));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&qbar[w]);
           }
+          ++loads[w];
         }
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&qbar[w]);
-      }
       if (it.end >= hi) break;
       Num::next_item(p, G, it);
     }
@@ -630,16 +711,23 @@ bool cache_map(CUtensorMap* map, void* base, const PagedArgs& p, long long ps, l
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether the call surely has two items or more per SM: the tokens' full items alone.
+bool whole_items(const AttnArgs& a) {
+  const int nsm = device_sm_count() > 0 ? device_sm_count() : 152;
+  return (long long)a.p.N * (a.p.Hq / a.p.Hk) / ROWS * a.p.Hk >= 2ll * nsm;
+}
+
 template <int D>
 cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int box, cudaStream_t s) {
   const int bytes = TcLay<D>::BYTES + 1024;
   cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  const int grid = launch_ctas(a, ROWS, KT, MIN_UNITS);
+  const bool whole = whole_items(a);
+  const unsigned grid = whole ? (unsigned)most_items(a, ROWS) : (unsigned)launch_ctas(a, ROWS, KT, MIN_UNITS);
   prof_mark(K_ATTN_TC, s, true);
-  e = launch_pdl(paged_attn_tc_kernel<D>, dim3(grid), dim3(THREADS), bytes, s, a, box, km, vm);
+  e = launch_pdl(paged_attn_tc_kernel<D>, dim3(grid), dim3(THREADS), bytes, s, a, box, (int)whole, km, vm);
   prof_mark(K_ATTN_TC, s, false);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || whole) return e;
   prof_mark(K_ATTN_TC_JOIN, s, true);
   e = launch_pdl(paged_attn_tc_join_kernel<D>, dim3(grid, ROWS / 32), dim3(32 * JOIN_WARPS), 0, s, a);
   prof_mark(K_ATTN_TC_JOIN, s, false);
@@ -654,6 +742,7 @@ bool paged_attn_tc_applies(const AttnArgs& a) {
 }
 
 size_t paged_attn_tc_workspace(const AttnArgs& a) {
+  if (whole_items(a)) return 0;
   const int grid = launch_ctas(a, ROWS, KT, MIN_UNITS);
   return a.p.D == 64 ? Parts<ROWS, 64>::bytes(grid) : Parts<ROWS, 128>::bytes(grid);
 }
