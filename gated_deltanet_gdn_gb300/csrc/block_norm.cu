@@ -900,17 +900,31 @@ __global__ void __launch_bounds__(32 * WG_LANES) block_norm_wgrad_kernel(NormArg
   if (l == 0 && blockIdx.x * 32 + k0 < a.C) out[blockIdx.x * 32 + k0] = from_f32<T>(t);
 }
 
+// CTAs of a kernel that an SM holds at once (asked for once per kernel).
+template <class K>
+int resident(K kern, int threads) {
+  int n = 0;
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) == cudaSuccess && n > 0 ? n : 1;
+}
+
 template <class T, int VEC, int NV, int SUB, bool HEAD>
 cudaError_t run(const NormArgs& a, int threads, bool bwd, int* parts, cudaStream_t s) {
+  const auto fwd_kernel = block_norm_fwd_kernel<T, VEC, NV, SUB, HEAD>;
+  const auto bwd_kernel = block_norm_bwd_kernel<T, VEC, NV, SUB, HEAD>;
   const long long rows = (long long)a.R * a.G, per = SUB ? SUB_THREADS / (SUB ? SUB : 1) : 1;
-  long long grid = (rows + per - 1) / per;
-  // part-warp rows: resident CTAs only, each walking its rows with the next one's loads ahead
-  const long long most = bwd ? norm_bwd_parts(a.C) : SUB ? 152 * NORM_CTAS_PER_SM : grid;
+  long long grid = (rows + per - 1) / per, most = grid;
+  if (SUB) {
+    // part-warp rows: one wave of CTAs, each walking its rows with the next one's loads ahead
+    // (with a third of a wave more, the B8 T4096 H6 D128 forward took 34 us in place of 31)
+    static const int per_sm_fwd = resident(fwd_kernel, SUB_THREADS), per_sm_bwd = resident(bwd_kernel, SUB_THREADS);
+    const int nsm = device_sm_count();
+    most = (long long)(nsm > 0 ? nsm : 152) * (bwd ? per_sm_bwd : per_sm_fwd);
+  }
+  if (bwd && most > norm_bwd_parts(a.C)) most = norm_bwd_parts(a.C);
   if (grid > most) grid = most;
   if (bwd) *parts = (int)grid;
   prof_mark(bwd ? K_NORM_BWD : K_NORM_FWD, s, true);
-  const cudaError_t e = launch_pdl(bwd ? block_norm_bwd_kernel<T, VEC, NV, SUB, HEAD> : block_norm_fwd_kernel<T, VEC, NV, SUB, HEAD>,
-                                   dim3((unsigned)grid), dim3(threads), 0, s, a);
+  const cudaError_t e = launch_pdl(bwd ? bwd_kernel : fwd_kernel, dim3((unsigned)grid), dim3(threads), 0, s, a);
   prof_mark(bwd ? K_NORM_BWD : K_NORM_FWD, s, false);
   return e;
 }

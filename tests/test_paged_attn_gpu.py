@@ -183,3 +183,72 @@ def test_bad_pages_and_lengths_are_reported():
         gdn.gdn_paged_attn(q, kc, vc, table, cu, long, 0.1, max_q=max_q, max_kv=64)
         assert gdn.gdn_check_device_error() == gdn.binding.GDN_ERR_INTERNAL
     assert gdn.gdn_check_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("chunk", [1, 20])
+def test_more_sequences_than_a_warp_has_lanes(dtype, chunk):
+    new = [chunk if b % 5 else 0 for b in range(70)]
+    length = [n + (b * 37) % 400 if n else 0 for b, n in enumerate(new)]
+    c = Paged(new, length, 4, 2, 64, 16, dtype, seed=21)
+    _check(c, c.normal(c.N, 4, 64), 0.125)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new", [1, 24])
+def test_one_long_sequence_over_every_sm(dtype, new):
+    """One item (or two) of 40,000 keys, cut between all CTAs and joined."""
+    c = Paged([new], [40000], 6, 1, 64, 64, dtype, seed=23)
+    _check(c, c.normal(new, 6, 64), 0.125)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_cache_shared_by_all_heads_through_a_zero_stride(dtype):
+    """One stored KV head expanded to four (head stride 0)."""
+    c = Paged([1, 50], [60, 333], 8, 1, 128, 32, dtype, seed=25)
+    q = c.normal(c.N, 8, 128)
+    kc, vc, table, cu, lens = c.cuda()
+    kc, vc = kc.expand(-1, 4, -1, -1), vc.expand(-1, 4, -1, -1)
+    out = gdn.gdn_paged_attn(q.cuda(), kc, vc, table, cu, lens, 0.1, max_q=50, max_kv=333)
+    ref, mag, rlse, size = attention(c, q, 0.1)
+    tol, _ = attention_bounds(c, ref, mag, rlse, size)
+    assert bool(((out.double().cpu() - ref).abs() <= tol).all())
+
+
+def _device_form(q, kc, vc, cu, lens, table, scale):
+    """The same on the GPU in float64, sequence by sequence, for problems too large for the CPU form:
+    (out, |v|-weighted out, largest sum |q k| scale)."""
+    out, mag = torch.zeros(q.shape, dtype=torch.float64, device="cuda"), torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    size, page, Hk = 0.0, kc.shape[2], kc.shape[1]
+    G = q.shape[1] // Hk
+    for b in range(len(lens)):
+        t0, t1, n = int(cu[b]), int(cu[b + 1]), int(lens[b])
+        pages = table[b, :-(-n // page)].long()
+        hidden = torch.arange(n, device="cuda")[None, :] > (n - (t1 - t0) + torch.arange(t1 - t0, device="cuda"))[:, None]
+        for h in range(Hk):
+            k, v = (c[pages, h].reshape(-1, q.shape[2])[:n].double() for c in (kc, vc))
+            x = q[t0:t1, h * G:(h + 1) * G].double().transpose(0, 1)
+            size = max(size, float((x.abs() @ k.abs().T).max()) * scale)
+            p = torch.softmax((x @ k.T * scale).masked_fill(hidden, -float("inf")), -1)
+            out[t0:t1, h * G:(h + 1) * G] = (p @ v).transpose(0, 1)
+            mag[t0:t1, h * G:(h + 1) * G] = (p @ v.abs()).transpose(0, 1)
+    return out.cpu(), mag.cpu(), size
+
+
+@pytest.mark.parametrize("D,Hq,Hk,new,past", [(128, 48, 8, [700, 1, 513, 40, 1000], [0, 900, 100, 7, 0]),
+                                              (64, 24, 24, [1500, 2300, 200], [0, 31, 4000]),
+                                              (128, 30, 2, [3000, 130], [250, 1])])
+@pytest.mark.parametrize("page", [16, 128])
+def test_many_items(D, Hq, Hk, new, past, page):
+    """More than two items of 256 rows per SM: a CTA per item; groups that do not divide a tile among them."""
+    length = [a + b for a, b in zip(new, past)]
+    c = Paged(new, length, Hq, Hk, D, page, "bf16", seed=27)
+    q = c.normal(c.N, Hq, D, std=1.5)
+    assert c.N * (Hq // Hk) // 256 * Hk >= 304
+    kc, vc, table, cu, lens = c.cuda()
+    scale = D ** -0.5
+    out = gdn.gdn_paged_attn(q.cuda(), kc, vc, table, cu, lens, scale, max_q=max(new), max_kv=max(length)).double().cpu()
+    ref, mag, size = _device_form(q.cuda(), kc, vc, c.cu, c.lens, table, scale)
+    tol, _ = attention_bounds(c, ref, mag, torch.zeros(1), size)
+    assert bool(((out - ref).abs() <= tol).all()), float(((out - ref).abs() / tol).max())
+    assert gdn.gdn_check_device_error() == 0
