@@ -25,9 +25,10 @@
 //    queries are on their way, and its first product done, while this item's output is
 //    written. An item that a CTA holds whole is written at once; at the ends of a CTA's run
 //    the parts go to the workspace and a second kernel joins them in the order of the CTAs.
-//  * many items (two or more per SM): a CTA per item, the longest first and the KV heads of
-//    a run of rows side by side. The CTAs that run at the same time then read the same keys
-//    at the same time, which the L2 serves once.
+//  * many items (two or more per SM): the grid has a CTA per item, the longest first and the
+//    KV heads of a run of rows side by side; the CTAs that run at the same time then read
+//    the same keys at the same time, which the L2 serves once. A running CTA takes over the
+//    next one not yet launched (cluster launch control) and goes on with its item, as above.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -40,6 +41,7 @@ namespace {
 constexpr int ROWS = 256, HALF = 128, KT = 128;  // query rows of an item, of a tile; keys of a tile
 constexpr int THREADS = 384;  // three warpgroups: two of softmax, and one of the warps below
 constexpr int MMA_WARP = 8, KEY_WARP = 9, VALUE_WARP = 10, QUERY_WARP = 11;
+constexpr int ITEM_READERS = 11;  // warps that read the next item: all but the query warp, which finds it
 // Registers a thread, moved from the third warpgroup to the softmax (which holds 128 scores):
 // the launch has 168 each, 2 * 216 + 72 = 3 * 168.
 constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
@@ -54,6 +56,27 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Asks for a CTA of the grid that has not been launched; the answer (16 bytes) lands in
+// shared memory and completes on the barrier.
+__device__ __forceinline__ void ask_next_cta(void* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The CTA taken over, or -1 when all have been launched.
+__device__ __forceinline__ int next_cta(const void* answer) {
+  uint32_t some, x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 r;\n .reg .b32 y, z, w;\n ld.shared.b128 r, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n}\n"
+      : "=r"(some), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  return some ? (int)x : -1;
+}
+
 template <int D>
 struct TcLay {
   static constexpr int SLOT = KT * D * 2;                // one K or V tile
@@ -63,12 +86,15 @@ struct TcLay {
   static constexpr int OUT = RING + SLOTS * SLOT;        // two fp32 [128][32] stages of a merge
   static constexpr int ML = OUT + HALF * 32 * 4;         // m, l of both row tiles, before the second stage's use
   static constexpr int BAR = OUT + 2 * HALF * 32 * 4;
-  // barriers: full[SLOTS], empty[SLOTS], then q, qfree, s, o [2] each, p [2][2] (row tile,
-  // half of the keys), drained
-  static constexpr int NBAR = 2 * SLOTS + 13;
-  static constexpr int RUN = BAR + (NBAR + 1) / 2 * 16;
-  static constexpr int TSLOT = RUN + 128;
+  // barriers: full[SLOTS], empty[SLOTS], then q, qfree, s, o, p, item, itemfree [2] each,
+  // drained, answer
+  static constexpr int NBAR = 2 * SLOTS + 16;
+  static constexpr int RUN = BAR + NBAR * 8;      // the CTA's run
+  static constexpr int ITEM = RUN + 80;           // the next items, two in turn
+  static constexpr int ANSWER = ITEM + 2 * 48;
+  static constexpr int TSLOT = ANSWER + 16;
   static constexpr int BYTES = TSLOT + 16;
+  static_assert(sizeof(Numbering<ROWS, KT, 0>::Run) <= 80 && sizeof(Item) <= 48, "run and items");
   static_assert(BYTES + 1024 <= 227 * 1024, "one CTA per SM");
   // tensor memory columns
   static constexpr int S = 0, O = 256, P = D == 128 ? 0 : 256 + 2 * D;
@@ -243,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     paged_attn_tc_kernel(AttnArgs a, int box_rows, int whole_items, const __grid_constant__ CUtensorMap k_map,
                          const __grid_constant__ CUtensorMap v_map) {
   pdl_wait();
-  pdl_trigger();
+  if (!whole_items) pdl_trigger();
   typedef TcLay<D> L;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
@@ -252,7 +278,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
   uint64_t *full = bars, *empty = bars + L::SLOTS, *qbar = bars + 2 * L::SLOTS, *qfree = qbar + 2, *sbar = qfree + 2,
-           *obar = sbar + 2, *pbar = obar + 2, *drained = pbar + 4;
+           *obar = sbar + 2, *pbar = obar + 2, *ibar = pbar + 2, *ifree = ibar + 2, *drained = ifree + 2,
+           *abar = drained + 1;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::TSLOT);
   // one warp finds the CTA's run of units while others set up
   Num::Run* run = reinterpret_cast<Num::Run*>(sm + L::RUN);
@@ -267,14 +294,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_relinquish();
   } else if (tid == 32) {
     for (int i = 0; i < L::NBAR; ++i) mbar_init(&bars[i], 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&pbar[i], HALF);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&pbar[i], HALF);
+      mbar_init(&ifree[i], ITEM_READERS);
+    }
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = *tslot;
-  const long long lo = run->lo, hi = run->hi;
+  const long long lo = run->lo;
+  long long hi = run->hi;
   PartHead* head = part_heads<ROWS, D>(a.ws, gridDim.x) + blockIdx.x;
   if (lo == hi) {  // no share
     if (tid == 0 && !whole_items) head->more = 0;
@@ -282,6 +313,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     return;
   }
   Item it = run->first;
+  // the warp's next item: of the CTA's run, or the one that the query warp has put down
+  uint32_t items = 0;
+  auto next_item = [&]() {
+    if (!whole_items) {
+      if (it.end >= hi) return false;
+      Num::next_item(p, G, it);
+      return true;
+    }
+    const uint32_t i = items & 1;
+    mbar_wait(&ibar[i], items >> 1 & 1, p.err);
+    it = *reinterpret_cast<const Item*>(sm + L::ITEM + 48 * i);
+    hi = it.end;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ifree[i]);
+    ++items;
+    return it.b >= 0;
+  };
 
   if (warp < MMA_WARP) {
     // ---------------------------------------------------------------- softmax
@@ -478,13 +526,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       tc_fence_before();
-      if (it.end >= hi) {
-        if (tid == 0 && !whole_items)
-          *head = PartHead{it.start >= lo && it.end > hi ? holder(run->total, run->ncta, it.end - 1) - (int)blockIdx.x : 0,
-                           g.row0, g.rows, it.s.first, it.h, {0, 0, 0}};
-        break;
-      }
-      Num::next_item(p, G, it);
+      if (it.end >= hi && tid == 0 && !whole_items)
+        *head = PartHead{it.start >= lo && it.end > hi ? holder(run->total, run->ncta, it.end - 1) - (int)blockIdx.x : 0,
+                         g.row0, g.rows, it.s.first, it.h, {0, 0, 0}};
+      if (!next_item()) break;
     }
   } else {
     fewer_registers<OTHER_REGS>();
@@ -575,8 +620,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         commit_elected(&empty[vslot]);
         if (more) commit_elected(&empty[kslot]);
       }
-      if (it.end >= hi) break;
-      Num::next_item(p, G, it);
+      if (!next_item()) break;
     }
     commit_elected(drained);
     mbar_drain(drained, 0);
@@ -617,8 +661,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       base += 2 * n;
-      if (it.end >= hi) break;
-      Num::next_item(p, G, it);
+      if (!next_item()) break;
     }
     // after a failed wait loads may still be on their way: the last one of every slot used
     if (lane == 0 && !value)
@@ -641,8 +684,33 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           ++loads[w];
         }
-      if (it.end >= hi) break;
-      Num::next_item(p, G, it);
+      if (!whole_items) {
+        if (!next_item()) break;
+        continue;
+      }
+      // find the next item while this one is in work, and put it down for the other warps
+      if (lane == 0) {
+        mbar_arrive_expect_tx(abar, 16);
+        ask_next_cta(sm + L::ANSWER, abar);
+      }
+      __syncwarp();
+      Num::Run r;
+      r.first = it;
+      const bool some = mbar_wait(abar, items & 1, p.err);
+      const int cta = some ? next_cta(sm + L::ANSWER) : -1;
+      if (cta < 0 || !Num::pick(p, G, lane, cta, r)) r.first.b = -1;
+      const uint32_t i = items & 1;
+      if (items > 1) mbar_wait(&ifree[i], (items >> 1 & 1) ^ 1, p.err);
+      if (lane == 0) {
+        *reinterpret_cast<Item*>(sm + L::ITEM + 48 * i) = r.first;
+        fence_proxy_async();  // the answer has been read before the next one is written
+        mbar_arrive(&ibar[i]);
+      }
+      __syncwarp();
+      ++items;
+      it = r.first;
+      hi = it.end;
+      if (it.b < 0) break;
     }
   }
   __syncthreads();
