@@ -192,16 +192,39 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
         }
       } else {
         // each step of eight channels starts from zero and is added in fp32: the tensor core's own
-        // accumulation truncates, which over D channels costs a digit
+        // accumulation truncates, which over D channels costs a digit. Two steps at a time, so
+        // that four chains of three dependent products overlap.
 #pragma unroll
-        for (int k0 = 0; k0 < D; k0 += 8) {
-          float x[1][2][4];
-          zero<1, 2>(x);
-          warp_gemm_tf32x3<1, 2>(x, aview<false>(Qs), bview<false>(Kt), 0, 0, k0, k0 + 8, lane);
+        for (int k0 = 0; k0 < D; k0 += 16) {
+          uint32_t ah[2][4], al[2][4], bh[2][2][2], bl[2][2][2];
+          float x[2][2][4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int u = 0; u < 2; ++u) {
+            const int k = k0 + 8 * u + t;
+            tf32_split(Qs.at(g, k), ah[u][0], al[u][0]);
+            tf32_split(Qs.at(g + 8, k), ah[u][1], al[u][1]);
+            tf32_split(Qs.at(g, k + 4), ah[u][2], al[u][2]);
+            tf32_split(Qs.at(g + 8, k + 4), ah[u][3], al[u][3]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[0][j][e] += x[0][j][e];
+            for (int j = 0; j < 2; ++j) {
+              tf32_split(Kt.at(8 * j + g, k), bh[u][j][0], bl[u][j][0]);
+              tf32_split(Kt.at(8 * j + g, k + 4), bh[u][j][1], bl[u][j][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[u][j][e] = 0.f;
+            }
+          }
+#pragma unroll
+          for (int term = 0; term < 3; ++term)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) mma_tf32(x[u][j], term == 0 ? al[u] : ah[u], term == 1 ? bl[u][j] : bh[u][j]);
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[0][j][e] += x[u][j][e];
         }
       }
       // scores in base 2; hidden keys are -inf
@@ -273,19 +296,29 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
           tf32_split(s[0][j][3], ah[j][3], al[j][3]);
         }
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          float x[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int n0 = 0; n0 < D / 8; n0 += 4) {  // four chains of six dependent products
+          uint32_t bh[4][2][2], bl[4][2][2];
+          float x[4][4];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t bh[2], bl[2];
-            tf32_split(Vt.at(j * 8 + 2 * t, n * 8 + g), bh[0], bl[0]);
-            tf32_split(Vt.at(j * 8 + 2 * t + 1, n * 8 + g), bh[1], bl[1]);
-            mma_tf32(x, al[j], bh);
-            mma_tf32(x, ah[j], bl);
-            mma_tf32(x, ah[j], bh);
+          for (int n = 0; n < 4; ++n) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              tf32_split(Vt.at(j * 8 + 2 * t, (n0 + n) * 8 + g), bh[n][j][0], bl[n][j][0]);
+              tf32_split(Vt.at(j * 8 + 2 * t + 1, (n0 + n) * 8 + g), bh[n][j][1], bl[n][j][1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][e] += x[e];
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int term = 0; term < 3; ++term)
+#pragma unroll
+              for (int n = 0; n < 4; ++n) mma_tf32(x[n], term == 0 ? al[j] : ah[j], term == 1 ? bl[n][j] : bh[n][j]);
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n0 + n][e] += x[n][e];
         }
       }
       __syncwarp();  // the stage is loaded again by other lanes
