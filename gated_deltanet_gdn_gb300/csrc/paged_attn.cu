@@ -16,14 +16,24 @@
 //    the workspace and a second kernel joins them in the order of the CTAs.
 // The products run on mma.sync: a 16-row tile would leave seven eighths of a 128-row
 // tcgen05 tile empty, and the tensor rate is not what bounds this kernel. In bf16 the
-// probabilities are rounded to bf16 for the second product (their sum is not); fp32 uses
-// the three-term TF32 split for both.
+// probabilities are rounded to bf16 for the second product (their sum is not); fp32 splits
+// every operand of both into two TF32 parts.
 #include "paged_attn.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int ROWS = 16, UNIT = 16;
+
+// x = hi + lo for the split products, by cutting the mantissa: hi keeps tf32's 11 bits,
+// lo the other 13, of which the tensor core takes 11 (off by at most 2^-22 of x). Two plain
+// instructions; rounding conversions, at a quarter of the rate, took most of the kernel's
+// time (55 us in place of 50 for three chunks of up to 200 tokens, D = 64). All four terms are
+// taken: with cut parts lo lo has the sign of the product, and would bias every sum.
+__device__ __forceinline__ void tf32_cut(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
 
 template <class T, int D>
 struct Lay {
@@ -32,8 +42,8 @@ struct Lay {
   static constexpr int THREADS = WARPS * 32;
   static constexpr int TILE = UNIT * D * (int)sizeof(T);  // bytes of one K or V unit
   static constexpr int STAGES = 3;
-  static constexpr int Q = 0;                              // [16][D] T, swizzled
-  static constexpr int RING = ROWS * D * (int)sizeof(T);
+  static constexpr int Q = 0;                              // [16][D] T, swizzled; fp32: hi, then lo
+  static constexpr int RING = (sizeof(T) == 2 ? 1 : 2) * ROWS * D * (int)sizeof(T);
   static constexpr int MROWS = 4096 / (WARPS * D);         // rows merged at a time
   static constexpr int MERGE = RING + WARPS * STAGES * 2 * TILE;
   static constexpr int ML = MERGE + WARPS * MROWS * D * 4;  // float m[WARPS][16], l[WARPS][16]
@@ -124,7 +134,19 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
 #pragma unroll
     for (int i = 0; i < QN; ++i) {
       const int q = tid + i * L::THREADS;
-      if (q < ROWS * QCH) *reinterpret_cast<uint4*>(Qs.ptr(q / QCH, q % QCH * QV)) = qr[i];
+      if (q >= ROWS * QCH) continue;
+      T* at = Qs.ptr(q / QCH, q % QCH * QV);
+      if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(at) = qr[i];
+      } else {  // split once for the item
+        uint4 h, l;
+        tf32_cut(__uint_as_float(qr[i].x), h.x, l.x);
+        tf32_cut(__uint_as_float(qr[i].y), h.y, l.y);
+        tf32_cut(__uint_as_float(qr[i].z), h.z, l.z);
+        tf32_cut(__uint_as_float(qr[i].w), h.w, l.w);
+        *reinterpret_cast<uint4*>(at) = h;
+        *reinterpret_cast<uint4*>(at + ROWS * D) = l;
+      }
     }
   };
   load_q(cur);
@@ -193,7 +215,7 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
       } else {
         // each step of eight channels starts from zero and is added in fp32: the tensor core's own
         // accumulation truncates, which over D channels costs a digit. Two steps at a time, so
-        // that four chains of three dependent products overlap.
+        // that four chains of dependent products overlap.
 #pragma unroll
         for (int k0 = 0; k0 < D; k0 += 16) {
           uint32_t ah[2][4], al[2][4], bh[2][2][2], bl[2][2][2];
@@ -201,24 +223,26 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int k = k0 + 8 * u + t;
-            tf32_split(Qs.at(g, k), ah[u][0], al[u][0]);
-            tf32_split(Qs.at(g + 8, k), ah[u][1], al[u][1]);
-            tf32_split(Qs.at(g, k + 4), ah[u][2], al[u][2]);
-            tf32_split(Qs.at(g + 8, k + 4), ah[u][3], al[u][3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const T* at = Qs.ptr(g + 8 * (e & 1), k + 4 * (e >> 1));
+              ah[u][e] = __float_as_uint(at[0]);
+              al[u][e] = __float_as_uint(at[ROWS * D]);
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              tf32_split(Kt.at(8 * j + g, k), bh[u][j][0], bl[u][j][0]);
-              tf32_split(Kt.at(8 * j + g, k + 4), bh[u][j][1], bl[u][j][1]);
+              tf32_cut(Kt.at(8 * j + g, k), bh[u][j][0], bl[u][j][0]);
+              tf32_cut(Kt.at(8 * j + g, k + 4), bh[u][j][1], bl[u][j][1]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) x[u][j][e] = 0.f;
             }
           }
 #pragma unroll
-          for (int term = 0; term < 3; ++term)
+          for (int term = 0; term < 4; ++term)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) mma_tf32(x[u][j], term == 0 ? al[u] : ah[u], term == 1 ? bl[u][j] : bh[u][j]);
+              for (int j = 0; j < 2; ++j) mma_tf32(x[u][j], term < 2 ? al[u] : ah[u], term % 2 == 0 ? bl[u][j] : bh[u][j]);
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -290,21 +314,21 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
         uint32_t ah[2][4], al[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          tf32_split(s[0][j][0], ah[j][0], al[j][0]);
-          tf32_split(s[0][j][2], ah[j][1], al[j][1]);
-          tf32_split(s[0][j][1], ah[j][2], al[j][2]);
-          tf32_split(s[0][j][3], ah[j][3], al[j][3]);
+          tf32_cut(s[0][j][0], ah[j][0], al[j][0]);
+          tf32_cut(s[0][j][2], ah[j][1], al[j][1]);
+          tf32_cut(s[0][j][1], ah[j][2], al[j][2]);
+          tf32_cut(s[0][j][3], ah[j][3], al[j][3]);
         }
 #pragma unroll
-        for (int n0 = 0; n0 < D / 8; n0 += 4) {  // four chains of six dependent products
+        for (int n0 = 0; n0 < D / 8; n0 += 4) {  // four chains of dependent products
           uint32_t bh[4][2][2], bl[4][2][2];
           float x[4][4];
 #pragma unroll
           for (int n = 0; n < 4; ++n) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              tf32_split(Vt.at(j * 8 + 2 * t, (n0 + n) * 8 + g), bh[n][j][0], bl[n][j][0]);
-              tf32_split(Vt.at(j * 8 + 2 * t + 1, (n0 + n) * 8 + g), bh[n][j][1], bl[n][j][1]);
+              tf32_cut(Vt.at(j * 8 + 2 * t, (n0 + n) * 8 + g), bh[n][j][0], bl[n][j][0]);
+              tf32_cut(Vt.at(j * 8 + 2 * t + 1, (n0 + n) * 8 + g), bh[n][j][1], bl[n][j][1]);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
@@ -312,9 +336,9 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int term = 0; term < 3; ++term)
+            for (int term = 0; term < 4; ++term)
 #pragma unroll
-              for (int n = 0; n < 4; ++n) mma_tf32(x[n], term == 0 ? al[j] : ah[j], term == 1 ? bl[n][j] : bh[n][j]);
+              for (int n = 0; n < 4; ++n) mma_tf32(x[n], term < 2 ? al[j] : ah[j], term % 2 == 0 ? bl[n][j] : bh[n][j]);
 #pragma unroll
           for (int n = 0; n < 4; ++n)
 #pragma unroll
