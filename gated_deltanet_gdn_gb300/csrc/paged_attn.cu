@@ -16,8 +16,8 @@
 //    the workspace and a second kernel joins them in the order of the CTAs.
 // The products run on mma.sync: a 16-row tile would leave seven eighths of a 128-row
 // tcgen05 tile empty, and the tensor rate is not what bounds this kernel. In bf16 the
-// probabilities are rounded to bf16 for the second product (their sum is not); fp32 splits
-// every operand of both into two TF32 parts.
+// probabilities are rounded to bf16 for the second product (their sum is not); fp32 uses
+// three-term TF32 products for both.
 #include "paged_attn.cuh"
 
 namespace gdn {
@@ -25,11 +25,12 @@ namespace {
 
 constexpr int ROWS = 16, UNIT = 16;
 
-// x = hi + lo for the split products, by cutting the mantissa: hi keeps tf32's 11 bits,
-// lo the other 13, of which the tensor core takes 11 (off by at most 2^-22 of x). Two plain
-// instructions; rounding conversions, at a quarter of the rate, took most of the kernel's
-// time (55 us in place of 50 for three chunks of up to 200 tokens, D = 64). All four terms are
-// taken: with cut parts lo lo has the sign of the product, and would bias every sum.
+// x = hi + lo for the split products, by cutting the mantissa: hi keeps tf32's 11 bits, lo
+// the other 13, of which the tensor core takes 11 (off by at most 2^-22 of x). Two plain
+// instructions, for keys and values; rounding conversions, at a quarter of the rate, took
+// much of the kernel's time. Queries and probabilities, split rarely, are rounded
+// (tf32_split): their lo has either sign, so the lo lo terms that the three-term products
+// leave out do not bias the sums, as they would between two cut operands.
 __device__ __forceinline__ void tf32_cut(float x, uint32_t& hi, uint32_t& lo) {
   hi = __float_as_uint(x) & 0xffffe000u;
   lo = __float_as_uint(x - __uint_as_float(hi));
@@ -37,11 +38,12 @@ __device__ __forceinline__ void tf32_cut(float x, uint32_t& hi, uint32_t& lo) {
 
 template <class T, int D>
 struct Lay {
-  // as many warps as the rings of three stages leave room for
-  static constexpr int WARPS = D * sizeof(T) <= 256 ? 8 : 4;
+  // As many warps as the rings leave room for: eight of three stages, or with fp32 rows of
+  // 128 (16 KB a stage), where the arithmetic bounds it, six of two.
+  static constexpr int WARPS = D * sizeof(T) <= 256 ? 8 : 6;
   static constexpr int THREADS = WARPS * 32;
   static constexpr int TILE = UNIT * D * (int)sizeof(T);  // bytes of one K or V unit
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = D * sizeof(T) <= 256 ? 3 : 2;
   static constexpr int Q = 0;                              // [16][D] T, swizzled; fp32: hi, then lo
   static constexpr int RING = (sizeof(T) == 2 ? 1 : 2) * ROWS * D * (int)sizeof(T);
   static constexpr int MROWS = 4096 / (WARPS * D);         // rows merged at a time
@@ -49,6 +51,7 @@ struct Lay {
   static constexpr int ML = MERGE + WARPS * MROWS * D * 4;  // float m[WARPS][16], l[WARPS][16]
   static constexpr int TOT = ML + 2 * WARPS * ROWS * 4;        // float m[16], l[16] of the CTA
   static constexpr int BYTES = TOT + 2 * ROWS * 4;
+  static_assert(BYTES + 1024 <= 227 * 1024, "one CTA per SM");
 };
 
 typedef Numbering<ROWS, UNIT, 0> Num;
@@ -140,10 +143,10 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
         *reinterpret_cast<uint4*>(at) = qr[i];
       } else {  // split once for the item
         uint4 h, l;
-        tf32_cut(__uint_as_float(qr[i].x), h.x, l.x);
-        tf32_cut(__uint_as_float(qr[i].y), h.y, l.y);
-        tf32_cut(__uint_as_float(qr[i].z), h.z, l.z);
-        tf32_cut(__uint_as_float(qr[i].w), h.w, l.w);
+        tf32_split(__uint_as_float(qr[i].x), h.x, l.x);
+        tf32_split(__uint_as_float(qr[i].y), h.y, l.y);
+        tf32_split(__uint_as_float(qr[i].z), h.z, l.z);
+        tf32_split(__uint_as_float(qr[i].w), h.w, l.w);
         *reinterpret_cast<uint4*>(at) = h;
         *reinterpret_cast<uint4*>(at + ROWS * D) = l;
       }
@@ -238,11 +241,11 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
             }
           }
 #pragma unroll
-          for (int term = 0; term < 4; ++term)
+          for (int term = 0; term < 3; ++term)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) mma_tf32(x[u][j], term < 2 ? al[u] : ah[u], term % 2 == 0 ? bl[u][j] : bh[u][j]);
+              for (int j = 0; j < 2; ++j) mma_tf32(x[u][j], term == 0 ? al[u] : ah[u], term == 1 ? bl[u][j] : bh[u][j]);
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -314,10 +317,10 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
         uint32_t ah[2][4], al[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          tf32_cut(s[0][j][0], ah[j][0], al[j][0]);
-          tf32_cut(s[0][j][2], ah[j][1], al[j][1]);
-          tf32_cut(s[0][j][1], ah[j][2], al[j][2]);
-          tf32_cut(s[0][j][3], ah[j][3], al[j][3]);
+          tf32_split(s[0][j][0], ah[j][0], al[j][0]);
+          tf32_split(s[0][j][2], ah[j][1], al[j][1]);
+          tf32_split(s[0][j][1], ah[j][2], al[j][2]);
+          tf32_split(s[0][j][3], ah[j][3], al[j][3]);
         }
 #pragma unroll
         for (int n0 = 0; n0 < D / 8; n0 += 4) {  // four chains of dependent products
@@ -336,9 +339,9 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int term = 0; term < 4; ++term)
+            for (int term = 0; term < 3; ++term)
 #pragma unroll
-              for (int n = 0; n < 4; ++n) mma_tf32(x[n], term < 2 ? al[j] : ah[j], term % 2 == 0 ? bl[n][j] : bh[n][j]);
+              for (int n = 0; n < 4; ++n) mma_tf32(x[n], term == 0 ? al[j] : ah[j], term == 1 ? bl[n][j] : bh[n][j]);
 #pragma unroll
           for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -509,7 +512,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attn_workspace(const AttnArgs& a) {
-  const int warps = a.p.D * (a.p.bf16 ? 2 : 4) <= 256 ? 8 : 4, grid = launch_ctas(a, ROWS, UNIT, warps);
+  const int warps = a.p.D * (a.p.bf16 ? 2 : 4) <= 256 ? 8 : 6, grid = launch_ctas(a, ROWS, UNIT, warps);
   const size_t own = a.p.D == 64 ? Parts<ROWS, 64>::bytes(grid) : Parts<ROWS, 128>::bytes(grid);
   const size_t tc = paged_attn_tc_applies(a) ? paged_attn_tc_workspace(a) : 0;
   return own > tc ? own : tc;
