@@ -195,6 +195,17 @@ int device_sm_count() {
   return n;
 }
 
+cudaError_t allow_shared(const void* kernel, int bytes, std::atomic<unsigned long long>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev >= 0 && dev < MAX_DEVICES ? 1ull << dev : 0ull;
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 void prof_mark(KernelId id, cudaStream_t s, bool begin) {
   if (!g_prof_on) return;
   std::lock_guard<std::mutex> lock(g_prof_mutex);

@@ -957,7 +957,8 @@ cudaError_t run_stream(const NormArgs& a, int* parts, bool* fits, cudaStream_t s
   if (stages > MAX_STAGES) stages = MAX_STAGES;
   const int bytes = head + stages * stage;
   auto kern = block_norm_stream_kernel<T, NV, MAXT, BWD, SPLIT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_shared(reinterpret_cast<const void*>(kern), BUDGET, &allowed);
   if (e != cudaSuccess) return e;
   long long grid = (long long)a.R * a.G;
   if (grid > (long long)nsm * per_sm) grid = (long long)nsm * per_sm;

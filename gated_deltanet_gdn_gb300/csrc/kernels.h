@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace gdn {
 
 constexpr int C = 64;       // chunk length (tokens)
@@ -327,6 +329,9 @@ void prof_mark(KernelId id, cudaStream_t s, bool begin);
 unsigned* device_error_word();
 // SMs of the current device (0 if it cannot be read).
 int device_sm_count();
+// Lets a kernel use `bytes` of dynamic shared memory on the current device; asked of the
+// runtime once per device (`done`: the kernel's own, a bit per device).
+cudaError_t allow_shared(const void* kernel, int bytes, std::atomic<unsigned long long>* done);
 
 // Each returns a cudaError_t from the launches (cudaSuccess when all were accepted).
 cudaError_t launch_chunk_fwd(const ChunkFwdArgs& a, cudaStream_t s);

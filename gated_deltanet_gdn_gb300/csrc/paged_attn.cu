@@ -496,7 +496,8 @@ template <class T, int D>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
   typedef Lay<T, D> L;
   const int bytes = L::BYTES + 1024;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_shared(reinterpret_cast<const void*>(paged_attn_kernel<T, D>), bytes, &allowed);
   if (e != cudaSuccess) return e;
   const int grid = launch_ctas(a, ROWS, UNIT, L::WARPS);
   prof_mark(K_ATTN, s, true);

@@ -788,7 +788,8 @@ bool whole_items(const AttnArgs& a) {
 template <int D>
 cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm, int box, cudaStream_t s) {
   const int bytes = TcLay<D>::BYTES + 1024;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_shared(reinterpret_cast<const void*>(paged_attn_tc_kernel<D>), bytes, &allowed);
   if (e != cudaSuccess) return e;
   const bool whole = whole_items(a);
   const unsigned grid = whole ? (unsigned)most_items(a, ROWS) : (unsigned)launch_ctas(a, ROWS, KT, MIN_UNITS);
