@@ -510,23 +510,22 @@ __device__ __forceinline__ uint4 rounded(const f2 (&x)[2], const float*) {
   unpk(x[1], c, d);
   return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
 }
-// act(g) and act'(g) of a pair, as `activation`.
-__device__ __forceinline__ void activation2(f2 g, int sigmoid, f2& a, f2& d) {
-  if (!sigmoid) {
-    const f2 one = pk(1.f, 1.f);
-    float t0, t1;
-    unpk(mul2(g, pk(-1.4426950408889634f, -1.4426950408889634f)), t0, t1);
-    unpk(add2(pk(ex2_approx(t0), ex2_approx(t1)), one), t0, t1);
-    const f2 s = pk(rcp_approx(t0), rcp_approx(t1));
-    a = mul2(g, s);
-    d = mul2(s, fma2(g, fma2(s, pk(-1.f, -1.f), one), one));
-  } else {
-    float g2[2], a2[2], d2[2];
-    unpk(g, g2[0], g2[1]);
-    activation<2>(g2, 1, a2, d2);
-    a = pk(a2[0], a2[1]);
-    d = pk(d2[0], d2[1]);
-  }
+// act(g) and act'(g) of a pair, as `activation`, in one form without a branch: with
+// e = exp(-g), s = 1 / (1 + e) and 1 - s = e s (which keeps its accuracy; inf 0 of a
+// large -g is 1),
+//   silu:  g s, s (1 + g (1 - s))        sigmoid:  s, s (0 + 1 (1 - s))
+__device__ __forceinline__ void activation2(f2 g, bool sigmoid, f2& a, f2& d) {
+  const f2 one = pk(1.f, 1.f);
+  float t0, t1;
+  unpk(mul2(g, pk(-1.4426950408889634f, -1.4426950408889634f)), t0, t1);
+  const f2 e = pk(ex2_approx(t0), ex2_approx(t1));
+  unpk(add2(e, one), t0, t1);
+  const f2 s = pk(rcp_approx(t0), rcp_approx(t1));
+  unpk(mul2(e, s), t0, t1);
+  const f2 rest = pk(fminf(t0, 1.f), fminf(t1, 1.f));
+  const f2 f = sigmoid ? one : g;
+  a = mul2(f, s);
+  d = mul2(s, fma2(f, rest, sigmoid ? pk(0.f, 0.f) : one));
 }
 
 constexpr int MAX_STAGES = 8;
@@ -546,24 +545,39 @@ static_assert(sizeof(StreamShared) <= STREAM_HEAD, "barriers and sums before the
 // filling warpgroup's (384 of them: 3 * 160 + 32 = 4 * 128; 512: 4 * 112 + 32 = 5 * 96).
 constexpr int SPLIT_LOW = 32;
 constexpr int split_high(int maxt) { return maxt == 384 ? 160 : 112; }
-template <class T, int NV, int MAXT, bool BWD, bool SPLIT>
-__global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ? 1 : 2)
+//
+// FULL: the residual and the norm before the next block are there (GATE: the gate too);
+// weights that are missing are ones. Nothing in the row's loops branches then, so that the
+// loads and conversions of a whole segment are interleaved: a thread beyond the row's end
+// works on the first columns and leaves its results out. (With a branch per part the
+// 8192 x 6144 backward took 200 us in place of 161.)
+//
+// The backward keeps only h between its segments and forms act and act' again (6144 wide:
+// 144 us, against 156 with all three in registers), except below 2048 columns of bf16,
+// where two CTAs per SM have the registers (164 us; formed again 170).
+constexpr int stream_ctas(int nv, int maxt, bool bwd, bool full) {  // per SM, of MAXT workers
+  return bwd ? (maxt == 256 || (maxt == 384 && nv == 1 && full) ? 2 : 1) : maxt > 384 ? 1 : 2;
+}
+template <class T, int NV, int MAXT, bool BWD, bool SPLIT, bool FULL, bool GATE>
+__global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), stream_ctas(NV, MAXT, BWD, FULL))
     block_norm_stream_kernel(NormArgs a, int stages) {
   constexpr int VEC = 16 / (int)sizeof(T), NP = VEC / 2;
   pdl_wait();
   pdl_trigger();
   extern __shared__ __align__(128) uint8_t smem[];
   StreamShared* sh = reinterpret_cast<StreamShared*>(smem);
-  const bool post = a.w_post != nullptr, pre = a.w_pre != nullptr, gated = a.gate != nullptr, scaled = a.res_scale != nullptr;
+  const bool post = a.w_post, pre = FULL || a.w_pre, gated = FULL ? GATE : a.gate != nullptr;
+  const bool weighed = FULL || a.w_post, scaled = FULL || a.res_scale;  // by ones, if need be
   // which tensor of a stage is which input (x is 0)
   int nt = 1;
   const int tg = gated ? nt++ : 0;
-  const int tr = a.residual && (!BWD || pre) ? nt++ : 0;
-  const int th = BWD && a.dh ? nt++ : 0;
+  const int tr = FULL || (a.residual && (!BWD || pre)) ? nt++ : 0;
+  const int th = BWD && (FULL || a.dh) ? nt++ : 0;
   const int ty = BWD && pre ? nt++ : 0;
   const int workers = blockDim.x - (SPLIT ? 128 : 32);
   const uint32_t bytes = (uint32_t)a.C * sizeof(T);
-  const uint32_t ring = STREAM_HEAD + (BWD ? 3 * bytes : 0);  // offset of the ring
+  constexpr bool KEEP = BWD || (FULL && MAXT == 384);  // weights in shared memory
+  const uint32_t ring = STREAM_HEAD + (KEEP ? 3 * bytes : 0);  // offset of the ring
   const unsigned rows = (unsigned)a.R * (unsigned)a.G, grid = gridDim.x;
   const T* kind = nullptr;  // names the type for the packing functions
   for (int i = threadIdx.x; i < 64; i += blockDim.x) (&sh->buf[0][0])[i] = 0.f;
@@ -621,24 +635,28 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
     }
     return s;
   };
-  // this thread's columns, and their weights: in registers, or in the backward (whose sums
-  // take them) in shared memory before the ring, each thread its own
+  // this thread's columns, and their weights: in registers, or where those are short in
+  // shared memory before the ring, each thread its own
   const int col0 = threadIdx.x * VEC, cstep = workers * VEC;
-  uint4 wreg[BWD ? 1 : 3][NV];
+  uint4 wreg[KEEP ? 1 : 3][NV];
   const void* const wsrc[3] = {a.w_post, a.w_pre, a.res_scale};
 #pragma unroll
   for (int t = 0; t < 3; ++t)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = col0 + i * cstep;
-      uint4 u = make_uint4(0u, 0u, 0u, 0u);
+      f2 ones[NP];
+#pragma unroll
+      for (int e = 0; e < NP; ++e) ones[e] = pk(1.f, 1.f);
+      uint4 u = rounded(ones, kind);
       if (c < a.C && wsrc[t]) u = *reinterpret_cast<const uint4*>(static_cast<const T*>(wsrc[t]) + c);
-      if constexpr (!BWD) wreg[t][i] = u;
+      if constexpr (!KEEP) wreg[t][i] = u;
       else if (c < a.C) *reinterpret_cast<uint4*>(smem + STREAM_HEAD + (size_t)t * bytes + c * sizeof(T)) = u;
     }
+  if constexpr (FULL) asm volatile("bar.sync 1, %0;" ::"r"(workers) : "memory");  // the first columns', for all
   enum { POST = 0, PRE = 1, SCALE = 2 };
   auto weight = [&](int t, int i, int c, f2 (&w)[NP]) {
-    if constexpr (!BWD) pairs_of(wreg[t][i], w, kind);
+    if constexpr (!KEEP) pairs_of(wreg[t][i], w, kind);
     else pairs_of(*reinterpret_cast<const uint4*>(smem + STREAM_HEAD + (size_t)t * bytes + c * sizeof(T)), w, kind);
   };
   const f2 zero2 = pk(0.f, 0.f);
@@ -674,12 +692,14 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
         f2 ss = zero2;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int c = col0 + i * cstep;
-          if (c >= a.C) continue;
-          f2 x[NP];
+          const int col = col0 + i * cstep, c = FULL && col >= a.C ? 0 : col;
+          const bool in_row = col < a.C;
+          if (!FULL && !in_row) continue;
+          f2 x[NP], part = ss;
           fetch(0, c, x);
 #pragma unroll
-          for (int e = 0; e < NP; ++e) ss = fma2(x[e], x[e], ss);
+          for (int e = 0; e < NP; ++e) part = fma2(x[e], x[e], part);
+          if (in_row) ss = part;
         }
         r1 = rsqrtf(total(ss) * invC + a.eps);
       }
@@ -687,11 +707,12 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
       f2 h[NV][NP], hh = zero2;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = col0 + i * cstep;
-        if (c >= a.C) continue;
+        const int col = col0 + i * cstep, c = FULL && col >= a.C ? 0 : col;
+        const bool in_row = col < a.C;
+        if (!FULL && !in_row) continue;
         f2 w[NP];
         fetch(0, c, h[i]);
-        if (post) {
+        if (weighed) {
           weight(POST, i, c, w);
 #pragma unroll
           for (int e = 0; e < NP; ++e) h[i][e] = mul2(mul2(h[i][e], r1p), w[e]);
@@ -715,9 +736,11 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
 #pragma unroll
           for (int e = 0; e < NP; ++e) h[i][e] = add2(h[i][e], w[e]);
         }
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.h) + row * a.C + c) = rounded(h[i], kind);
+        if (in_row) *reinterpret_cast<uint4*>(static_cast<T*>(a.h) + row * a.C + c) = rounded(h[i], kind);
+        f2 part = hh;
 #pragma unroll
-        for (int e = 0; e < NP; ++e) hh = fma2(h[i][e], h[i][e], hh);
+        for (int e = 0; e < NP; ++e) part = fma2(h[i][e], h[i][e], part);
+        if (in_row) hh = part;
       }
       release();
       if (pre) {
@@ -725,13 +748,14 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
         const f2 r2p = pk(r2, r2);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int c = col0 + i * cstep;
-          if (c >= a.C) continue;
+          const int col = col0 + i * cstep, c = FULL && col >= a.C ? 0 : col;
+          const bool in_row = col < a.C;
+          if (!FULL && !in_row) continue;
           f2 w[NP];
           weight(PRE, i, c, w);
 #pragma unroll
           for (int e = 0; e < NP; ++e) w[e] = mul2(mul2(h[i][e], r2p), w[e]);
-          *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * a.C + c) = rounded(w, kind);
+          if (in_row) *reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * a.C + c) = rounded(w, kind);
         }
       }
       if (threadIdx.x == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(r1, r2);
@@ -739,14 +763,17 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
       const float r1 = post ? st.x : 1.f, r2 = pre ? st.y : 1.f;
       const f2 r1p = pk(r1, r1), r2p = pk(r2, r2);
       f2 h[NV][NP], ac[NV][NP], nd[NV][NP];  // h, act(gate), n act'(gate)
+      // act and act' wait in registers or are formed again from the gate
+      constexpr bool AGAIN = FULL && GATE && MAXT > 256;
       f2 s2 = zero2;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = col0 + i * cstep;
-        if (c >= a.C) continue;
+        const int col = col0 + i * cstep, c = FULL && col >= a.C ? 0 : col;
+        const bool in_row = col < a.C;
+        if (!FULL && !in_row) continue;
         f2 n[NP], w[NP];
         fetch(0, c, n);
-        if (post) {
+        if (weighed) {
           weight(POST, i, c, w);
 #pragma unroll
           for (int e = 0; e < NP; ++e) n[e] = mul2(mul2(n[e], r1p), w[e]);
@@ -757,7 +784,7 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
           for (int e = 0; e < NP; ++e) {
             f2 ad;
             activation2(w[e], a.sigmoid, ac[i][e], ad);
-            nd[i][e] = mul2(n[e], ad);
+            if (!AGAIN) nd[i][e] = mul2(n[e], ad);
             n[e] = mul2(n[e], ac[i][e]);  // m
           }
         }
@@ -775,12 +802,14 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
           }
           fetch(ty, c, dy);
           weight(PRE, i, c, w);
+          f2 part = s2;
 #pragma unroll
           for (int e = 0; e < NP; ++e) {
             h[i][e] = n[e];
-            s2 = fma2(mul2(dy[e], w[e]), n[e], s2);
+            part = fma2(mul2(dy[e], w[e]), n[e], part);
             sw2[i][e] = fma2(mul2(dy[e], r2p), n[e], sw2[i][e]);
           }
+          if (in_row) s2 = part;
         }
       }
       f2 c2 = zero2;
@@ -791,8 +820,9 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
       f2 s1 = zero2;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = col0 + i * cstep;
-        if (c >= a.C) continue;
+        const int col = col0 + i * cstep, c = FULL && col >= a.C ? 0 : col;
+        const bool in_row = col < a.C;
+        if (!FULL && !in_row) continue;
         f2 D[NP], x[NP], w[NP];
         if (th) {
           fetch(th, c, D);
@@ -807,13 +837,24 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
 #pragma unroll
           for (int e = 0; e < NP; ++e) D[e] = fma2(h[i][e], c2, fma2(mul2(dy[e], w[e]), r2p, D[e]));
         }
-        if (a.dresidual) *reinterpret_cast<uint4*>(static_cast<T*>(a.dresidual) + row * a.C + c) = rounded(D, kind);
+        if (in_row && (FULL || a.dresidual)) *reinterpret_cast<uint4*>(static_cast<T*>(a.dresidual) + row * a.C + c) = rounded(D, kind);
         fetch(0, c, x);
-        if (scaled) {
-          if (post) weight(POST, i, c, w);
+        if constexpr (AGAIN) {
+          f2 gate[NP];
+          fetch(tg, c, gate);
+          weight(POST, i, c, w);
 #pragma unroll
           for (int e = 0; e < NP; ++e) {
-            f2 m = post ? mul2(mul2(x[e], r1p), w[e]) : x[e];
+            f2 ad;
+            activation2(gate[e], a.sigmoid, ac[i][e], ad);
+            nd[i][e] = mul2(mul2(mul2(x[e], r1p), w[e]), ad);
+          }
+        }
+        if (scaled) {
+          if (weighed) weight(POST, i, c, w);
+#pragma unroll
+          for (int e = 0; e < NP; ++e) {
+            f2 m = weighed ? mul2(mul2(x[e], r1p), w[e]) : x[e];
             if (gated) m = mul2(m, ac[i][e]);
             ssc[i][e] = fma2(D[e], m, ssc[i][e]);
           }
@@ -822,22 +863,24 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
           for (int e = 0; e < NP; ++e) D[e] = mul2(D[e], w[e]);
         }
         if (gated) {
-          if (a.dgate) {
+          if (FULL || a.dgate) {
 #pragma unroll
             for (int e = 0; e < NP; ++e) w[e] = mul2(D[e], nd[i][e]);
-            *reinterpret_cast<uint4*>(static_cast<T*>(a.dgate) + row * a.C + c) = rounded(w, kind);
+            if (in_row) *reinterpret_cast<uint4*>(static_cast<T*>(a.dgate) + row * a.C + c) = rounded(w, kind);
           }
 #pragma unroll
           for (int e = 0; e < NP; ++e) D[e] = mul2(D[e], ac[i][e]);
         }
-        if (post) {
+        if (weighed) {
           weight(POST, i, c, w);
+          f2 part = s1;
 #pragma unroll
           for (int e = 0; e < NP; ++e) {
             sw1[i][e] = fma2(D[e], mul2(x[e], r1p), sw1[i][e]);
             D[e] = mul2(D[e], w[e]);
-            s1 = fma2(D[e], x[e], s1);
+            part = fma2(D[e], x[e], part);
           }
+          if (in_row) s1 = part;
         }
 #pragma unroll
         for (int e = 0; e < NP; ++e) h[i][e] = D[e];  // now u
@@ -849,13 +892,14 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), BWD || MAXT > 384 ?
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = col0 + i * cstep;
-        if (c >= a.C) continue;
+        const int col = col0 + i * cstep, c = FULL && col >= a.C ? 0 : col;
+        const bool in_row = col < a.C;
+        if (!FULL && !in_row) continue;
         f2 x[NP];
         fetch(0, c, x);
 #pragma unroll
         for (int e = 0; e < NP; ++e) x[e] = fma2(x[e], c1, mul2(h[i][e], r1p));
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.C + c) = rounded(x, kind);
+        if (in_row) *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.C + c) = rounded(x, kind);
       }
       release();
     }
@@ -938,25 +982,30 @@ cudaError_t run_narrow(const NormArgs& a, bool bwd, int* parts, cudaStream_t s) 
 // Wide rows: persistent CTAs, as many per SM as leave each a ring of two stages or more and
 // the SM its registers; the ring takes the rest of the shared memory. *fits: whether one
 // stage does.
-template <class T, int NV, int MAXT, bool BWD, bool SPLIT>
+template <class T, int NV, int MAXT, bool BWD, bool SPLIT, bool FULL = false, bool GATE = false>
 cudaError_t run_stream(const NormArgs& a, int* parts, bool* fits, cudaStream_t s) {
   const int nsm = device_sm_count();
   if (nsm < 1) return cudaErrorInvalidDevice;
   constexpr int VEC = 16 / (int)sizeof(T), STEP = SPLIT ? 128 : 32, BUDGET = 226 * 1024;
   const int workers = ((a.C / VEC + NV - 1) / NV + STEP - 1) / STEP * STEP;
   const bool pre = a.w_pre != nullptr;
+  if constexpr (!FULL) {
+    if (a.residual && pre && (!BWD || (a.dh && a.dresidual && (!a.gate || a.dgate))))
+      return a.gate ? run_stream<T, NV, MAXT, BWD, SPLIT, true, true>(a, parts, fits, s)
+                    : run_stream<T, NV, MAXT, BWD, SPLIT, true, false>(a, parts, fits, s);
+  }
   const int tensors = 1 + (a.gate != nullptr) + (a.residual && (!BWD || pre)) + (BWD && a.dh) + (BWD && pre);
-  const int row = a.C * (int)sizeof(T), stage = tensors * row, head = STREAM_HEAD + (BWD ? 3 * row : 0);
+  const int row = a.C * (int)sizeof(T), stage = tensors * row, head = STREAM_HEAD + (BWD || (FULL && MAXT == 384) ? 3 * row : 0);
   *fits = head + stage <= BUDGET;
   if (!*fits) return cudaSuccess;
-  int per_sm = (BWD ? 384 : 768) / workers;
+  int per_sm = stream_ctas(NV, MAXT, BWD, FULL) * MAXT / workers;
   if (per_sm < 1) per_sm = 1;
   if (per_sm > NORM_CTAS_PER_SM) per_sm = NORM_CTAS_PER_SM;
   while (per_sm > 1 && BUDGET / per_sm - 1024 < 2 * stage + head) --per_sm;  // 1 KB of each CTA is the system's
   int stages = (BUDGET / per_sm - (per_sm > 1 ? 1024 : 0) - head) / stage;
   if (stages > MAX_STAGES) stages = MAX_STAGES;
   const int bytes = head + stages * stage;
-  auto kern = block_norm_stream_kernel<T, NV, MAXT, BWD, SPLIT>;
+  auto kern = block_norm_stream_kernel<T, NV, MAXT, BWD, SPLIT, FULL, GATE>;
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t e = allow_shared(reinterpret_cast<const void*>(kern), BUDGET, &allowed);
   if (e != cudaSuccess) return e;
@@ -985,12 +1034,15 @@ cudaError_t pick(const NormArgs& a, bool vec, bool bwd, int* parts, cudaStream_t
       else if (n <= 1024) e = run_stream<T, 2, 512, false, false>(a, parts, &fits, s);
       else if constexpr (sizeof(T) == 4) e = run_stream<T, 4, 512, false, false>(a, parts, &fits, s);
     } else if constexpr (sizeof(T) == 2) {
-      // eight columns' sums per thread, or sixteen with the registers split
-      if (n <= 384) e = run_stream<T, 1, 384, true, false>(a, parts, &fits, s);
+      // eight columns' sums per thread, two CTAs per SM, while those fit in the registers
+      // (16,000 rows of 2560: 164 us; one CTA 196), or sixteen with the registers split
+      if (n <= 256) e = run_stream<T, 1, 256, true, false>(a, parts, &fits, s);
+      else if (n <= 384) e = run_stream<T, 1, 384, true, false>(a, parts, &fits, s);
       else if (n <= 768) e = run_stream<T, 2, 384, true, true>(a, parts, &fits, s);
       else e = run_stream<T, 2, 512, true, true>(a, parts, &fits, s);
     } else {
-      if (n <= 768) e = run_stream<T, 2, 384, true, false>(a, parts, &fits, s);
+      if (n <= 512) e = run_stream<T, 2, 256, true, false>(a, parts, &fits, s);
+      else if (n <= 1024) e = run_stream<T, 2, 512, true, false>(a, parts, &fits, s);
       else if (n <= 1536) e = run_stream<T, 4, 384, true, true>(a, parts, &fits, s);
       else e = run_stream<T, 4, 512, true, true>(a, parts, &fits, s);
     }

@@ -116,6 +116,16 @@ def test_every_choice_of_parts(dtype, width, on):
     check(p, dh, dy, dtype, sigmoid=bool(on & 1))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", [None, "silu", "sigmoid"])
+@pytest.mark.parametrize("width", [1032, 2056, 2560, 3080, 5000, 6152, 8184])
+def test_wide_rows_that_end_inside_a_step(dtype, gate, width):
+    """Widths at which threads of the last step have no column, one row more than the SMs have CTAs."""
+    parts = dict(FULL, gate=gate is not None)
+    p, dh, dy = make((457, 1, width), dtype, parts, seed=width)
+    check(p, dh, dy, dtype, sigmoid=gate == "sigmoid")
+
+
 @pytest.mark.parametrize("width", [128, 640, 101])
 def test_without_dh(width):
     p, _, dy = make((20, 1, width), "f32", FULL, seed=2)
