@@ -499,7 +499,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t e = allow_shared(reinterpret_cast<const void*>(paged_attn_kernel<T, D>), bytes, &allowed);
   if (e != cudaSuccess) return e;
-  const int grid = launch_ctas(a, ROWS, UNIT, L::WARPS);
+  const int grid = launch_ctas(a, ROWS, UNIT, 0, L::WARPS);
   prof_mark(K_ATTN, s, true);
   e = launch_pdl(paged_attn_kernel<T, D>, dim3(grid), dim3(L::THREADS), bytes, s, a);
   prof_mark(K_ATTN, s, false);
@@ -513,7 +513,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attn_workspace(const AttnArgs& a) {
-  const int warps = a.p.D * (a.p.bf16 ? 2 : 4) <= 256 ? 8 : 6, grid = launch_ctas(a, ROWS, UNIT, warps);
+  const int warps = a.p.D * (a.p.bf16 ? 2 : 4) <= 256 ? 8 : 6, grid = launch_ctas(a, ROWS, UNIT, 0, warps);
   const size_t own = a.p.D == 64 ? Parts<ROWS, 64>::bytes(grid) : Parts<ROWS, 128>::bytes(grid);
   const size_t tc = paged_attn_tc_applies(a) ? paged_attn_tc_workspace(a) : 0;
   return own > tc ? own : tc;

@@ -56,6 +56,9 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
 // Asks for a CTA of the grid that has not been launched; the answer (16 bytes) lands in
 // shared memory and completes on the barrier.
 __device__ __forceinline__ void ask_next_cta(void* answer, uint64_t* bar) {
@@ -101,31 +104,48 @@ struct TcLay {
   static constexpr int P_STEP = D == 128 ? 128 : 64;     // between the two tiles' P
 };
 
-// Four MMAs along K (64 channels of Q and K, or 64 keys of P and V), called by a whole warp
-// and issued by the lane that elect.sync names, the same one every time. The descriptors'
-// steps are added inside: kept outside, the compiler holds every step of every tile in
-// registers, and the warp spends more time on them than the tensor cores on the products.
-__device__ __forceinline__ void umma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 x, y;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n setp.eq.b32 p, 0, 0;\n"
-      " add.s64 x, %1, 2;\n add.s64 y, %2, 2;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n"
-      " add.s64 x, %1, 4;\n add.s64 y, %2, 4;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n"
-      " add.s64 x, %1, 6;\n add.s64 y, %2, 6;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
+// The products of a tile and the arrival on their barrier when they have completed, in one
+// block: called by a whole warp and issued by the lane that one elect.sync names. What the
+// warp executes between a wait and the first product is on the path softmax, products,
+// softmax, so the descriptors' steps are added inside (kept outside, the compiler holds
+// every step of every tile in registers).
+//
+// S = Q K^T, 16 channels a step: both K-major in panels of 64 channels of 16 KB each.
+#define GDN_SS_STEP(X) " add.s64 x, %1, " #X ";\n add.s64 y, %2, " #X ";\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n"
+template <int D>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint64_t* bar) {
+  if constexpr (D == 64)
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, 0, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n setp.eq.b32 p, 0, 0;\n"
+        GDN_SS_STEP(2) GDN_SS_STEP(4) GDN_SS_STEP(6)
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(smem_u32(bar))
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, 0, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n setp.eq.b32 p, 0, 0;\n"
+        GDN_SS_STEP(2) GDN_SS_STEP(4) GDN_SS_STEP(6) GDN_SS_STEP(1024) GDN_SS_STEP(1026) GDN_SS_STEP(1028) GDN_SS_STEP(1030)
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(smem_u32(bar))
+        : "memory");
 }
-// A[tmem]: 16-bit pairs in 32-bit columns; B MN-major, 2048 bytes a step.
-__device__ __forceinline__ void umma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+#undef GDN_SS_STEP
+// O (+)= P V, 16 keys a step. P in tensor memory: 16-bit pairs in 32-bit columns; V MN-major,
+// 2048 bytes a step.
+#define GDN_TS_STEP(X, Y) " add.u32 x, %1, " #X ";\n add.s64 y, %2, " #Y ";\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n"
+__device__ __forceinline__ void issue_output(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint64_t* bar) {
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .b32 x;\n .reg .b64 y;\n elect.sync _|q, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
       " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n setp.eq.b32 p, 0, 0;\n"
-      " add.u32 x, %1, 8;\n add.s64 y, %2, 128;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n"
-      " add.u32 x, %1, 16;\n add.s64 y, %2, 256;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n"
-      " add.u32 x, %1, 24;\n add.s64 y, %2, 384;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      GDN_TS_STEP(8, 128) GDN_TS_STEP(16, 256) GDN_TS_STEP(24, 384) GDN_TS_STEP(32, 512) GDN_TS_STEP(40, 640)
+      GDN_TS_STEP(48, 768) GDN_TS_STEP(56, 896)
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(smem_u32(bar))
       : "memory");
 }
+#undef GDN_TS_STEP
 // umma_commit by the elected lane.
 __device__ __forceinline__ void commit_elected(uint64_t* bar) {
   asm volatile(
@@ -268,6 +288,10 @@ template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
     paged_attn_tc_kernel(AttnArgs a, int box_rows, int whole_items, const __grid_constant__ CUtensorMap k_map,
                          const __grid_constant__ CUtensorMap v_map) {
+  if (threadIdx.x == 0) {
+    prefetch_map(&k_map);
+    prefetch_map(&v_map);
+  }
   pdl_wait();
   if (!whole_items) pdl_trigger();
   typedef TcLay<D> L;
@@ -526,9 +550,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       tc_fence_before();
-      if (it.end >= hi && tid == 0 && !whole_items)
-        *head = PartHead{it.start >= lo && it.end > hi ? holder(run->total, run->ncta, it.end - 1) - (int)blockIdx.x : 0,
-                         g.row0, g.rows, it.s.first, it.h, {0, 0, 0}};
       if (!next_item()) break;
     }
   } else {
@@ -538,6 +559,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ---------------------------------------------------------------- products
     constexpr uint32_t id_s = umma_idesc_bf16(HALF, KT), id_o = umma_idesc_bf16(HALF, D, false, true);
     constexpr int PANEL = KT * 128;
+    static_assert(PANEL / 16 == 1024, "issue_scores' panels");
     const uint32_t acc = __shfl_sync(0xffffffffu, tm, 0);
     const uint64_t dq = desc_kmajor(sm + L::Q), dring = desc_kmajor(sm + L::RING),
                    dvring = desc_mnmajor(sm + L::RING, PANEL);
@@ -558,10 +580,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int tiles = __shfl_sync(0xffffffffu, g.tiles(), 0), keys = __shfl_sync(0xffffffffu, it.s.len - g.t0 * KT, 0);
       auto scores = [&](int w, int kslot, bool last) {
         const uint64_t q = dq + (uint64_t)(w * (HALF * D * 2 / 16)), k = dring + (uint64_t)(kslot * (L::SLOT / 16));
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-          umma4_ss(acc + L::S + w * 128, q + h * (PANEL / 16), k + h * (PANEL / 16), id_s, h > 0);
-        commit_elected(&sbar[w]);
+        issue_scores<D>(acc + L::S + w * 128, q, k, id_s, &sbar[w]);
         if (last) commit_elected(&qfree[w]);  // the item's queries are done with
       };
       // the first scores of each row tile: of one key tile, or of the first two
@@ -596,18 +615,15 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
         }
         bool kready = false;
+        const uint64_t v = dvring + (uint64_t)(vslot * (L::SLOT / 16));
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int j = alone ? i >> 1 : i;  // the row tile's own count
           if (alone ? (i & 1) == w : i < need[w]) {
             mbar_wait(&pbar[w], np >> w & 1, p.err);
             tc_fence_after();
-            const uint64_t v = dvring + (uint64_t)(vslot * (L::SLOT / 16));
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              umma4_ts(acc + L::O + w * D, acc + L::P + w * L::P_STEP + 32 * h, v + h * 512, id_o, (j > 0 || h > 0) ? 1u : 0u);
+            issue_output(acc + L::O + w * D, acc + L::P + w * L::P_STEP, v, id_o, j > 0, &obar[w]);
             np ^= 1u << w;
-            commit_elected(&obar[w]);
             if (j + 1 < need[w]) {
               if (!kready) {
                 mbar_wait(&full[kslot], kphase, p.err);
@@ -669,7 +685,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_drain(&full[at % L::SLOTS], at / L::SLOTS & 1);
     __syncwarp();
   } else if (warp == QUERY_WARP) {
-    // ---------------------------------------------------------------- queries, after the first item's
+    // ---------------------------------------------------------------- queries, after the first item's, and the join's head
     uint32_t loads[2] = {0, 0};
     for (bool first = true;; first = false) {
       const Segment g = segment(it, G, lo, hi);
@@ -685,8 +701,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           ++loads[w];
         }
       if (!whole_items) {
-        if (!next_item()) break;
-        continue;
+        if (next_item()) continue;
+        if (lane == 0)
+          *head = PartHead{it.start >= lo && it.end > hi ? holder(run->total, run->ncta, it.end - 1) - (int)blockIdx.x : 0,
+                           g.row0, g.rows, it.s.first, it.h, {0, 0, 0}};
+        break;
       }
       // find the next item while this one is in work, and put it down for the other warps
       if (lane == 0) {
@@ -792,7 +811,7 @@ cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
   cudaError_t e = allow_shared(reinterpret_cast<const void*>(paged_attn_tc_kernel<D>), bytes, &allowed);
   if (e != cudaSuccess) return e;
   const bool whole = whole_items(a);
-  const unsigned grid = whole ? (unsigned)most_items(a, ROWS) : (unsigned)launch_ctas(a, ROWS, KT, MIN_UNITS);
+  const unsigned grid = whole ? (unsigned)most_items(a, ROWS) : (unsigned)launch_ctas(a, ROWS, KT, OVER, MIN_UNITS);
   prof_mark(K_ATTN_TC, s, true);
   e = launch_pdl(paged_attn_tc_kernel<D>, dim3(grid), dim3(THREADS), bytes, s, a, box, (int)whole, km, vm);
   prof_mark(K_ATTN_TC, s, false);
@@ -812,7 +831,7 @@ bool paged_attn_tc_applies(const AttnArgs& a) {
 
 size_t paged_attn_tc_workspace(const AttnArgs& a) {
   if (whole_items(a)) return 0;
-  const int grid = launch_ctas(a, ROWS, KT, MIN_UNITS);
+  const int grid = launch_ctas(a, ROWS, KT, OVER, MIN_UNITS);
   return a.p.D == 64 ? Parts<ROWS, 64>::bytes(grid) : Parts<ROWS, 128>::bytes(grid);
 }
 
