@@ -23,6 +23,10 @@
 // The sums over rows of the weight gradients stay in the registers of the threads that own
 // the columns while a CTA walks its rows (a fixed stride, so the order of the sums is
 // fixed); one partial row per CTA goes to the workspace and a second kernel adds them.
+//
+// Bound by memory, less what the reductions and conversions leave uncovered. bf16, all parts,
+// 8,192 rows of 6,144: forward 84 us (0.90 of the copy rate on its bytes), backward 144 us
+// (0.84). Gated norm of 196,608 heads of 128: forward 31 us (0.73), backward 52 us (0.73).
 #include "common.cuh"
 #include "kernels.h"
 

@@ -29,6 +29,13 @@
 //    KV heads of a run of rows side by side; the CTAs that run at the same time then read
 //    the same keys at the same time, which the L2 serves once. A running CTA takes over the
 //    next one not yet launched (cluster launch control) and goes on with its item, as above.
+//
+// Measured, heads of 128: a chunk of 2,048 tokens over 63k keys (16 and 4 heads, 128 items)
+// 690-700 us, 1.56 PFLOP/s, in bursts and 780 us under the power limit (by items: 793 in
+// bursts); six prompts of up to 4,096 tokens (48 and 8 heads, 3,408 items) 595-616 us,
+// 1.2 PFLOP/s (by runs: 837 us), where an item's output, queries and first softmax take
+// about a fifth; 16 x 8 draft tokens over up to 16k keys (16 and 2 heads) 51 us, of which
+// the stream of keys is 24 us and the start, merge and join the rest.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -43,7 +50,8 @@ constexpr int THREADS = 384;  // three warpgroups: two of softmax, and one of th
 constexpr int MMA_WARP = 8, KEY_WARP = 9, VALUE_WARP = 10, QUERY_WARP = 11;
 constexpr int ITEM_READERS = 11;  // warps that read the next item: all but the query warp, which finds it
 // Registers a thread, moved from the third warpgroup to the softmax (which holds 128 scores):
-// the launch has 168 each, 2 * 216 + 72 = 3 * 168.
+// the launch has 168 each, 2 * 216 + 72 = 3 * 168. (Six prompts of up to 4,096 tokens: 622 us; 208 and 88
+// 662 us, 224 and 56 697 us.)
 constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
 constexpr float RESCALE = 8.f;  // growth of the maximum (base 2) that rescales O
 
@@ -798,7 +806,9 @@ bool cache_map(CUtensorMap* map, void* base, const PagedArgs& p, long long ps, l
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether the call surely has two items or more per SM: the tokens' full items alone.
+// Whether the call surely has two items or more per SM: the tokens' full items alone. Below
+// that the ragged last round costs more than the parts (128 items: 793 us, by runs 711);
+// above, the shared reads of keys gain more (3,408 items: 622 us, by runs 837).
 bool whole_items(const AttnArgs& a) {
   const int nsm = device_sm_count() > 0 ? device_sm_count() : 152;
   return (long long)a.p.N * (a.p.Hq / a.p.Hk) / ROWS * a.p.Hk >= 2ll * nsm;
