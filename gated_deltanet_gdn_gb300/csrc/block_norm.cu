@@ -14,8 +14,9 @@
 //   u = dn w_post; dx = r1 (u - x r1^2 mean(u x));  dw_post = sum dn x r1
 //
 // Every input is read once. Three forms, by the width of a row:
-//  * narrow rows (up to 32 vectors of 16 bytes; the norm of a head): a part of a warp per
-//    row, reductions by shuffle, the next row's vectors loaded while this one's are used;
+//  * narrow rows (up to 32 vectors of 16 bytes; the norm of a head, which has kernels of its
+//    own): a part of a warp per row, reductions by shuffle, the next rows' vectors loaded
+//    while this one's are used;
 //  * wide rows: persistent CTAs, one row at a time, the inputs of the next rows on their
 //    way through a ring in shared memory (bulk copies by a warp of their own);
 //  * rows whose width, strides or pointers do not allow 16-byte accesses: element by
@@ -26,7 +27,7 @@
 //
 // Bound by memory, less what the reductions and conversions leave uncovered. bf16, all parts,
 // 8,192 rows of 6,144: forward 84 us (0.90 of the copy rate on its bytes), backward 144 us
-// (0.84). Gated norm of 196,608 heads of 128: forward 31 us (0.73), backward 52 us (0.73).
+// (0.84). Gated norm of 196,608 heads of 128: forward 29 us (0.78), backward 45 us (0.84).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -142,18 +143,16 @@ struct RowIn {
   Raw<T, VEC> x[NV], gate[NV], res[NV], dh[NV], dy[NV];
 };
 
-// HEAD: only w_post and gate can be present (the norm of a head's output); the rest is
-// compiled out, which halves the registers.
-template <class T, int VEC, int NV, int SUB, bool HEAD>
+template <class T, int VEC, int NV, int SUB>
 __global__ void __launch_bounds__(SUB ? SUB_THREADS : NORM_THREADS_MAX)
     block_norm_fwd_kernel(NormArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ __align__(16) float buf[2][32];
   const Place<SUB> at;
-  const T *wpost = static_cast<const T*>(a.w_post), *rscale = HEAD ? nullptr : static_cast<const T*>(a.res_scale),
-          *wpre = HEAD ? nullptr : static_cast<const T*>(a.w_pre), *gate = static_cast<const T*>(a.gate),
-          *res = HEAD ? nullptr : static_cast<const T*>(a.residual);
+  const T *wpost = static_cast<const T*>(a.w_post), *rscale = static_cast<const T*>(a.res_scale),
+          *wpre = static_cast<const T*>(a.w_pre), *gate = static_cast<const T*>(a.gate),
+          *res = static_cast<const T*>(a.residual);
   const float invC = 1.f / (float)a.C;
   // a part-warp's rows end together: the whole warp stays in the loop for the shuffles
   constexpr unsigned PER = SUB ? SUB_THREADS / (SUB ? SUB : 1) : 1;  // rows of a CTA at a time
@@ -253,18 +252,18 @@ __global__ void __launch_bounds__(SUB ? SUB_THREADS : NORM_THREADS_MAX)
   }
 }
 
-template <class T, int VEC, int NV, int SUB, bool HEAD>
-__global__ void __launch_bounds__(SUB ? SUB_THREADS : NORM_THREADS_MAX, HEAD ? 3 : 1)
+template <class T, int VEC, int NV, int SUB>
+__global__ void __launch_bounds__(SUB ? SUB_THREADS : NORM_THREADS_MAX)
     block_norm_bwd_kernel(NormArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ __align__(16) float buf[2][32];
   const Place<SUB> at;
-  const T *gate = static_cast<const T*>(a.gate), *res = HEAD ? nullptr : static_cast<const T*>(a.residual),
-          *wpost = static_cast<const T*>(a.w_post), *rscale = HEAD ? nullptr : static_cast<const T*>(a.res_scale),
-          *wpre = HEAD ? nullptr : static_cast<const T*>(a.w_pre), *dhp = static_cast<const T*>(a.dh),
-          *dyp = HEAD ? nullptr : static_cast<const T*>(a.dy);
-  T* dres = HEAD ? nullptr : static_cast<T*>(a.dresidual);
+  const T *gate = static_cast<const T*>(a.gate), *res = static_cast<const T*>(a.residual),
+          *wpost = static_cast<const T*>(a.w_post), *rscale = static_cast<const T*>(a.res_scale),
+          *wpre = static_cast<const T*>(a.w_pre), *dhp = static_cast<const T*>(a.dh),
+          *dyp = static_cast<const T*>(a.dy);
+  T* dres = static_cast<T*>(a.dresidual);
   const float invC = 1.f / (float)a.C;
   constexpr unsigned PER = SUB ? SUB_THREADS / (SUB ? SUB : 1) : 1;  // rows of a CTA at a time
   const unsigned rows = (unsigned)a.R * (unsigned)a.G, last = (rows + PER - 1) / PER * PER;
@@ -457,13 +456,13 @@ __global__ void __launch_bounds__(SUB ? SUB_THREADS : NORM_THREADS_MAX, HEAD ? 3
     }
   };
   if (a.dw_post) put(0, sw1);
-  if (!HEAD && a.dw_pre) put(1, sw2);
-  if (!HEAD && a.dres_scale) put(2, ssc);
+  if (a.dw_pre) put(1, sw2);
+  if (a.dres_scale) put(2, ssc);
 }
 
-// ---------------------------------------------------------------- wide rows
+// ---------------------------------------------------------------- packed arithmetic
 // Packed fp32 pairs: one instruction does the fp32 operation on both halves, each rounded
-// as the scalar one. The wide kernels are close to the issue rate, which this halves for
+// as the scalar one. The kernels below are close to the issue rate, which this halves for
 // most of their arithmetic.
 typedef uint64_t f2;
 __device__ __forceinline__ f2 pk(float lo, float hi) {
@@ -532,6 +531,196 @@ __device__ __forceinline__ void activation2(f2 g, bool sigmoid, f2& a, f2& d) {
   d = mul2(s, fma2(f, rest, sigmoid ? pk(0.f, 0.f) : one));
 }
 
+// ---------------------------------------------------------------- a head's output
+// Rows of up to 32 vectors with w_post and gate alone, the norm of a head's output: SUB
+// lanes a row, a weight that is missing is ones. What a row costs beside its arithmetic counts
+// here (eight elements a thread): strided places are stepped, not divided. The next two rows
+// are on their way while one is used, since the loads of one do not cover the latency:
+// 196,608 rows of 128 in bf16 take 71 us in both directions, with one row ahead 80.
+
+// Place of a thread's vector in an input with row and group strides, row after row of its walk.
+struct HeadWalk {
+  long long at, by, wrap;
+  __device__ __forceinline__ HeadWalk(unsigned row, unsigned step, unsigned G, long long rs, long long gs, int c)
+      : at((long long)(row / G) * rs + (long long)(row % G) * gs + c),
+        by((long long)(step / G) * rs + (long long)(step % G) * gs),
+        wrap(rs - (long long)G * gs) {}
+  __device__ __forceinline__ void next(bool over) { at += over ? by + wrap : by; }
+};
+template <int SUB>
+__device__ __forceinline__ float head_sum(f2 v2) {
+  float v, hi;
+  unpk(v2, v, hi);
+  v += hi;
+#pragma unroll
+  for (int off = SUB / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+template <class T, int SUB, bool GATE>
+__global__ void __launch_bounds__(SUB_THREADS) block_norm_head_fwd_kernel(NormArgs a) {
+  constexpr int VEC = 16 / (int)sizeof(T), NP = VEC / 2, PER = SUB_THREADS / SUB;
+  pdl_wait();
+  pdl_trigger();
+  const Place<SUB> at;
+  const T *kind = nullptr, *x = static_cast<const T*>(a.x), *gate = static_cast<const T*>(a.gate);
+  const int c = at.lane * VEC;
+  const bool mine = c < a.C, post = a.w_post != nullptr;
+  const unsigned G = (unsigned)a.G, rows = (unsigned)a.R * G, last = (rows + PER - 1) / PER * PER, dg = at.step % G;
+  const float invC = 1.f / (float)a.C;
+  HeadWalk wx(at.row, at.step, G, a.x_rs, a.x_gs, c), wg(at.row, at.step, G, a.gate_rs, a.gate_gs, c);
+  unsigned g = at.row % G;
+  f2 w[NP];
+#pragma unroll
+  for (int e = 0; e < NP; ++e) w[e] = pk(1.f, 1.f);
+  if (post && mine) pairs_of(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.w_post) + c), w, kind);
+  struct Row {
+    uint4 x, gate;
+  } row0, row1;  // the next two rows
+  row0.x = row0.gate = row1.x = row1.gate = make_uint4(0u, 0u, 0u, 0u);
+  auto fetch = [&](unsigned row, Row& in) {
+    if (mine && row < rows) {
+      in.x = *reinterpret_cast<const uint4*>(x + wx.at);
+      if (GATE) in.gate = *reinterpret_cast<const uint4*>(gate + wg.at);
+    }
+    g += dg;
+    const bool over = g >= G;
+    if (over) g -= G;
+    wx.next(over);
+    if (GATE) wg.next(over);
+  };
+  auto use = [&](unsigned row, Row& in) {
+    f2 v[NP], t[NP], ss = pk(0.f, 0.f);
+    pairs_of(in.x, v, kind);
+    if (GATE) pairs_of(in.gate, t, kind);
+    fetch(row + 2 * at.step, in);
+    float r1 = 1.f;
+    if (post) {
+#pragma unroll
+      for (int e = 0; e < NP; ++e) ss = fma2(v[e], v[e], ss);
+      r1 = rsqrtf(head_sum<SUB>(ss) * invC + a.eps);
+    }
+    const f2 r1p = pk(r1, r1);
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      v[e] = mul2(mul2(v[e], r1p), w[e]);
+      if (GATE) {
+        f2 ac, ad;
+        activation2(t[e], a.sigmoid, ac, ad);
+        v[e] = mul2(v[e], ac);
+      }
+    }
+    if (row < rows) {
+      if (mine) *reinterpret_cast<uint4*>(static_cast<T*>(a.h) + (size_t)row * (unsigned)a.C + c) = rounded(v, kind);
+      if (at.lane == 0) *reinterpret_cast<float2*>(a.stats + 2 * (size_t)row) = make_float2(r1, 1.f);
+    }
+  };
+  fetch(at.row, row0);
+  fetch(at.row + at.step, row1);
+  for (unsigned row = at.row; row < last; row += 2 * at.step) {
+    use(row, row0);
+    if (row + at.step < last) use(row + at.step, row1);
+  }
+}
+
+template <class T, int SUB, bool GATE>
+__global__ void __launch_bounds__(SUB_THREADS, 2) block_norm_head_bwd_kernel(NormArgs a) {
+  constexpr int VEC = 16 / (int)sizeof(T), NP = VEC / 2, PER = SUB_THREADS / SUB;
+  pdl_wait();
+  pdl_trigger();
+  const Place<SUB> at;
+  const T *kind = nullptr, *x = static_cast<const T*>(a.x), *gate = static_cast<const T*>(a.gate),
+          *dh = static_cast<const T*>(a.dh);
+  const int c = at.lane * VEC;
+  const bool mine = c < a.C, post = a.w_post != nullptr;
+  const unsigned G = (unsigned)a.G, rows = (unsigned)a.R * G, last = (rows + PER - 1) / PER * PER, dg = at.step % G;
+  const float invC = 1.f / (float)a.C;
+  HeadWalk wx(at.row, at.step, G, a.x_rs, a.x_gs, c), wg(at.row, at.step, G, a.gate_rs, a.gate_gs, c),
+      wd(at.row, at.step, G, a.dh_rs, a.dh_gs, c);
+  unsigned g = at.row % G;
+  const f2 zero2 = pk(0.f, 0.f);
+  f2 w[NP], sw[NP];  // the weights, and their gradients' sums over this thread's rows
+#pragma unroll
+  for (int e = 0; e < NP; ++e) {
+    w[e] = pk(1.f, 1.f);
+    sw[e] = zero2;
+  }
+  if (post && mine) pairs_of(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.w_post) + c), w, kind);
+  struct Row {
+    uint4 x, gate, dh;
+    float r1;
+  } row0, row1;  // the next two rows
+  row0.r1 = row1.r1 = 1.f;
+  auto fetch = [&](unsigned row, Row& in) {
+    if (mine && row < rows) {
+      in.x = *reinterpret_cast<const uint4*>(x + wx.at);
+      if (GATE) in.gate = *reinterpret_cast<const uint4*>(gate + wg.at);
+      in.dh = dh ? *reinterpret_cast<const uint4*>(dh + wd.at) : make_uint4(0u, 0u, 0u, 0u);
+      if (post) in.r1 = a.stats[2 * (size_t)row];
+    } else {
+      in.x = in.gate = in.dh = make_uint4(0u, 0u, 0u, 0u);  // nothing for the sums
+    }
+    g += dg;
+    const bool over = g >= G;
+    if (over) g -= G;
+    wx.next(over);
+    if (GATE) wg.next(over);
+    wd.next(over);
+  };
+  auto use = [&](unsigned row, Row& in) {
+    const size_t out = (size_t)row * (unsigned)a.C + c;
+    const bool store = mine && row < rows;
+    f2 xv[NP], t[NP], D[NP], s1 = zero2;
+    pairs_of(in.x, xv, kind);
+    if (GATE) pairs_of(in.gate, t, kind);
+    pairs_of(in.dh, D, kind);
+    const float r1 = in.r1;
+    fetch(row + 2 * at.step, in);
+    const f2 r1p = pk(r1, r1);
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+      const f2 xr = mul2(xv[e], r1p);
+      if (GATE) {
+        f2 ac, ad;
+        activation2(t[e], a.sigmoid, ac, ad);
+        t[e] = mul2(mul2(D[e], mul2(xr, w[e])), ad);  // dgate
+        D[e] = mul2(D[e], ac);
+      }
+      sw[e] = fma2(D[e], xr, sw[e]);
+      D[e] = mul2(D[e], w[e]);
+      s1 = fma2(D[e], xv[e], s1);
+    }
+    if (GATE && store && a.dgate) *reinterpret_cast<uint4*>(static_cast<T*>(a.dgate) + out) = rounded(t, kind);
+    f2 c1 = zero2;
+    if (post) {
+      const float m = -head_sum<SUB>(s1) * invC * r1 * r1 * r1;
+      c1 = pk(m, m);
+    }
+#pragma unroll
+    for (int e = 0; e < NP; ++e) D[e] = fma2(xv[e], c1, mul2(D[e], r1p));
+    if (store) *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + out) = rounded(D, kind);
+  };
+  fetch(at.row, row0);
+  fetch(at.row + at.step, row1);
+  for (unsigned row = at.row; row < last; row += 2 * at.step) {
+    use(row, row0);
+    if (row + at.step < last) use(row + at.step, row1);
+  }
+  if (!a.dw_post) return;
+  // this CTA's sums: the groups of lanes column by column, in their order
+  __shared__ __align__(16) float cols[SUB_THREADS * VEC];
+#pragma unroll
+  for (int e = 0; e < NP; ++e) *reinterpret_cast<f2*>(cols + threadIdx.x * VEC + 2 * e) = sw[e];
+  __syncthreads();
+  for (int q = threadIdx.x; q < SUB * VEC; q += SUB_THREADS) {
+    if (q >= a.C) continue;
+    float t = 0.f;
+    for (int k = 0; k < PER; ++k) t += cols[k * SUB * VEC + q];
+    a.partial[(size_t)blockIdx.x * 3 * a.C + q] = t;
+  }
+}
+
+// ---------------------------------------------------------------- wide rows
 constexpr int MAX_STAGES = 8;
 struct StreamShared {
   float buf[2][32];
@@ -955,18 +1144,18 @@ int resident(K kern, int threads) {
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) == cudaSuccess && n > 0 ? n : 1;
 }
 
-template <class T, int VEC, int NV, int SUB, bool HEAD>
-cudaError_t run(const NormArgs& a, int threads, bool bwd, int* parts, cudaStream_t s) {
-  const auto fwd_kernel = block_norm_fwd_kernel<T, VEC, NV, SUB, HEAD>;
-  const auto bwd_kernel = block_norm_bwd_kernel<T, VEC, NV, SUB, HEAD>;
+// SUB lanes per row (0: a CTA); per_sm: CTAs of the forward's and the backward's kernel that
+// an SM holds.
+template <int SUB, class K>
+cudaError_t run_rows(K fwd_kernel, K bwd_kernel, const int* per_sm, const NormArgs& a, int threads, bool bwd, int* parts,
+                     cudaStream_t s) {
   const long long rows = (long long)a.R * a.G, per = SUB ? SUB_THREADS / (SUB ? SUB : 1) : 1;
   long long grid = (rows + per - 1) / per, most = grid;
   if (SUB) {
     // part-warp rows: one wave of CTAs, each walking its rows with the next one's loads ahead
     // (with a third of a wave more, the B8 T4096 H6 D128 forward took 34 us in place of 31)
-    static const int per_sm_fwd = resident(fwd_kernel, SUB_THREADS), per_sm_bwd = resident(bwd_kernel, SUB_THREADS);
     const int nsm = device_sm_count();
-    most = (long long)(nsm > 0 ? nsm : 152) * (bwd ? per_sm_bwd : per_sm_fwd);
+    most = (long long)(nsm > 0 ? nsm : 152) * per_sm[bwd];
   }
   if (bwd && most > norm_bwd_parts(a.C)) most = norm_bwd_parts(a.C);
   if (grid > most) grid = most;
@@ -976,11 +1165,22 @@ cudaError_t run(const NormArgs& a, int threads, bool bwd, int* parts, cudaStream
   prof_mark(bwd ? K_NORM_BWD : K_NORM_FWD, s, false);
   return e;
 }
+template <class T, int VEC, int NV, int SUB>
+cudaError_t run(const NormArgs& a, int threads, bool bwd, int* parts, cudaStream_t s) {
+  const auto fwd = block_norm_fwd_kernel<T, VEC, NV, SUB>, bwd_kernel = block_norm_bwd_kernel<T, VEC, NV, SUB>;
+  static const int per_sm[2] = {resident(fwd, SUB_THREADS), resident(bwd_kernel, SUB_THREADS)};
+  return run_rows<SUB>(fwd, bwd_kernel, per_sm, a, threads, bwd, parts, s);
+}
+template <class T, int SUB, bool GATE>
+cudaError_t run_head(const NormArgs& a, bool bwd, int* parts, cudaStream_t s) {
+  const auto fwd = block_norm_head_fwd_kernel<T, SUB, GATE>, bwd_kernel = block_norm_head_bwd_kernel<T, SUB, GATE>;
+  static const int per_sm[2] = {resident(fwd, SUB_THREADS), resident(bwd_kernel, SUB_THREADS)};
+  return run_rows<SUB>(fwd, bwd_kernel, per_sm, a, SUB_THREADS, bwd, parts, s);
+}
 template <class T, int SUB>
 cudaError_t run_narrow(const NormArgs& a, bool bwd, int* parts, cudaStream_t s) {
-  constexpr int V = 16 / (int)sizeof(T);
-  const bool head = !a.residual && !a.res_scale && !a.w_pre;
-  return head ? run<T, V, 1, SUB, true>(a, SUB_THREADS, bwd, parts, s) : run<T, V, 1, SUB, false>(a, SUB_THREADS, bwd, parts, s);
+  if (a.residual || a.res_scale || a.w_pre) return run<T, 16 / (int)sizeof(T), 1, SUB>(a, SUB_THREADS, bwd, parts, s);
+  return a.gate ? run_head<T, SUB, true>(a, bwd, parts, s) : run_head<T, SUB, false>(a, bwd, parts, s);
 }
 
 // Wide rows: persistent CTAs, as many per SM as leave each a ring of two stages or more and
@@ -1053,9 +1253,9 @@ cudaError_t pick(const NormArgs& a, bool vec, bool bwd, int* parts, cudaStream_t
     if (e != cudaSuccess || fits) return e;
     // the inputs of one fp32 row above 28 KB, all parts present, exceed the shared memory
   }
-  if (a.C <= 128) return run<T, 1, 4, 32, false>(a, SUB_THREADS, bwd, parts, s);
-  if (a.C <= 2048) return run<T, 1, 4, 0, false>(a, ((a.C + 3) / 4 + 31) / 32 * 32, bwd, parts, s);
-  return run<T, 1, 16, 0, false>(a, ((a.C + 15) / 16 + 31) / 32 * 32, bwd, parts, s);
+  if (a.C <= 128) return run<T, 1, 4, 32>(a, SUB_THREADS, bwd, parts, s);
+  if (a.C <= 2048) return run<T, 1, 4, 0>(a, ((a.C + 3) / 4 + 31) / 32 * 32, bwd, parts, s);
+  return run<T, 1, 16, 0>(a, ((a.C + 15) / 16 + 31) / 32 * 32, bwd, parts, s);
 }
 
 }  // namespace
