@@ -64,7 +64,7 @@ def ext_commands(out: str) -> List[List[str]]:
     return [[cxx, "-O2", "-std=c++17", "-fPIC", *(f"-I{i}" for i in inc),
              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
              "-c", os.path.join(CSRC, "binding_ext.cpp"), "-o", obj],
-            [cxx, "-shared", "-o", out, obj, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+            [cxx, "-shared", "-o", out, obj, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
              "-lc10_cuda", "-L" + PKG, "-l:libgdn.so", "-Wl,-rpath,$ORIGIN"]]
 
 
