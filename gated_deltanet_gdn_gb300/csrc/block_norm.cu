@@ -1137,6 +1137,16 @@ __global__ void __launch_bounds__(32 * WG_LANES) block_norm_wgrad_kernel(NormArg
   if (l == 0 && blockIdx.x * 32 + k0 < a.C) out[blockIdx.x * 32 + k0] = from_f32<T>(t);
 }
 
+// The fewest CTAs, `per` rows at a time, that take as many turns as `grid` of them: fewer rows
+// of partial sums in the same time (1,021 rows of 1,001 fp32: 511 CTAs in place of 912, 21.7 us
+// for both directions in place of 24.0).
+long long even(long long rows, long long per, long long grid) {
+  const long long blocks = (rows + per - 1) / per;
+  if (grid < 1 || blocks < 1) return grid;
+  const long long turns = (blocks + grid - 1) / grid;
+  return (blocks + turns - 1) / turns;
+}
+
 // CTAs of a kernel that an SM holds at once (asked for once per kernel).
 template <class K>
 int resident(K kern, int threads) {
@@ -1159,7 +1169,7 @@ cudaError_t run_rows(K fwd_kernel, K bwd_kernel, const int* per_sm, const NormAr
   }
   if (bwd && most > norm_bwd_parts(a.C)) most = norm_bwd_parts(a.C);
   if (grid > most) grid = most;
-  if (bwd) *parts = (int)grid;
+  if (bwd) *parts = (int)(grid = even(rows, per, grid));
   prof_mark(bwd ? K_NORM_BWD : K_NORM_FWD, s, true);
   const cudaError_t e = launch_pdl(bwd ? bwd_kernel : fwd_kernel, dim3((unsigned)grid), dim3(threads), 0, s, a);
   prof_mark(bwd ? K_NORM_BWD : K_NORM_FWD, s, false);
@@ -1216,7 +1226,7 @@ cudaError_t run_stream(const NormArgs& a, int* parts, bool* fits, cudaStream_t s
   long long grid = (long long)a.R * a.G;
   if (grid > (long long)nsm * per_sm) grid = (long long)nsm * per_sm;
   if (BWD && grid > norm_bwd_parts(a.C)) grid = norm_bwd_parts(a.C);
-  if (BWD) *parts = (int)grid;
+  if (BWD) *parts = (int)(grid = even((long long)a.R * a.G, 1, grid));
   prof_mark(BWD ? K_NORM_BWD : K_NORM_FWD, s, true);
   e = launch_pdl(kern, dim3((unsigned)grid), dim3(workers + (SPLIT ? 128 : 32)), bytes, s, a, stages);
   prof_mark(BWD ? K_NORM_BWD : K_NORM_FWD, s, false);
