@@ -149,6 +149,23 @@ def test_strided_rows(dtype, width):
         check(p, dh, dy, dtype, cuda=cuda)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("parts", [("post", "gate"), ("post",), ("gate",)])
+def test_many_strided_heads(dtype, parts):
+    """Heads out of wider rows, more of them than are in work at once: every step of the walk over rows and
+    groups, with groups left over."""
+    R, G, C = 9001, 5, 64
+    p, dh, dy = make((R, G, C), dtype, {k: k in parts for k in FULL}, seed=len(parts))
+    cuda = {}
+    for i, (k, v) in enumerate(p.items()):
+        cuda[k] = None if v is None else v.cuda()
+        if v is not None and v.dim() == 3:
+            wide = torch.full((R, G + i + 1, C + 16), 9.0, dtype=v.dtype, device="cuda")
+            wide[:, 1:G + 1, 8:8 + C] = v.cuda()
+            cuda[k] = wide[:, 1:G + 1, 8:8 + C]
+    check(p, dh, dy, dtype, cuda=cuda)
+
+
 def test_formulas_against_central_differences():
     """float64: the gradients above are the derivatives of the forward above."""
     for sigmoid in (False, True):
