@@ -7,8 +7,9 @@
 // value is used for 16 query rows, so HBM bounds it: 4 D bytes per key in bf16 against
 // 64 D flop. What matters is a deep, even stream of loads:
 //  * the keys of all items are cut into units of 16 (inside one page, page sizes being
-//    multiples of 16) and numbered through; each CTA takes an equal run of them, whatever
-//    the lengths of the sequences, and its warps take every WARPS-th unit of the run;
+//    multiples of 16) and numbered through, with units for an item's start and end in front;
+//    each CTA takes an equal run of them, whatever the lengths of the sequences, and its
+//    warps take every WARPS-th unit of the run;
 //  * each warp streams its units through a ring of its own (cp.async, 16 bytes a lane)
 //    that runs ahead across item boundaries, with no barrier between warps;
 //  * at an item's end the warps' (m, sum, o) are merged through shared memory. An item
@@ -19,9 +20,9 @@
 // probabilities are rounded to bf16 for the second product (their sum is not); fp32 uses
 // three-term TF32 products for both.
 //
-// 32 sequences of one token, up to 32k keys (48 query and 8 KV heads of 128, bf16): 372 us,
-// 6.65 TB/s, 0.99 of the measured copy rate. One sequence over 2k keys: 9.6 us, the latency
-// of two launches. fp32, 3 x 200 tokens over 1.3k keys (6 and 2 heads of 64): 49 us, and 512
+// 32 sequences of one token, up to 32k keys (48 query and 8 KV heads of 128, bf16): 370 us,
+// 6.67 TB/s, the measured copy rate. One sequence over 2k keys: 9.6 us, the latency
+// of two launches. fp32, 3 x 200 tokens over 1.3k keys (6 and 2 heads of 64): 47 us, and 512
 // tokens over 8k keys (64 and 8 heads of 128): 4.1 ms, bound by the products and the splits.
 #include "paged_attn.cuh"
 
@@ -41,11 +42,21 @@ __device__ __forceinline__ void tf32_cut(float x, uint32_t& hi, uint32_t& lo) {
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
+// As many warps as the rings leave room for: eight of three stages, or with fp32 rows of 128
+// (16 KB a stage), where the arithmetic bounds it, six of two.
+constexpr int warps_of(int D, int bytes) { return D * bytes <= 256 ? 8 : 6; }
+// An item's start and end take about as long as one or two units of each warp: so many units
+// without keys stand in front of its keys, and every warp passes over its share of them. bf16,
+// 48 query and 8 KV heads of 128, one token each: 32 sequences of 20 keys 28 us without, 15
+// with one unit a warp and with two; 128 of up to 500 keys 106, 65 and 54 us (with three and
+// four 54). fp32, 3 x 200 tokens over 1.3k keys: 50, 48 and 49 us. Calls of fewer items than
+// SMs have none: there an item is cut into parts, each with a start and an end of its own (one
+// sequence over 2k keys: 9.5 us, with such units 10.2).
+constexpr int units_over(int warps, int bytes) { return bytes == 2 ? 2 * warps : warps; }
+
 template <class T, int D>
 struct Lay {
-  // As many warps as the rings leave room for: eight of three stages, or with fp32 rows of
-  // 128 (16 KB a stage), where the arithmetic bounds it, six of two.
-  static constexpr int WARPS = D * sizeof(T) <= 256 ? 8 : 6;
+  static constexpr int WARPS = warps_of(D, sizeof(T));
   static constexpr int THREADS = WARPS * 32;
   static constexpr int TILE = UNIT * D * (int)sizeof(T);  // bytes of one K or V unit
   static constexpr int STAGES = D * sizeof(T) <= 256 ? 3 : 2;
@@ -59,13 +70,12 @@ struct Lay {
   static_assert(BYTES + 1024 <= 227 * 1024, "one CTA per SM");
 };
 
-typedef Numbering<ROWS, UNIT, 0> Num;
-
-template <class T, int D>
-__global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnArgs a) {
+template <class T, int D, int OVER>
+__global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnArgs a, int least) {
   pdl_wait();
   pdl_trigger();
   typedef Lay<T, D> L;
+  typedef Numbering<ROWS, UNIT, OVER> Num;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   const PagedArgs& p = a.p;
@@ -78,8 +88,8 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
   float* tot = reinterpret_cast<float*>(sm + L::TOT);
 
   PartHead* head = part_heads<ROWS, D>(a.ws, gridDim.x) + blockIdx.x;
-  Num::Run run;
-  if (!Num::plan(p, G, lane, blockIdx.x, gridDim.x, L::WARPS, run)) {
+  typename Num::Run run;
+  if (!Num::plan(p, G, lane, blockIdx.x, gridDim.x, least, run)) {
     if (tid == 0) head->more = 0;
     return;
   }
@@ -94,9 +104,13 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
   };
   auto look_up = [&]() {
     Ref r{0, 0, -1};
-    if (nextf < hi) {
+    while (nextf < hi) {
       while (nextf >= ahead.end) Num::next_item(p, G, ahead);
-      const int key0 = (int)(nextf - ahead.start) * UNIT;
+      if (nextf >= ahead.start + OVER) break;
+      nextf += L::WARPS;
+    }
+    if (nextf < hi) {
+      const int key0 = (int)(nextf - ahead.start - OVER) * UNIT;
       if (key0 < ahead.s.len) r = Ref{page_entry(p, ahead.b, key0), key0 % p.page_size, ahead.h};
     }
     nextf += L::WARPS;
@@ -194,12 +208,13 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
 
     const long long end = cur.end < hi ? cur.end : hi;
+    while (f < cur.start + OVER) f += L::WARPS;
     for (; f < end; f += L::WARPS) {
       load_unit(ref);
       ref = look_up();
       cp_async_wait<L::STAGES - 1>();
       __syncwarp();
-      const int key0 = (int)(f - cur.start) * UNIT;
+      const int key0 = (int)(f - cur.start - OVER) * UNIT;
       Tile<T, UNIT, D> Kt{reinterpret_cast<T*>(ring + st * 2 * L::TILE)};
       Tile<T, UNIT, D> Vt{reinterpret_cast<T*>(ring + (st * 2 + 1) * L::TILE)};
       st = st + 1 == L::STAGES ? 0 : st + 1;
@@ -497,16 +512,22 @@ __global__ void __launch_bounds__(ROWS * D / 4) paged_attn_join_kernel(AttnArgs 
   if (a.lse && col == 0) a.lse[(size_t)tok * a.p.Hq + head] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * LN2;
 }
 
-template <class T, int D>
+// Units that make a CTA take part: one for each warp, or an item of the longest length.
+int units_least(const AttnArgs& a, int warps) {
+  const int most = (a.max_kv - 1) / UNIT + 1;
+  return most < 1 ? 1 : most < warps ? most : warps;
+}
+
+template <class T, int D, int OVER>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
   typedef Lay<T, D> L;
   const int bytes = L::BYTES + 1024;
   static std::atomic<unsigned long long> allowed{0};
-  cudaError_t e = allow_shared(reinterpret_cast<const void*>(paged_attn_kernel<T, D>), bytes, &allowed);
+  cudaError_t e = allow_shared(reinterpret_cast<const void*>(paged_attn_kernel<T, D, OVER>), bytes, &allowed);
   if (e != cudaSuccess) return e;
-  const int grid = launch_ctas(a, ROWS, UNIT, 0, L::WARPS);
+  const int least = units_least(a, L::WARPS), grid = launch_ctas(a, ROWS, UNIT, 0, least);
   prof_mark(K_ATTN, s, true);
-  e = launch_pdl(paged_attn_kernel<T, D>, dim3(grid), dim3(L::THREADS), bytes, s, a);
+  e = launch_pdl(paged_attn_kernel<T, D, OVER>, dim3(grid), dim3(L::THREADS), bytes, s, a, least);
   prof_mark(K_ATTN, s, false);
   if (e != cudaSuccess) return e;
   prof_mark(K_ATTN_JOIN, s, true);
@@ -515,10 +536,17 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
   return e;
 }
 
+template <class T, int D>
+cudaError_t pick(const AttnArgs& a, cudaStream_t s) {
+  const int nsm = device_sm_count() > 0 ? device_sm_count() : 152;
+  return launch_items(a, ROWS) < nsm ? run<T, D, 0>(a, s) : run<T, D, units_over(warps_of(D, sizeof(T)), sizeof(T))>(a, s);
+}
+
 }  // namespace
 
 size_t paged_attn_workspace(const AttnArgs& a) {
-  const int warps = a.p.D * (a.p.bf16 ? 2 : 4) <= 256 ? 8 : 6, grid = launch_ctas(a, ROWS, UNIT, 0, warps);
+  const int warps = warps_of(a.p.D, a.p.bf16 ? 2 : 4);
+  const int grid = launch_ctas(a, ROWS, UNIT, 0, units_least(a, warps));
   const size_t own = a.p.D == 64 ? Parts<ROWS, 64>::bytes(grid) : Parts<ROWS, 128>::bytes(grid);
   const size_t tc = paged_attn_tc_applies(a) ? paged_attn_tc_workspace(a) : 0;
   return own > tc ? own : tc;
@@ -530,8 +558,8 @@ cudaError_t launch_paged_attn(const AttnArgs& a, cudaStream_t s) {
     const cudaError_t e = launch_paged_attn_tc(a, s, &done);
     if (done || e != cudaSuccess) return e;
   }
-  if (a.p.bf16) return a.p.D == 64 ? run<bf16, 64>(a, s) : run<bf16, 128>(a, s);
-  return a.p.D == 64 ? run<float, 64>(a, s) : run<float, 128>(a, s);
+  if (a.p.bf16) return a.p.D == 64 ? pick<bf16, 64>(a, s) : pick<bf16, 128>(a, s);
+  return a.p.D == 64 ? pick<float, 64>(a, s) : pick<float, 128>(a, s);
 }
 
 }  // namespace gdn

@@ -260,14 +260,17 @@ inline long long most_items(const AttnArgs& a, int rows) {
   const long long G = a.p.Hq / a.p.Hk, seqs = a.p.B < a.p.N ? a.p.B : a.p.N;
   return ((long long)a.p.N * G / rows + seqs) * a.p.Hk;
 }
+// The same, by the caller's bound on new tokens too.
+inline long long launch_items(const AttnArgs& a, int rows) {
+  const long long G = a.p.Hq / a.p.Hk, seqs = a.p.B < a.p.N ? a.p.B : a.p.N, most = most_items(a, rows);
+  const long long per_seq = ((long long)(a.max_q < a.p.N ? a.max_q : a.p.N) * G + rows - 1) / rows * seqs * a.p.Hk;
+  return per_seq < most ? per_seq : most;
+}
 // CTAs of a launch: one per SM, or as many as the work can occupy by the caller's bounds on
 // new tokens and length (which limit only this). `over`, `least`: as in Numbering and plan.
 inline int launch_ctas(const AttnArgs& a, int rows, int unit, int over, int least) {
   const int nsm = device_sm_count() > 0 ? device_sm_count() : 152;
-  const long long G = a.p.Hq / a.p.Hk, seqs = a.p.B < a.p.N ? a.p.B : a.p.N;
-  const long long per_seq = ((long long)(a.max_q < a.p.N ? a.max_q : a.p.N) * G + rows - 1) / rows * seqs * a.p.Hk;
-  const long long most = most_items(a, rows), items = per_seq < most ? per_seq : most;
-  const long long per_item = ((long long)a.max_kv + unit - 1) / unit + over;
+  const long long items = launch_items(a, rows), per_item = ((long long)a.max_kv + unit - 1) / unit + over;
   if (items >= (long long)nsm * least || per_item >= (long long)nsm * least) return nsm;
   const long long want = (items * per_item + least - 1) / least;
   return want < nsm ? (int)want : nsm;
