@@ -70,6 +70,11 @@ struct Lay {
   static_assert(BYTES + 1024 <= 227 * 1024, "one CTA per SM");
 };
 
+// What a part's sum and output count for beside the maximum M of all parts. A maximum of
+// -inf alone does not say that a part is empty: maxima pass over NaN, which then stands in
+// the sum and the output, and reaches the row's through the factor 0. Empty is a sum of 0.
+__device__ __forceinline__ float part_factor(float m, float M) { return m == -INFINITY ? 0.f : exp2f(m - M); }
+
 template <class T, int D, int OVER>
 __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnArgs a, int least) {
   pdl_wait();
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
       for (int w = 0; w < L::WARPS; ++w) M = fmaxf(M, sml[w * ROWS + tid]);
 #pragma unroll
       for (int w = 0; w < L::WARPS; ++w)
-        if (sml[w * ROWS + tid] != -INFINITY) lt += sml[(L::WARPS + w) * ROWS + tid] * exp2f(sml[w * ROWS + tid] - M);
+        lt += sml[(L::WARPS + w) * ROWS + tid] * part_factor(sml[w * ROWS + tid], M);
       tot[tid] = M;
       tot[ROWS + tid] = lt;
       if (tid < rows) {
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
           part[ROWS * D + ROWS + tid] = lt;
         } else if (a.lse) {
           const int qr = row0 + tid;
-          a.lse[(size_t)(cur.s.first + qr / G) * p.Hq + cur.h * G + qr % G] = M == -INFINITY ? -INFINITY : (M + log2f(lt)) * LN2;
+          a.lse[(size_t)(cur.s.first + qr / G) * p.Hq + cur.h * G + qr % G] = lt == 0.f ? -INFINITY : (M + log2f(lt)) * LN2;
         }
       }
     }
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
     for (int e = 0; e < 2; ++e) {
       float M = -INFINITY;
       for (int w = 0; w < L::WARPS; ++w) M = fmaxf(M, sml[w * ROWS + g + 8 * e]);
-      fac[e] = m[e] == -INFINITY ? 0.f : exp2f(m[e] - M);
+      fac[e] = part_factor(m[e], M);
     }
     for (int r0 = 0; r0 < rows; r0 += L::MROWS) {
 #pragma unroll
@@ -438,7 +443,7 @@ __global__ void __launch_bounds__(Lay<T, D>::THREADS, 1) paged_attn_kernel(AttnA
         }
         if (whole) {
           const int qr = row0 + r, tok = cur.s.first + qr / G, head_ = cur.h * G + qr % G;
-          const float inv = tot[r] == -INFINITY ? 0.f : 1.f / tot[ROWS + r];
+          const float inv = tot[ROWS + r] == 0.f ? 0.f : 1.f / tot[ROWS + r];
 #pragma unroll
           for (int e = 0; e < 4; ++e) sum[e] *= inv;
           st4(static_cast<T*>(a.out) + tok * a.o_ts + head_ * a.o_hs + col, sum);
@@ -491,25 +496,25 @@ __global__ void __launch_bounds__(ROWS * D / 4) paged_attn_join_kernel(AttnArgs 
 #pragma unroll
     for (int i = 0; i < BATCH; ++i)
       if (q0 + i <= h.more) top = fmaxf(top, m[i]);
-    const float f = M == -INFINITY ? 0.f : exp2f(M - top);
+    const float f = part_factor(M, top);
     M = top;
     l *= f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] *= f;
 #pragma unroll
     for (int i = 0; i < BATCH; ++i)
-      if (q0 + i <= h.more && m[i] != -INFINITY) {
-        const float w = exp2f(m[i] - M);
+      if (q0 + i <= h.more) {
+        const float w = part_factor(m[i], M);
         o[0] += v[i].x * w; o[1] += v[i].y * w; o[2] += v[i].z * w; o[3] += v[i].w * w;
         l += s[i] * w;
       }
   }
   const int G = a.p.Hq / a.p.Hk, qr = h.row0 + r, tok = h.first + qr / G, head = h.h * G + qr % G;
-  const float inv = M == -INFINITY ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] *= inv;
   st4(static_cast<T*>(a.out) + tok * a.o_ts + head * a.o_hs + col, o);
-  if (a.lse && col == 0) a.lse[(size_t)tok * a.p.Hq + head] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * LN2;
+  if (a.lse && col == 0) a.lse[(size_t)tok * a.p.Hq + head] = l == 0.f ? -INFINITY : (M + log2f(l)) * LN2;
 }
 
 // Units that make a CTA take part: one for each warp, or an item of the longest length.

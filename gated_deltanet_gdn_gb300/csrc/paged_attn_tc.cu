@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
       }
       const bool whole = it.start >= lo && it.end <= hi;
-      bool live = row < g.rows, none = need == 0 || m == -INFINITY;
+      bool live = row < g.rows, none = need == 0 || l == 0.f;  // (not by the maximum, which passes over NaN)
       if (g.alone) {
         if (g.need[1] > 0) {
           // merge the second row tile into the first, 32 columns at a time through shared memory
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const float f = m == -INFINITY ? 0.f : ex2(m - M), of = om == -INFINITY ? 0.f : ex2(om - M);
           l = l * f + ml[(3 - w) * HALF + r] * of;
           m = M;
-          none = M == -INFINITY;
+          none = l == 0.f;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             float* at = stage + (i & 1) * HALF * 32 + r * 32;  // chunks of four columns, swizzled by row
@@ -769,9 +769,9 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_attn_tc_join_kernel(Att
 #pragma unroll 4
   for (int q = 0; q <= h.more; ++q) {
     const float m = part[ROWS * D + row];
-    const bool some = m != -INFINITY;  // a part without keys has no o
-    const float f = some ? ex2(m - M) : 0.f;
-    l += some ? part[ROWS * D + ROWS + row] * f : 0.f;
+    const float lp = part[ROWS * D + ROWS + row], f = m == -INFINITY ? 0.f : ex2(m - M);
+    const bool some = lp != 0.f;  // a part without keys has no o; NaN counts, whatever its maximum
+    l += lp * f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float4 v = *reinterpret_cast<const float4*>(part + ((size_t)(c40 + i * JOIN_WARPS) * ROWS + row) * 4);
@@ -782,14 +782,14 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_attn_tc_join_kernel(Att
     part = rest + q * STEP;
   }
   const int G = a.p.Hq / a.p.Hk, q = h.row0 + row, tok = h.first + q / G, head = h.h * G + q % G;
-  const float inv = M == -INFINITY ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   bf16* dst = static_cast<bf16*>(a.out) + tok * a.o_ts + head * a.o_hs;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float v[4] = {o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv};
     st4(dst + (c40 + i * JOIN_WARPS) * 4, v);
   }
-  if (a.lse && c40 == 0) a.lse[(size_t)tok * a.p.Hq + head] = M == -INFINITY ? -INFINITY : (M + log2f(l)) * LN2;
+  if (a.lse && c40 == 0) a.lse[(size_t)tok * a.p.Hq + head] = l == 0.f ? -INFINITY : (M + log2f(l)) * LN2;
 }
 
 // [pages][heads][rows][D] bf16 with the cache's strides; box: 64 channels of `box` rows.
