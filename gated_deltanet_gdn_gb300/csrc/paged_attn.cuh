@@ -209,11 +209,12 @@ struct Numbering {
   }
   // Item `idx` as a run of its own: the KV heads of a run of rows side by side, the items of
   // a sequence from its last, the one with the most keys, and the sequences likewise. False
-  // when there are fewer items.
+  // when there are fewer items. Item 0's caller reports the lengths of all sequences.
   static __device__ __forceinline__ bool pick(const PagedArgs& p, int G, int lane, int idx, Run& r) {
     int i = idx / p.Hk;
     Item& it = r.first;
     it.h = idx % p.Hk;
+    bool found = false;
     for (int b0 = p.B - 1; b0 >= 0; b0 -= 32) {
       const int b = b0 - lane;
       const Seq s = b >= 0 ? load_seq(p, b, idx == 0) : Seq{0, 0, 0};
@@ -224,7 +225,7 @@ struct Numbering {
         const int o = __shfl_up_sync(0xffffffffu, inc, off);
         if (lane >= off) inc += o;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, inc > i);
+      const unsigned hit = __ballot_sync(0xffffffffu, !found && inc > i);
       if (hit) {
         const int l = __ffs(hit) - 1;
         it.b = b0 - l;
@@ -233,11 +234,12 @@ struct Numbering {
         it.start = r.lo = 0;
         it.end = r.hi = r.total = item_units(it.s, G, it.i);
         r.ncta = 1;
-        return true;
+        found = true;
+        if (idx != 0) break;
       }
       i -= __shfl_sync(0xffffffffu, inc, 31);
     }
-    return false;
+    return found;
   }
   // CTAs that take part: enough units for each to have `least`.
   static __device__ __forceinline__ int active_ctas(long long total, int grid, int least) {
