@@ -416,10 +416,12 @@ __global__ void __launch_bounds__(SUB ? SUB_THREADS : NORM_THREADS_MAX)
     for (int i = 0; i < NV; ++i) {
       const int c = (at.lane + i * at.lanes) * VEC;
       if (!live || c >= a.C) continue;
-      float xv[VEC];
-      in.x[i].get(xv);
+      if (wpost) {  // (0 x is not 0 when x is not finite)
+        float xv[VEC];
+        in.x[i].get(xv);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) u[i][e] = r1 * (u[i][e] - xv[e] * c1);
+        for (int e = 0; e < VEC; ++e) u[i][e] = r1 * (u[i][e] - xv[e] * c1);
+      }
       Raw<T, VEC> raw;
       raw.set(u[i]);
       raw.store(static_cast<T*>(a.dx) + j * a.C + c);
@@ -691,13 +693,12 @@ __global__ void __launch_bounds__(SUB_THREADS, 2) block_norm_head_bwd_kernel(Nor
       s1 = fma2(D[e], xv[e], s1);
     }
     if (GATE && store && a.dgate) *reinterpret_cast<uint4*>(static_cast<T*>(a.dgate) + out) = rounded(t, kind);
-    f2 c1 = zero2;
-    if (post) {
+    if (post) {  // without it dx is D (0 x is not 0 when x is not finite)
       const float m = -head_sum<SUB>(s1) * invC * r1 * r1 * r1;
-      c1 = pk(m, m);
-    }
+      const f2 c1 = pk(m, m);
 #pragma unroll
-    for (int e = 0; e < NP; ++e) D[e] = fma2(xv[e], c1, mul2(D[e], r1p));
+      for (int e = 0; e < NP; ++e) D[e] = fma2(xv[e], c1, mul2(D[e], r1p));
+    }
     if (store) *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + out) = rounded(D, kind);
   };
   fetch(at.row, row0);
@@ -1092,6 +1093,10 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), stream_ctas(NV, MAX
         fetch(0, c, x);
 #pragma unroll
         for (int e = 0; e < NP; ++e) x[e] = fma2(x[e], c1, mul2(h[i][e], r1p));
+        if (!FULL && !post) {  // 0 x is not 0 when x is not finite (and with FULL, h and all of its row are not)
+#pragma unroll
+          for (int e = 0; e < NP; ++e) x[e] = h[i][e];
+        }
         if (in_row) *reinterpret_cast<uint4*>(static_cast<T*>(a.dx) + row * a.C + c) = rounded(x, kind);
       }
       release();
