@@ -88,25 +88,40 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// act(g) and act'(g). The hardware's approximate exponential and reciprocal are off by
-// |g| 2^-24 and 2^-23; with the exact ones the arithmetic, not memory, bounds the kernels.
-// silu' = s (1 + g (1 - s)) takes 1 - s as it is (an error of |g| 2^-24 beside the 1);
-// the sigmoid's s (1 - s) takes both sides from exp(-|g|), so that 1 - s keeps its relative
-// accuracy where s is near 1. Neither form overflows: exp(-g) = inf gives s = 0.
-template <int VEC>
+// exp(-g) and 1 / x for the gates of rows of type T. bf16 takes the hardware's approximate
+// exponential and reciprocal: relative errors of |g| 2^-24 (the rounded argument) + 2^-22 and
+// 2^-23, far below bf16's own 2^-8, and with expf the arithmetic, not memory, bounds the
+// kernels. fp32 keeps fp32's accuracy, with twice the bytes per element to cover it: expf, and
+// the reciprocal with its subnormals, both within one unit in the last place (4,096 rows of
+// 6,144, both directions: 249 us, as with bf16's forms; with a division 271).
+template <class T>
+__device__ __forceinline__ float exp_neg(float g) {
+  if constexpr (sizeof(T) == 2) return ex2_approx(g * -1.4426950408889634f);
+  else return expf(-g);
+}
+template <class T>
+__device__ __forceinline__ float inverse(float x) {
+  if constexpr (sizeof(T) == 2) return rcp_approx(x);
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// act(g) and act'(g). silu' = s (1 + g (1 - s)) takes 1 - s as it is (an error of |g| 2^-24
+// beside the 1); the sigmoid's s (1 - s) takes both sides from exp(-|g|), so that 1 - s keeps its
+// relative accuracy where s is near 1. Neither form overflows: exp(-g) = inf gives s = 0.
+template <class T, int VEC>
 __device__ __forceinline__ void activation(const float (&g)[VEC], int sigmoid, float (&a)[VEC], float (&d)[VEC]) {
-  constexpr float L2E = 1.4426950408889634f;
   if (!sigmoid) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const float s = rcp_approx(1.f + ex2_approx(g[e] * -L2E));
+      const float s = inverse<T>(1.f + exp_neg<T>(g[e]));
       a[e] = g[e] * s;
       d[e] = s * fmaf(g[e], 1.f - s, 1.f);
     }
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const float x = ex2_approx(fabsf(g[e]) * -L2E), big = rcp_approx(1.f + x), small = x * big;
+      const float x = exp_neg<T>(fabsf(g[e])), big = inverse<T>(1.f + x), small = x * big;
       a[e] = g[e] >= 0.f ? big : small;
       d[e] = big * small;
     }
@@ -209,7 +224,7 @@ __global__ void __launch_bounds__(SUB ? SUB_THREADS : NORM_THREADS_MAX)
       if (gate) {
         float ac[VEC], ad[VEC];
         in.gate[i].get(w);
-        activation<VEC>(w, a.sigmoid, ac, ad);
+        activation<T, VEC>(w, a.sigmoid, ac, ad);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[i][e] *= ac[e];
       }
@@ -325,7 +340,7 @@ __global__ void __launch_bounds__(SUB ? SUB_THREADS : NORM_THREADS_MAX)
       if (gate) {
         float w[VEC];
         in.gate[i].get(w);
-        activation<VEC>(w, a.sigmoid, ac, ad);
+        activation<T, VEC>(w, a.sigmoid, ac, ad);
       }
       if (rscale) {
         raw.load(rscale + c);
@@ -519,13 +534,20 @@ __device__ __forceinline__ uint4 rounded(const f2 (&x)[2], const float*) {
 // e = exp(-g), s = 1 / (1 + e) and 1 - s = e s (which keeps its accuracy; inf 0 of a
 // large -g is 1),
 //   silu:  g s, s (1 + g (1 - s))        sigmoid:  s, s (0 + 1 (1 - s))
-__device__ __forceinline__ void activation2(f2 g, bool sigmoid, f2& a, f2& d) {
+template <class T>
+__device__ __forceinline__ void activation2(f2 g, bool sigmoid, f2& a, f2& d, const T*) {
   const f2 one = pk(1.f, 1.f);
   float t0, t1;
-  unpk(mul2(g, pk(-1.4426950408889634f, -1.4426950408889634f)), t0, t1);
-  const f2 e = pk(ex2_approx(t0), ex2_approx(t1));
+  f2 e;  // exp(-g); bf16's product with log2 e stays packed
+  if constexpr (sizeof(T) == 2) {
+    unpk(mul2(g, pk(-1.4426950408889634f, -1.4426950408889634f)), t0, t1);
+    e = pk(ex2_approx(t0), ex2_approx(t1));
+  } else {
+    unpk(g, t0, t1);
+    e = pk(exp_neg<T>(t0), exp_neg<T>(t1));
+  }
   unpk(add2(e, one), t0, t1);
-  const f2 s = pk(rcp_approx(t0), rcp_approx(t1));
+  const f2 s = pk(inverse<T>(t0), inverse<T>(t1));
   unpk(mul2(e, s), t0, t1);
   const f2 rest = pk(fminf(t0, 1.f), fminf(t1, 1.f));
   const f2 f = sigmoid ? one : g;
@@ -608,7 +630,7 @@ __global__ void __launch_bounds__(SUB_THREADS) block_norm_head_fwd_kernel(NormAr
       v[e] = mul2(mul2(v[e], r1p), w[e]);
       if (GATE) {
         f2 ac, ad;
-        activation2(t[e], a.sigmoid, ac, ad);
+        activation2(t[e], a.sigmoid, ac, ad, kind);
         v[e] = mul2(v[e], ac);
       }
     }
@@ -684,7 +706,7 @@ __global__ void __launch_bounds__(SUB_THREADS, 2) block_norm_head_bwd_kernel(Nor
       const f2 xr = mul2(xv[e], r1p);
       if (GATE) {
         f2 ac, ad;
-        activation2(t[e], a.sigmoid, ac, ad);
+        activation2(t[e], a.sigmoid, ac, ad, kind);
         t[e] = mul2(mul2(D[e], mul2(xr, w[e])), ad);  // dgate
         D[e] = mul2(D[e], ac);
       }
@@ -916,7 +938,7 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), stream_ctas(NV, MAX
 #pragma unroll
           for (int e = 0; e < NP; ++e) {
             f2 ac, ad;
-            activation2(w[e], a.sigmoid, ac, ad);
+            activation2(w[e], a.sigmoid, ac, ad, kind);
             h[i][e] = mul2(h[i][e], ac);
           }
         }
@@ -977,7 +999,7 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), stream_ctas(NV, MAX
 #pragma unroll
           for (int e = 0; e < NP; ++e) {
             f2 ad;
-            activation2(w[e], a.sigmoid, ac[i][e], ad);
+            activation2(w[e], a.sigmoid, ac[i][e], ad, kind);
             if (!AGAIN) nd[i][e] = mul2(n[e], ad);
             n[e] = mul2(n[e], ac[i][e]);  // m
           }
@@ -1040,7 +1062,7 @@ __global__ void __launch_bounds__(MAXT + (SPLIT ? 128 : 32), stream_ctas(NV, MAX
 #pragma unroll
           for (int e = 0; e < NP; ++e) {
             f2 ad;
-            activation2(gate[e], a.sigmoid, ac[i][e], ad);
+            activation2(gate[e], a.sigmoid, ac[i][e], ad, kind);
             nd[i][e] = mul2(mul2(mul2(x[e], r1p), w[e]), ad);
           }
         }

@@ -377,7 +377,9 @@ int gdn_paged_attn(const gdn_paged_dims* dims, const gdn_paged_cache* cache, con
  *     y = h / sqrt(mean(h^2) + eps) * w_pre         only with w_pre
  * With x the output of the rule per head (G = H, C = Dv), w_post and gate this is
  * the gated output norm; with G = 1, all parts, the step between two blocks.
- * Arithmetic is float32; y is formed from h before h is rounded.
+ * Arithmetic is float32, with functions accurate to one unit in the last place; of
+ * bf16 rows the gate takes the hardware's approximate exponential and reciprocal
+ * (relative error |gate| 2^-24 + 2^-21). y is formed from h before h is rounded.
  *   x, gate, residual, dh, dy   [R, G, C], any row and group strides (elements)
  *   w_post, res_scale, w_pre    [C]
  *   h, y, dx, dgate, dresidual  [R, G, C] contiguous
