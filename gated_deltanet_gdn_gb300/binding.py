@@ -510,6 +510,7 @@ class BlockNorm(torch.autograd.Function):
         return h, y
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dh, dy):
         x, gate, residual, w_post, res_scale, w_pre, stats = ctx.saved_tensors
         g = gdn_block_norm_bwd(x, stats, None if dh is None else dh.contiguous(),
@@ -520,5 +521,5 @@ class BlockNorm(torch.autograd.Function):
 
 def block_norm(x, *, gate=None, residual=None, w_post=None, res_scale=None, w_pre=None, eps: float = 1e-6,
                flags: int = 0):
-    """(h, y) of gdn_block_norm_fwd, differentiable through autograd (y is None without w_pre)."""
+    """(h, y) of gdn_block_norm_fwd, differentiable once through autograd (y is None without w_pre)."""
     return BlockNorm.apply(x, gate, residual, w_post, res_scale, w_pre, float(eps), int(flags))
