@@ -507,16 +507,21 @@ class BlockNorm(torch.autograd.Function):
                                          w_pre=w_pre, eps=eps, flags=flags)
         ctx.save_for_backward(x, gate, residual, w_post, res_scale, w_pre, stats)
         ctx.eps, ctx.flags = eps, flags
+        ctx.set_materialize_grads(False)  # an unused output's gradient is None, not zeros to be read
         return h, y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dh, dy):
+        if dh is None and dy is None:
+            return (None,) * 8
         x, gate, residual, w_post, res_scale, w_pre, stats = ctx.saved_tensors
+        # without dy the norm before the next block is left out: dh passes it by, its weight gets zeros
         g = gdn_block_norm_bwd(x, stats, None if dh is None else dh.contiguous(),
-                               None if dy is None else dy.contiguous(), gate=gate, residual=residual,
-                               w_post=w_post, res_scale=res_scale, w_pre=w_pre, eps=ctx.eps, flags=ctx.flags)
-        return g["dx"], g["dgate"], g["dresidual"], g["dw_post"], g["dres_scale"], g["dw_pre"], None, None
+                               None if dy is None else dy.contiguous(), gate=gate, residual=residual, w_post=w_post,
+                               res_scale=res_scale, w_pre=None if dy is None else w_pre, eps=ctx.eps, flags=ctx.flags)
+        dw_pre = torch.zeros_like(w_pre) if dy is None and w_pre is not None else g["dw_pre"]
+        return g["dx"], g["dgate"], g["dresidual"], g["dw_post"], g["dres_scale"], dw_pre, None, None
 
 
 def block_norm(x, *, gate=None, residual=None, w_post=None, res_scale=None, w_pre=None, eps: float = 1e-6,
