@@ -505,8 +505,9 @@ class BlockNorm(torch.autograd.Function):
     def forward(ctx, x, gate, residual, w_post, res_scale, w_pre, eps, flags):
         h, y, stats = gdn_block_norm_fwd(x, gate=gate, residual=residual, w_post=w_post, res_scale=res_scale,
                                          w_pre=w_pre, eps=eps, flags=flags)
-        ctx.save_for_backward(x, gate, residual, w_post, res_scale, w_pre, stats)
-        ctx.eps, ctx.flags = eps, flags
+        # the residual's values are read only where the norm before the next block is
+        ctx.save_for_backward(x, gate, residual if w_pre is not None else None, w_post, res_scale, w_pre, stats)
+        ctx.eps, ctx.flags, ctx.has_residual = eps, flags, residual is not None
         ctx.set_materialize_grads(False)  # an unused output's gradient is None, not zeros to be read
         return h, y
 
@@ -521,7 +522,8 @@ class BlockNorm(torch.autograd.Function):
                                None if dy is None else dy.contiguous(), gate=gate, residual=residual, w_post=w_post,
                                res_scale=res_scale, w_pre=None if dy is None else w_pre, eps=ctx.eps, flags=ctx.flags)
         dw_pre = torch.zeros_like(w_pre) if dy is None and w_pre is not None else g["dw_pre"]
-        return g["dx"], g["dgate"], g["dresidual"], g["dw_post"], g["dres_scale"], dw_pre, None, None
+        dresidual = dh if residual is None and ctx.has_residual else g["dresidual"]
+        return g["dx"], g["dgate"], dresidual, g["dw_post"], g["dres_scale"], dw_pre, None, None
 
 
 def block_norm(x, *, gate=None, residual=None, w_post=None, res_scale=None, w_pre=None, eps: float = 1e-6,

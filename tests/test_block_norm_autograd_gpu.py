@@ -1,4 +1,5 @@
-"""block_norm under autograd: second derivatives are refused; outputs that a loss does not use."""
+"""block_norm under autograd: second derivatives are refused, outputs that a loss does not use, what is kept
+for the backward."""
 import pytest
 import torch
 
@@ -63,3 +64,23 @@ def test_neither_output_used_or_no_norm_before():
     ref = formulas(p, dh)
     for k, g in zip(d, got):
         assert float((g.double().cpu() - ref[NAMES[k]]).norm() / ref[NAMES[k]].norm()) <= 2.0 ** -16, k
+
+
+@pytest.mark.parametrize("pre", [False, True])
+def test_the_residual_is_kept_only_where_its_values_are_read(pre):
+    """Without a norm before the next block the residual's gradient is dh itself."""
+    p, dh, dy = make((4096, 1, 1024), "f32", dict(FULL, pre=pre), seed=4)
+    d = _leaves(p)
+    leaf = d.pop("residual")
+    residual = leaf * 1.0
+    size = residual.nbytes
+    h, y = gdn.block_norm(d["x"], residual=residual, **{k: v for k, v in d.items() if k != "x"}, eps=EPS)
+    before = torch.cuda.memory_allocated()
+    del residual
+    freed = before - torch.cuda.memory_allocated()
+    assert freed == (0 if pre else size)
+    outs, gs = ([h, y], [dh.cuda(), dy.cuda()]) if pre else ([h], [dh.cuda()])
+    got = torch.autograd.grad(outs, [leaf, d["x"]], gs)
+    ref, mag = formulas(p, dh, dy), formulas(p, dh, dy, size=True)
+    for g, n in zip(got, ("dresidual", "dx")):
+        assert bool(((g.double().cpu() - ref[n]).abs() <= UNIT["f32"] * ref[n].abs() + 2.0 ** -16 * mag[n] + 1e-30).all()), n
