@@ -393,7 +393,8 @@ def gdn_kv_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, *, q=
                   sin=None, flags: int = 0) -> Optional[torch.Tensor]:
     """Store packed new tokens' k, v [N, Hk, D] in the paged cache [pages, Hk, page size, D], in place;
     with cos, sin (fp32 [positions, rot / 2]) k is rotated by its position, and so is q [N, Hq, D].
-    kv_lens counts the new tokens. Returns the rotated q (q_out, which may be q), or None without q."""
+    kv_lens counts the new tokens. Returns the rotated q (q_out, which may be q), or None without q.
+    Serving only: with gradients enabled, tensors that require them are refused."""
     return (_ext or _compiled()).kv_append(k, v, k_cache, v_cache, page_table, cu_seqlens, kv_lens, q, q_out, cos,
                                            sin, flags)
 
@@ -408,7 +409,8 @@ def gdn_paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, scale: 
     """Causal attention of the packed new tokens q [N, Hq, D] over the paged cache their keys were
     appended to. max_q, max_kv: the caller's bounds on new tokens and length of one sequence (they
     choose the kernel and its split; without them the largest possible are taken). lse: optional fp32
-    [N, Hq] output, the log of each row's softmax sum. Returns out [N, Hq, D]."""
+    [N, Hq] output, the log of each row's softmax sum. Returns out [N, Hq, D]. Serving only: with
+    gradients enabled, tensors that require them are refused."""
     return (_ext or _compiled()).paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, scale, max_q,
                                             max_kv, out, lse, workspace)
 

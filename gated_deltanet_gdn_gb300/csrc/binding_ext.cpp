@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -92,6 +93,13 @@ long long step(const Tensor& t, int64_t d) { return t.size(d) == 1 ? 0 : t.strid
 void unit_channels(const Tensor& t, const char* name) {
   if (t.numel() > 0 && t.size(-1) != 1 && t.stride(-1) != 1)
     refuse(name, std::string(name) + " must have contiguous channels");
+}
+
+// The paged calls have no backward: a gradient that would be lost without a word is refused.
+void no_gradient(const Tensor* t, const char* name) {
+  if (t && c10::GradMode::is_enabled() && t->requires_grad())
+    refuse(name, std::string(name) + " requires a gradient, and this call has no backward: call it under torch.no_grad() or detach " + name,
+           GDN_ERR_UNSUPPORTED);
 }
 
 gdn_tokens tokens(const Tensor& t, at::IntArrayRef shape, const Tensor& like, const char* name) {
@@ -195,6 +203,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor &table = tensor(a[4], "page_table"), &cu = tensor(a[5], "cu_seqlens"), &lens = tensor(a[6], "kv_lens");
     const Tensor *q = optional_tensor(a[7], "q"), *qo = optional_tensor(a[8], "q_out"),
                  *cos = optional_tensor(a[9], "cos"), *sin = optional_tensor(a[10], "sin");
+    no_gradient(&k, "k"); no_gradient(&v, "v"); no_gradient(&kc, "k_cache"); no_gradient(&vc, "v_cache");
+    no_gradient(q, "q"); no_gradient(qo, "q_out"); no_gradient(cos, "cos"); no_gradient(sin, "sin");
     if (q && q->dim() != 3) refuse("q", "q must be [N, heads, D]");
     gdn_paged_dims d;
     gdn_paged_cache c;
@@ -234,6 +244,9 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("paged_attn", a, n, 12, [&]() -> PyObject* {
     const Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache");
     const Tensor &table = tensor(a[3], "page_table"), &cu = tensor(a[4], "cu_seqlens"), &lens = tensor(a[5], "kv_lens");
+    const Tensor *out = optional_tensor(a[9], "out"), *lse = optional_tensor(a[10], "lse");
+    no_gradient(&q, "q"); no_gradient(&kc, "k_cache"); no_gradient(&vc, "v_cache"); no_gradient(out, "out");
+    no_gradient(lse, "lse");
     if (q.dim() != 3) refuse("q", "q must be [N, heads, D]");
     gdn_paged_dims d;
     gdn_paged_cache c;
@@ -244,7 +257,6 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long long cap = (long long)d.max_pages * d.page_size;
     const int max_q = a[7] == Py_None ? (d.N > 0 ? d.N : 1) : to_int(integer(a[7]), "max_q");
     const int max_kv = a[8] == Py_None ? (int)(cap < 1 ? 1 : cap > INT_MAX ? INT_MAX : cap) : to_int(integer(a[8]), "max_kv");
-    const Tensor *out = optional_tensor(a[9], "out"), *lse = optional_tensor(a[10], "lse");
     Tensor own;
     c10::DataPtr ws;
     if (!out) {

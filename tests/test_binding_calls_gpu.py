@@ -1,0 +1,51 @@
+"""The compiled calls as a Python program meets them: gradients they cannot give."""
+import pytest
+import torch
+
+import gated_deltanet_gdn_gb300 as gdn
+
+from paged_reference import Paged
+
+pytestmark = pytest.mark.gpu
+
+
+def _setup():
+    c = Paged([3, 1], [20, 40], 4, 2, 64, 16, "bf16", seed=41)
+    q, k, v = (c.normal(4, h, 64).cuda() for h in (4, 2, 2))
+    return q, k, v, c.cuda()
+
+
+@pytest.mark.parametrize("name", ["q", "k_cache", "v_cache", "out"])
+def test_attention_refuses_to_lose_a_gradient(name):
+    q, _, _, (kc, vc, *where) = _setup()
+    t = dict(q=q, k_cache=kc, v_cache=vc, out=torch.empty_like(q))
+
+    def call():
+        return gdn.gdn_paged_attn(t["q"], t["k_cache"], t["v_cache"], *where, 0.1, max_q=3, max_kv=40, out=t["out"])
+
+    plain = call().clone()
+    t[name].requires_grad_()
+    with pytest.raises(gdn.GdnError, match=name):
+        call()
+    with torch.no_grad():
+        assert torch.equal(call(), plain)
+    with torch.inference_mode():
+        assert torch.equal(call(), plain)
+    t[name] = t[name].detach()
+    assert torch.equal(call(), plain)
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v", "k_cache", "v_cache", "q_out"])
+def test_append_refuses_to_lose_a_gradient(name):
+    q, k, v, (kc, vc, *where) = _setup()
+    t = dict(q=q, k=k, v=v, k_cache=kc, v_cache=vc, q_out=torch.empty_like(q))
+
+    def call():
+        return gdn.gdn_kv_append(t["k"], t["v"], t["k_cache"], t["v_cache"], *where, q=t["q"], q_out=t["q_out"])
+
+    plain = call().clone()
+    t[name].requires_grad_()
+    with pytest.raises(gdn.GdnError, match=name):
+        call()
+    with torch.no_grad():
+        assert torch.equal(call(), plain)
