@@ -105,8 +105,8 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
     global _lib
     with _lock:
         if _lib is None:
-            if build_if_needed and _build.is_stale():
-                _build.build()
+            if build_if_needed and _build.lib_is_stale():
+                _build.build_lib()
             if not os.path.exists(_build.LIB_PATH):
                 raise RuntimeError(f"libgdn.so not found at {_build.LIB_PATH}; run the package build first")
             lib = ctypes.CDLL(_build.LIB_PATH)
@@ -165,11 +165,14 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
 
 
 def _compiled():
-    """The compiled argument marshalling of the paged cache and block norm calls (csrc/binding_ext.cpp)."""
+    """The compiled argument marshalling of the paged cache and block norm calls (csrc/binding_ext.cpp), built
+    first when missing or stale."""
     global _ext
     load()
     with _lock:
         if _ext is None:
+            if _build.ext_is_stale():
+                _build.build_ext()
             spec = importlib.util.spec_from_file_location("_gdn_ext", _build.EXT_PATH)
             ext = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(ext)

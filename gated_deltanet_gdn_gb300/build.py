@@ -3,8 +3,8 @@
 Each .cu translation unit compiles in parallel to an object file under
 ``_build/``; the objects link into ``libgdn.so`` next to this file (in-tree,
 never installed). The binding's extension (``binding_ext.cpp``, the host compiler,
-PyTorch's headers) compiles beside them and links against it. Only one ``-gencode``
-(compute_103a -> sm_103a) is built.
+PyTorch's headers) compiles beside them and links against it; the library does not need it.
+Only one ``-gencode`` (compute_103a -> sm_103a) is built.
 """
 from __future__ import annotations
 
@@ -37,18 +37,25 @@ def nvcc_path() -> str:
     return cand
 
 
-def _inputs() -> List[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
-    files.append(os.path.join(INCLUDE, "gdn.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+def _older(path: str, suffixes) -> bool:
+    """Whether `path` is missing, or older than the sources with these suffixes, the header or this file."""
+    if not os.path.exists(path):
+        return True
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(suffixes)]
+    t = os.path.getmtime(path)
+    return any(os.path.getmtime(f) > t for f in files + [os.path.join(INCLUDE, "gdn.h"), os.path.abspath(__file__)])
+
+
+def lib_is_stale() -> bool:
+    return _older(LIB_PATH, (".cu", ".cuh", ".h"))
+
+
+def ext_is_stale() -> bool:
+    return _older(EXT_PATH, (".cpp",))
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(EXT_PATH):
-        return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(EXT_PATH))
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    return lib_is_stale() or ext_is_stale()
 
 
 def ext_commands(out: str) -> List[List[str]]:
@@ -78,9 +85,9 @@ def _run(what: str, cmd: List[str], verbose: bool) -> None:
         print(r.stdout, r.stderr, flush=True)
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags: Optional[List[str]] = None) -> str:
-    """Compile and link libgdn.so and the binding's extension if missing or older than their sources."""
-    if not force and not is_stale():
+def build_lib(force: bool = False, verbose: bool = False, extra_flags: Optional[List[str]] = None) -> str:
+    """Compile and link libgdn.so if missing or older than its sources."""
+    if not force and not lib_is_stale():
         return LIB_PATH
     nvcc = nvcc_path()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -91,16 +98,41 @@ def build(force: bool = False, verbose: bool = False, extra_flags: Optional[List
         _run(f"nvcc on {src}", [nvcc, *flags, "-c", os.path.join(CSRC, src), "-o", obj], verbose)
         return obj
 
-    tmp, ext_tmp = (f"{p}.{os.getpid()}.tmp" for p in (LIB_PATH, EXT_PATH))
-    ext_compile, ext_link = ext_commands(ext_tmp)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        ext = ex.submit(_run, "compiling binding_ext.cpp", ext_compile, verbose)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        ext.result()
+    tmp = f"{LIB_PATH}.{os.getpid()}.tmp"
     _run("link", [nvcc, *ARCH, "-shared", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB_PATH)
-    _run("link of the binding's extension", ext_link, verbose)
-    os.replace(ext_tmp, EXT_PATH)
+    return LIB_PATH
+
+
+def _compile_ext(verbose: bool) -> List[str]:
+    """Compile the binding's extension; its link command."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    compile_, link = ext_commands(f"{EXT_PATH}.{os.getpid()}.tmp")
+    _run("compiling binding_ext.cpp", compile_, verbose)
+    return link
+
+
+def _link_ext(link: List[str], verbose: bool) -> str:
+    _run("link of the binding's extension", link, verbose)
+    os.replace(link[link.index("-o") + 1], EXT_PATH)
+    return EXT_PATH
+
+
+def build_ext(verbose: bool = False) -> str:
+    """Compile the binding's extension and link it against libgdn.so."""
+    return _link_ext(_compile_ext(verbose), verbose)
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags: Optional[List[str]] = None) -> str:
+    """Bring libgdn.so and the binding's extension up to date, side by side. The library does not need the
+    extension (Python's and PyTorch's headers): where that fails, the error comes after the library is in place."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        ext = ex.submit(_compile_ext, verbose) if force or ext_is_stale() else None
+        build_lib(force, verbose, extra_flags)
+        if ext is not None:
+            _link_ext(ext.result(), verbose)
     return LIB_PATH
 
 
