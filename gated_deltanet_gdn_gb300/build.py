@@ -12,6 +12,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 from typing import List, Optional
 
@@ -50,8 +51,23 @@ def lib_is_stale() -> bool:
     return _older(LIB_PATH, (".cu", ".cuh", ".h"))
 
 
+def _ext_stamp() -> str:
+    return os.path.join(BUILD_DIR, "binding_ext.stamp")
+
+
+def _ext_against() -> str:
+    """What the extension's binary interface depends on beside its source."""
+    import torch
+
+    return f"Python {sys.version}, PyTorch {torch.__version__}"
+
+
 def ext_is_stale() -> bool:
-    return _older(EXT_PATH, (".cpp",))
+    """Also when it was compiled against another Python or PyTorch."""
+    if _older(EXT_PATH, (".cpp",)) or not os.path.exists(_ext_stamp()):
+        return True
+    with open(_ext_stamp()) as f:
+        return f.read() != _ext_against()
 
 
 def is_stale() -> bool:
@@ -117,6 +133,8 @@ def _compile_ext(verbose: bool) -> List[str]:
 def _link_ext(link: List[str], verbose: bool) -> str:
     _run("link of the binding's extension", link, verbose)
     os.replace(link[link.index("-o") + 1], EXT_PATH)
+    with open(_ext_stamp(), "w") as f:
+        f.write(_ext_against())
     return EXT_PATH
 
 
@@ -137,6 +155,4 @@ def build(force: bool = False, verbose: bool = False, extra_flags: Optional[List
 
 
 if __name__ == "__main__":
-    import sys
-
     print(build(force="--force" in sys.argv, verbose=True))

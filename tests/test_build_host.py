@@ -50,3 +50,24 @@ def test_the_rule_loads_without_the_extension(monkeypatch):
     assert binding.gdn_version() == 100
     with pytest.raises(RuntimeError, match="Python.h"):
         binding.gdn_block_norm_fwd(None)
+
+
+def test_another_pytorch_or_python_makes_the_extension_stale(tree, monkeypatch):
+    """The extension is compiled against their binary interfaces."""
+    import sys
+
+    import torch
+
+    b.build()
+    assert not b.ext_is_stale()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", torch.__version__ + ".other")
+        assert b.ext_is_stale() and not b.lib_is_stale()
+        b.build()
+        assert not b.ext_is_stale()
+    assert b.ext_is_stale()
+    b.build()
+    with monkeypatch.context() as m:
+        m.setattr(sys, "version", "3.99 " + sys.version)
+        assert b.ext_is_stale()
+    assert not b.is_stale()
