@@ -46,6 +46,15 @@ std::string show(at::IntArrayRef v) {
   return s + "]";
 }
 
+// Other Python threads run while a call allocates and launches, which waits when the launch
+// queue or the memory is full.
+struct NoGil {
+  PyThreadState* state = PyEval_SaveThread();
+  NoGil() = default;
+  NoGil(const NoGil&) = delete;
+  ~NoGil() { PyEval_RestoreThread(state); }
+};
+
 struct NotTensor {};
 const Tensor* optional_tensor(PyObject* o, const char* name) {
   if (o == Py_None) return nullptr;
@@ -161,8 +170,8 @@ Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, c10::Device dev) {
 }
 
 // Scratch of at least `need` bytes on the current device: the caller's, or new.
-void* scratch(PyObject* given, size_t need, const Tensor& like, c10::DataPtr* own) {
-  if (const Tensor* w = optional_tensor(given, "workspace")) {
+void* scratch(const Tensor* w, size_t need, const Tensor& like, c10::DataPtr* own) {
+  if (w) {
     on_device(*w, like.device(), "workspace");
     if (!w->is_contiguous() || w->nbytes() < need)
       refuse("workspace", "workspace must be contiguous and hold " + std::to_string(need) + " bytes");
@@ -214,11 +223,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor own;
     if (q) {
       qt = tokens(*q, {d.N, d.Hq, d.D}, kc, "q");
-      if (!qo) {
-        own = fresh(q->sizes(), kc.scalar_type(), kc.device());
-        qo = &own;
-      }
-      qot = tokens(*qo, q->sizes(), kc, "q_out");
+      if (qo) qot = tokens(*qo, q->sizes(), kc, "q_out");
     }
     if (!cos != !sin) refuse("cos", "cos and sin go together");
     const float *cp = nullptr, *sp = nullptr;
@@ -229,9 +234,16 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       positions = to_int(cos->size(0), "positions");
       rot = to_int(2 * cos->size(1), "rot");
     }
-    const c10::cuda::OptionalCUDAGuard guard(kc.device());
-    check("gdn_kv_append", gdn_kv_append(&d, &c, &kt, &vt, q ? &qt : nullptr, q ? &qot : nullptr, cp, sp, positions, rot,
-                                         c10::cuda::getCurrentCUDAStream(kc.device().index()).stream()));
+    {
+      const NoGil nogil;
+      const c10::cuda::OptionalCUDAGuard guard(kc.device());
+      if (q && !qo) {
+        own = fresh(q->sizes(), kc.scalar_type(), kc.device());
+        qot = tokens(own, q->sizes(), kc, "q_out");
+      }
+      check("gdn_kv_append", gdn_kv_append(&d, &c, &kt, &vt, q ? &qt : nullptr, q ? &qot : nullptr, cp, sp, positions, rot,
+                                           c10::cuda::getCurrentCUDAStream(kc.device().index()).stream()));
+    }
     if (!q) Py_RETURN_NONE;
     if (own.defined()) return wrap(own);
     Py_INCREF(a[8]);
@@ -257,22 +269,27 @@ PyObject* paged_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long long cap = (long long)d.max_pages * d.page_size;
     const int max_q = a[7] == Py_None ? (d.N > 0 ? d.N : 1) : to_int(integer(a[7]), "max_q");
     const int max_kv = a[8] == Py_None ? (int)(cap < 1 ? 1 : cap > INT_MAX ? INT_MAX : cap) : to_int(integer(a[8]), "max_kv");
+    const Tensor* given = optional_tensor(a[11], "workspace");
     Tensor own;
-    c10::DataPtr ws;
-    if (!out) {
-      own = fresh(q.sizes(), kc.scalar_type(), kc.device());
-      out = &own;
-    }
-    const gdn_tokens ot = tokens(*out, q.sizes(), kc, "out");
+    gdn_tokens ot{};
+    if (out) ot = tokens(*out, q.sizes(), kc, "out");
     if (lse) {
       if (lse->scalar_type() != at::kFloat || lse->sizes() != at::IntArrayRef({d.N, d.Hq}) || !lse->is_contiguous())
         refuse("lse", "lse must be a contiguous float32 [N, Hq]");
       on_device(*lse, kc.device(), "lse");
     }
-    const c10::cuda::OptionalCUDAGuard guard(kc.device());
-    void* w = scratch(a[11], gdn_paged_attn_workspace_bytes(&d, max_q, max_kv), kc, &ws);
-    check("gdn_paged_attn", gdn_paged_attn(&d, &c, &qt, (float)scale, max_q, max_kv, &ot, lse ? lse->data_ptr<float>() : nullptr,
-                                           w, c10::cuda::getCurrentCUDAStream(kc.device().index()).stream()));
+    {
+      const NoGil nogil;
+      const c10::cuda::OptionalCUDAGuard guard(kc.device());
+      c10::DataPtr ws;
+      if (!out) {
+        own = fresh(q.sizes(), kc.scalar_type(), kc.device());
+        ot = tokens(own, q.sizes(), kc, "out");
+      }
+      void* w = scratch(given, gdn_paged_attn_workspace_bytes(&d, max_q, max_kv), kc, &ws);
+      check("gdn_paged_attn", gdn_paged_attn(&d, &c, &qt, (float)scale, max_q, max_kv, &ot, lse ? lse->data_ptr<float>() : nullptr,
+                                             w, c10::cuda::getCurrentCUDAStream(kc.device().index()).stream()));
+    }
     if (own.defined()) return wrap(own);
     Py_INCREF(a[9]);
     return a[9];
@@ -340,14 +357,17 @@ PyObject* block_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded("block_norm_fwd", a, n, 8, [&]() -> PyObject* {
     const Norm q(a[0], a + 1, number(a[6]), integer(a[7]));
     const Tensor& x = *q.part[0];
-    const c10::cuda::OptionalCUDAGuard guard(x.device());
-    const Tensor h = fresh(x.sizes(), x.scalar_type(), x.device());
-    Tensor y;
-    if (q.p.w_pre) y = fresh(x.sizes(), x.scalar_type(), x.device());
-    const Tensor stats = fresh({q.d.R, q.d.G, 2}, at::kFloat, x.device());
-    check("gdn_block_norm_fwd", gdn_block_norm_fwd(&q.d, &q.p, h.data_ptr(), y.defined() ? y.data_ptr() : nullptr,
-                                                   stats.data_ptr<float>(),
-                                                   c10::cuda::getCurrentCUDAStream(x.device().index()).stream()));
+    Tensor h, y, stats;
+    {
+      const NoGil nogil;
+      const c10::cuda::OptionalCUDAGuard guard(x.device());
+      h = fresh(x.sizes(), x.scalar_type(), x.device());
+      if (q.p.w_pre) y = fresh(x.sizes(), x.scalar_type(), x.device());
+      stats = fresh({q.d.R, q.d.G, 2}, at::kFloat, x.device());
+      check("gdn_block_norm_fwd", gdn_block_norm_fwd(&q.d, &q.p, h.data_ptr(), y.defined() ? y.data_ptr() : nullptr,
+                                                     stats.data_ptr<float>(),
+                                                     c10::cuda::getCurrentCUDAStream(x.device().index()).stream()));
+    }
     PyObject* yo = y.defined() ? wrap(y) : Py_NewRef(Py_None);
     return Py_BuildValue("(NNN)", wrap(h), yo, wrap(stats));
   });
@@ -364,21 +384,25 @@ PyObject* block_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse("stats", "stats must be the forward's");
     on_device(stats, x.device(), "stats");
     const gdn_rows rh = rows(dh, x, "dh"), ry = rows(dy, x, "dy");
-    const c10::cuda::OptionalCUDAGuard guard(x.device());
+    const Tensor* given = optional_tensor(a[11], "workspace");
     Tensor g[6];
-    c10::DataPtr ws;
-    void* p[6];
-    for (int i = 0; i < 6; ++i) {
-      // without rows nothing is launched, and the weights' sums are zero
-      if (q.part[i])
-        g[i] = q.d.R == 0 ? at::zeros(q.part[i]->sizes(), x.options())
-                          : fresh(q.part[i]->sizes(), x.scalar_type(), x.device());
-      p[i] = g[i].defined() ? g[i].data_ptr() : nullptr;
+    {
+      const NoGil nogil;
+      const c10::cuda::OptionalCUDAGuard guard(x.device());
+      c10::DataPtr ws;
+      void* p[6];
+      for (int i = 0; i < 6; ++i) {
+        // without rows nothing is launched, and the weights' sums are zero
+        if (q.part[i])
+          g[i] = q.d.R == 0 ? at::zeros(q.part[i]->sizes(), x.options())
+                            : fresh(q.part[i]->sizes(), x.scalar_type(), x.device());
+        p[i] = g[i].defined() ? g[i].data_ptr() : nullptr;
+      }
+      const gdn_norm_grads grads{p[0], p[1], p[2], p[3], p[4], p[5]};
+      void* w = scratch(given, gdn_block_norm_workspace_bytes(&q.d), x, &ws);
+      check("gdn_block_norm_bwd", gdn_block_norm_bwd(&q.d, &q.p, stats.data_ptr<float>(), dh ? &rh : nullptr, dy ? &ry : nullptr,
+                                                     &grads, w, c10::cuda::getCurrentCUDAStream(x.device().index()).stream()));
     }
-    const gdn_norm_grads grads{p[0], p[1], p[2], p[3], p[4], p[5]};
-    void* w = scratch(a[11], gdn_block_norm_workspace_bytes(&q.d), x, &ws);
-    check("gdn_block_norm_bwd", gdn_block_norm_bwd(&q.d, &q.p, stats.data_ptr<float>(), dh ? &rh : nullptr, dy ? &ry : nullptr,
-                                                   &grads, w, c10::cuda::getCurrentCUDAStream(x.device().index()).stream()));
     PyObject* out = PyTuple_New(6);
     for (int i = 0; out && i < 6; ++i) PyTuple_SET_ITEM(out, i, g[i].defined() ? wrap(g[i]) : Py_NewRef(Py_None));
     return out;

@@ -1,4 +1,7 @@
-"""The compiled calls as a Python program meets them: gradients they cannot give."""
+"""The compiled calls as a Python program meets them: gradients they cannot give, other threads."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -49,3 +52,37 @@ def test_append_refuses_to_lose_a_gradient(name):
         call()
     with torch.no_grad():
         assert torch.equal(call(), plain)
+
+
+def test_other_threads_run_while_a_launch_waits():
+    """More launches than the queue holds behind a kernel of about a second: the launching thread waits, and a
+    second thread keeps its turns."""
+    _, k, v, (kc, vc, *where) = _setup()
+    gdn.gdn_kv_append(k, v, kc, vc, *where)
+    torch.cuda.synchronize()
+    stop, gap = threading.Event(), [0.0]
+
+    def watch():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gap[0] = max(gap[0], now - last)
+            last = now
+
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    torch.cuda._sleep(1_800_000_000)
+    end.record()
+    t = threading.Thread(target=watch)
+    t.start()
+    try:
+        for _ in range(6000):
+            gdn.gdn_kv_append(k, v, kc, vc, *where)
+    finally:
+        stop.set()
+        t.join()
+        torch.cuda.synchronize()
+    span = start.elapsed_time(end) / 1e3
+    assert span > 0.5  # the queue was full for most of this
+    assert gap[0] < span / 4, (gap[0], span)
