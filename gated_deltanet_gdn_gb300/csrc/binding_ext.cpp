@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
@@ -198,8 +199,8 @@ PyObject* guarded(const char* fn, PyObject* const* args, Py_ssize_t n, Py_ssize_
       PyErr_SetString(PyExc_RuntimeError, r.msg.c_str());
     }
   } catch (const NotTensor&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // PyTorch's own, as its calls raise them (out of memory among them)
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

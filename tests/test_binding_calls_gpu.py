@@ -1,4 +1,5 @@
-"""The compiled calls as a Python program meets them: gradients they cannot give, other threads."""
+"""The compiled calls as a Python program meets them: gradients they cannot give, other threads, memory that
+is not there."""
 import threading
 import time
 
@@ -86,3 +87,15 @@ def test_other_threads_run_while_a_launch_waits():
     span = start.elapsed_time(end) / 1e3
     assert span > 0.5  # the queue was full for most of this
     assert gap[0] < span / 4, (gap[0], span)
+
+
+def test_out_of_memory_is_pytorchs_error():
+    """Outputs beyond the process's share of the memory: the error that programs catch to try a smaller batch."""
+    x = torch.zeros(1, 1, 4096, device="cuda").expand(1 << 20, 1, 4096)  # 16 GB as a contiguous output
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (1 << 30)) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            gdn.gdn_block_norm_fwd(x)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
