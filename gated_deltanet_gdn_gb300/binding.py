@@ -411,7 +411,8 @@ def gdn_paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, scale: 
                    workspace=None) -> torch.Tensor:
     """Causal attention of the packed new tokens q [N, Hq, D] over the paged cache their keys were
     appended to. max_q, max_kv: the caller's bounds on new tokens and length of one sequence (they
-    choose the kernel and its split; without them the largest possible are taken). lse: optional fp32
+    choose the kernel and its split; without them the largest possible are taken, which sends short
+    decoding calls to the kernel of chunks: give max_q=1 there). lse: optional fp32
     [N, Hq] output, the log of each row's softmax sum. Returns out [N, Hq, D]. Serving only: with
     gradients enabled, tensors that require them are refused."""
     return (_ext or _compiled()).paged_attn(q, k_cache, v_cache, page_table, cu_seqlens, kv_lens, scale, max_q,

@@ -20,8 +20,8 @@
 // probabilities are rounded to bf16 for the second product (their sum is not); fp32 uses
 // three-term TF32 products for both.
 //
-// 32 sequences of one token, up to 32k keys (48 query and 8 KV heads of 128, bf16): 370 us,
-// 6.67 TB/s, the measured copy rate. One sequence over 2k keys: 9.6 us, the latency
+// 32 sequences of one token, up to 32k keys (48 query and 8 KV heads of 128, bf16): 364-373 us,
+// 6.6-6.8 TB/s, the measured copy rate. One sequence over 2k keys: 10 us, the latency
 // of two launches. fp32, 3 x 200 tokens over 1.3k keys (6 and 2 heads of 64): 47 us, and 512
 // tokens over 8k keys (64 and 8 heads of 128): 4.1 ms, bound by the products and the splits.
 #include "paged_attn.cuh"

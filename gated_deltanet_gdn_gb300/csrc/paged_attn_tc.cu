@@ -25,17 +25,21 @@
 //    queries are on their way, and its first product done, while this item's output is
 //    written. An item that a CTA holds whole is written at once; at the ends of a CTA's run
 //    the parts go to the workspace and a second kernel joins them in the order of the CTAs.
-//  * many items (two or more per SM): the grid has a CTA per item, the longest first and the
-//    KV heads of a run of rows side by side; the CTAs that run at the same time then read
-//    the same keys at the same time, which the L2 serves once. A running CTA takes over the
-//    next one not yet launched (cluster launch control) and goes on with its item, as above.
+//  * many items (two or more per SM): the grid has a CTA per item, the sequences from the last,
+//    each one's items from its longest and the KV heads of a run of rows side by side; the
+//    CTAs that run at the same time then read the same keys at the same time, which the L2
+//    serves once. A running CTA takes over the next one not yet launched (cluster launch
+//    control) and goes on with its item, as above. An item is not cut here: 32 sequences that
+//    decode over 16k to 62k keys beside a prompt of 8,192 tokens (48 and 8 heads) take 1,250 us
+//    when they stand behind the prompt and 1,464 us in front of it, in calls of their own 774
+//    and 565 us.
 //
 // Measured, heads of 128: a chunk of 2,048 tokens over 63k keys (16 and 4 heads, 128 items)
-// 690-700 us, 1.56 PFLOP/s, in bursts and 780 us under the power limit (by items: 793 in
-// bursts); six prompts of up to 4,096 tokens (48 and 8 heads, 3,408 items) 595-616 us,
-// 1.2 PFLOP/s (by runs: 837 us), where an item's output, queries and first softmax take
-// about a fifth; 16 x 8 draft tokens over up to 16k keys (16 and 2 heads) 51 us, of which
-// the stream of keys is 24 us and the start, merge and join the rest.
+// 690-700 us, 1.56 PFLOP/s, in bursts and 770-790 us under the power limit; six prompts of up
+// to 4,096 tokens (48 and 8 heads, 3,408 items) 604-626 us, 1.2 PFLOP/s, whichever order
+// their lengths have (604-610 ascending, descending and mixed), where an item's output, queries and
+// first softmax take about a fifth; 16 x 8 draft tokens over up to 16k keys (16 and 2 heads)
+// 50 us, of which the stream of keys is 24 us and the start, merge and join the rest.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -50,8 +54,8 @@ constexpr int THREADS = 384;  // three warpgroups: two of softmax, and one of th
 constexpr int MMA_WARP = 8, KEY_WARP = 9, VALUE_WARP = 10, QUERY_WARP = 11;
 constexpr int ITEM_READERS = 11;  // warps that read the next item: all but the query warp, which finds it
 // Registers a thread, moved from the third warpgroup to the softmax (which holds 128 scores):
-// the launch has 168 each, 2 * 216 + 72 = 3 * 168. (Six prompts of up to 4,096 tokens: 622 us; 208 and 88
-// 662 us, 224 and 56 697 us.)
+// the launch has 168 each, 2 * 216 + 72 = 3 * 168. (Six prompts of up to 4,096 tokens: 610 us; 208 and 88
+// 610 us, 224 and 56 662 us.)
 constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
 constexpr float RESCALE = 8.f;  // growth of the maximum (base 2) that rescales O
 
@@ -807,8 +811,12 @@ bool cache_map(CUtensorMap* map, void* base, const PagedArgs& p, long long ps, l
 }
 
 // Whether the call surely has two items or more per SM: the tokens' full items alone. Below
-// that the ragged last round costs more than the parts (128 items: 793 us, by runs 711);
-// above, the shared reads of keys gain more (3,408 items: 622 us, by runs 837).
+// that the ragged last round can cost more than the parts; above, prompts gain from the shared
+// reads of keys, and chunks lose 6 % at most. us by items / by runs, 16 and 4 heads of 128:
+//   items                              128      200      304      450       800         1,600
+//   2 sequences over 16k keys       217/205  420/307  450/457  676/690  1,352/1,272  2,975/2,947
+//   2 prompts                        29/43    45/57    74/78   113/121    260/274      872/909
+//   6 prompts, 5 to 25 % of the tokens  -     37/49    47/66    68/94     139/178      412/444
 bool whole_items(const AttnArgs& a) {
   const int nsm = device_sm_count() > 0 ? device_sm_count() : 152;
   return (long long)a.p.N * (a.p.Hq / a.p.Hk) / ROWS * a.p.Hk >= 2ll * nsm;
@@ -834,6 +842,15 @@ cudaError_t run(const AttnArgs& a, const CUtensorMap& km, const CUtensorMap& vm,
 
 }  // namespace
 
+// bf16 with more rows than one item of the few-rows kernel has. us of that kernel / of this one,
+// two KV heads of 128, by query rows of a KV head:
+//   rows                          16       24       32       64        128
+//   1 sequence, 2,000 keys     16/27    18/27    19/27    21/29     20/27
+//   16 sequences, 2,000 keys   27/31    29/31    29/33    39/33     57/33
+//   64 sequences, 2,000 keys   43/55    64/55    66/57   117/57    188/57
+//   16 sequences, 30,000 keys 106/113  178/113  176/113  322/113   471/113
+// (A second item of 16 rows reads and multiplies all keys again; one short sequence, whose keys
+// one item leaves most SMs without, is the exception and stays on the rule.)
 bool paged_attn_tc_applies(const AttnArgs& a) {
   const long long G = a.p.Hq / a.p.Hk;
   return a.p.bf16 && (a.max_q < a.p.N ? a.max_q : a.p.N) * G > 16;

@@ -299,7 +299,8 @@ int gdn_replay_state(const gdn_dims* dims, int L, const float* ckpt, const void*
  * position kv_lens[b] - n + i, and the same arrays serve the append and the
  * attention after it. A token with a negative position (kv_lens[b] < n) is not
  * kept, and sees no key: its attention row is zero (lse -infinity). Rows from
- * cu_seqlens[B] on are padding: nothing is read or written for them.
+ * cu_seqlens[B] on are padding: their values are not used and nothing is written
+ * for them.
  *
  * Token tensors are [N, heads, D] with any token and head strides (in elements,
  * 0 or more); channels are contiguous. Pointers are 16-byte aligned and every
@@ -356,12 +357,14 @@ int gdn_kv_append(const gdn_paged_dims* dims, const gdn_paged_cache* cache, cons
  * chunk and a whole prompt are the same call. Scores, maxima, sums and outputs
  * accumulate in float32; with bf16 the probabilities are rounded to bf16 for the
  * product with v. lse (NULL or [N, Hq] float32): log sum_j exp(scale q . k_j).
- * Cached rows past a sequence's length may hold anything, NaN included. A
- * non-finite value in a visible row reaches the outputs of every row that
- * sees it and may reach rows of the same sequence that stand before it.
+ * Cached rows past a sequence's length may hold anything, NaN included. A NaN
+ * in a query or in a visible key makes NaN of the output row and its lse, one
+ * in a visible value of that channel of the output; a non-finite value may also
+ * reach rows of the same sequence that stand before it.
  * max_q and max_kv bound the new tokens and the length of any one sequence
  * (0 < max_q <= N, 0 < max_kv): they choose the kernel and its split, never the
- * result. workspace: gdn_paged_attn_workspace_bytes(dims, max_q, max_kv) bytes,
+ * result. (Bounds that are far too large cost time: 32 decoding sequences over 2k
+ * keys, groups of 6 heads, 66 us, with max_q = N 82 us.) workspace: gdn_paged_attn_workspace_bytes(dims, max_q, max_kv) bytes,
  * 256-byte aligned, no initialisation needed, not shared by calls that overlap. */
 size_t gdn_paged_attn_workspace_bytes(const gdn_paged_dims* dims, int max_q, int max_kv);
 int gdn_paged_attn(const gdn_paged_dims* dims, const gdn_paged_cache* cache, const gdn_tokens* q,
@@ -386,7 +389,9 @@ int gdn_paged_attn(const gdn_paged_dims* dims, const gdn_paged_cache* cache, con
  *   stats                       [R, G, 2] float32, written by the forward for the
  *                               backward: the two inverse norms (1 where absent)
  * All but stats have dims.dtype. Any C up to 8192 (else GDN_ERR_UNSUPPORTED);
- * multiples of 16 bytes in C, strides and pointers take the wide loads. R * G up
+ * multiples of 16 bytes in C, strides and pointers (the weights' too) take the
+ * wide loads; other rows go element by element, and so does the backward of
+ * float32 rows above 28 KB with all parts. R * G up
  * to 2^31 - 1. eps finite and not negative.
  * The backward takes the forward's inputs and stats, dh (NULL = zeros) and dy
  * (with w_pre), and writes every gradient that is not NULL in grads; gradients of
