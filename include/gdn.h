@@ -364,7 +364,8 @@ int gdn_kv_append(const gdn_paged_dims* dims, const gdn_paged_cache* cache, cons
  * max_q and max_kv bound the new tokens and the length of any one sequence
  * (0 < max_q <= N, 0 < max_kv): they choose the kernel and its split, never the
  * result. (Bounds that are far too large cost time: 32 decoding sequences over 2k
- * keys, groups of 6 heads, 66 us, with max_q = N 82 us.) workspace: gdn_paged_attn_workspace_bytes(dims, max_q, max_kv) bytes,
+ * keys, groups of 6 heads, 66 us, with max_q = N 82 us.)
+ * workspace: gdn_paged_attn_workspace_bytes(dims, max_q, max_kv) bytes,
  * 256-byte aligned, no initialisation needed, not shared by calls that overlap. */
 size_t gdn_paged_attn_workspace_bytes(const gdn_paged_dims* dims, int max_q, int max_kv);
 int gdn_paged_attn(const gdn_paged_dims* dims, const gdn_paged_cache* cache, const gdn_tokens* q,

@@ -71,3 +71,26 @@ def test_nan_key(dtype, D, layout, where):
             hit[tok, head * G:(head + 1) * G] = True
     out, lse = _call(c, q)
     _expect(c, out, lse, hit)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_nan_value(dtype, D, layout):
+    """One channel of one cached value: that channel of the rows that see it (earlier rows of the sequence may
+    have it too), and nothing else."""
+    new, length, Hq, Hk = LAYOUTS[layout]
+    c = Paged(new, length, Hq, Hk, D, 64, dtype, seed=D + 2)
+    q = c.normal(c.N, Hq, D)
+    b, head, G, key = len(new) - 1, Hk - 1, Hq // Hk, length[-1] // 2
+    c.vc[int(c.table[b, key // c.page]), head, key % c.page, 7] = NAN
+    out, lse = _call(c, q)
+    may = torch.zeros(c.N, Hq, D, dtype=torch.bool)
+    must = may.clone()
+    for tok, seq, pos in c.tokens():
+        if seq == b:
+            may[tok, head * G:(head + 1) * G, 7] = True
+            must[tok, head * G:(head + 1) * G, 7] = pos >= key
+    assert bool(torch.isnan(out[must]).all()) and bool(torch.isfinite(out[~may]).all())
+    assert bool(torch.isfinite(lse).all())
+    assert gdn.gdn_check_device_error() == 0
