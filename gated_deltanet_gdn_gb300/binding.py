@@ -11,7 +11,7 @@ import ctypes
 import importlib.util
 import os
 import threading
-from typing import Dict, Optional, Tuple
+from typing import Dict, NamedTuple, Optional, Tuple
 
 import torch
 
@@ -32,6 +32,9 @@ GDN_FLAG_QK_L2NORM = 2
 GDN_FLAG_CHUNK128 = 4
 GDN_FLAG_ROPE_PAIRS = 16
 GDN_FLAG_GATE_SIGMOID = 32
+GDN_FLAG_CONV_SILU = 64
+GDN_FLAG_DT_SOFTPLUS = 128
+GDN_FLAG_ZERO_PADDING = 256
 GDN_CHUNK = 64
 GDN_CHUNK128 = 128
 
@@ -42,8 +45,11 @@ EXPORTED = ("gdn_chunk_residual_bytes", "gdn_chunk_bwd_workspace_bytes", "gdn_ch
             "gdn_chunk_fwd_noalloc", "gdn_replay_buffer_bytes", "gdn_replay_decode",
             "gdn_replay_state", "gdn_selftest_wait_timeout", "gdn_kv_append",
             "gdn_paged_attn_workspace_bytes", "gdn_paged_attn", "gdn_block_norm_fwd",
-            "gdn_block_norm_workspace_bytes", "gdn_block_norm_bwd")
-KERNEL_COUNT = 29
+            "gdn_block_norm_workspace_bytes", "gdn_block_norm_bwd", "gdn_causal_conv_fwd",
+            "gdn_causal_conv_workspace_bytes", "gdn_causal_conv_bwd", "gdn_selective_scan_residual_bytes",
+            "gdn_selective_scan_workspace_bytes", "gdn_selective_scan_fwd",
+            "gdn_selective_scan_bwd_workspace_bytes", "gdn_selective_scan_bwd", "gdn_page_plan")
+KERNEL_COUNT = 40
 GDN_REPLAY_MAX_TOKENS = 8
 
 
@@ -87,6 +93,35 @@ class GdnNormParts(ctypes.Structure):
 
 class GdnNormGrads(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("dx", "dgate", "dresidual", "dw_post", "dres_scale", "dw_pre")]
+
+
+class GdnPacked(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("B", ctypes.c_int), ("pool", ctypes.c_int), ("cu_seqlens", _vp), ("kv_lens", _vp),
+                ("slots", _vp)]
+
+
+class GdnConvDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("C", "taps", "dtype", "flags")]
+
+
+class GdnScanDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("D", "G", "S", "dtype", "flags")]
+
+
+class GdnScanParts(ctypes.Structure):
+    _fields_ = [(n, GdnRows) for n in ("u", "dt", "z", "B", "C")] + [(n, _vp) for n in ("A", "skip", "dt_bias", "h0")]
+
+
+class GdnScanGrads(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("du", "ddt", "dz", "dB", "dC", "dA", "dskip", "ddt_bias", "dh0")]
+
+
+class GdnPlanDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "page_size", "max_pages", "num_free", "max_tokens")]
+
+
+class GdnPlanOut(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("cu_seqlens", "kv_lens", "free_count", "requests", "positions", "slots")]
 
 
 class GdnError(RuntimeError):
@@ -160,13 +195,33 @@ def load(build_if_needed: bool = True) -> ctypes.CDLL:
             lib.gdn_block_norm_workspace_bytes.restype = sz
             lib.gdn_block_norm_bwd.argtypes = [pn, pa, vp, pr, pr, pg, vp, vp]
             lib.gdn_block_norm_bwd.restype = i
+            pq, pv, ps, pi = (ctypes.POINTER(c) for c in (GdnPacked, GdnConvDims, GdnScanDims, GdnScanParts))
+            lib.gdn_causal_conv_fwd.argtypes = [pv, pq, pr, vp, vp, vp, i, pr, vp, vp]
+            lib.gdn_causal_conv_fwd.restype = i
+            lib.gdn_causal_conv_workspace_bytes.argtypes = [pv, pq]
+            lib.gdn_causal_conv_workspace_bytes.restype = sz
+            lib.gdn_causal_conv_bwd.argtypes = [pv, pq, pr, vp, vp, vp, pr, vp, vp, vp, vp, vp, vp, vp]
+            lib.gdn_causal_conv_bwd.restype = i
+            lib.gdn_selective_scan_residual_bytes.argtypes = [ps, pq]
+            lib.gdn_selective_scan_residual_bytes.restype = sz
+            lib.gdn_selective_scan_workspace_bytes.argtypes = [ps, pq, i]
+            lib.gdn_selective_scan_workspace_bytes.restype = sz
+            lib.gdn_selective_scan_fwd.argtypes = [ps, pq, pi, i, pr, vp, vp, vp, vp]
+            lib.gdn_selective_scan_fwd.restype = i
+            lib.gdn_selective_scan_bwd_workspace_bytes.argtypes = [ps, pq, i]
+            lib.gdn_selective_scan_bwd_workspace_bytes.restype = sz
+            lib.gdn_selective_scan_bwd.argtypes = [ps, pq, pi, vp, i, pr, vp, ctypes.POINTER(GdnScanGrads), vp, vp]
+            lib.gdn_selective_scan_bwd.restype = i
+            lib.gdn_page_plan.argtypes = [ctypes.POINTER(GdnPlanDims), vp, _ll, vp, vp, vp, vp,
+                                          ctypes.POINTER(GdnPlanOut), vp]
+            lib.gdn_page_plan.restype = i
             _lib = lib
     return _lib
 
 
 def _compiled():
-    """The compiled argument marshalling of the paged cache and block norm calls (csrc/binding_ext.cpp), built
-    first when missing or stale."""
+    """The compiled argument marshalling of the paged cache, block norm, convolution, scan and plan calls
+    (csrc/binding_ext.cpp), built first when missing or stale."""
     global _ext
     load()
     with _lock:
@@ -439,6 +494,68 @@ def gdn_block_norm_bwd(x, stats, dh, dy=None, *, gate=None, residual=None, w_pos
     return dict(zip(("dx", "dgate", "dresidual", "dw_post", "dres_scale", "dw_pre"), grads))
 
 
+def gdn_causal_conv_fwd(x, weight, bias=None, *, state0=None, state_final=None, slots=None, cu_seqlens=None,
+                        kv_lens=None, max_q: Optional[int] = None, flags: int = 0, out=None):
+    """Short causal convolution of every channel along the tokens (2 to 4 taps, weight [C, taps]), with silu by
+    GDN_FLAG_CONV_SILU. x is [B, T, C], or packed [N, C] with cu_seqlens [B + 1]; states are the last taps - 1 inputs,
+    [B, taps - 1, C], or rows `slots` [B] of pools (state_final may be state0: in place; a negative slot
+    has no state). With kv_lens (cached tokens with the new ones) a sequence without earlier tokens starts from
+    zeros. max_q: the caller's bound on one sequence's new tokens. Returns (y, state_final). Packed rows behind the
+    last sequence are zeros, or in a given `out` left as they were. For gradients: causal_conv."""
+    return (_ext or _compiled()).causal_conv_fwd(x, weight, bias, state0, state_final, slots, cu_seqlens, kv_lens, max_q,
+                                                 flags, out)
+
+
+def gdn_causal_conv_bwd(x, weight, bias, dy, *, state0=None, dstate=None, cu_seqlens=None, flags: int = 0,
+                        workspace=None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients of gdn_causal_conv_fwd from dy and dstate (of the final states, or None): dx, dweight, dbias (with
+    a bias) and dstate0 (with state0)."""
+    grads = (_ext or _compiled()).causal_conv_bwd(x, weight, bias, dy, state0, dstate, cu_seqlens, flags, workspace)
+    return dict(zip(("dx", "dweight", "dbias", "dstate0"), grads))
+
+
+def gdn_selective_scan_fwd(u, dt, A, B, C, *, D=None, z=None, dt_bias=None, h0=None, h_final=None, slots=None,
+                           cu_seqlens=None, kv_lens=None, max_q: Optional[int] = None, flags: int = 0, save: bool = False,
+                           out=None, workspace=None):
+    """Selective state space scan: h_t = exp(delta_t A) h_{t-1} + delta_t u_t B_t, y_t = (C_t . h_t + D u_t) silu(z_t),
+    delta = dt + dt_bias or, with GDN_FLAG_DT_SOFTPLUS, its softplus. u, dt, z are [B, T, D], or packed [N, D] with
+    cu_seqlens; B, C [..., groups, S] (S 8, 16, 32 or 64); A [D, S], D and dt_bias [D] and the states [B, D, S] float32.
+    States, slots, kv_lens and max_q as in gdn_causal_conv_fwd. Returns (y, h_final, residuals): the
+    residuals (with save) are the backward's. For gradients: selective_scan."""
+    return (_ext or _compiled()).selective_scan_fwd(u, dt, A, B, C, D, z, dt_bias, h0, h_final, slots, cu_seqlens, kv_lens,
+                                                    max_q, flags, save, out, workspace)
+
+
+def gdn_selective_scan_bwd(u, dt, A, B, C, dy, residuals, *, D=None, z=None, dt_bias=None, dh_final=None,
+                           need_dh0: bool = False, cu_seqlens=None, max_q: Optional[int] = None, flags: int = 0,
+                           workspace=None) -> Dict[str, Optional[torch.Tensor]]:
+    """Gradients of gdn_selective_scan_fwd from dy and dh_final (or None): du, ddt, dA, dB, dC, dD, dz, ddt_bias and,
+    with need_dh0, dh0; None for absent parts."""
+    grads = (_ext or _compiled()).selective_scan_bwd(u, dt, A, B, C, D, z, dt_bias, dy, residuals, dh_final, need_dh0,
+                                                     cu_seqlens, max_q, flags, workspace)
+    return dict(zip(("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0"), grads))
+
+
+class PagePlan(NamedTuple):
+    """What gdn_page_plan returns, all on the device."""
+
+    cu_seqlens: torch.Tensor  # [B + 1] packed offsets of the granted new tokens
+    kv_lens: torch.Tensor  # [B] cached tokens after the step
+    free_count: torch.Tensor  # [1] pages left on the free list
+    requests: torch.Tensor  # [max_tokens] request of each packed row, -1 behind the last
+    positions: torch.Tensor  # [max_tokens] its position in the request
+    slots: torch.Tensor  # [max_tokens] int64: its place in the cache, page * page_size + row
+
+
+def gdn_page_plan(page_table, kv_lens, new_tokens, free_pages, free_count, *, page_size: int, max_tokens: int) -> PagePlan:
+    """Plan a serving step from kv_lens [B] and new_tokens [B] (negative: tokens given back): pages are pushed
+    on and popped off the stack free_pages[:free_count], page_table and free_pages change in place, and requests that
+    do not fit the free pages or max_tokens have no tokens in the step. The results feed gdn_kv_append,
+    gdn_paged_attn, gdn_causal_conv_fwd and gdn_selective_scan_fwd; nothing is read back to the host."""
+    return PagePlan(*(_ext or _compiled()).page_plan(page_table, kv_lens, new_tokens, free_pages, free_count, page_size,
+                                                     max_tokens))
+
+
 def gdn_selftest_wait_timeout(max_tries: int = 1024, device: Optional[torch.device] = None,
                               cycles: Optional[torch.Tensor] = None) -> None:
     """Launch the library's wait-timeout self-test kernel (see include/gdn.h). cycles: an
@@ -536,3 +653,62 @@ def block_norm(x, *, gate=None, residual=None, w_post=None, res_scale=None, w_pr
                flags: int = 0):
     """(h, y) of gdn_block_norm_fwd, differentiable once through autograd (y is None without w_pre)."""
     return BlockNorm.apply(x, gate, residual, w_post, res_scale, w_pre, float(eps), int(flags))
+
+
+class CausalConv(torch.autograd.Function):
+    """gdn_causal_conv_fwd with the library's backward."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, state0, cu_seqlens, max_q, flags):
+        y, state = gdn_causal_conv_fwd(x, weight, bias, state0=state0, cu_seqlens=cu_seqlens, max_q=max_q, flags=flags)
+        ctx.save_for_backward(x, weight, bias, state0, cu_seqlens)
+        ctx.flags = flags
+        ctx.set_materialize_grads(False)
+        return y, state
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dstate):
+        if dy is None and dstate is None:
+            return (None,) * 7
+        x, weight, bias, state0, cu_seqlens = ctx.saved_tensors
+        dy = torch.zeros_like(x) if dy is None else dy.contiguous()
+        g = gdn_causal_conv_bwd(x, weight, bias, dy, state0=state0, dstate=None if dstate is None else dstate.contiguous(),
+                                cu_seqlens=cu_seqlens, flags=ctx.flags)
+        return g["dx"], g["dweight"], g["dbias"], g["dstate0"], None, None, None
+
+
+def causal_conv(x, weight, bias=None, state0=None, *, cu_seqlens=None, max_q: Optional[int] = None, flags: int = 0):
+    """(y, state_final) of gdn_causal_conv_fwd, differentiable once through autograd."""
+    return CausalConv.apply(x, weight, bias, state0, cu_seqlens, max_q, int(flags))
+
+
+class SelectiveScan(torch.autograd.Function):
+    """gdn_selective_scan_fwd with the library's backward."""
+
+    @staticmethod
+    def forward(ctx, u, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, max_q, flags):
+        y, h, kept = gdn_selective_scan_fwd(u, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens,
+                                            max_q=max_q, flags=flags, save=any(ctx.needs_input_grad))
+        ctx.save_for_backward(u, dt, A, B, C, D, z, dt_bias, cu_seqlens, kept)
+        ctx.max_q, ctx.flags = max_q, flags
+        ctx.set_materialize_grads(False)
+        return y, h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh):
+        if dy is None and dh is None:
+            return (None,) * 12
+        u, dt, A, B, C, D, z, dt_bias, cu_seqlens, kept = ctx.saved_tensors
+        dy = torch.zeros_like(u) if dy is None else dy.contiguous()
+        g = gdn_selective_scan_bwd(u, dt, A, B, C, dy, kept, D=D, z=z, dt_bias=dt_bias,
+                                   dh_final=None if dh is None else dh.contiguous(), need_dh0=ctx.needs_input_grad[8],
+                                   cu_seqlens=cu_seqlens, max_q=ctx.max_q, flags=ctx.flags)
+        return (g["du"], g["ddt"], g["dA"], g["dB"], g["dC"], g["dD"], g["dz"], g["ddt_bias"], g["dh0"], None, None, None)
+
+
+def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, cu_seqlens=None,
+                   max_q: Optional[int] = None, flags: int = 0):
+    """(y, h_final) of gdn_selective_scan_fwd, differentiable once through autograd."""
+    return SelectiveScan.apply(u, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, max_q, int(flags))

@@ -165,7 +165,12 @@ const char* kKernelNames[K_COUNT] = {"chunk_prep_kernel",    "chunk_scan_fwd_ker
                                      "chunk_bwd_sync_zero_kernel", "chunk_merge128_kernel",
                                      "chunk_mid128_kernel", "block_norm_fwd_kernel", "block_norm_bwd_kernel",
                                      "block_norm_wgrad_kernel", "kv_append_kernel", "paged_attn_kernel",
-                                     "paged_attn_join_kernel", "paged_attn_tc_kernel", "paged_attn_tc_join_kernel"};
+                                     "paged_attn_join_kernel", "paged_attn_tc_kernel", "paged_attn_tc_join_kernel",
+                                     "causal_conv_fwd_kernel", "causal_conv_bwd_kernel", "causal_conv_wgrad_kernel",
+                                     "selective_scan_kernel (chunk ends)", "selective_scan_carry_kernel",
+                                     "selective_scan_kernel", "selective_step_kernel",
+                                     "selective_scan_bwd_sum_kernel", "selective_scan_bwd_kernel",
+                                     "selective_scan_join_kernel", "page_plan_kernel"};
 
 }  // namespace
 

@@ -1,4 +1,4 @@
-// Compiled argument marshalling of the paged cache and block norm calls: takes the tensors
+// Compiled argument marshalling of the paged cache, block norm, convolution, selective scan and plan calls: takes the tensors
 // apart, checks them, allocates what the caller left out and calls the C ABI on the current
 // stream. Nothing is computed here.
 //
@@ -8,6 +8,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/DimVector.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/zeros.h>
@@ -18,6 +19,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <array>
 #include <climits>
 #include <initializer_list>
 #include <string>
@@ -105,7 +108,8 @@ void unit_channels(const Tensor& t, const char* name) {
     refuse(name, std::string(name) + " must have contiguous channels");
 }
 
-// The paged calls have no backward: a gradient that would be lost without a word is refused.
+// A gradient that would be lost without a word is refused: the paged calls have no backward, the mixers' has functions of
+// its own.
 void no_gradient(const Tensor* t, const char* name) {
   if (t && c10::GradMode::is_enabled() && t->requires_grad())
     refuse(name, std::string(name) + " requires a gradient, and this call has no backward: call it under torch.no_grad() or detach " + name,
@@ -410,6 +414,339 @@ PyObject* block_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The sequences of a convolution or scan call: [B, T, ...] tensors, or [N, ...] with cu_seqlens.
+struct Seqs {
+  gdn_packed q{};
+  at::DimVector lead;  // [B, T] or [N]
+  int max_q = 1;
+  c10::Device dev;
+  at::ScalarType type;
+  Seqs(const Tensor& x, const char* name, const Tensor* slots, const Tensor* cu, const Tensor* lens, PyObject* max_q_)
+      : dev(x.device()), type(x.scalar_type()) {
+    on_device(x, dev, name);
+    dtype_code(x);
+    if (cu) {
+      if (x.dim() != 2) refuse(name, std::string(name) + " must be [tokens, channels] with cu_seqlens");
+      if (cu->dim() != 1 || cu->size(0) < 1) refuse("cu_seqlens", "cu_seqlens must be [sequences + 1]");
+      q.B = to_int(cu->size(0) - 1, "B");
+      int_array(*cu, {(int64_t)q.B + 1}, dev, "cu_seqlens");
+      q.cu_seqlens = cu->data_ptr<int>();
+      max_q = (int)std::max<int64_t>(x.size(0), 1);
+      if (max_q_ != Py_None) max_q = to_int(integer(max_q_), "max_q");
+    } else {
+      if (x.dim() != 3) refuse(name, std::string(name) + " must be [sequences, tokens, channels], or [tokens, channels] with cu_seqlens");
+      q.B = to_int(x.size(0), "B");
+      max_q = to_int(std::max<int64_t>(x.size(1), 1), "tokens");
+    }
+    for (int64_t i = 0; i + 1 < x.dim(); ++i) lead.push_back(x.size(i));
+    q.N = to_int(x.dim() == 2 ? x.size(0) : x.size(0) * x.size(1), "N");
+    q.pool = q.B;
+    if (lens) {
+      int_array(*lens, {q.B}, dev, "kv_lens");
+      q.kv_lens = lens->data_ptr<int>();
+    }
+    if (slots) {
+      int_array(*slots, {q.B}, dev, "slots");
+      q.slots = slots->data_ptr<int>();
+      with_slots = true;
+    }
+  }
+  // [lead..., tail...] with contiguous channels; the leading dimensions fold into one.
+  gdn_rows rows(const Tensor* t, at::IntArrayRef tail, const char* name) const {
+    if (!t) return gdn_rows{};
+    at::DimVector want(lead);
+    want.append(tail.begin(), tail.end());
+    if (t->sizes() != at::IntArrayRef(want) || t->scalar_type() != type)
+      refuse(name, std::string(name) + " must be " + c10::toString(type) + " " + show(want) + ", got " +
+                       c10::toString(t->scalar_type()) + " " + show(t->sizes()));
+    on_device(*t, dev, name);
+    if (t->numel() == 0) return gdn_rows{t->data_ptr(), 0, 0};
+    unit_channels(*t, name);
+    const int64_t nl = (int64_t)lead.size();
+    long long rs = step(*t, nl - 1);
+    if (nl == 2 && t->size(0) > 1) {
+      if (t->size(1) == 1) rs = t->stride(0);
+      else if (t->stride(0) != t->size(1) * t->stride(1))
+        refuse(name, std::string("the leading dimensions of ") + name + " must fold into one");
+    }
+    return gdn_rows{t->data_ptr(), rs, tail.size() == 2 ? step(*t, nl) : 0};
+  }
+  // Rows to be written: no two of them on the same memory.
+  gdn_rows out_rows(const Tensor& t, int64_t width, const char* name) const {
+    const gdn_rows r = rows(&t, {width}, name);
+    if (q.N > 1 && width > 0 && r.row_stride < width) refuse(name, std::string(name) + " must have rows of its own");
+    return r;
+  }
+  // A contiguous tensor [rows of the pool or sequences, tail...].
+  void* state(const Tensor* t, at::IntArrayRef tail, at::ScalarType want, bool pooled, const char* name) {
+    if (!t) return nullptr;
+    if (t->dim() != 1 + (int64_t)tail.size() || t->sizes().slice(1) != tail || t->scalar_type() != want || !t->is_contiguous())
+      refuse(name, std::string(name) + " must be contiguous " + c10::toString(want) + " [" + (pooled ? "rows" : "sequences") +
+                       ", ...] with rows " + show(tail) + ", got " + c10::toString(t->scalar_type()) + " " + show(t->sizes()));
+    on_device(*t, dev, name);
+    if (with_slots && pooled) {
+      if (pool_known && t->size(0) != q.pool) refuse(name, "the state pools must have the same number of rows");
+      q.pool = to_int(t->size(0), "pool");
+      pool_known = true;
+    } else if (t->size(0) != q.B) {
+      refuse(name, std::string(name) + " must have a row for each of the " + std::to_string(q.B) + " sequences");
+    }
+    return t->data_ptr();
+  }
+  bool with_slots = false, pool_known = false;
+};
+const void* exactly(const Tensor* t, at::IntArrayRef sizes, at::ScalarType type, c10::Device dev, const char* name) {
+  if (!t) return nullptr;
+  if (t->sizes() != sizes || t->scalar_type() != type || !t->is_contiguous())
+    refuse(name, std::string(name) + " must be contiguous " + c10::toString(type) + " " + show(sizes) + ", got " +
+                     c10::toString(t->scalar_type()) + " " + show(t->sizes()));
+  on_device(*t, dev, name);
+  return t->data_ptr();
+}
+void* stream_of(c10::Device dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
+
+struct Conv {
+  gdn_conv_dims d;
+  const void *w, *bias;
+  Conv(const Seqs& s, const Tensor& x, const Tensor& weight, const Tensor* b, long long flags) {
+    const int64_t C = x.size(-1);
+    if (weight.dim() != 2) refuse("weight", "weight must be [channels, taps]");
+    d.C = to_int(C, "C");
+    d.taps = to_int(weight.size(1), "taps");
+    d.dtype = dtype_code(x);
+    d.flags = (int)flags;
+    w = exactly(&weight, {C, weight.size(1)}, s.type, s.dev, "weight");
+    bias = exactly(b, {C}, s.type, s.dev, "bias");
+  }
+};
+
+// (x, weight, bias, state0, state_final, slots, cu_seqlens, kv_lens, max_q, flags, out) -> (y, state_final)
+PyObject* causal_conv_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("causal_conv_fwd", a, n, 11, [&]() -> PyObject* {
+    const Tensor &x = tensor(a[0], "x"), &weight = tensor(a[1], "weight");
+    const Tensor *bias = optional_tensor(a[2], "bias"), *state0 = optional_tensor(a[3], "state0"),
+                 *state_final = optional_tensor(a[4], "state_final"), *slots = optional_tensor(a[5], "slots"),
+                 *out = optional_tensor(a[10], "out");
+    no_gradient(&x, "x"); no_gradient(&weight, "weight"); no_gradient(bias, "bias"); no_gradient(state0, "state0");
+    no_gradient(state_final, "state_final"); no_gradient(out, "out");
+    Seqs s(x, "x", slots, optional_tensor(a[6], "cu_seqlens"), optional_tensor(a[7], "kv_lens"), a[8]);
+    Conv c(s, x, weight, bias, integer(a[9]));
+    const gdn_rows xr = s.rows(&x, {c.d.C}, "x");
+    const std::array<int64_t, 2> row{c.d.taps - 1, c.d.C};
+    const void* s0 = s.state(state0, row, s.type, true, "state0");
+    void* sf = s.state(state_final, row, s.type, true, "state_final");
+    if (slots && !state_final) refuse("state_final", "with slots give state_final (it may be state0)");
+    gdn_rows yr{};
+    if (out) yr = s.out_rows(*out, c.d.C, "out");
+    Tensor y, sfo;
+    {
+      const NoGil nogil;
+      const c10::cuda::OptionalCUDAGuard guard(s.dev);
+      if (!out) {
+        y = fresh(x.sizes(), s.type, s.dev);
+        yr = s.rows(&y, {c.d.C}, "out");
+        c.d.flags |= GDN_FLAG_ZERO_PADDING;
+      }
+      if (!state_final) {
+        sfo = fresh({s.q.B, row[0], row[1]}, s.type, s.dev);
+        sf = sfo.data_ptr();
+      }
+      check("gdn_causal_conv_fwd", gdn_causal_conv_fwd(&c.d, &s.q, &xr, c.w, c.bias, s0, s.max_q, &yr, sf, stream_of(s.dev)));
+    }
+    return Py_BuildValue("(NN)", out ? Py_NewRef(a[10]) : wrap(y), state_final ? Py_NewRef(a[4]) : wrap(sfo));
+  });
+}
+
+// (x, weight, bias, dy, state0, dstate, cu_seqlens, flags, workspace) -> (dx, dweight, dbias, dstate0)
+PyObject* causal_conv_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("causal_conv_bwd", a, n, 9, [&]() -> PyObject* {
+    const Tensor &x = tensor(a[0], "x"), &weight = tensor(a[1], "weight"), &dy = tensor(a[3], "dy");
+    const Tensor *bias = optional_tensor(a[2], "bias"), *state0 = optional_tensor(a[4], "state0"),
+                 *dstate = optional_tensor(a[5], "dstate"), *given = optional_tensor(a[8], "workspace");
+    Seqs s(x, "x", nullptr, optional_tensor(a[6], "cu_seqlens"), nullptr, Py_None);
+    Conv c(s, x, weight, bias, integer(a[7]));
+    const gdn_rows xr = s.rows(&x, {c.d.C}, "x"), dyr = s.rows(&dy, {c.d.C}, "dy");
+    const std::array<int64_t, 2> row{c.d.taps - 1, c.d.C};
+    const void *s0 = s.state(state0, row, s.type, false, "state0"), *ds = s.state(dstate, row, s.type, false, "dstate");
+    Tensor g[4];
+    {
+      const NoGil nogil;
+      const c10::cuda::OptionalCUDAGuard guard(s.dev);
+      const bool none = s.q.N == 0 && s.q.B == 0;  // nothing is launched, and the weights' sums are zero
+      g[0] = fresh(x.sizes(), s.type, s.dev);
+      g[1] = none ? at::zeros(weight.sizes(), weight.options()) : fresh(weight.sizes(), s.type, s.dev);
+      if (bias) g[2] = none ? at::zeros(bias->sizes(), bias->options()) : fresh(bias->sizes(), s.type, s.dev);
+      if (state0) g[3] = fresh(state0->sizes(), s.type, s.dev);
+      c10::DataPtr ws;
+      void* w = scratch(given, gdn_causal_conv_workspace_bytes(&c.d, &s.q), x, &ws);
+      check("gdn_causal_conv_bwd",
+            gdn_causal_conv_bwd(&c.d, &s.q, &xr, c.w, c.bias, s0, &dyr, ds, g[0].data_ptr(), g[1].data_ptr(),
+                                bias ? g[2].data_ptr() : nullptr, state0 ? g[3].data_ptr() : nullptr, w, stream_of(s.dev)));
+    }
+    PyObject* r = PyTuple_New(4);
+    for (int i = 0; r && i < 4; ++i) PyTuple_SET_ITEM(r, i, g[i].defined() ? wrap(g[i]) : Py_NewRef(Py_None));
+    return r;
+  });
+}
+
+// The inputs that the scan's forward and backward share: (u, dt, A, B, C, D, z, dt_bias)
+struct Scan {
+  gdn_scan_dims d;
+  gdn_scan_parts p{};
+  const Tensor* part[8];
+  Scan(const Seqs& s, PyObject* const* a, long long flags) {
+    static const char* const names[8] = {"u", "dt", "A", "B", "C", "D", "z", "dt_bias"};
+    for (int i = 0; i < 8; ++i) part[i] = i < 5 ? &tensor(a[i], names[i]) : optional_tensor(a[i], names[i]);
+    const Tensor &A = *part[2], &B = *part[3];
+    const int64_t D = part[0]->size(-1);
+    if (A.dim() != 2) refuse("A", "A must be [channels, states]");
+    if (B.dim() != part[0]->dim() + 1) refuse("B", "B and C must be [..., groups, states]");
+    d.D = to_int(D, "D");
+    d.G = to_int(B.size(-2), "G");
+    d.S = to_int(A.size(1), "S");
+    d.dtype = dtype_code(*part[0]);
+    d.flags = (int)flags;
+    p.u = s.rows(part[0], {D}, names[0]);
+    p.dt = s.rows(part[1], {D}, names[1]);
+    p.A = static_cast<const float*>(exactly(&A, {D, d.S}, at::kFloat, s.dev, names[2]));
+    p.B = s.rows(&B, {d.G, d.S}, names[3]);
+    p.C = s.rows(part[4], {d.G, d.S}, names[4]);
+    p.skip = static_cast<const float*>(exactly(part[5], {D}, at::kFloat, s.dev, names[5]));
+    p.z = s.rows(part[6], {D}, names[6]);
+    p.dt_bias = static_cast<const float*>(exactly(part[7], {D}, at::kFloat, s.dev, names[7]));
+  }
+};
+
+// (u, dt, A, B, C, D, z, dt_bias, h0, h_final, slots, cu_seqlens, kv_lens, max_q, flags, save, out, workspace)
+// -> (y, h_final, residuals or None)
+PyObject* selective_scan_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("selective_scan_fwd", a, n, 18, [&]() -> PyObject* {
+    const Tensor& u = tensor(a[0], "u");
+    const Tensor *h0 = optional_tensor(a[8], "h0"), *h_final = optional_tensor(a[9], "h_final"),
+                 *slots = optional_tensor(a[10], "slots"), *out = optional_tensor(a[16], "out"),
+                 *given = optional_tensor(a[17], "workspace");
+    Seqs s(u, "u", slots, optional_tensor(a[11], "cu_seqlens"), optional_tensor(a[12], "kv_lens"), a[13]);
+    Scan c(s, a, integer(a[14]));
+    static const char* const names[8] = {"u", "dt", "A", "B", "C", "D", "z", "dt_bias"};
+    for (int i = 0; i < 8; ++i) no_gradient(c.part[i], names[i]);
+    no_gradient(h0, "h0"); no_gradient(h_final, "h_final"); no_gradient(out, "out");
+    const int save = PyObject_IsTrue(a[15]);
+    if (save < 0) return nullptr;
+    const std::array<int64_t, 2> row{c.d.D, c.d.S};
+    c.p.h0 = static_cast<const float*>(s.state(h0, row, at::kFloat, true, "h0"));
+    float* hf = static_cast<float*>(s.state(h_final, row, at::kFloat, true, "h_final"));
+    if (slots && !h_final) refuse("h_final", "with slots give h_final (it may be h0)");
+    gdn_rows yr{};
+    if (out) yr = s.out_rows(*out, c.d.D, "out");
+    Tensor y, hfo, kept;
+    {
+      const NoGil nogil;
+      const c10::cuda::OptionalCUDAGuard guard(s.dev);
+      if (!out) {
+        y = fresh(u.sizes(), s.type, s.dev);
+        yr = s.rows(&y, {c.d.D}, "out");
+        c.d.flags |= GDN_FLAG_ZERO_PADDING;
+      }
+      if (!h_final) {
+        hfo = fresh({s.q.B, row[0], row[1]}, at::kFloat, s.dev);
+        hf = hfo.data_ptr<float>();
+      }
+      float* rp = nullptr;
+      if (save) {
+        // an element at least, so that a call without tokens has residuals too
+        kept = fresh({(int64_t)std::max<size_t>(gdn_selective_scan_residual_bytes(&c.d, &s.q) / sizeof(float), 4)}, at::kFloat, s.dev);
+        rp = kept.data_ptr<float>();
+      }
+      c10::DataPtr ws;
+      const size_t need = gdn_selective_scan_workspace_bytes(&c.d, &s.q, s.max_q);
+      void* w = need || given ? scratch(given, need, u, &ws) : nullptr;
+      check("gdn_selective_scan_fwd", gdn_selective_scan_fwd(&c.d, &s.q, &c.p, s.max_q, &yr, hf, rp, w, stream_of(s.dev)));
+    }
+    return Py_BuildValue("(NNN)", out ? Py_NewRef(a[16]) : wrap(y), h_final ? Py_NewRef(a[9]) : wrap(hfo),
+                         save ? wrap(kept) : Py_NewRef(Py_None));
+  });
+}
+
+// (u, dt, A, B, C, D, z, dt_bias, dy, residuals, dh_final, need_dh0, cu_seqlens, max_q, flags, workspace)
+// -> (du, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0)
+PyObject* selective_scan_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("selective_scan_bwd", a, n, 16, [&]() -> PyObject* {
+    const Tensor &u = tensor(a[0], "u"), &dy = tensor(a[8], "dy"), &kept = tensor(a[9], "residuals");
+    const Tensor *dh = optional_tensor(a[10], "dh_final"), *given = optional_tensor(a[15], "workspace");
+    const int need_dh0 = PyObject_IsTrue(a[11]);
+    if (need_dh0 < 0) return nullptr;
+    Seqs s(u, "u", nullptr, optional_tensor(a[12], "cu_seqlens"), nullptr, a[13]);
+    const Scan c(s, a, integer(a[14]));
+    const gdn_rows dyr = s.rows(&dy, {c.d.D}, "dy");
+    const std::array<int64_t, 2> row{c.d.D, c.d.S};
+    const float* dhp = static_cast<const float*>(s.state(dh, row, at::kFloat, false, "dh_final"));
+    const int64_t size = (int64_t)std::max<size_t>(gdn_selective_scan_residual_bytes(&c.d, &s.q) / sizeof(float), 4);
+    if (kept.scalar_type() != at::kFloat || kept.sizes() != at::IntArrayRef({size}) || !kept.is_contiguous())
+      refuse("residuals", "residuals must be the forward's");
+    on_device(kept, s.dev, "residuals");
+    Tensor g[9];
+    {
+      const NoGil nogil;
+      const c10::cuda::OptionalCUDAGuard guard(s.dev);
+      const bool none = s.q.N == 0 && s.q.B == 0;  // nothing is launched, and the parameters' sums are zero
+      for (int i = 0; i < 8; ++i)
+        if (c.part[i])
+          g[i] = none ? at::zeros(c.part[i]->sizes(), c.part[i]->options())
+                      : fresh(c.part[i]->sizes(), c.part[i]->scalar_type(), s.dev);
+      if (need_dh0) g[8] = fresh({s.q.B, row[0], row[1]}, at::kFloat, s.dev);
+      auto fp = [&](int i) { return g[i].defined() ? g[i].data_ptr<float>() : nullptr; };
+      const gdn_scan_grads grads{g[0].data_ptr(), g[1].data_ptr(), g[6].defined() ? g[6].data_ptr() : nullptr, g[3].data_ptr(),
+                                 g[4].data_ptr(), fp(2), fp(5), fp(7), fp(8)};
+      c10::DataPtr ws;
+      void* w = scratch(given, gdn_selective_scan_bwd_workspace_bytes(&c.d, &s.q, s.max_q), u, &ws);
+      check("gdn_selective_scan_bwd", gdn_selective_scan_bwd(&c.d, &s.q, &c.p, kept.data_ptr<float>(), s.max_q, &dyr, dhp, &grads,
+                                                             w, stream_of(s.dev)));
+    }
+    PyObject* r = PyTuple_New(9);
+    for (int i = 0; r && i < 9; ++i) PyTuple_SET_ITEM(r, i, g[i].defined() ? wrap(g[i]) : Py_NewRef(Py_None));
+    return r;
+  });
+}
+
+// (page_table, kv_lens, new_tokens, free_pages, free_count, page_size, max_tokens)
+// -> (cu_seqlens, kv_lens, free_count, requests, positions, slots)
+PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("page_plan", a, n, 7, [&]() -> PyObject* {
+    const Tensor &table = tensor(a[0], "page_table"), &lens = tensor(a[1], "kv_lens"), &fresh_tokens = tensor(a[2], "new_tokens"),
+                 &pages = tensor(a[3], "free_pages"), &count = tensor(a[4], "free_count");
+    const c10::Device dev = table.device();
+    if (table.dim() != 2) refuse("page_table", "page_table must be [requests, pages per request]");
+    if (pages.dim() != 1) refuse("free_pages", "free_pages must be [pages]");
+    const int64_t B = table.size(0);
+    int_array(table, {B, table.size(1)}, dev, "page_table");
+    int_array(lens, {B}, dev, "kv_lens");
+    int_array(fresh_tokens, {B}, dev, "new_tokens");
+    int_array(pages, {pages.size(0)}, dev, "free_pages");
+    int_array(count, {1}, dev, "free_count");
+    gdn_plan_dims d;
+    d.B = to_int(B, "B");
+    d.page_size = to_int(integer(a[5]), "page_size");
+    d.max_pages = to_int(table.size(1), "max_pages");
+    d.num_free = to_int(pages.size(0), "num_free");
+    d.max_tokens = to_int(integer(a[6]), "max_tokens");
+    Tensor o[6];
+    {
+      const NoGil nogil;
+      const c10::cuda::OptionalCUDAGuard guard(dev);
+      const int64_t sizes[6] = {B + 1, B, 1, d.max_tokens, d.max_tokens, d.max_tokens};
+      for (int i = 0; i < 6; ++i) o[i] = fresh({sizes[i]}, i == 5 ? at::kLong : at::kInt, dev);
+      const gdn_plan_out out{o[0].data_ptr<int>(), o[1].data_ptr<int>(), o[2].data_ptr<int>(), o[3].data_ptr<int>(),
+                             o[4].data_ptr<int>(), reinterpret_cast<long long*>(o[5].data_ptr<int64_t>())};
+      check("gdn_page_plan", gdn_page_plan(&d, table.data_ptr<int>(), B > 1 ? table.stride(0) : table.size(1), lens.data_ptr<int>(),
+                                           fresh_tokens.data_ptr<int>(), pages.data_ptr<int>(), count.data_ptr<int>(), &out,
+                                           stream_of(dev)));
+    }
+    PyObject* r = PyTuple_New(6);
+    for (int i = 0; r && i < 6; ++i) PyTuple_SET_ITEM(r, i, wrap(o[i]));
+    return r;
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_XSETREF(g_error, Py_NewRef(cls));
   Py_RETURN_NONE;
@@ -420,6 +757,11 @@ PyMethodDef methods[] = {{"kv_append", FAST(kv_append), nullptr},
                          {"paged_attn", FAST(paged_attn), nullptr},
                          {"block_norm_fwd", FAST(block_norm_fwd), nullptr},
                          {"block_norm_bwd", FAST(block_norm_bwd), nullptr},
+                         {"causal_conv_fwd", FAST(causal_conv_fwd), nullptr},
+                         {"causal_conv_bwd", FAST(causal_conv_bwd), nullptr},
+                         {"selective_scan_fwd", FAST(selective_scan_fwd), nullptr},
+                         {"selective_scan_bwd", FAST(selective_scan_bwd), nullptr},
+                         {"page_plan", FAST(page_plan), nullptr},
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdn_ext", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

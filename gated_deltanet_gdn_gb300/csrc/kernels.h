@@ -290,6 +290,67 @@ struct AttnArgs {
 // page outside the cache, or a position beyond the rotation table.
 constexpr unsigned ERR_PAGE = 4u;
 
+// Bit set where a state's row lies outside its pool.
+constexpr unsigned ERR_SLOT = 8u;
+
+// Packed sequences and the rows of their states (packed.cuh).
+struct PackedArgs {
+  int N, B, T;       // rows; sequences; tokens of each without cu
+  const int* cu;     // [B + 1] or NULL
+  const int* lens;   // [B] cached tokens with the new ones, or NULL: every sequence goes on from its state
+  const int* slots;  // [B] rows of the state pools, or NULL: row b
+  int pool;          // rows of the pools
+  int zero_tail;     // rows behind the last sequence become zeros (else they are left alone)
+  unsigned* err;
+};
+
+// Short causal convolution (causal_conv.cu). Strides in elements; weights [C][taps].
+constexpr int CONV_MAX_TAPS = 4;
+struct ConvArgs {
+  PackedArgs q;
+  int C, taps, bf16, silu;
+  const void *x, *w, *bias, *state0, *dy, *dstate;
+  long long x_ts, dy_ts, y_ts;
+  void *y, *state_final;
+  void *dx, *dw, *dbias, *dstate0;
+  float* partial;  // [conv_bwd_parts][taps + 1][C]
+  int run;         // tokens of a thread
+  int max_q;
+};
+
+// Selective state space scan (selective_scan.cu, selective_scan_bwd.cu): D channels in G groups, NS states each.
+struct ScanArgs {
+  PackedArgs q;
+  int D, G, NS, bf16, softplus;
+  const void *u, *dt, *z, *B, *C, *dy;
+  long long u_ts, dt_ts, z_ts, b_ts, b_gs, c_ts, c_gs, dy_ts, y_ts;
+  const float *A, *skip, *bias, *h0;
+  void* y;
+  float* h_final;
+  float* kept;  // states at every scan_tile(NS) tokens, or NULL
+  int max_q;
+  // backward
+  const float* dh_final;
+  void *du, *ddt, *dz, *dB, *dC;
+  float *dA, *dskip, *dbias, *dh0;
+  void* ws;
+};
+// Tokens between two kept states (a tile of the kernels).
+constexpr int scan_tile(int NS) { return NS == 8 ? 8 : 16; }
+
+// Plan of a serving step (page_plan.cu).
+constexpr int PLAN_MAX_REQUESTS = 8192;
+struct PlanArgs {
+  int B, page_size, max_pages, max_tokens, num_free;
+  int* page_table;
+  long long pt_stride;
+  const int *kv_lens, *new_tokens, *free_count;
+  int* free_pages;
+  int *cu, *lens_out, *count_out, *requests, *positions;
+  long long* slots;
+  unsigned* err;
+};
+
 // Kernel identifiers for the optional per-launch timing (gdn_profile_* in the C ABI).
 enum KernelId {
   K_PREP = 0,      // chunk_prep_kernel
@@ -321,7 +382,18 @@ enum KernelId {
   K_ATTN_JOIN = 26,     // paged_attn_join_kernel: joins the parts of split rows
   K_ATTN_TC = 27,       // paged_attn_tc_kernel (tcgen05)
   K_ATTN_TC_JOIN = 28,  // paged_attn_tc_join_kernel
-  K_COUNT = 29
+  K_CONV_FWD = 29,      // causal_conv_fwd_kernel
+  K_CONV_BWD = 30,      // causal_conv_bwd_kernel
+  K_CONV_WGRAD = 31,    // causal_conv_wgrad_kernel: adds the backward's partial weight gradients
+  K_SCAN_SUM = 32,      // selective_scan_kernel without outputs: what each chunk adds to the state
+  K_SCAN_CARRY = 33,    // selective_scan_carry_kernel: the states at the chunks' starts
+  K_SSCAN = 34,         // selective_scan_kernel
+  K_SSTEP = 35,         // selective_step_kernel: one token a sequence
+  K_SSCAN_RSUM = 36,    // selective_scan_bwd_sum_kernel: what each chunk adds to the adjoint
+  K_SSCAN_BWD = 37,     // selective_scan_bwd_kernel
+  K_SSCAN_JOIN = 38,    // selective_scan_join_kernel: adds the backward's partial sums
+  K_PAGE_PLAN = 39,     // page_plan_kernel
+  K_COUNT = 40
 };
 // Records a CUDA event on s before (begin = true) or after a launch when timing is on.
 void prof_mark(KernelId id, cudaStream_t s, bool begin);
@@ -383,5 +455,16 @@ size_t paged_attn_workspace(const AttnArgs& a);  // bytes of AttnArgs::ws
 bool paged_attn_tc_applies(const AttnArgs& a);
 size_t paged_attn_tc_workspace(const AttnArgs& a);
 cudaError_t launch_paged_attn_tc(const AttnArgs& a, cudaStream_t s, bool* done);
+// Short causal convolution (causal_conv.cu). wide: widths, strides and pointers allow 16-byte accesses.
+cudaError_t launch_causal_conv(const ConvArgs& a, bool wide, cudaStream_t s);
+cudaError_t launch_causal_conv_bwd(const ConvArgs& a, bool wide, cudaStream_t s);
+size_t causal_conv_workspace(const ConvArgs& a);
+// Selective scan. wide: accesses of four elements.
+cudaError_t launch_selective_scan(const ScanArgs& a, bool wide, cudaStream_t s);
+size_t selective_scan_workspace(const ScanArgs& a);
+cudaError_t launch_selective_scan_bwd(const ScanArgs& a, bool wide, cudaStream_t s);
+size_t selective_scan_bwd_workspace(const ScanArgs& a);
+// Plan of a serving step (page_plan.cu).
+cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t s);
 
 }  // namespace gdn

@@ -424,6 +424,138 @@ int gdn_block_norm_bwd(const gdn_norm_dims* dims, const gdn_norm_parts* parts, c
                        const gdn_rows* dh, const gdn_rows* dy, const gdn_norm_grads* grads,
                        void* workspace, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The recurrent mixers' other operators: the short causal convolution in front of
+ * a mixer, and the selective state space scan, a mixer beside the rule.
+ *
+ * Sequences. gdn_packed says which rows of [N, ...] tensors belong to which
+ * sequence: with cu_seqlens rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (the
+ * arrays of the paged calls above serve here too; a sequence may be empty), without
+ * it sequence b has the N / B rows from b N / B on. Rows from cu_seqlens[B] on are padding:
+ * their values are not used; outputs there are left as they were, or become zero with
+ * GDN_FLAG_ZERO_PADDING; gradients there are zero.
+ * States lie in pools of `pool` rows; sequence b's is row slots[b] (row b without
+ * slots; then pool >= B). A negative slot means no state: the sequence starts from
+ * zeros and its last state is not kept. A slot of pool or more counts as negative
+ * and sets bit 8 of the device error word. Two sequences of a call must not have
+ * the same slot. With kv_lens (cached tokens with the new ones) a sequence whose
+ * new tokens are its first starts from zeros whatever its slot holds. Initial and
+ * final states may be the same memory (in-place carry). A sequence without tokens
+ * hands its initial state on. Rows of the pools that no sequence has are left alone.
+ * The arrays are device memory, read by the kernels only: a captured graph replays
+ * with other lengths. max_q (> 0) bounds the tokens of one sequence; it chooses the
+ * kernels' split and changes results by no more than the order of float32 sums.
+ * Row tensors are [N, C] with any row stride; multiples of 16 bytes (the scan: of
+ * four elements) in C, strides and pointers take the wide loads, others go element by
+ * element. The backward calls take no slots and no kv_lens.
+ * Errors: GDN_ERR_INVALID_ARG as above (N not a multiple of B without cu_seqlens, pool too
+ * small, unknown flags); GDN_ERR_UNSUPPORTED for sizes out of the given ranges, N above
+ * 2^30 or more CTAs than a grid holds. */
+typedef struct {
+  int N, B, pool;
+  const int* cu_seqlens; /* [B + 1] or NULL */
+  const int* kv_lens;    /* [B] or NULL */
+  const int* slots;      /* [B] or NULL */
+} gdn_packed;
+#define GDN_FLAG_CONV_SILU 64
+#define GDN_FLAG_DT_SOFTPLUS 128
+#define GDN_FLAG_ZERO_PADDING 256
+
+/* Short causal convolution, every channel by itself:
+ *     pre_t = bias + sum_j w_j x_{t - taps + 1 + j},   y_t = pre_t, or silu(pre_t) by flag
+ * with the state, the taps - 1 inputs before the first token, in front of a sequence
+ * (zeros without one). x, y, dy, dx [N, C], weight [C, taps], bias [C] (NULL = none), state0 and
+ * state_final [pool, taps - 1, C] (NULL = zeros; not wanted), all of dims.dtype.
+ * taps 2 to 4 (else GDN_ERR_UNSUPPORTED). Arithmetic is float32, rounded once;
+ * silu takes the hardware's approximate exponential and reciprocal.
+ * The backward takes the forward's inputs, dy and dstate (the gradient of state_final, [B,
+ * taps - 1, C] or NULL) and writes dx [N, C] contiguous, dweight, and, where not NULL,
+ * dbias and dstate0 [B, taps - 1, C]. Weight gradients are summed in float32 in a
+ * fixed order. workspace: gdn_causal_conv_workspace_bytes, 256-byte aligned. */
+typedef struct {
+  int C, taps;
+  int dtype;
+  int flags; /* GDN_FLAG_CONV_SILU, GDN_FLAG_ZERO_PADDING */
+} gdn_conv_dims;
+int gdn_causal_conv_fwd(const gdn_conv_dims* dims, const gdn_packed* seqs, const gdn_rows* x,
+                        const void* weight, const void* bias, const void* state0, int max_q,
+                        const gdn_rows* y, void* state_final, void* stream);
+size_t gdn_causal_conv_workspace_bytes(const gdn_conv_dims* dims, const gdn_packed* seqs);
+int gdn_causal_conv_bwd(const gdn_conv_dims* dims, const gdn_packed* seqs, const gdn_rows* x,
+                        const void* weight, const void* bias, const void* state0, const gdn_rows* dy,
+                        const void* dstate, void* dx, void* dweight, void* dbias, void* dstate0,
+                        void* workspace, void* stream);
+
+/* Selective state space scan. Per channel d of group g = d / (D / G) and state n:
+ *     delta_t = dt_t + dt_bias, or softplus of it by flag
+ *     h_t = exp(delta_t A[d][n]) h_{t-1} + delta_t u_t B_t[g][n]
+ *     y_t = (sum_n C_t[g][n] h_t[n] + skip[d] u_t) silu(z_t)
+ * u, dt, z, y, dy [N, D]; B, C [N, G, S] with any row and group strides; of dims.dtype. A [D, S], skip
+ * [D], dt_bias [D], h0 and h_final [pool, D, S] are float32 (16-byte aligned). z, skip, dt_bias and h0 may be
+ * NULL (no gate, zeros), h_final too (not wanted). S is 8, 16, 32 or 64 and D a multiple of G
+ * (else GDN_ERR_UNSUPPORTED, GDN_ERR_INVALID_ARG). States and sums are float32, outputs
+ * rounded once; exp, softplus and silu take the hardware's approximate functions (relative
+ * error of a few 2^-23). Values are not clipped: A of any sign.
+ * residuals: NULL, or gdn_selective_scan_residual_bytes for the backward (states at every 8 or 16 tokens,
+ * float32). workspace: gdn_selective_scan_workspace_bytes (may be 0, then NULL), 256-byte aligned.
+ * The backward takes the forward's inputs and residuals, dy and dh_final ([B, D, S] or NULL) and writes
+ * the gradients, contiguous, du, ddt, dB, dC and dz of dims.dtype, dA, dskip, ddt_bias and dh0 ([B, D, S])
+ * float32; dz, dskip, ddt_bias and dh0 may be NULL, and must be for absent parts (dh0 excepted: it may
+ * be wanted without h0). Sums over tokens and channels are float32, in a fixed order. */
+typedef struct {
+  int D, G, S;
+  int dtype;
+  int flags; /* GDN_FLAG_DT_SOFTPLUS, GDN_FLAG_ZERO_PADDING */
+} gdn_scan_dims;
+typedef struct {
+  gdn_rows u, dt, z, B, C;
+  const float *A, *skip, *dt_bias, *h0;
+} gdn_scan_parts;
+typedef struct {
+  void *du, *ddt, *dz, *dB, *dC;
+  float *dA, *dskip, *ddt_bias, *dh0;
+} gdn_scan_grads;
+size_t gdn_selective_scan_residual_bytes(const gdn_scan_dims* dims, const gdn_packed* seqs);
+size_t gdn_selective_scan_workspace_bytes(const gdn_scan_dims* dims, const gdn_packed* seqs, int max_q);
+int gdn_selective_scan_fwd(const gdn_scan_dims* dims, const gdn_packed* seqs, const gdn_scan_parts* parts,
+                           int max_q, const gdn_rows* y, float* h_final, float* residuals,
+                           void* workspace, void* stream);
+size_t gdn_selective_scan_bwd_workspace_bytes(const gdn_scan_dims* dims, const gdn_packed* seqs, int max_q);
+int gdn_selective_scan_bwd(const gdn_scan_dims* dims, const gdn_packed* seqs, const gdn_scan_parts* parts,
+                           const float* residuals, int max_q, const gdn_rows* dy, const float* dh_final,
+                           const gdn_scan_grads* grads, void* workspace, void* stream);
+
+/* Plan of a serving step over the paged cache, on the device: from each request's
+ * cached length and its new tokens, the pages it takes or gives back and the packed
+ * arrays that the step's calls read.
+ * kv_lens, new_tokens [B]: a positive count asks for that many new tokens, a negative one gives
+ * the last tokens back (a rejected draft; -length or less: all of them, a finished request). free_pages
+ * [num_free] is a stack of page numbers, its first free_count[0] valid. Pages given
+ * back are pushed in order of request and position; then request after request pops
+ * the pages it needs, in order of position. A request is granted whole or not at all: it is
+ * where the pages asked for by it and by the requests before it are at most those there are (or it needs
+ * none), and its tokens and those before it at most max_tokens; else it has no
+ * tokens in the step and keeps its length. A request that does not fit a row of page_table, or a length
+ * outside it (which counts as clamped to it), sets bit 4 of the device error word, the former with no
+ * tokens, and so does a stack that overflows.
+ * page_table (rows of max_pages, stride apart) and free_pages are changed in place;
+ * entries of pages given back stay as they were. Outputs, none the same memory as an
+ * input: cu_seqlens [B + 1], kv_lens [B] (after the step), free_count [1], and for each of the max_tokens packed
+ * rows the request, its position in it and its slot in the cache (page * page_size + row, 64-bit), -1
+ * behind the last token.
+ * B up to 8192, max_tokens up to 2^30, page_size 1 or more (else GDN_ERR_UNSUPPORTED, GDN_ERR_INVALID_ARG). */
+typedef struct {
+  int B, page_size, max_pages, num_free, max_tokens;
+} gdn_plan_dims;
+typedef struct {
+  int *cu_seqlens, *kv_lens, *free_count;
+  int *requests, *positions; /* [max_tokens] */
+  long long* slots;          /* [max_tokens] */
+} gdn_plan_out;
+int gdn_page_plan(const gdn_plan_dims* dims, int* page_table, long long page_table_stride, const int* kv_lens,
+                  const int* new_tokens, int* free_pages, const int* free_count, const gdn_plan_out* out,
+                  void* stream);
+
 /* Self-test of the failure path: launches a one-thread kernel that first waits,
  * with the library's cross-CTA counter wait (the one the forward's output CTAs use
  * on the scan), for a counter nothing raises, and gives up after max_tries polls
@@ -444,7 +576,7 @@ int gdn_selftest_wait_timeout(unsigned max_tries, unsigned long long* cycles, vo
  * (bits, OR-ed: 1 = a kernel gave up waiting for one of its own asynchronous
  * copies; 2 = a replay fill count was outside [0, L]; 4 = a paged call met a
  * length beyond its page table, a page outside the cache, or a position beyond
- * the rotation table).
+ * the rotation table, or a plan a full stack; 8 = a state's slot outside its pool).
  * Synchronises the device. Returns GDN_OK when the word was zero,
  * GDN_ERR_INTERNAL when it was not, GDN_ERR_CUDA if the read failed. */
 int gdn_check_device_error(void);
@@ -478,7 +610,10 @@ int gdn_version(void);
  * 20 the mid-block records (GDN_FLAG_CHUNK128 only), 21 block norms forward,
  * 22 backward and 23 the sums of its weight gradients, 24 paged cache append,
  * 25 paged attention of few rows and 26 the join of its parts, 27 paged attention on
- * tcgen05 tensor cores and 28 the join of its parts; gdn_kernel_name(id) names them
+ * tcgen05 tensor cores and 28 the join of its parts, 29 causal convolution forward, 30 backward
+ * and 31 the sums of its weight gradients, 32 the selective scan's chunk ends, 33 their
+ * carry and 34 the scan, 35 the scan of single tokens, 36 the backward's chunk ends,
+ * 37 the scan backward and 38 the join of its partial sums, 39 the plan of a step; gdn_kernel_name(id) names them
  * ("" for an unknown id). Not part of the paper's method: instrumentation. */
 int gdn_profile_enable(int on);
 int gdn_profile_read(double* ms, int* launches, int n);
