@@ -174,6 +174,16 @@ Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, c10::Device dev) {
   return Tensor(at::detail::empty_cuda(sizes, type, dev, std::nullopt));
 }
 
+// A contiguous vector of n elements, `at` bytes into memory that it shares (at a multiple of their size).
+Tensor part_of(const Tensor& all, int64_t at, int64_t n, at::ScalarType type) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                      c10::scalarTypeToTypeMeta(type));
+  c10::TensorImpl* const impl = t.unsafeGetTensorImpl();
+  impl->set_storage_offset(at / (int64_t)c10::elementSize(type));
+  impl->set_sizes_contiguous({n});
+  return t;
+}
+
 // Scratch of at least `need` bytes on the current device: the caller's, or new.
 void* scratch(const Tensor* w, size_t need, const Tensor& like, c10::DataPtr* own) {
   if (w) {
@@ -733,14 +743,20 @@ PyObject* page_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     {
       const NoGil nogil;
       const c10::cuda::OptionalCUDAGuard guard(dev);
-      const int64_t sizes[6] = {B + 1, B, 1, d.max_tokens, d.max_tokens, d.max_tokens};
-      for (int i = 0; i < 6; ++i) o[i] = fresh({sizes[i]}, i == 5 ? at::kLong : at::kInt, dev);
-      const gdn_plan_out out{o[0].data_ptr<int>(), o[1].data_ptr<int>(), o[2].data_ptr<int>(), o[3].data_ptr<int>(),
-                             o[4].data_ptr<int>(), reinterpret_cast<long long*>(o[5].data_ptr<int64_t>())};
+      // one allocation for all six, on 16-byte boundaries (six took half of the call's time)
+      const int64_t sizes[6] = {d.max_tokens, d.max_tokens, d.max_tokens, B + 1, B, 1};
+      int64_t at[7] = {0};
+      for (int i = 0; i < 6; ++i) at[i + 1] = at[i] + (sizes[i] * (i ? 4 : 8) + 15) / 16 * 16;
+      const Tensor all = fresh({at[6]}, at::kByte, dev);
+      for (int i = 0; i < 6; ++i) o[i] = part_of(all, at[i], sizes[i], i ? at::kInt : at::kLong);
+      const gdn_plan_out out{o[3].data_ptr<int>(), o[4].data_ptr<int>(), o[5].data_ptr<int>(), o[1].data_ptr<int>(),
+                             o[2].data_ptr<int>(), reinterpret_cast<long long*>(o[0].data_ptr<int64_t>())};
       check("gdn_page_plan", gdn_page_plan(&d, table.data_ptr<int>(), B > 1 ? table.stride(0) : table.size(1), lens.data_ptr<int>(),
                                            fresh_tokens.data_ptr<int>(), pages.data_ptr<int>(), count.data_ptr<int>(), &out,
                                            stream_of(dev)));
     }
+    std::rotate(o, o + 3, o + 6);  // cu_seqlens, kv_lens, free_count, slots, requests, positions
+    std::rotate(o + 3, o + 4, o + 6);
     PyObject* r = PyTuple_New(6);
     for (int i = 0; r && i < 6; ++i) PyTuple_SET_ITEM(r, i, wrap(o[i]));
     return r;

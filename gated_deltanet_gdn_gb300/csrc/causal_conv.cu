@@ -4,15 +4,18 @@
 //
 // Bound by memory: forward reads x and writes y, backward reads x and dy and writes dx.
 // A thread owns a vector of channels and a run of tokens, keeps the window of the last K
-// inputs in registers and has a batch of BATCH tokens' loads in flight; neighbouring
+// inputs in registers and has the next BATCH tokens' loads in flight while it works on these; neighbouring
 // threads own neighbouring vectors, so rows are read whole. A run reads the K - 1 inputs
 // before it again (from L2). The sequence's first run alone reads the state and alone writes the next one, so
 // that both may be the same memory however long the sequence is.
 //
 // Backward, with dpre = dy act'(pre): dx_t = sum_j w_j dpre_{t + K - 1 - j} looks K - 1 tokens ahead, so a run forms
 // pre and dpre for its own tokens and K - 1 more, and its weight gradient dw_j = sum_t dpre_t x_{t - K + 1 + j} for
-// its own. A thread takes several runs, so that the partial weight gradients, added in a fixed
-// order by a second kernel, stay a small share of the traffic.
+// its own. Runs are as long as a few threads per lane of the GPU allow, so that the partial weight gradients, added in a
+// fixed order by a second kernel, stay a small share of the traffic.
+//
+// Values go two by two through the fp32 instructions (fma.rn.f32x2): with one by one, the arithmetic of 2304 channels x
+// 32,768 tokens took as long as their bytes (75 us forward, 200 us backward).
 #include "packed.cuh"
 #include "pairs.cuh"
 
@@ -20,37 +23,11 @@ namespace gdn {
 namespace {
 
 constexpr int THREADS = 128;
-constexpr int BATCH = 8;       // tokens whose loads are in flight
-constexpr int BWD_BATCH = 4;
 
-template <class T, int V>
-__device__ __forceinline__ void load_v(const T* p, float (&x)[V]) {
-  if constexpr (V == 1) {
-    x[0] = to_f32(*p);
-  } else {
-    alignas(16) T e[V];
-    if constexpr (sizeof(T) * V == 16) *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
-    else *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = to_f32(e[i]);
-  }
-}
-template <class T, int V>
-__device__ __forceinline__ void store_v(T* p, const float (&x)[V]) {
-  if constexpr (V == 1) {
-    *p = from_f32<T>(x[0]);
-  } else {
-    alignas(16) T e[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) e[i] = from_f32<T>(x[i]);
-    if constexpr (sizeof(T) * V == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
-    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
-  }
-}
-// The vector as loaded, to be converted where it is used.
+// V channels of a token as they lie in memory, and as pairs (V = 1: one pair, its second half unused).
 template <class T, int V>
 struct Raw {
-  static constexpr int W = (int)sizeof(T) * V >= 4 ? (int)sizeof(T) * V / 4 : 1;
+  static constexpr int W = (int)sizeof(T) * V >= 4 ? (int)sizeof(T) * V / 4 : 1, NP = V > 1 ? V / 2 : 1;
   uint32_t w[W];
   __device__ __forceinline__ void load(const T* p) {
     if constexpr (sizeof(T) * V == 16) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
@@ -62,68 +39,84 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < W; ++i) w[i] = 0;
   }
-  __device__ __forceinline__ void floats(float (&x)[V]) const {
+  __device__ __forceinline__ void pairs(f32x2 (&x)[NP]) const {
     if constexpr (V == 1) {
-      x[0] = __uint_as_float(w[0]);
+      x[0] = pack2(__uint_as_float(w[0]), 0.f);
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = __uint_as_float(w[i]);
+      for (int i = 0; i < NP; ++i) x[i] = pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     } else {
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
+      for (int i = 0; i < NP; ++i) x[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
   }
 };
+template <class T, int V>
+__device__ __forceinline__ void load_v(const T* p, f32x2 (&x)[Raw<T, V>::NP]) {
+  Raw<T, V> r;
+  r.load(p);
+  r.pairs(x);
+}
+template <class T, int V>
+__device__ __forceinline__ void store_v(T* p, const f32x2 (&x)[Raw<T, V>::NP]) {
+  if constexpr (V == 1) {
+    *p = from_f32<T>(split2(x[0]).x);
+  } else {
+    alignas(16) T e[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 f = split2(x[i]);
+      store2(e + 2 * i, f.x, f.y);
+    }
+    if constexpr (sizeof(T) * V == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
+    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+  }
+}
 
 // Weights [C][K] of channels c .. c + V - 1, and the bias.
-template <class T, int V, int K>
-__device__ __forceinline__ void load_weights(const ConvArgs& a, int c, float (&w)[K][V], float (&bias)[V]) {
+template <class T, int V, int K, int NP>
+__device__ __forceinline__ void load_weights(const ConvArgs& a, int c, f32x2 (&w)[K][NP], f32x2 (&bias)[NP]) {
   const T* wp = static_cast<const T*>(a.w) + (long long)c * K;
+  float flat[2 * NP * K];
   if constexpr (V == 1) {
 #pragma unroll
-    for (int j = 0; j < K; ++j) w[j][0] = to_f32(wp[j]);
+    for (int j = 0; j < 2 * K; ++j) flat[j] = j < K ? to_f32(wp[j]) : 0.f;
   } else {
-    float flat[V * K];
 #pragma unroll
     for (int i = 0; i < V * K; i += V) {
-      float part[V];
+      f32x2 part[NP];
       load_v<T, V>(wp + i, part);
 #pragma unroll
-      for (int e = 0; e < V; ++e) flat[i + e] = part[e];
+      for (int e = 0; e < NP; ++e) {
+        const float2 f = split2(part[e]);
+        flat[i + 2 * e] = f.x;
+        flat[i + 2 * e + 1] = f.y;
+      }
     }
-#pragma unroll
-    for (int j = 0; j < K; ++j)
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[j][e] = flat[e * K + j];
   }
 #pragma unroll
-  for (int e = 0; e < V; ++e) bias[e] = 0.f;
+  for (int j = 0; j < K; ++j)
+#pragma unroll
+    for (int e = 0; e < NP; ++e) w[j][e] = pack2(flat[2 * e * K + j], flat[(2 * e + 1) * K + j]);
+#pragma unroll
+  for (int e = 0; e < NP; ++e) bias[e] = both(0.f);
   if (a.bias) load_v<T, V>(static_cast<const T*>(a.bias) + c, bias);
 }
 
-// The K - 1 inputs before token t of the sequence: its own rows, or the state's (zeros without one).
+// The input i - (K - 1) before token t of the sequence: its own row, or the state's (zeros without one).
 template <class T, int V, int K>
-__device__ __forceinline__ void load_past(const ConvArgs& a, const Chunk& k, int t, const T* state, int c, float (&past)[K - 1][V]) {
-  const T* x = static_cast<const T*>(a.x);
-#pragma unroll
-  for (int i = 0; i < K - 1; ++i) {
-    const int at = t - (K - 1) + i;
-    if (at >= 0) {
-      load_v<T, V>(x + (k.first + (long long)at) * a.x_ts + c, past[i]);
-    } else if (state) {
-      load_v<T, V>(state + (long long)(at + K - 1) * a.C + c, past[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) past[i][e] = 0.f;
-    }
-  }
+__device__ __forceinline__ void load_past(const ConvArgs& a, const Chunk& k, int at, const T* state, int c,
+                                          f32x2 (&past)[Raw<T, V>::NP]) {
+  Raw<T, V> r;
+  r.zero();
+  if (at >= 0) r.load(static_cast<const T*>(a.x) + (k.first + (long long)at) * a.x_ts + c);
+  else if (state) r.load(state + (long long)(at + K - 1) * a.C + c);
+  r.pairs(past);
 }
 
-template <class T, int V, int K, bool SILU>
+template <class T, int V, int K, bool SILU, int BATCH>
 __global__ void __launch_bounds__(THREADS) causal_conv_fwd_kernel(ConvArgs a) {
+  constexpr int NP = Raw<T, V>::NP;
   pdl_wait();
   pdl_trigger();
   const int vecs = a.C / V;
@@ -133,14 +126,25 @@ __global__ void __launch_bounds__(THREADS) causal_conv_fwd_kernel(ConvArgs a) {
   if (number >= packed_numbers(a.q, a.run)) return;
   Chunk k;
   if (!packed_chunk(a.q, number, a.run, &k)) return;
-  T* y = static_cast<T*>(a.y);
   const int t0 = k.j * a.run, t1 = min(k.len, t0 + a.run);
+  T* y = static_cast<T*>(a.y) + (k.first + (long long)t0) * a.y_ts + c;
   if (k.b == a.q.B) {
-    float none[V] = {};
+    f32x2 none[NP];
+#pragma unroll
+    for (int e = 0; e < NP; ++e) none[e] = both(0.f);
     if (a.q.zero_tail)
-      for (int t = t0; t < t1; ++t) store_v<T, V>(y + (k.first + (long long)t) * a.y_ts + c, none);
+      for (int t = t0; t < t1; ++t, y += a.y_ts) store_v<T, V>(y, none);
     return;
   }
+  const T* x = static_cast<const T*>(a.x) + (k.first + (long long)t0) * a.x_ts + c;
+  Raw<T, V> raw[BATCH];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (t + i < t1) raw[i].load(x + i * a.x_ts);
+    x += BATCH * a.x_ts;
+  };
+  fetch(t0);
   const T* state = nullptr;
   T* next = nullptr;
   if (k.j == 0) {  // runs are longer than a state
@@ -149,65 +153,49 @@ __global__ void __launch_bounds__(THREADS) causal_conv_fwd_kernel(ConvArgs a) {
     if (slot >= 0 && a.state0 && packed_goes_on(a.q, k.b, k.len)) state = static_cast<const T*>(a.state0) + at;
     if (slot >= 0 && a.state_final) next = static_cast<T*>(a.state_final) + at;
   }
-  float w[K][V], bias[V], win[K][V];  // win[K - 1]: the current input
-  float old[K - 1][V];
-  load_past<T, V, K>(a, k, t0, state, c, old);
+  f32x2 w[K][NP], bias[NP], win[K][NP];  // win[K - 1]: the current input
 #pragma unroll
-  for (int i = 0; i < K - 1; ++i)
-#pragma unroll
-    for (int e = 0; e < V; ++e) win[i][e] = old[i][e];
+  for (int i = 0; i < K - 1; ++i) load_past<T, V, K>(a, k, t0 - (K - 1) + i, state, c, win[i]);
   load_weights<T, V, K>(a, c, w, bias);
-  const T* x = static_cast<const T*>(a.x) + (long long)k.first * a.x_ts + c;
-  y += (long long)k.first * a.y_ts + c;
+  // The last K - 1 of the state's inputs and the sequence's: all that this thread reads of the state is
+  // read by now, whatever it writes.
+  if (next) {
+    f32x2 last[K - 1][NP];
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) load_past<T, V, K>(a, k, k.len - (K - 1) + i, state, c, last[i]);
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) store_v<T, V>(next + (long long)i * a.C + c, last[i]);
+  }
   for (int t = t0; t < t1; t += BATCH) {
-    Raw<T, V> raw[BATCH];
+    Raw<T, V> now[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) now[i] = raw[i];
+    fetch(t + BATCH);
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      if (t + i < t1) raw[i].load(x + (long long)(t + i) * a.x_ts);
-      else raw[i].zero();
-    }
+      now[i].pairs(win[K - 1]);
+      f32x2 out[NP];
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      raw[i].floats(win[K - 1]);
-      float out[V];
+      for (int e = 0; e < NP; ++e) {
+        f32x2 pre = bias[e];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float pre = bias[e];
-#pragma unroll
-        for (int j = 0; j < K; ++j) pre = fmaf(w[j][e], win[j][e], pre);
-        out[e] = SILU ? pre * sigmoid(pre) : pre;
+        for (int j = 0; j < K; ++j) pre = fma2(w[j][e], win[j][e], pre);
+        out[e] = SILU ? mul2(pre, sigmoid2(pre)) : pre;
       }
-      if (t + i < t1) store_v<T, V>(y + (long long)(t + i) * a.y_ts, out);
+      if (t + i < t1) store_v<T, V>(y, out);
+      y += a.y_ts;
 #pragma unroll
       for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-        for (int e = 0; e < V; ++e) win[j][e] = win[j + 1][e];
+        for (int e = 0; e < NP; ++e) win[j][e] = win[j + 1][e];
     }
-  }
-  if (next) {  // the last K - 1 of the state's inputs and the sequence's
-    float last[K - 1][V];
-#pragma unroll
-    for (int i = 0; i < K - 1; ++i) {
-      const int at = k.len - (K - 1) + i;
-      if (at >= 0) {
-        load_v<T, V>(x + (long long)at * a.x_ts, last[i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          last[i][e] = 0.f;
-#pragma unroll
-          for (int o = 0; o < K - 1; ++o) last[i][e] = o == at + K - 1 ? old[o][e] : last[i][e];
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < K - 1; ++i) store_v<T, V>(next + (long long)i * a.C + c, last[i]);
   }
 }
 
 // Gradients. Token indexes run from -(K - 1), the state's inputs, to len - 1.
 template <class T, int V, int K, bool SILU>
-__global__ void __launch_bounds__(THREADS) causal_conv_bwd_kernel(ConvArgs a, int parts, long long numbers) {
+__global__ void __launch_bounds__(THREADS, 4) causal_conv_bwd_kernel(ConvArgs a, int parts, long long numbers) {
+  constexpr int NP = Raw<T, V>::NP, BATCH = 4;
   pdl_wait();
   pdl_trigger();
   const int vecs = a.C / V;
@@ -215,99 +203,111 @@ __global__ void __launch_bounds__(THREADS) causal_conv_bwd_kernel(ConvArgs a, in
   const int part = (int)(item / vecs);
   const int c = (int)(item - (long long)part * vecs) * V;
   if (part >= parts) return;
-  float w[K][V], bias[V], dw[K][V] = {}, db[V] = {};
+  f32x2 w[K][NP], bias[NP], dw[K][NP], db[NP];
+#pragma unroll
+  for (int e = 0; e < NP; ++e) {
+    db[e] = both(0.f);
+#pragma unroll
+    for (int j = 0; j < K; ++j) dw[j][e] = both(0.f);
+  }
   load_weights<T, V, K>(a, c, w, bias);
   for (long long number = part; number < numbers; number += parts) {
     Chunk k;
     if (!packed_chunk(a.q, number, a.run, &k)) continue;
-    T* dx = static_cast<T*>(a.dx) + (long long)k.first * a.C + c;
     const int t0 = k.j * a.run, t1 = min(k.len, t0 + a.run);
+    T* dx = static_cast<T*>(a.dx) + (k.first + (long long)t0) * a.C + c;  // of token t0, moving on with the tokens
     if (k.b == a.q.B) {
-      float none[V] = {};
-      for (int t = t0; t < t1; ++t) store_v<T, V>(dx + (long long)t * a.C, none);
+      f32x2 none[NP];
+#pragma unroll
+      for (int e = 0; e < NP; ++e) none[e] = both(0.f);
+      for (int t = t0; t < t1; ++t, dx += a.C) store_v<T, V>(dx, none);
       continue;
     }
     const long long held = (long long)k.b * (K - 1) * a.C + c;
     const T* state = a.state0 ? static_cast<const T*>(a.state0) + held - c : nullptr;
     const T* dstate = a.dstate ? static_cast<const T*>(a.dstate) + held : nullptr;
-    float win[K][V], dpre[K][V];  // inputs t - K + 1 .. t and their outputs' gradients
+    // inputs whose gradients are this run's: its own tokens, and the state's for the first run
+    const int from = k.j == 0 ? -(K - 1) : t0, stop = t1 + K - 1, real = min(stop, k.len);
+    const T* x = static_cast<const T*>(a.x) + (k.first + (long long)t0) * a.x_ts + c;
+    const T* dy = static_cast<const T*>(a.dy) + (k.first + (long long)t0) * a.dy_ts + c;
+    Raw<T, V> rx[BATCH], rd[BATCH];
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        rx[i].zero();
+        rd[i].zero();
+        if (t + i < real) {
+          rx[i].load(x + i * a.x_ts);
+          rd[i].load(dy + i * a.dy_ts);
+        }
+      }
+      x += BATCH * a.x_ts;
+      dy += BATCH * a.dy_ts;
+    };
+    fetch(t0);
+    f32x2 win[K][NP], dpre[K][NP];  // inputs t - K + 1 .. t and their outputs' gradients
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) load_past<T, V, K>(a, k, t0 - (K - 1) + i, state, c, win[i]);
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
-      for (int e = 0; e < V; ++e) dpre[j][e] = 0.f;
-    {
-      float old[K - 1][V];
-      load_past<T, V, K>(a, k, t0, state, c, old);
+      for (int e = 0; e < NP; ++e) dpre[j][e] = both(0.f);
+    dx -= (K - 1) * (long long)a.C;  // the gradient that is complete at token t is of token t - (K - 1)
+    for (int t = t0; t < stop; t += BATCH) {
+      Raw<T, V> nx[BATCH], nd[BATCH];
 #pragma unroll
-      for (int i = 0; i < K - 1; ++i)
-#pragma unroll
-        for (int e = 0; e < V; ++e) win[i][e] = old[i][e];
-    }
-    const T* x = static_cast<const T*>(a.x) + (long long)k.first * a.x_ts + c;
-    const T* dy = static_cast<const T*>(a.dy) + (long long)k.first * a.dy_ts + c;
-    // the gradient of input t, once dpre of t .. t + K - 1 is in dpre[0 .. K - 1]
-    auto emit = [&](int t) {
-      float g[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        g[e] = 0.f;
-#pragma unroll
-        for (int j = 0; j < K; ++j) g[e] = fmaf(w[j][e], dpre[K - 1 - j][e], g[e]);
+      for (int i = 0; i < BATCH; ++i) {
+        nx[i] = rx[i];
+        nd[i] = rd[i];
       }
-      // the last K - 1 inputs are the next state
-      if (dstate && t >= k.len - (K - 1)) {
-        float more[V];
-        load_v<T, V>(dstate + (long long)(t - (k.len - (K - 1))) * a.C, more);
+      fetch(t + BATCH);
 #pragma unroll
-        for (int e = 0; e < V; ++e) g[e] += more[e];
-      }
-      if (t >= 0) store_v<T, V>(dx + (long long)t * a.C, g);
-      else if (a.dstate0) store_v<T, V>(static_cast<T*>(a.dstate0) + held + (long long)(t + K - 1) * a.C, g);
-    };
-    // inputs whose gradients are this run's: its own tokens, and the state's for the first run
-    const int from = k.j == 0 ? -(K - 1) : t0, stop = t1 + K - 1;
-    for (int t = t0; t < stop; t += BWD_BATCH) {
-      Raw<T, V> rx[BWD_BATCH], rd[BWD_BATCH];
+      for (int i = 0; i < BATCH; ++i) {
+        const int at = t + i, done = at - (K - 1);
+        nx[i].pairs(win[K - 1]);
+        nd[i].pairs(dpre[K - 1]);
+        if constexpr (SILU) {
 #pragma unroll
-      for (int i = 0; i < BWD_BATCH; ++i) {
-        if (t + i < min(stop, k.len)) {
-          rx[i].load(x + (long long)(t + i) * a.x_ts);
-          rd[i].load(dy + (long long)(t + i) * a.dy_ts);
-        } else {
-          rx[i].zero();
-          rd[i].zero();
-        }
-      }
+          for (int e = 0; e < NP; ++e) {
+            f32x2 pre = bias[e];
 #pragma unroll
-      for (int i = 0; i < BWD_BATCH; ++i) {
-        const int at = t + i;
-        rx[i].floats(win[K - 1]);
-        float g[V];
-        rd[i].floats(g);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          if (SILU) {
-            float pre = bias[e];
-#pragma unroll
-            for (int j = 0; j < K; ++j) pre = fmaf(w[j][e], win[j][e], pre);
-            const float s = sigmoid(pre);
-            g[e] = at < k.len ? g[e] * fmaf(pre * s, 1.f - s, s) : 0.f;
+            for (int j = 0; j < K; ++j) pre = fma2(w[j][e], win[j][e], pre);
+            const f32x2 s = sigmoid2(pre);  // silu' = s + pre s (1 - s)
+            dpre[K - 1][e] = mul2(dpre[K - 1][e], fma2(mul2(pre, s), fma2(s, both(-1.f), both(1.f)), s));
+            if (at >= k.len) dpre[K - 1][e] = both(0.f);
           }
-          dpre[K - 1][e] = g[e];
         }
         if (at < t1) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            db[e] += dpre[K - 1][e];
+          for (int e = 0; e < NP; ++e) {
+            db[e] = add2(db[e], dpre[K - 1][e]);
 #pragma unroll
-            for (int j = 0; j < K; ++j) dw[j][e] = fmaf(dpre[K - 1][e], win[j][e], dw[j][e]);
+            for (int j = 0; j < K; ++j) dw[j][e] = fma2(dpre[K - 1][e], win[j][e], dw[j][e]);
           }
         }
-        if (at - (K - 1) >= from && at - (K - 1) < t1) emit(at - (K - 1));
+        if (done >= from && done < t1) {
+          f32x2 g[NP];
+#pragma unroll
+          for (int e = 0; e < NP; ++e) {
+            g[e] = mul2(w[0][e], dpre[K - 1][e]);
+#pragma unroll
+            for (int j = 1; j < K; ++j) g[e] = fma2(w[j][e], dpre[K - 1 - j][e], g[e]);
+          }
+          // the last K - 1 inputs are the next state
+          if (dstate && done >= k.len - (K - 1)) {
+            f32x2 more[NP];
+            load_v<T, V>(dstate + (long long)(done - (k.len - (K - 1))) * a.C, more);
+#pragma unroll
+            for (int e = 0; e < NP; ++e) g[e] = add2(g[e], more[e]);
+          }
+          if (done >= 0) store_v<T, V>(dx, g);
+          else if (a.dstate0) store_v<T, V>(static_cast<T*>(a.dstate0) + held + (long long)(done + K - 1) * a.C, g);
+        }
+        dx += a.C;
 #pragma unroll
         for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
+          for (int e = 0; e < NP; ++e) {
             win[j][e] = win[j + 1][e];
             dpre[j][e] = dpre[j + 1][e];
           }
@@ -318,7 +318,11 @@ __global__ void __launch_bounds__(THREADS) causal_conv_bwd_kernel(ConvArgs a, in
 #pragma unroll
   for (int j = 0; j < K + 1; ++j)
 #pragma unroll
-    for (int e = 0; e < V; ++e) to[(long long)j * a.C + e] = j < K ? dw[j < K ? j : 0][e] : db[e];
+    for (int e = 0; e < NP; ++e) {
+      const float2 f = split2(j < K ? dw[j < K ? j : 0][e] : db[e]);
+      to[(long long)j * a.C + 2 * e] = f.x;
+      if (V > 1) to[(long long)j * a.C + 2 * e + 1] = f.y;
+    }
 }
 
 // Adds the partial weight gradients: 8 warps take every eighth part of 32 channels, then add up in order.
@@ -344,44 +348,58 @@ __global__ void __launch_bounds__(256) causal_conv_wgrad_kernel(ConvArgs a, int 
   else if (a.dbias) static_cast<T*>(a.dbias)[c] = from_f32<T>(s);
 }
 
-// Tokens of a run: short ones for more threads when tokens are few, long ones for fewer repeated
+// Tokens of a forward run: short ones for more threads when tokens are few, long ones for fewer repeated
 // inputs, at least a thread in 16 warps an SM.
-int run_of(const ConvArgs& a, int vecs, int least) {
+int run_of(const ConvArgs& a, int vecs) {
   const long long threads = (long long)152 * 16 * 32;
-  int run = 64;
-  while (run > least && (long long)a.q.N / run * vecs < threads) run /= 2;
+  int run = 128;
+  while (run > 16 && (long long)a.q.N / run * vecs < threads) run /= 2;
   return run;
+}
+// Backward: as many parts of the weight gradients as give 32 warps an SM, a run or two for each part (at least 16 tokens: a
+// run reads and forms 3 tokens more).
+constexpr int BWD_WARPS = 32;
+void bwd_plan(ConvArgs* a, int vecs, int* parts, long long* numbers) {
+  const long long most = ((long long)152 * BWD_WARPS * 32 + vecs - 1) / vecs;
+  if (a->q.cu) {
+    const long long left = most > a->q.B + 1 ? most - a->q.B - 1 : 1;
+    a->run = (int)((a->q.N + left - 1) / left);
+  } else {
+    const long long per = a->q.B > 0 && most > a->q.B ? most / a->q.B : 1;
+    a->run = (int)((a->q.T + per - 1) / per);
+  }
+  if (a->run < 16) a->run = 16;
+  *numbers = packed_numbers(a->q, a->run);
+  *parts = (int)(*numbers < most ? *numbers : most);
 }
 template <class T>
 constexpr int fwd_vec() {
   return 16 / (int)sizeof(T);
 }
-// Parts of the weight gradients: threads for 8 warps an SM, and no more than there are runs.
-long long parts_of(const ConvArgs& a, int vecs) {
-  const long long numbers = packed_numbers(a.q, a.run), most = ((long long)152 * 16 * 32 + vecs - 1) / vecs;
-  return numbers < most ? numbers : most;
-}
 
 template <class T, int V, int K, bool SILU>
 cudaError_t fwd(ConvArgs a, cudaStream_t s) {
   const int vecs = a.C / V;
-  a.run = a.max_q <= BATCH ? BATCH : run_of(a, vecs, 2 * BATCH);
+  constexpr int FEW = 8;
+  const bool few = a.max_q <= FEW;  // a run for every sequence: the loads of four tokens suffice
+  a.run = few ? FEW : run_of(a, vecs);
   const long long blocks = (packed_numbers(a.q, a.run) * vecs + THREADS - 1) / THREADS;
   if (blocks > 0x7fffffff) return cudaErrorNotSupported;
   prof_mark(K_CONV_FWD, s, true);
-  const cudaError_t e = launch_pdl(causal_conv_fwd_kernel<T, V, K, SILU>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a);
+  const cudaError_t e = few ? launch_pdl(causal_conv_fwd_kernel<T, V, K, SILU, 1>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a)
+                            : launch_pdl(causal_conv_fwd_kernel<T, V, K, SILU, 8>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a);
   prof_mark(K_CONV_FWD, s, false);
   return e;
 }
 template <class T, int V, int K, bool SILU>
 cudaError_t bwd(ConvArgs a, cudaStream_t s) {
   const int vecs = a.C / V;
-  a.run = run_of(a, vecs, 16);
-  const int parts = (int)parts_of(a, vecs);
+  int parts;
+  long long numbers;
+  bwd_plan(&a, vecs, &parts, &numbers);
   const long long blocks = ((long long)parts * vecs + THREADS - 1) / THREADS;
   prof_mark(K_CONV_BWD, s, true);
-  cudaError_t e = launch_pdl(causal_conv_bwd_kernel<T, V, K, SILU>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a, parts,
-                             packed_numbers(a.q, a.run));
+  cudaError_t e = launch_pdl(causal_conv_bwd_kernel<T, V, K, SILU>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a, parts, numbers);
   prof_mark(K_CONV_BWD, s, false);
   if (e != cudaSuccess) return e;
   prof_mark(K_CONV_WGRAD, s, true);
@@ -419,8 +437,10 @@ size_t causal_conv_workspace(const ConvArgs& a0) {
   size_t most = 0;
   for (int V : {1, 4}) {  // whichever width the call's pointers and strides allow
     if (a.C % V) continue;
-    a.run = run_of(a, a.C / V, 16);
-    const size_t n = (size_t)parts_of(a, a.C / V) * (a.taps + 1) * a.C * sizeof(float);
+    int parts;
+    long long numbers;
+    bwd_plan(&a, a.C / V, &parts, &numbers);
+    const size_t n = (size_t)parts * (a.taps + 1) * a.C * sizeof(float);
     most = n > most ? n : most;
   }
   return most;

@@ -327,7 +327,7 @@ struct ScanArgs {
   const float *A, *skip, *bias, *h0;
   void* y;
   float* h_final;
-  float* kept;  // states at every scan_tile(NS) tokens, or NULL
+  float* kept;  // states before every SCAN_KEEP tokens, or NULL
   int max_q;
   // backward
   const float* dh_final;
@@ -335,8 +335,8 @@ struct ScanArgs {
   float *dA, *dskip, *dbias, *dh0;
   void* ws;
 };
-// Tokens between two kept states (a tile of the kernels).
-constexpr int scan_tile(int NS) { return NS == 8 ? 8 : 16; }
+// Tokens between two kept states.
+constexpr int SCAN_KEEP = 8;
 
 // Plan of a serving step (page_plan.cu).
 constexpr int PLAN_MAX_REQUESTS = 8192;

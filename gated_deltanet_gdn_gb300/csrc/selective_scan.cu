@@ -6,20 +6,21 @@ namespace gdn {
 namespace {
 
 constexpr int WARPS = 4;
+constexpr int STATES = 8, CTAS = 3;  // states of a lane, CTAs of an SM
 
 template <class Shape>
 struct WarpShared {
-  float delta[Shape::TT * Shape::CW], du[Shape::TT * Shape::CW], y[Shape::TT * Shape::CW];
+  float delta[Shape::TT * Shape::LD], du[Shape::TT * Shape::LD], y[Shape::TT * Shape::LD];
   float B[Shape::TT * Shape::NS], C[Shape::TT * Shape::NS];
 };
 
 // SUM: what a chunk adds to the state (from zeros) and the sum of its delta, no outputs.
 // start: [chunks][D][NS] states at the chunks' starts (SUM: written as the chunks' own ends), sums: [chunks][D].
 template <class T, int NS, bool WIDE, bool SUM>
-__global__ void __launch_bounds__(32 * WARPS) selective_scan_kernel(ScanArgs a, int L, int tiles, long long warps, float* start,
-                                                                    float* sums) {
-  using Shape = ScanShape<NS>;
-  constexpr int S = Shape::S, P = Shape::P, CW = Shape::CW, TT = Shape::TT;
+__global__ void __launch_bounds__(32 * WARPS, CTAS) selective_scan_kernel(ScanArgs a, int L, int tiles, long long warps, float* start,
+                                                                       float* sums) {
+  using Shape = ScanShape<NS, STATES>;
+  constexpr int S = Shape::S, P = Shape::P, LD = Shape::LD, TT = Shape::TT, N = STATES / 2;
   __shared__ __align__(16) WarpShared<Shape> shared[WARPS];
   pdl_wait();
   pdl_trigger();
@@ -41,108 +42,123 @@ __global__ void __launch_bounds__(32 * WARPS) selective_scan_kernel(ScanArgs a, 
   }
   if (SUM && t1 == k.len) return;  // nothing comes after it
 
-  f32x2 A[2][4], h[2][4];
+  f32x2 A[4][N], h[4][N];
   load_states<Shape>(a.A, w, A);
-  const f32x2 log2e = pack2(LOG2E, LOG2E);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    A[0][i] = mul2(A[0][i], log2e);
-    A[1][i] = mul2(A[1][i], log2e);
-    h[0][i] = h[1][i] = pack2(0.f, 0.f);
-  }
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      A[c][i] = mul2(A[c][i], both(LOG2E));
+      h[c][i] = both(0.f);
+    }
   const int slot = SUM || (start && t1 != k.len) ? -1 : packed_slot(a.q, k.b);
   const long long row = (long long)a.D * NS;
   if constexpr (!SUM) {
     if (start) load_states<Shape>(start + number * row, w, h);
     else if (slot >= 0 && a.h0 && packed_goes_on(a.q, k.b, k.len)) load_states<Shape>(a.h0 + slot * row, w, h);
   }
-  float bias[4] = {}, skip[4] = {}, total[4] = {};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < w.n) {
-      if (a.bias) bias[i] = a.bias[w.c + i];
-      if (!SUM && a.skip) skip[i] = a.skip[w.c + i];
-    }
+  f32x2 bias[2], skip[2], total[2] = {both(0.f), both(0.f)};
+  load_channels(a.bias, w, bias);
+  load_channels(SUM ? nullptr : a.skip, w, skip);
   float* kept = nullptr;
-  if (!SUM && a.kept) kept = a.kept + (packed_number(a.q, k.b, k.first, TT) + t0 / TT) * row;
+  if (!SUM && a.kept) kept = a.kept + (packed_number(a.q, k.b, k.first, SCAN_KEEP) + t0 / SCAN_KEEP) * row;
 
   ScanRows<Shape, WIDE, T> ru, rd, rz;
   ScanMix<Shape, WIDE, T> rb, rc;
-  auto fetch = [&](int t) {
-    const int rows = t1 - t;
-    ru.load(a.u, k.first + (long long)t, a.u_ts, rows, w);
-    rd.load(a.dt, k.first + (long long)t, a.dt_ts, rows, w);
-    rb.load(a.B, k.first + (long long)t, a.b_ts, a.b_gs, rows, w);
-    if (!SUM) rc.load(a.C, k.first + (long long)t, a.c_ts, a.c_gs, rows, w);
+  RowPtr<T> pu, pd, pz, py;
+  MixPtr<T> pb, pc;
+  {
+    const long long row0 = k.first + (long long)t0;
+    pu.set(a.u, row0, a.u_ts, w);
+    pd.set(a.dt, row0, a.dt_ts, w);
+    pb.set(a.B, row0, a.b_ts, a.b_gs, w);
+    pc.set(a.C, row0, a.c_ts, a.c_gs, w);
+    pz.set(a.z, row0, a.z_ts, w);
+    py.set(a.y, row0, a.y_ts, w);
+  }
+  const bool whole = __all_sync(0xffffffffu, w.n == 4);  // every lane has its channels
+  auto fetch = [&](int rows) {
+    if (whole && rows >= TT) {
+      ru.template load<true>(pu, rows, w);
+      rd.template load<true>(pd, rows, w);
+      rb.template load<true>(pb, rows, w);
+      if (!SUM) rc.template load<true>(pc, rows, w);
+    } else {
+      ru.template load<false>(pu, rows, w);
+      rd.template load<false>(pd, rows, w);
+      rb.template load<false>(pb, rows, w);
+      if (!SUM) rc.template load<false>(pc, rows, w);
+    }
+    pu.p += pu.tile;
+    pd.p += pd.tile;
+    pb.p += pb.tile;
+    pc.p += pc.tile;
   };
-  if (t0 < t1) fetch(t0);
+  fetch(t1 - t0);
   for (int t = t0; t < t1; t += TT) {
     const int rows = t1 - t < TT ? t1 - t : TT;
+    const bool full = whole && rows == TT;
     const ScanRows<Shape, WIDE, T> cu = ru;
     __syncwarp();
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int r = p * S + w.s;
-      float d[4], u[4];
-      quad_floats(rd.v[p], d);
-      quad_floats(cu.v[p], u);
+      f32x2 d[2], u[2];
+      quad_pairs(rd.v[p], d);
+      quad_pairs(cu.v[p], u);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        d[i] += bias[i];
-        if (a.softplus) d[i] = softplus(d[i]);
-        if (r >= rows) d[i] = 0.f;  // leaves the state as it is
-        if (SUM) total[i] += d[i];
-        u[i] *= d[i];
+      for (int i = 0; i < 2; ++i) {
+        d[i] = add2(d[i], bias[i]);
+        if (a.softplus) d[i] = softplus2(d[i]);
+        if (!full && r >= rows) d[i] = both(0.f);  // leaves the state as it is
+        if (SUM) total[i] = add2(total[i], d[i]);
+        u[i] = mul2(u[i], d[i]);
       }
-      *reinterpret_cast<float4*>(sm.delta + r * CW + 4 * w.q) = make_float4(d[0], d[1], d[2], d[3]);
-      *reinterpret_cast<float4*>(sm.du + r * CW + 4 * w.q) = make_float4(u[0], u[1], u[2], u[3]);
+      store_pairs(sm.delta + r * LD + 4 * w.q, d);
+      store_pairs(sm.du + r * LD + 4 * w.q, u);
     }
     rb.store(sm.B, w);
     if (!SUM) rc.store(sm.C, w);
     __syncwarp();
-    if (kept) {
+    if (kept && (t - t0) % SCAN_KEEP == 0) {
       store_states<Shape>(kept, w, h);
       kept += row;
     }
-    if (!SUM && a.z) rz.load(a.z, k.first + (long long)t, a.z_ts, rows, w);
-    if (t + TT < t1) fetch(t + TT);
+    if (!SUM) {
+      if (full && a.z) rz.template load<true>(pz, rows, w);
+      else rz.template load<false>(pz, a.z ? rows : 0, w);
+      pz.p += pz.tile;
+    }
+    fetch(t1 - t - TT);  // no rows are left behind the last tile
     for (int r0 = 0; r0 < rows; r0 += 4) {
-      float out[4][2];
+      float out[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = r0 + i;
-        const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(sm.delta + r * CW + 4 * w.q);
-        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sm.du + r * CW + 4 * w.q);
-        const float4 bq = *reinterpret_cast<const float4*>(sm.B + r * NS + 4 * w.s);
-        const float bn[4] = {bq.x, bq.y, bq.z, bq.w};
-        float cn[4];
-        if constexpr (!SUM) {
-          const float4 cq = *reinterpret_cast<const float4*>(sm.C + r * NS + 4 * w.s);
-          cn[0] = cq.x; cn[1] = cq.y; cn[2] = cq.z; cn[3] = cq.w;
-        }
-        f32x2 y[2];
+        const float4 dq = *reinterpret_cast<const float4*>(sm.delta + r * LD + 4 * w.q);
+        const float4 xq = *reinterpret_cast<const float4*>(sm.du + r * LD + 4 * w.q);
+        const float d[4] = {dq.x, dq.y, dq.z, dq.w}, x[4] = {xq.x, xq.y, xq.z, xq.w};
+        f32x2 b[N], c[N];
+        load_row(b, sm.B + r * NS + STATES * w.s);
+        if constexpr (!SUM) load_row(c, sm.C + r * NS + STATES * w.s);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const f32x2 b2 = pack2(bn[n], bn[n]);
+        for (int e = 0; e < 4; ++e) {
+          f32x2 y;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 arg = split2(mul2(e ? d.y : d.x, A[e][n]));
-            h[e][n] = fma2(pack2(ex2(arg.x), ex2(arg.y)), h[e][n], mul2(e ? x.y : x.x, b2));
-            if constexpr (!SUM) {
-              const f32x2 c2 = pack2(cn[n], cn[n]);
-              y[e] = n == 0 ? mul2(h[e][n], c2) : fma2(h[e][n], c2, y[e]);
-            }
+          for (int n = 0; n < N; ++n) {
+            h[e][n] = fma2(ex2_2(scale2(d[e], A[e][n])), h[e][n], scale2(x[e], b[n]));
+            if constexpr (!SUM) y = n == 0 ? mul2(h[e][n], c[n]) : fma2(h[e][n], c[n], y);
+          }
+          if constexpr (!SUM) {
+            const float2 f = split2(y);
+            out[i][e] = f.x + f.y;
           }
         }
-        if constexpr (!SUM) {
-          const float2 y0 = split2(y[0]), y1 = split2(y[1]);
-          const float v[4] = {y0.x, y0.y, y1.x, y1.y};
-          sum_quad<S>(v, w.s, out[i]);
-        }
+        if constexpr (!SUM) sum_quad<S>(out[i], w.s);
       }
       if constexpr (!SUM) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) put_quad<S>(sm.y + (r0 + i) * CW + 4 * w.q, w.s, out[i]);
+        for (int i = 0; i < 4; ++i) put_quad<S>(sm.y + (r0 + i) * LD + 4 * w.q, w.s, out[i]);
       }
     }
     if constexpr (!SUM) {
@@ -150,29 +166,32 @@ __global__ void __launch_bounds__(32 * WARPS) selective_scan_kernel(ScanArgs a, 
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int r = p * S + w.s;
-        if (r >= rows) continue;
-        float y[4], u[4];
-        ld4(y, sm.y + r * CW + 4 * w.q);
-        quad_floats(cu.v[p], u);
+        if (!full && r >= rows) continue;
+        f32x2 y[2], u[2];
+        load_pairs(y, sm.y + r * LD + 4 * w.q);
+        quad_pairs(cu.v[p], u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = fmaf(skip[i], u[i], y[i]);
+        for (int i = 0; i < 2; ++i) y[i] = fma2(skip[i], u[i], y[i]);
         if (a.z) {
-          float z[4];
-          quad_floats(rz.v[p], z);
+          f32x2 z[2];
+          quad_pairs(rz.v[p], z);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] *= z[i] * sigmoid(z[i]);
+          for (int i = 0; i < 2; ++i) y[i] = mul2(y[i], mul2(z[i], sigmoid2(z[i])));
         }
-        store_quad<WIDE>(static_cast<T*>(a.y) + (k.first + (long long)t + r) * a.y_ts + w.c, y, w.n);
+        store_quad<WIDE>(const_cast<T*>(py.p) + p * py.step, y, w.n);
       }
+      py.p += py.tile;
     }
   }
   if constexpr (SUM) {
     store_states<Shape>(start + number * row, w, h);
+    const float2 s0 = split2(total[0]), s1 = split2(total[1]);
+    float v[4] = {s0.x, s0.y, s1.x, s1.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int d = 1; d < S; d *= 2) total[i] += __shfl_xor_sync(0xffffffffu, total[i], d);
-      if (w.s == 0 && i < w.n) sums[number * a.D + w.c + i] = total[i];
+      for (int d = 1; d < S; d *= 2) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+      if (w.s == 0 && i < w.n) sums[number * a.D + w.c + i] = v[i];
     }
   } else if (t1 == k.len && slot >= 0 && a.h_final) {
     store_states<Shape>(a.h_final + slot * row, w, h);
@@ -213,11 +232,100 @@ __global__ void __launch_bounds__(128) selective_scan_carry_kernel(ScanArgs a, i
   }
 }
 
-int split_of(const ScanArgs& a) { return scan_split(a, ScanCost{90, 130, 60, 12}); }
+// One token a sequence, or few: a warp per sequence and 512 / NS channels, nothing staged. Bound by the states, which are
+// read and written once (32 sequences x 6144 channels x 16 states: 25 MB), so registers are kept low for
+// many warps, and everything a token needs is on its way before the first result is used.
+template <class T, int NS, bool WIDE>
+__global__ void __launch_bounds__(32 * WARPS, 5) selective_step_kernel(ScanArgs a, int tiles, int warps) {
+  using Shape = ScanShape<NS, 4>;
+  constexpr int S = Shape::S;
+  pdl_wait();
+  pdl_trigger();
+  const int at = blockIdx.x * WARPS + threadIdx.x / 32;
+  if (at >= warps) return;
+  const int b = at / tiles;
+  const ScanPlace<Shape> w(a, at - b * tiles);
+  int first, len;
+  packed_bounds(a.q, b, &first, &len);
+  if (b == a.q.B) {  // rows behind the last sequence
+    const float none[4] = {};
+    if (a.q.zero_tail)
+      for (int t = w.s; t < len; t += S)
+        store_quad<WIDE>(static_cast<T*>(a.y) + (first + (long long)t) * a.y_ts + w.c, none, w.n);
+    return;
+  }
+  const int slot = packed_slot(a.q, b);
+  const long long row = (long long)a.D * NS;
+  f32x2 A[4][2], h[4][2], bias[2], skip[2];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e][0] = h[e][1] = both(0.f);
+  if (slot >= 0 && a.h0 && packed_goes_on(a.q, b, len)) load_states<Shape>(a.h0 + slot * row, w, h);
+  load_states<Shape>(a.A, w, A);
+  load_channels(a.bias, w, bias);
+  load_channels(a.skip, w, skip);
+  for (int t = 0; t < len; ++t) {
+    const long long r = first + (long long)t;
+    const Quad<T> qu = load_quad<WIDE>(static_cast<const T*>(a.u) + r * a.u_ts + w.c, w.n);
+    const Quad<T> qd = load_quad<WIDE>(static_cast<const T*>(a.dt) + r * a.dt_ts + w.c, w.n);
+    const Quad<T> qz = load_quad<WIDE>(static_cast<const T*>(a.z) + r * a.z_ts + w.c, a.z ? w.n : 0);
+    const Quad<T> qb = load_quad<WIDE>(static_cast<const T*>(a.B) + r * a.b_ts + w.g * a.b_gs + 4 * w.s, 4);
+    const Quad<T> qc = load_quad<WIDE>(static_cast<const T*>(a.C) + r * a.c_ts + w.g * a.c_gs + 4 * w.s, 4);
+    f32x2 d[2], u[2], bn[2], cn[2];
+    float v[4];
+    quad_pairs(qd, d);
+    quad_pairs(qu, u);
+    quad_pairs(qb, bn);
+    quad_pairs(qc, cn);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      d[i] = add2(d[i], bias[i]);
+      if (a.softplus) d[i] = softplus2(d[i]);
+      const float2 df = split2(d[i]), xf = split2(mul2(d[i], u[i]));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int e = 2 * i + j;
+        const float de = j ? df.y : df.x, xe = j ? xf.y : xf.x;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          h[e][n] = fma2(ex2_2(mul2(scale2(de, A[e][n]), both(LOG2E))), h[e][n], scale2(xe, bn[n]));
+        const float2 f = split2(fma2(h[e][1], cn[1], mul2(h[e][0], cn[0])));
+        v[e] = f.x + f.y;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int f = 1; f < S; f *= 2) v[e] += __shfl_xor_sync(0xffffffffu, v[e], f);
+    if (w.s == 0) {
+      f32x2 y[2] = {fma2(skip[0], u[0], pack2(v[0], v[1])), fma2(skip[1], u[1], pack2(v[2], v[3]))};
+      if (a.z) {
+        f32x2 z[2];
+        quad_pairs(qz, z);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) y[i] = mul2(y[i], mul2(z[i], sigmoid2(z[i])));
+      }
+      store_quad<WIDE>(static_cast<T*>(a.y) + r * a.y_ts + w.c, y, w.n);
+    }
+  }
+  if (slot >= 0 && a.h_final) store_states<Shape>(a.h_final + slot * row, w, h);
+}
+constexpr int FEW = 2;  // tokens of a sequence up to which the step kernel is taken
+
+int split_of(const ScanArgs& a) { return scan_split(a, ScanCost{190, 260, 120, 4 * CTAS, STATES}); }
 
 template <class T, int NS, bool WIDE>
 cudaError_t run(const ScanArgs& a, cudaStream_t s) {
-  const int L = split_of(a), tiles = scan_tiles(a.D, a.G, NS);
+  if (a.max_q <= FEW && !a.kept) {
+    const int tiles = scan_tiles(a.D, a.G, NS, 4);
+    const long long warps = packed_numbers(a.q, SCAN_WHOLE) * tiles;
+    if (warps > 0x7fffffff) return cudaErrorNotSupported;
+    prof_mark(K_SSTEP, s, true);
+    const cudaError_t e = launch_pdl(selective_step_kernel<T, NS, WIDE>, dim3((unsigned)((warps + WARPS - 1) / WARPS)),
+                                     dim3(32 * WARPS), 0, s, a, tiles, (int)warps);
+    prof_mark(K_SSTEP, s, false);
+    return e;
+  }
+  const int L = split_of(a), tiles = scan_tiles(a.D, a.G, NS, STATES);
   const long long numbers = packed_numbers(a.q, L), warps = numbers * tiles, blocks = (warps + WARPS - 1) / WARPS;
   if (blocks > 0x7fffffff) return cudaErrorNotSupported;
   const dim3 grid((unsigned)blocks), block(32 * WARPS);
@@ -254,7 +362,7 @@ cudaError_t pick(const ScanArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t selective_scan_workspace(const ScanArgs& a) {
+size_t selective_scan_workspace(const ScanArgs& a) {  // that of the split, which few tokens never need
   const int L = split_of(a);
   if (L == SCAN_WHOLE) return 0;
   return (size_t)packed_numbers(a.q, L) * a.D * (a.NS + 1) * sizeof(float);

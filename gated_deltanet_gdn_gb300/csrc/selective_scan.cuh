@@ -7,14 +7,14 @@
 // Bound by arithmetic: one exponential and four products per token, channel and state (32 and 128 a
 // clock and SM: 16 states x 768 channels x 32,768 tokens cannot take less than 44 us, their
 // bytes 30 us), so the layout is made to keep everything else off the inner loop:
-//  * a lane holds 4 channels x 4 states. NS / 4 lanes share four channels (a quad), so a step's values are read from
-//    shared memory in four 16-byte loads and the sum over states takes 3 (NS = 16) shuffles for 16 states;
-//    a lane per channel with all its states would take 32 shuffles in the backward's sums over channels;
+//  * a lane holds 4 channels x SP states (8 forward, 4 backward, whose registers hold several tokens' states). NS / SP
+//    lanes share four channels (a quad). What a step reads from shared memory grows with the sides of this tile and its
+//    products with the area: with 4 x 4 the reads alone took as long as the exponentials;
 //  * what is per token and channel only (softplus, delta u, the gate, conversions) is done once for a tile of
-//    scan_tile(NS) tokens, spread over all lanes, and passed through shared memory;
-//  * a warp owns its tile and its shared memory: no barrier of a CTA anywhere, loads of the next
+//    TT tokens, spread over all lanes, and passed through shared memory;
+//  * a warp owns its tile and its shared memory: no barrier of a CTA in the forward, loads of the next
 //    tile are in flight during the steps;
-//  * two channels go through each fp32 instruction (fma.rn.f32x2), which halves the issue slots.
+//  * two values go through each fp32 instruction (fma.rn.f32x2), which halves the issue slots.
 //
 // Few channels and long sequences do not fill the SMs: a chunk per warp then, in three launches. The first
 // scans every chunk but the last from zeros and keeps its last state and the sum of its delta, since a
@@ -28,30 +28,32 @@
 
 namespace gdn {
 
-template <int NS_>
+template <int NS_, int SP_>
 struct ScanShape {
-  static constexpr int NS = NS_, S = NS / 4, Q = 32 / S, CW = 4 * Q, TT = scan_tile(NS), P = TT / S;
+  static constexpr int NS = NS_, SP = SP_, S = NS / SP, Q = 32 / S, CW = 4 * Q, TT = 4 * S < SCAN_KEEP ? 4 * S : SCAN_KEEP,
+                       P = TT > S ? TT / S : 1;
   static constexpr int BV = (TT * NS / 4 + 31) / 32;  // quads of B (and of C) a lane loads for a tile
-  static_assert(P >= 1 && P * S == TT, "whole passes");
+  // Row length of a tile in shared memory: eight lanes' vectors, of 8 / S quads and S rows, on different banks.
+  static constexpr int LD = CW + (S == 1 ? 0 : S < 8 ? 32 / S : 4);
+  static_assert(P * S >= TT && SCAN_KEEP % TT == 0, "whole tiles between kept states");
 };
 
-// Tiles of channels of all groups (a warp's channels belong to one group).
-inline int scan_tiles(int D, int G, int NS) {
-  const int cw = 512 / NS, dg = D / G;
+// Warps for the channels of all groups (a warp's channels belong to one group).
+inline int scan_tiles(int D, int G, int NS, int SP) {
+  const int cw = 128 * SP / NS, dg = D / G;
   return G * ((dg + cw - 1) / cw);
 }
 
 constexpr int SCAN_WHOLE = 0x40000000;  // chunk length where sequences are not split
 
-// Clocks of a warp's step (512 products of channel and state) that weigh a split against whole sequences: in a full SM
-// sub-partition; of a warp with no other beside it; in the launch before that gives the chunks' ends; and the warps an
-// SM holds.
+// Clocks of a warp's step that weigh a split against whole sequences: in a full SM sub-partition; of a warp with no
+// other beside it; in the launch before that gives the chunks' ends (forward); the warps an SM holds; and the states of a lane.
 struct ScanCost {
-  int full, alone, ends, resident;
+  int full, alone, ends, resident, states;
 };
-// Chunk length, a multiple of the tile: SCAN_WHOLE, or as many chunks as fill the SMs once.
+// Chunk length, a multiple of 32: SCAN_WHOLE, or as many chunks as fill the SMs once.
 inline int scan_split(const ScanArgs& a, ScanCost cost) {
-  const long long tiles = scan_tiles(a.D, a.G, a.NS), steps = a.q.N * tiles, parts = 152 * 4;
+  const long long tiles = scan_tiles(a.D, a.G, a.NS, cost.states), steps = a.q.N * tiles, parts = 152 * 4;
   const long long busy = steps * cost.full / parts, one = (long long)a.max_q * cost.alone;
   const long long whole = busy > one ? busy : one;
   const long long split = steps * (cost.full + cost.ends) / parts + 12000;  // and two more launches
@@ -60,13 +62,13 @@ inline int scan_split(const ScanArgs& a, ScanCost cost) {
   const long long warps = (long long)152 * cost.resident * a.max_q, each = steps > 0 ? warps / steps : 0;
   if (each < 2) return SCAN_WHOLE;
   const int L = (int)((a.max_q + each - 1) / each);
-  return L < 64 ? 64 : (L + 15) / 16 * 16;
+  return L < 64 ? 64 : (L + 31) / 32 * 32;
 }
 
 // A warp's place: its channels and the chunk it works on.
 template <class Shape>
 struct ScanPlace {
-  int lane, s, q, g, c, n;  // states 4 s .. 4 s + 3 of channels c .. c + n - 1 (n up to 4) of group g
+  int lane, s, q, g, c, n;  // states SP s .. SP s + SP - 1 of channels c .. c + n - 1 (n up to 4) of group g
   __device__ __forceinline__ ScanPlace(const ScanArgs& a, int tile) {
     lane = threadIdx.x % 32;
     s = lane % Shape::S;
@@ -79,102 +81,177 @@ struct ScanPlace {
   }
 };
 
-// [channel][state] rows of fp32 as pairs of channels: x[0][i] channels 0, 1 and x[1][i] channels 2, 3 of state i.
+// [channel][state] rows of fp32: pairs of neighbouring states of each channel.
 template <class Shape>
-__device__ __forceinline__ void load_states(const float* p, const ScanPlace<Shape>& w, f32x2 (&x)[2][4]) {
-  float f[4][4];
+__device__ __forceinline__ void load_states(const float* p, const ScanPlace<Shape>& w, f32x2 (&x)[4][Shape::SP / 2]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < w.n) v = *reinterpret_cast<const float4*>(p + (long long)(w.c + i) * Shape::NS + 4 * w.s);
-    f[i][0] = v.x; f[i][1] = v.y; f[i][2] = v.z; f[i][3] = v.w;
-  }
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[0][i] = pack2(f[0][i], f[1][i]);
-    x[1][i] = pack2(f[2][i], f[3][i]);
-  }
+    for (int n = 0; n < Shape::SP / 4; ++n) {
+      ulonglong2 v = {0ull, 0ull};
+      if (i < w.n) v = *reinterpret_cast<const ulonglong2*>(p + (long long)(w.c + i) * Shape::NS + Shape::SP * w.s + 4 * n);
+      x[i][2 * n] = v.x;
+      x[i][2 * n + 1] = v.y;
+    }
 }
 template <class Shape>
-__device__ __forceinline__ void store_states(float* p, const ScanPlace<Shape>& w, const f32x2 (&x)[2][4]) {
-  float2 f[2][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[0][i] = split2(x[0][i]);
-    f[1][i] = split2(x[1][i]);
-  }
+__device__ __forceinline__ void store_states(float* p, const ScanPlace<Shape>& w, const f32x2 (&x)[4][Shape::SP / 2]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (i < w.n) {
-      const float4 v = i % 2 == 0 ? make_float4(f[i / 2][0].x, f[i / 2][1].x, f[i / 2][2].x, f[i / 2][3].x)
-                                  : make_float4(f[i / 2][0].y, f[i / 2][1].y, f[i / 2][2].y, f[i / 2][3].y);
-      *reinterpret_cast<float4*>(p + (long long)(w.c + i) * Shape::NS + 4 * w.s) = v;
+#pragma unroll
+      for (int n = 0; n < Shape::SP / 4; ++n)
+        *reinterpret_cast<ulonglong2*>(p + (long long)(w.c + i) * Shape::NS + Shape::SP * w.s + 4 * n) =
+            make_ulonglong2(x[i][2 * n], x[i][2 * n + 1]);
     }
 }
+// SP consecutive floats as pairs.
+template <int N>
+__device__ __forceinline__ void load_row(f32x2 (&x)[N], const float* p) {
+#pragma unroll
+  for (int n = 0; n < N / 2; ++n) {
+    const ulonglong2 v = reinterpret_cast<const ulonglong2*>(p)[n];
+    x[2 * n] = v.x;
+    x[2 * n + 1] = v.y;
+  }
+}
+// The other way about, for four states a lane: x[e][i] holds channels 2 e' and 2 e' + 1, e' = e ^ flip_c, of state
+// i' = i ^ 2 flip_n. (Lanes that take their channels or states in another order exchange sums without selecting.)
+template <class Shape>
+__device__ __forceinline__ void load_columns(const float* p, const ScanPlace<Shape>& w, int flip_c, int flip_n, f32x2 (&x)[2][4]) {
+  static_assert(Shape::SP == 4, "four states a lane");
+  p += (long long)w.c * Shape::NS + 4 * w.s;
+  float2 f[4][2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = i ^ (2 * flip_c);
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      f[i][n] = make_float2(0.f, 0.f);
+      if (c < w.n) f[i][n] = *reinterpret_cast<const float2*>(p + c * Shape::NS + 2 * (n ^ flip_n));
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      x[e][2 * n] = pack2(f[2 * e][n].x, f[2 * e + 1][n].x);
+      x[e][2 * n + 1] = pack2(f[2 * e][n].y, f[2 * e + 1][n].y);
+    }
+}
+template <class Shape>
+__device__ __forceinline__ void store_columns(float* p, const ScanPlace<Shape>& w, int flip_c, int flip_n, const f32x2 (&x)[2][4]) {
+  p += (long long)w.c * Shape::NS + 4 * w.s;
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const float2 a = split2(x[e][2 * n]), b = split2(x[e][2 * n + 1]);
+      const int c = 2 * (e ^ flip_c);
+      float2* to = reinterpret_cast<float2*>(p + c * Shape::NS + 2 * (n ^ flip_n));
+      if (c < w.n) to[0] = make_float2(a.x, b.x);
+      if (c + 1 < w.n) to[Shape::NS / 2] = make_float2(a.y, b.y);
+    }
+}
+// Four floats of channels c .. c + 3, zeros where there are none.
+template <class Shape>
+__device__ __forceinline__ void load_channels(const float* p, const ScanPlace<Shape>& w, f32x2 (&x)[2]) {
+  float f[4] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (p && i < w.n) f[i] = p[w.c + i];
+  x[0] = pack2(f[0], f[1]);
+  x[1] = pack2(f[2], f[3]);
+}
 
-// Rows p S + s of a tile (rows [0, rows) of it are real), as loaded.
+// A lane's place in a [rows, channels] tensor: rows s, S + s, ... of a tile. The pointer moves with the tiles, since
+// 64-bit products of rows and strides cost as much as a tile's arithmetic on them.
+template <class T>
+struct RowPtr {
+  const T* p;
+  long long step, tile;  // elements between a lane's rows, and between tiles
+  template <class Shape>
+  __device__ __forceinline__ void set(const void* base, long long row, long long ts, const ScanPlace<Shape>& w) {
+    p = static_cast<const T*>(base) + (row + w.s) * ts + w.c;
+    step = Shape::S * ts;
+    tile = Shape::TT * ts;
+  }
+};
+// Rows p S + s of a tile, as loaded. FULL: all rows and the warp's channels are real; else rows [0, rows) are, and the
+// others become zeros. (S above TT: some lanes have no row.)
 template <class Shape, bool WIDE, class T>
 struct ScanRows {
   Quad<T> v[Shape::P];
-  __device__ __forceinline__ void load(const void* base, long long row0, long long ts, int rows, const ScanPlace<Shape>& w) {
+  template <bool FULL>
+  __device__ __forceinline__ void load(const RowPtr<T>& from, int rows, const ScanPlace<Shape>& w) {
 #pragma unroll
     for (int p = 0; p < Shape::P; ++p) {
-      const int r = p * Shape::S + w.s;
-      v[p] = load_quad<WIDE>(static_cast<const T*>(base) + (row0 + r) * ts + w.c, r < rows ? w.n : 0);
+      const T* at = from.p + p * from.step;
+      if constexpr (FULL && Shape::S <= Shape::TT) v[p] = load_quad<WIDE>(at);
+      else v[p] = load_quad<WIDE>(at, p * Shape::S + w.s < rows ? w.n : 0);
     }
   }
 };
 // B or C of a tile: [TT][NS] of the warp's group.
+template <class T>
+struct MixPtr {
+  const T* p;
+  long long step, tile;
+  template <class Shape>
+  __device__ __forceinline__ void set(const void* base, long long row, long long ts, long long gs, const ScanPlace<Shape>& w) {
+    p = static_cast<const T*>(base) + (row + w.lane / (Shape::NS / 4)) * ts + w.g * gs + w.lane % (Shape::NS / 4) * 4;
+    step = 128 / Shape::NS * ts;
+    tile = Shape::TT * ts;
+  }
+};
 template <class Shape, bool WIDE, class T>
 struct ScanMix {
+  static constexpr int QUADS = Shape::TT * Shape::NS / 4;
   Quad<T> v[Shape::BV];
-  __device__ __forceinline__ void load(const void* base, long long row0, long long ts, long long gs, int rows,
-                                       const ScanPlace<Shape>& w) {
+  template <bool FULL>
+  __device__ __forceinline__ void load(const MixPtr<T>& from, int rows, const ScanPlace<Shape>& w) {
 #pragma unroll
     for (int i = 0; i < Shape::BV; ++i) {
-      const int k = w.lane + 32 * i, r = k / (Shape::NS / 4), n = k % (Shape::NS / 4) * 4;
-      v[i] = load_quad<WIDE>(static_cast<const T*>(base) + (row0 + r) * ts + w.g * gs + n, r < rows ? 4 : 0);
+      const T* at = from.p + i * from.step;
+      if constexpr (FULL && QUADS % 32 == 0) v[i] = load_quad<WIDE>(at);
+      else v[i] = load_quad<WIDE>(at, (w.lane + 32 * i) / (Shape::NS / 4) < rows && w.lane + 32 * i < QUADS ? 4 : 0);
     }
   }
   __device__ __forceinline__ void store(float* sm, const ScanPlace<Shape>& w) const {
 #pragma unroll
     for (int i = 0; i < Shape::BV; ++i) {
-      const int k = w.lane + 32 * i;
-      float f[4];
-      quad_floats(v[i], f);
-      if (k < Shape::TT * Shape::NS / 4) *reinterpret_cast<float4*>(sm + 4 * k) = make_float4(f[0], f[1], f[2], f[3]);
+      f32x2 f[2];
+      quad_pairs(v[i], f);
+      if (QUADS % 32 == 0 || w.lane + 32 * i < QUADS) store_pairs(sm + 4 * (w.lane + 32 * i), f);
     }
   }
 };
 
-// Sums of four values (channels of the quad) over its S lanes: lane s ends with channel s % 4 in out[0] (S >= 4),
-// or with channels 2 s, 2 s + 1 (S = 2).
+// Sums of four values (channels of the quad) over its S lanes: every lane ends with channels 4 s / S .. of them in front
+// (S = 1 all, S = 2 two; from 4 on channel s % 4).
 template <int S>
-__device__ __forceinline__ void sum_quad(const float (&v)[4], int s, float (&out)[2]) {
+__device__ __forceinline__ void sum_quad(float (&v)[4], int s) {
   constexpr unsigned ALL = 0xffffffffu;
-  constexpr int FAR = S == 2 ? 1 : 2;
-  const bool up = s & FAR;
-  float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
-  a += __shfl_xor_sync(ALL, up ? v[0] : v[2], FAR);
-  b += __shfl_xor_sync(ALL, up ? v[1] : v[3], FAR);
-  if constexpr (S == 2) {
-    out[0] = a;
-    out[1] = b;
-  } else {
+  if constexpr (S >= 2) {
+    constexpr int FAR = S == 2 ? 1 : 2;
+    const bool up = s & FAR;
+    const float a = up ? v[0] : v[2], b = up ? v[1] : v[3];
+    v[0] = (up ? v[2] : v[0]) + __shfl_xor_sync(ALL, a, FAR);
+    v[1] = (up ? v[3] : v[1]) + __shfl_xor_sync(ALL, b, FAR);
+  }
+  if constexpr (S >= 4) {
     const bool odd = s & 1;
-    float r = odd ? b : a;
-    r += __shfl_xor_sync(ALL, odd ? a : b, 1);
+    v[0] = (odd ? v[1] : v[0]) + __shfl_xor_sync(ALL, odd ? v[0] : v[1], 1);
 #pragma unroll
-    for (int d = 4; d < S; d *= 2) r += __shfl_xor_sync(ALL, r, d);
-    out[0] = r;
-    out[1] = 0.f;
+    for (int d = 4; d < S; d *= 2) v[0] += __shfl_xor_sync(ALL, v[0], d);
   }
 }
 // Stores sum_quad's result in the quad's place of a row.
 template <int S>
-__device__ __forceinline__ void put_quad(float* row_quad, int s, const float (&v)[2]) {
-  if constexpr (S == 2) *reinterpret_cast<float2*>(row_quad + 2 * s) = make_float2(v[0], v[1]);
-  else if (S == 4 || s < 4) row_quad[s % 4] = v[0];
+__device__ __forceinline__ void put_quad(float* at, int s, const float (&v)[4]) {
+  if constexpr (S == 1) *reinterpret_cast<float4*>(at) = make_float4(v[0], v[1], v[2], v[3]);
+  else if constexpr (S == 2) *reinterpret_cast<float2*>(at + 2 * s) = make_float2(v[0], v[1]);
+  else if (S == 4 || s < 4) at[s % 4] = v[0];
 }
 
 }  // namespace gdn

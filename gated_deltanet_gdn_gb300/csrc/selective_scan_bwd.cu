@@ -6,11 +6,12 @@
 //   ddelta = sum_n (G a h_{t-1}) A + u d(delta u)                 dA = sum_t (G a h_{t-1}) delta
 //   du = delta d(delta u) + dy' skip    ddt = ddelta softplus'    dz = dy (C.h + skip u) silu'(z)    dh0 = a_0 G_0
 //
-// Bound by arithmetic, 15 products and two exponentials per token, channel and state. The states are not
-// kept for every token but for every tile: a tile is scanned forward once from its kept state, which leaves
-// the states before each group of GROUP tokens in shared memory, then group by group from the
-// last: a group's states and factors are formed again into registers and read by the reverse steps. (All 16
-// states of a tile in shared memory instead would leave room for 5 warps an SM.)
+// Bound by arithmetic, 14 products and 2.5 exponentials per token, channel and state. The states are not
+// kept for every token but for every tile of SCAN_KEEP: a tile is scanned forward once from its kept state, which leaves
+// the state before every second token in shared memory, then pair by pair from the last: the state between a pair's
+// tokens is formed again, and a token's factors where they are used. So three states and one token's factors
+// are in registers at a time, 12 warps fit an SM, and the arithmetic's latency is hidden. (Four tokens' states and factors,
+// 255 registers and 8 warps: 607 against TIME_BWD us at B8 T4096 D768, 16 states.)
 //
 // A CTA's warps work on the same tokens of neighbouring channels, so their sums over channels (dB, dC) are added in
 // shared memory before they leave the SM; what is left per CTA, and the sums over the tokens
@@ -21,31 +22,37 @@ namespace gdn {
 namespace {
 
 constexpr int WARPS = 4;
-constexpr int GROUP = 4;  // tokens whose states are in registers at a time
+constexpr int SUM_STATES = 8, SUM_CTAS = 3;
 
 template <class Shape>
 struct BwdShared {
-  static constexpr int GROUPS = Shape::TT / GROUP;
-  float delta[Shape::TT * Shape::CW];
-  float du[Shape::TT * Shape::CW];   // delta u; then d(delta u)
-  float dy[Shape::TT * Shape::CW];   // dy'; then C.h
-  float gd[Shape::TT * Shape::CW];   // sum_n (G a h) A log2 e
+  static constexpr int TILE = Shape::TT * Shape::LD;
+  float delta[TILE];
+  float du[TILE];     // delta u; then d(delta u)
+  float dy[TILE];     // dy'
+  float u[TILE];
+  float slope[TILE];  // softplus'
+  float dz[TILE];     // dy silu'(z)
   float B[Shape::TT * Shape::NS], C[Shape::TT * Shape::NS];
-  float4 h[GROUPS * 4 * 32];         // states before each group, four vectors a lane
   float mix[Shape::TT * 2 * Shape::NS];  // dB, dC over the warp's channels
+  // States before every second token, four vectors a lane. Once a pair's are in registers, its place
+  // takes two rows of sum_n (G a h) A log2 e, then two of C.h.
+  float4 h[Shape::TT / 2][4 * 32];
+  static_assert(4 * Shape::LD <= 4 * 4 * 32, "four rows fit a pair's states");
 };
 
 // Partial sums in the workspace.
 struct BwdParts {
-  float* start;  // [chunks][D][NS] adjoints entering the chunks from behind (split only)
-  float* sums;   // [chunks][D] sums of delta (split only)
+  float* start;  // [half chunks][D][NS] adjoints entering the half chunks from behind (split only)
+  float* sums;   // [half chunks][D] sums of delta (split only)
   float* mix;    // [CTAs' channel tiles][N][2 NS]
   float* dA;     // [chunks][D][NS]
   float* vec;    // [chunks][2][D]: dskip, ddt_bias
 };
 struct BwdPlan {
-  int L, tiles;      // chunk length; CTAs' channel tiles of all groups
-  long long numbers; // chunks
+  int L, tiles;             // chunk length; CTAs' channel tiles of all groups
+  int half;                 // of it: the launches before the chunks' own work on twice as many (130 against 92 us)
+  long long numbers, halves;
   size_t start, sums, mix, dA, vec, total;  // bytes
 };
 int cta_tiles(const ScanArgs& a) {
@@ -54,33 +61,32 @@ int cta_tiles(const ScanArgs& a) {
 }
 BwdPlan plan_of(const ScanArgs& a) {
   BwdPlan p;
-  p.L = scan_split(a, ScanCost{330, 420, 75, 8});
+  p.L = scan_split(a, ScanCost{420, 900, 60, 12, 4});
   p.tiles = cta_tiles(a);
+  p.half = p.L / 2;
   p.numbers = packed_numbers(a.q, p.L);
+  p.halves = packed_numbers(a.q, p.half);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   const size_t states = up((size_t)p.numbers * a.D * a.NS * sizeof(float)), rows = up((size_t)p.numbers * a.D * sizeof(float));
   p.start = 0;
-  p.sums = p.start + (p.L == SCAN_WHOLE ? 0 : states);
-  p.mix = p.sums + (p.L == SCAN_WHOLE ? 0 : rows);
+  p.sums = p.start + (p.L == SCAN_WHOLE ? 0 : up((size_t)p.halves * a.D * a.NS * sizeof(float)));
+  p.mix = p.sums + (p.L == SCAN_WHOLE ? 0 : up((size_t)p.halves * a.D * sizeof(float)));
   p.dA = p.mix + up((size_t)p.tiles * a.q.N * 2 * a.NS * sizeof(float));
   p.vec = p.dA + states;
   p.total = p.vec + 2 * rows;
   return p;
 }
 
-template <bool WIDE, class T>
-__device__ __forceinline__ Quad<T> row_quad(const void* base, long long row, long long ts, int c, int n) {
-  return load_quad<WIDE>(static_cast<const T*>(base) + row * ts + c, n);
-}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // What a chunk hands to the one before it when nothing comes in from behind, and the sum of its delta.
 template <class T, int NS, bool WIDE>
-__global__ void __launch_bounds__(32 * WARPS) selective_scan_bwd_sum_kernel(ScanArgs a, int L, int tiles, long long warps, float* start,
-                                                                            float* sums) {
-  using Shape = ScanShape<NS>;
-  constexpr int S = Shape::S, P = Shape::P, CW = Shape::CW, TT = Shape::TT;
+__global__ void __launch_bounds__(32 * WARPS, SUM_CTAS) selective_scan_bwd_sum_kernel(ScanArgs a, int L, int tiles, long long warps,
+                                                                               float* start, float* sums) {
+  using Shape = ScanShape<NS, SUM_STATES>;
+  constexpr int S = Shape::S, P = Shape::P, LD = Shape::LD, TT = Shape::TT, N = Shape::SP / 2;
   struct Mine {
-    float delta[TT * CW], dy[TT * CW], C[TT * NS];
+    float delta[TT * LD], dy[TT * LD], C[TT * NS];
   };
   __shared__ __align__(16) Mine shared[WARPS];
   pdl_wait();
@@ -93,77 +99,93 @@ __global__ void __launch_bounds__(32 * WARPS) selective_scan_bwd_sum_kernel(Scan
   Chunk k;
   if (!packed_chunk(a.q, number, L, &k) || k.b == a.q.B || k.j == 0) return;
   const int t0 = k.j * L, t1 = k.len - t0 < L ? k.len : t0 + L;
-  f32x2 A[2][4], G[2][4];
+  f32x2 A[4][N], G[4][N];
   load_states<Shape>(a.A, w, A);
-  const f32x2 log2e = pack2(LOG2E, LOG2E);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    A[0][i] = mul2(A[0][i], log2e);
-    A[1][i] = mul2(A[1][i], log2e);
-    G[0][i] = G[1][i] = pack2(0.f, 0.f);
-  }
-  float bias[4] = {}, total[4] = {};
+  for (int c = 0; c < 4; ++c)
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (a.bias && i < w.n) bias[i] = a.bias[w.c + i];
+    for (int i = 0; i < N; ++i) {
+      A[c][i] = mul2(A[c][i], both(LOG2E));
+      G[c][i] = both(0.f);
+    }
+  f32x2 bias[2], total[2] = {both(0.f), both(0.f)};
+  load_channels(a.bias, w, bias);
   ScanRows<Shape, WIDE, T> rd, ry, rz;
   ScanMix<Shape, WIDE, T> rc;
-  auto fetch = [&](int t) {
-    const int rows = t1 - t;
-    rd.load(a.dt, k.first + (long long)t, a.dt_ts, rows, w);
-    ry.load(a.dy, k.first + (long long)t, a.dy_ts, rows, w);
-    if (a.z) rz.load(a.z, k.first + (long long)t, a.z_ts, rows, w);
-    rc.load(a.C, k.first + (long long)t, a.c_ts, a.c_gs, rows, w);
-  };
   const int last = t0 + (t1 - 1 - t0) / TT * TT;
-  fetch(last);
+  RowPtr<T> pd, py, pz;
+  MixPtr<T> pc;
+  {
+    const long long row0 = k.first + (long long)last;
+    pd.set(a.dt, row0, a.dt_ts, w);
+    py.set(a.dy, row0, a.dy_ts, w);
+    pz.set(a.z, row0, a.z_ts, w);
+    pc.set(a.C, row0, a.c_ts, a.c_gs, w);
+  }
+  const bool whole = __all_sync(0xffffffffu, w.n == 4);
+  auto fetch = [&](int rows) {
+    if (whole && rows >= TT) {
+      rd.template load<true>(pd, rows, w);
+      ry.template load<true>(py, rows, w);
+      if (a.z) rz.template load<true>(pz, rows, w);
+      rc.template load<true>(pc, rows, w);
+    } else {
+      rd.template load<false>(pd, rows, w);
+      ry.template load<false>(py, rows, w);
+      rz.template load<false>(pz, a.z ? rows : 0, w);
+      rc.template load<false>(pc, rows, w);
+    }
+    pd.p -= pd.tile;
+    py.p -= py.tile;
+    pz.p -= pz.tile;
+    pc.p -= pc.tile;
+  };
+  fetch(t1 - last);
   for (int t = last; t >= t0; t -= TT) {
     const int rows = t1 - t < TT ? t1 - t : TT;
     __syncwarp();
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int r = p * S + w.s;
-      float d[4], y[4], z[4];
-      quad_floats(rd.v[p], d);
-      quad_floats(ry.v[p], y);
-      if (a.z) quad_floats(rz.v[p], z);
+      f32x2 d[2], y[2], z[2];
+      quad_pairs(rd.v[p], d);
+      quad_pairs(ry.v[p], y);
+      quad_pairs(rz.v[p], z);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        d[i] += bias[i];
-        if (a.softplus) d[i] = softplus(d[i]);
-        if (r >= rows) d[i] = 0.f;
-        total[i] += d[i];
-        if (a.z) y[i] *= z[i] * sigmoid(z[i]);
+      for (int i = 0; i < 2; ++i) {
+        d[i] = add2(d[i], bias[i]);
+        if (a.softplus) d[i] = softplus2(d[i]);
+        if (r >= rows) d[i] = both(0.f);
+        total[i] = add2(total[i], d[i]);
+        if (a.z) y[i] = mul2(y[i], mul2(z[i], sigmoid2(z[i])));
       }
-      *reinterpret_cast<float4*>(sm.delta + r * CW + 4 * w.q) = make_float4(d[0], d[1], d[2], d[3]);
-      *reinterpret_cast<float4*>(sm.dy + r * CW + 4 * w.q) = make_float4(y[0], y[1], y[2], y[3]);
+      store_pairs(sm.delta + r * LD + 4 * w.q, d);
+      store_pairs(sm.dy + r * LD + 4 * w.q, y);
     }
     rc.store(sm.C, w);
     __syncwarp();
-    if (t > t0) fetch(t - TT);
+    fetch(t > t0 ? TT : 0);
 #pragma unroll 4
     for (int r = TT - 1; r >= 0; --r) {
-      const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(sm.delta + r * CW + 4 * w.q);
-      const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(sm.dy + r * CW + 4 * w.q);
-      const float4 cq = *reinterpret_cast<const float4*>(sm.C + r * NS + 4 * w.s);
-      const float cn[4] = {cq.x, cq.y, cq.z, cq.w};
+      const float4 dq = *reinterpret_cast<const float4*>(sm.delta + r * LD + 4 * w.q);
+      const float4 yq = *reinterpret_cast<const float4*>(sm.dy + r * LD + 4 * w.q);
+      const float d[4] = {dq.x, dq.y, dq.z, dq.w}, y[4] = {yq.x, yq.y, yq.z, yq.w};
+      f32x2 c[N];
+      load_row(c, sm.C + r * NS + Shape::SP * w.s);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const f32x2 c2 = pack2(cn[n], cn[n]);
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 arg = split2(mul2(e ? d.y : d.x, A[e][n]));
-          G[e][n] = mul2(pack2(ex2(arg.x), ex2(arg.y)), fma2(c2, e ? y.y : y.x, G[e][n]));
-        }
-      }
+        for (int n = 0; n < N; ++n) G[e][n] = mul2(ex2_2(scale2(d[e], A[e][n])), fma_by(y[e], c[n], G[e][n]));
     }
   }
   store_states<Shape>(start + number * a.D * NS, w, G);
+  const float2 s0 = split2(total[0]), s1 = split2(total[1]);
+  float v[4] = {s0.x, s0.y, s1.x, s1.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
 #pragma unroll
-    for (int d = 1; d < S; d *= 2) total[i] += __shfl_xor_sync(0xffffffffu, total[i], d);
-    if (w.s == 0 && i < w.n) sums[number * a.D + w.c + i] = total[i];
+    for (int d = 1; d < S; d *= 2) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+    if (w.s == 0 && i < w.n) sums[number * a.D + w.c + i] = v[i];
   }
 }
 
@@ -199,36 +221,69 @@ __global__ void __launch_bounds__(128) selective_scan_bwd_carry_kernel(ScanArgs 
   }
 }
 
-// Sums of eight values (dB and dC of the lane's states) over the warp's quads. A lane ends with 8 / min(Q, 8) of
-// them, from `base` on.
+// Whether lane s of a quad takes the channels' second pair first: the one whose sums it ends with.
+template <int S>
+__device__ __forceinline__ int pair_flip(int s) {
+  return S == 2 ? s & 1 : (s >> 1) & 1;
+}
+// Sums of four values (channels of the quad in each lane's order, x[0] those it ends with) over its S lanes: S = 2 leaves
+// two channels a lane, from 4 on the first of the two is channel s % 4.
+template <int S>
+__device__ __forceinline__ f32x2 sum_pairs(const f32x2 (&x)[2], int s) {
+  constexpr unsigned ALL = 0xffffffffu;
+  constexpr int FAR = S == 2 ? 1 : 2;
+  const float2 keep = split2(x[0]), give = split2(x[1]);
+  float a = keep.x + __shfl_xor_sync(ALL, give.x, FAR), b = keep.y + __shfl_xor_sync(ALL, give.y, FAR);
+  if constexpr (S >= 4) {
+    const bool odd = s & 1;
+    a = (odd ? b : a) + __shfl_xor_sync(ALL, odd ? a : b, 1);
+#pragma unroll
+    for (int d = 4; d < S; d *= 2) a += __shfl_xor_sync(ALL, a, d);
+    b = 0.f;
+  }
+  return pack2(a, b);
+}
+// Sums of eight values over the warp's quads: dB of the lane's four states in its order, then dC. The first step keeps the
+// lane's first two states, the next one state, the third dB or dC.
 template <class Shape>
-__device__ __forceinline__ int sum_mix(float (&v)[8], int q) {
-  int base = 0;
+__device__ __forceinline__ void put_mix(float* to, float (&v)[8], const ScanPlace<Shape>& w) {
+  constexpr unsigned ALL = 0xffffffffu;
+  constexpr int S = Shape::S, Q = Shape::Q;
+  float x[4] = {v[0], v[1], v[4], v[5]};  // dB, dB, dC, dC
+  {
+    const float give[4] = {v[2], v[3], v[6], v[7]};
 #pragma unroll
-  for (int lvl = 0, n = 8; (1 << lvl) < Shape::Q; ++lvl) {
-    const int far = Shape::S << lvl;
-    if (n > 1) {
-      n /= 2;
-      const bool up = (q >> lvl) & 1;
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, far);
-      }
-      base += up ? n : 0;
+    for (int i = 0; i < 4; ++i) x[i] += __shfl_xor_sync(ALL, give[i], S);
+  }
+  if constexpr (Q == 2) {
+    to[0] = x[0]; to[1] = x[1]; to[Shape::NS] = x[2]; to[Shape::NS + 1] = x[3];
+  } else {
+    const bool second = w.q & 2;
+    float b = (second ? x[1] : x[0]) + __shfl_xor_sync(ALL, second ? x[0] : x[1], 2 * S);
+    float c = (second ? x[3] : x[2]) + __shfl_xor_sync(ALL, second ? x[2] : x[3], 2 * S);
+    if constexpr (Q == 4) {
+      to[0] = b;
+      to[Shape::NS] = c;
     } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], far);
+      const bool last = w.q & 4;
+      b = (last ? c : b) + __shfl_xor_sync(ALL, last ? b : c, 4 * S);
+      if constexpr (Q == 16) b += __shfl_xor_sync(ALL, b, 8 * S);
+      if (Q == 8 || w.q < 8) to[0] = b;
     }
   }
-  return base;
+}
+// Where in a row of dB and dC put_mix's first result goes.
+template <class Shape>
+__device__ __forceinline__ int mix_place(const ScanPlace<Shape>& w) {
+  return 4 * w.s + 2 * (w.q & 1) + (Shape::Q > 2 ? (w.q >> 1) & 1 : 0) + (Shape::Q > 4 ? ((w.q >> 2) & 1) * Shape::NS : 0);
 }
 
 template <class T, int NS, bool WIDE>
-__global__ void __launch_bounds__(32 * WARPS) selective_scan_bwd_kernel(ScanArgs a, int L, int tiles, BwdParts parts) {
-  using Shape = ScanShape<NS>;
+__global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanArgs a, int L, int tiles, BwdParts parts) {
+  using Shape = ScanShape<NS, 4>;
   using Shared = BwdShared<Shape>;
-  constexpr int S = Shape::S, P = Shape::P, CW = Shape::CW, TT = Shape::TT, Q = Shape::Q;
-  constexpr int LEFT = 8 / (Q < 8 ? Q : 8);  // sums over quads that a lane ends with
+  constexpr int S = Shape::S, P = Shape::P, CW = Shape::CW, LD = Shape::LD, TT = Shape::TT;
+  static_assert(TT == SCAN_KEEP, "a kept state for every tile");
   extern __shared__ __align__(16) unsigned char raw_shared[];
   Shared* const all = reinterpret_cast<Shared*>(raw_shared);
   pdl_wait();
@@ -242,11 +297,12 @@ __global__ void __launch_bounds__(32 * WARPS) selective_scan_bwd_kernel(ScanArgs
   w.g = g;
   w.c = g * dg + ((tile - g * per) * WARPS + (int)threadIdx.x / 32) * CW + 4 * w.q;
   w.n = min(max((g + 1) * dg - w.c, 0), 4);
+  const int flip_c = pair_flip<S>(w.s), flip_n = w.q & 1;  // the lane's order of channels and states
   const long long row = (long long)a.D * NS;
   f32x2 A[2][4], G[2][4], dA[2][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dA[0][i] = dA[1][i] = G[0][i] = G[1][i] = pack2(0.f, 0.f);
-  float dskip[4] = {}, dbias[4] = {};
+  for (int i = 0; i < 4; ++i) dA[0][i] = dA[1][i] = G[0][i] = G[1][i] = both(0.f);
+  f32x2 dskip[2] = {both(0.f), both(0.f)}, dbias[2] = {both(0.f), both(0.f)};
 
   Chunk k;
   const bool used = packed_chunk(a.q, number, L, &k);
@@ -261,186 +317,205 @@ __global__ void __launch_bounds__(32 * WARPS) selective_scan_bwd_kernel(ScanArgs
     }
   } else if (used) {
     const int t0 = k.j * L, t1 = k.len - t0 < L ? k.len : t0 + L;
-    load_states<Shape>(a.A, w, A);
-    const f32x2 log2e = pack2(LOG2E, LOG2E);
+    load_columns<Shape>(a.A, w, flip_c, flip_n, A);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      A[0][i] = mul2(A[0][i], log2e);
-      A[1][i] = mul2(A[1][i], log2e);
+      A[0][i] = mul2(A[0][i], both(LOG2E));
+      A[1][i] = mul2(A[1][i], both(LOG2E));
     }
-    if (parts.start) load_states<Shape>(parts.start + number * row, w, G);
-    else if (a.dh_final) load_states<Shape>(a.dh_final + k.b * row, w, G);
-    float bias[4] = {}, skip[4] = {};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < w.n) {
-        if (a.bias) bias[i] = a.bias[w.c + i];
-        if (a.skip) skip[i] = a.skip[w.c + i];
-      }
-    const float* kept = a.kept + packed_number(a.q, k.b, k.first, TT) * row;
+    if (parts.start) {
+      const long long behind = packed_number(a.q, k.b, k.first, L / 2) + min(2 * k.j + 1, packed_per(k.len, L / 2) - 1);
+      load_columns<Shape>(parts.start + behind * row, w, flip_c, flip_n, G);
+    }
+    else if (a.dh_final) load_columns<Shape>(a.dh_final + k.b * row, w, flip_c, flip_n, G);
+    f32x2 bias[2], skip[2];
+    load_channels(a.bias, w, bias);
+    load_channels(a.skip, w, skip);
     const int last = t1 > t0 ? t0 + (t1 - 1 - t0) / TT * TT : t0 - TT;
+    const float* kept = a.kept + (packed_number(a.q, k.b, k.first, TT) + last / TT) * row;
+    RowPtr<T> pu, pd, py, pz;
+    MixPtr<T> pb, pc;
+    {
+      const long long row0 = k.first + (long long)last;
+      pu.set(a.u, row0, a.u_ts, w);
+      pd.set(a.dt, row0, a.dt_ts, w);
+      py.set(a.dy, row0, a.dy_ts, w);
+      pz.set(a.z, row0, a.z_ts, w);
+      pb.set(a.B, row0, a.b_ts, a.b_gs, w);
+      pc.set(a.C, row0, a.c_ts, a.c_gs, w);
+    }
+    long long to = ((long long)k.first + last + w.s) * a.D + w.c;  // the contiguous gradients' place
+    float* mix_to = parts.mix + ((long long)tile * a.q.N + k.first + last) * 2 * NS;
+    const bool whole = __all_sync(0xffffffffu, w.n == 4);
+    const int at = 4 * w.q, mix_at = mix_place<Shape>(w);
+    // pairs of the quad's values in the lane's order
+    auto load_quad_pairs = [&](f32x2 (&x)[2], const float* p) {
+      x[0] = *reinterpret_cast<const f32x2*>(p + 2 * flip_c);
+      x[1] = *reinterpret_cast<const f32x2*>(p + 2 - 2 * flip_c);
+    };
+    auto load_four = [&](float (&x)[4], const float* p) {
+      const float2 a0 = *reinterpret_cast<const float2*>(p + 2 * flip_n), a1 = *reinterpret_cast<const float2*>(p + 2 - 2 * flip_n);
+      x[0] = a0.x; x[1] = a0.y; x[2] = a1.x; x[3] = a1.y;
+    };
+    // token r of the tile forwards: the state before it, and after
+    auto step = [&](int r, const f32x2 (&before)[2][4], f32x2 (&after)[2][4]) {
+      f32x2 d[2], x[2];
+      float bn[4];
+      load_quad_pairs(d, sm.delta + r * LD + at);
+      load_quad_pairs(x, sm.du + r * LD + at);
+      load_four(bn, sm.B + r * NS + 4 * w.s);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) after[e][n] = fma2(ex2_2(mul2(d[e], A[e][n])), before[e][n], scale2(bn[n], x[e]));
+    };
+    // and backwards, its factors formed again: own gets the lane's part of the quad's d(delta u), sum_n (G a h) A log2 e and
+    // C.h, summed over the lanes
+    auto back = [&](int r, const f32x2 (&before)[2][4], const f32x2 (&after)[2][4], f32x2 (&own)[3]) {
+      f32x2 d[2], x[2], y[2], sums[3][2];
+      float bn[4], cn[4], mix[8];
+      load_quad_pairs(d, sm.delta + r * LD + at);
+      load_quad_pairs(x, sm.du + r * LD + at);
+      load_quad_pairs(y, sm.dy + r * LD + at);
+      load_four(bn, sm.B + r * NS + 4 * w.s);
+      load_four(cn, sm.C + r * NS + 4 * w.s);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        f32x2 db, dc;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          G[e][n] = fma_by(cn[n], y[e], G[e][n]);
+          dc = e ? fma2(after[e][n], y[e], dc) : mul2(after[e][n], y[e]);
+          db = e ? fma2(G[e][n], x[e], db) : mul2(G[e][n], x[e]);
+          sums[0][e] = n ? fma_by(bn[n], G[e][n], sums[0][e]) : scale2(bn[n], G[e][n]);
+          sums[2][e] = n ? fma_by(cn[n], after[e][n], sums[2][e]) : scale2(cn[n], after[e][n]);
+          G[e][n] = mul2(G[e][n], ex2_2(mul2(d[e], A[e][n])));
+          const f32x2 ga = mul2(G[e][n], before[e][n]);
+          sums[1][e] = n ? fma2(ga, A[e][n], sums[1][e]) : mul2(ga, A[e][n]);
+          dA[e][n] = fma2(ga, d[e], dA[e][n]);
+        }
+        const float2 b = split2(db), c = split2(dc);
+        mix[n] = b.x + b.y;
+        mix[4 + n] = c.x + c.y;
+      }
+#pragma unroll
+      for (int m = 0; m < 3; ++m)
+        if (m < 2 || a.z) own[m] = sum_pairs<S>(sums[m], w.s);
+      put_mix<Shape>(sm.mix + r * 2 * NS + mix_at, mix, w);
+    };
+    auto put = [&](float* row_quad, f32x2 v) {
+      const float2 f = split2(v);
+      if constexpr (S == 2) *reinterpret_cast<float2*>(row_quad + 2 * w.s) = f;
+      else if (S == 4 || w.s < 4) row_quad[w.s % 4] = f.x;
+    };
     for (int t = last; t >= t0; t -= TT) {
       const int rows = t1 - t < TT ? t1 - t : TT;
-      const long long row0 = k.first + (long long)t;
+      const bool full = whole && rows == TT;
+      f32x2 h[2][4];
       {
         ScanRows<Shape, WIDE, T> ru, rd, ry, rz;
         ScanMix<Shape, WIDE, T> rb, rc;
-        ru.load(a.u, row0, a.u_ts, rows, w);
-        rd.load(a.dt, row0, a.dt_ts, rows, w);
-        ry.load(a.dy, row0, a.dy_ts, rows, w);
-        if (a.z) rz.load(a.z, row0, a.z_ts, rows, w);
-        rb.load(a.B, row0, a.b_ts, a.b_gs, rows, w);
-        rc.load(a.C, row0, a.c_ts, a.c_gs, rows, w);
+        if (full) {
+          rd.template load<true>(pd, rows, w);
+          ru.template load<true>(pu, rows, w);
+          ry.template load<true>(py, rows, w);
+          if (a.z) rz.template load<true>(pz, rows, w);
+          rb.template load<true>(pb, rows, w);
+          rc.template load<true>(pc, rows, w);
+        } else {
+          rd.template load<false>(pd, rows, w);
+          ru.template load<false>(pu, rows, w);
+          ry.template load<false>(py, rows, w);
+          if (a.z) rz.template load<false>(pz, rows, w);
+          rb.template load<false>(pb, rows, w);
+          rc.template load<false>(pc, rows, w);
+        }
+        load_columns<Shape>(kept, w, flip_c, flip_n, h);
+        if (full && t > t0) {  // the next tile's rows and state to L2
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            prefetch_l2(pu.p - pu.tile + p * pu.step);
+            prefetch_l2(pd.p - pd.tile + p * pd.step);
+            prefetch_l2(py.p - py.tile + p * py.step);
+            if (a.z) prefetch_l2(pz.p - pz.tile + p * pz.step);
+          }
+          prefetch_l2(kept - row + (long long)(w.c + w.s % 4) * NS);
+        }
         __syncwarp();
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           const int r = p * S + w.s;
-          float d[4], u[4], y[4], z[4];
-          quad_floats(rd.v[p], d);
-          quad_floats(ru.v[p], u);
-          quad_floats(ry.v[p], y);
-          if (a.z) quad_floats(rz.v[p], z);
+          if (S > TT && r >= TT) continue;
+          f32x2 d[2], u[2], y[2], z[2];
+          quad_pairs(rd.v[p], d);
+          quad_pairs(ru.v[p], u);
+          quad_pairs(ry.v[p], y);
+          store_pairs(sm.u + r * LD + at, u);
+          if (a.softplus) {
+            f32x2 s[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            d[i] += bias[i];
-            if (a.softplus) d[i] = softplus(d[i]);
-            if (r >= rows) d[i] = 0.f;  // a step that changes nothing
-            u[i] *= d[i];
-            if (a.z) y[i] *= z[i] * sigmoid(z[i]);
+            for (int i = 0; i < 2; ++i) d[i] = softplus2(add2(d[i], bias[i]), &s[i]);
+            store_pairs(sm.slope + r * LD + at, s);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) d[i] = add2(d[i], bias[i]);
           }
-          *reinterpret_cast<float4*>(sm.delta + r * CW + 4 * w.q) = make_float4(d[0], d[1], d[2], d[3]);
-          *reinterpret_cast<float4*>(sm.du + r * CW + 4 * w.q) = make_float4(u[0], u[1], u[2], u[3]);
-          *reinterpret_cast<float4*>(sm.dy + r * CW + 4 * w.q) = make_float4(y[0], y[1], y[2], y[3]);
+          if (!full && r >= rows) d[0] = d[1] = both(0.f);  // a step that changes nothing
+#pragma unroll
+          for (int i = 0; i < 2; ++i) u[i] = mul2(u[i], d[i]);
+          if (a.z) {
+            quad_pairs(rz.v[p], z);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // silu' = s + z s (1 - s)
+              const f32x2 s = sigmoid2(z[i]), zs = mul2(z[i], s);
+              z[i] = mul2(y[i], fma2(zs, fma2(s, both(-1.f), both(1.f)), s));
+              y[i] = mul2(y[i], zs);
+            }
+            store_pairs(sm.dz + r * LD + at, z);
+          }
+          store_pairs(sm.delta + r * LD + at, d);
+          store_pairs(sm.du + r * LD + at, u);
+          store_pairs(sm.dy + r * LD + at, y);
         }
         rb.store(sm.B, w);
         rc.store(sm.C, w);
         __syncwarp();
       }
-      const int groups = (rows + GROUP - 1) / GROUP;
-      f32x2 h[2][4];
-      load_states<Shape>(kept + (long long)(t / TT) * row, w, h);
-      auto keep = [&](int i) {
+      // forward through the tile: the state before every second token is kept, the last one stays in registers
+      const int pairs = (rows + 1) / 2;
+      for (int i = 0; i < pairs; ++i) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            reinterpret_cast<ulonglong2*>(sm.h[i])[(2 * e + n) * 32 + w.lane] = make_ulonglong2(h[e][2 * n], h[e][2 * n + 1]);
+#pragma unroll
+        for (int r0 = 0; r0 < 2; ++r0) step(2 * i + r0, h, h);
+      }
+      for (int i = pairs - 1; i >= 0; --i) {
+        f32x2 h0[2][4], h1[2][4], own[2][3];  // states before the pair and between its tokens
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            ulonglong2 v;
-            v.x = h[e][2 * n];
-            v.y = h[e][2 * n + 1];
-            reinterpret_cast<ulonglong2*>(sm.h)[(i * 4 + 2 * e + n) * 32 + w.lane] = v;
+            const ulonglong2 v = reinterpret_cast<const ulonglong2*>(sm.h[i])[(2 * e + n) * 32 + w.lane];
+            h0[e][2 * n] = v.x;
+            h0[e][2 * n + 1] = v.y;
           }
-      };
-      for (int i = 0; i + 1 < groups; ++i) {
-        keep(i);
+        step(2 * i, h0, h1);
+        back(2 * i + 1, h1, h, own[1]);
+        back(2 * i, h0, h1, own[0]);
 #pragma unroll
-        for (int r0 = 0; r0 < GROUP; ++r0) {
-          const int r = i * GROUP + r0;
-          const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(sm.delta + r * CW + 4 * w.q);
-          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sm.du + r * CW + 4 * w.q);
-          const float4 bq = *reinterpret_cast<const float4*>(sm.B + r * NS + 4 * w.s);
-          const float bn[4] = {bq.x, bq.y, bq.z, bq.w};
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const f32x2 b2 = pack2(bn[n], bn[n]);
+          for (int n = 0; n < 4; ++n) h[e][n] = h0[e][n];
+        __syncwarp();  // every lane has read the pair's values and states
+        float* place = reinterpret_cast<float*>(sm.h[i]) + at;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 arg = split2(mul2(e ? d.y : d.x, A[e][n]));
-              h[e][n] = fma2(pack2(ex2(arg.x), ex2(arg.y)), h[e][n], mul2(e ? x.y : x.x, b2));
-            }
-          }
-        }
-      }
-      for (int i = groups - 1; i >= 0; --i) {
-        f32x2 hs[GROUP + 1][2][4], f[GROUP][2][4];  // states before and after the tokens, factors
-        if (i == groups - 1) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) hs[0][e][n] = h[e][n];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const ulonglong2 v = reinterpret_cast<const ulonglong2*>(sm.h)[(i * 4 + 2 * e + n) * 32 + w.lane];
-              hs[0][e][2 * n] = v.x;
-              hs[0][e][2 * n + 1] = v.y;
-            }
-        }
-#pragma unroll
-        for (int r0 = 0; r0 < GROUP; ++r0) {
-          const int r = i * GROUP + r0;
-          const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(sm.delta + r * CW + 4 * w.q);
-          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sm.du + r * CW + 4 * w.q);
-          const float4 bq = *reinterpret_cast<const float4*>(sm.B + r * NS + 4 * w.s);
-          const float bn[4] = {bq.x, bq.y, bq.z, bq.w};
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const f32x2 b2 = pack2(bn[n], bn[n]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 arg = split2(mul2(e ? d.y : d.x, A[e][n]));
-              f[r0][e][n] = pack2(ex2(arg.x), ex2(arg.y));
-              hs[r0 + 1][e][n] = fma2(f[r0][e][n], hs[r0][e][n], mul2(e ? x.y : x.x, b2));
-            }
-          }
-        }
-        float own[GROUP][3][2];
-#pragma unroll
-        for (int r0 = GROUP - 1; r0 >= 0; --r0) {
-          const int r = i * GROUP + r0;
-          const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(sm.delta + r * CW + 4 * w.q);
-          const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(sm.du + r * CW + 4 * w.q);
-          const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(sm.dy + r * CW + 4 * w.q);
-          const float4 bq = *reinterpret_cast<const float4*>(sm.B + r * NS + 4 * w.s);
-          const float4 cq = *reinterpret_cast<const float4*>(sm.C + r * NS + 4 * w.s);
-          const float bn[4] = {bq.x, bq.y, bq.z, bq.w}, cn[4] = {cq.x, cq.y, cq.z, cq.w};
-          f32x2 gx[2], gd[2], ch[2];
-          float mix[8];
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const f32x2 b2 = pack2(bn[n], bn[n]), c2 = pack2(cn[n], cn[n]);
-            f32x2 db, dc;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              G[e][n] = fma2(c2, e ? y.y : y.x, G[e][n]);
-              dc = e ? fma2(hs[r0 + 1][e][n], y.y, dc) : mul2(hs[r0 + 1][e][n], y.x);
-              db = e ? fma2(G[e][n], x.y, db) : mul2(G[e][n], x.x);
-              gx[e] = n ? fma2(G[e][n], b2, gx[e]) : mul2(G[e][n], b2);
-              ch[e] = n ? fma2(hs[r0 + 1][e][n], c2, ch[e]) : mul2(hs[r0 + 1][e][n], c2);
-              G[e][n] = mul2(G[e][n], f[r0][e][n]);
-              const f32x2 ga = mul2(G[e][n], hs[r0][e][n]);
-              gd[e] = n ? fma2(ga, A[e][n], gd[e]) : mul2(ga, A[e][n]);
-              dA[e][n] = fma2(ga, e ? d.y : d.x, dA[e][n]);
-            }
-            const float2 b = split2(db), c = split2(dc);
-            mix[n] = b.x + b.y;
-            mix[4 + n] = c.x + c.y;
-          }
-          const f32x2* const sums[3] = {gx, gd, ch};
-#pragma unroll
-          for (int m = 0; m < 3; ++m) {
-            if (m == 2 && !a.z) break;
-            const float2 v0 = split2(sums[m][0]), v1 = split2(sums[m][1]);
-            const float v[4] = {v0.x, v0.y, v1.x, v1.y};
-            sum_quad<S>(v, w.s, own[r0][m]);
-          }
-          const int base = sum_mix<Shape>(mix, w.q);
-          if (Q <= 8 || w.q < 8) {
-#pragma unroll
-            for (int m = 0; m < LEFT; ++m) {
-              const int v = base + m;
-              sm.mix[r * 2 * NS + (v < 4 ? 0 : NS - 4) + 4 * w.s + v] = mix[m];
-            }
-          }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int r0 = 0; r0 < GROUP; ++r0) {
-          const int to = (i * GROUP + r0) * CW + 4 * w.q;
-          put_quad<S>(sm.du + to, w.s, own[r0][0]);
-          put_quad<S>(sm.gd + to, w.s, own[r0][1]);
-          if (a.z) put_quad<S>(sm.dy + to, w.s, own[r0][2]);
+        for (int r0 = 0; r0 < 2; ++r0) {
+          put(sm.du + (2 * i + r0) * LD + at, own[r0][0]);
+          put(place + r0 * LD, own[r0][1]);
+          if (a.z) put(place + (2 + r0) * LD, own[r0][2]);
         }
       }
       __syncthreads();
@@ -448,58 +523,68 @@ __global__ void __launch_bounds__(32 * WARPS) selective_scan_bwd_kernel(ScanArgs
         float v = 0.f;
 #pragma unroll
         for (int j = 0; j < WARPS; ++j) v += all[j].mix[i];
-        parts.mix[((long long)tile * a.q.N + row0) * 2 * NS + i] = v;
+        mix_to[i] = v;
       }
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int r = p * S + w.s;
-        if (r >= rows) continue;
-        float d[4], u[4], y[4], raw[4], gx[4], gd[4], du[4], ddt[4];
-        quad_floats(row_quad<WIDE, T>(a.u, row0 + r, a.u_ts, w.c, w.n), u);
-        quad_floats(row_quad<WIDE, T>(a.dt, row0 + r, a.dt_ts, w.c, w.n), raw);
-        quad_floats(row_quad<WIDE, T>(a.dy, row0 + r, a.dy_ts, w.c, w.n), y);
-        ld4(d, sm.delta + r * CW + 4 * w.q);
-        ld4(gx, sm.du + r * CW + 4 * w.q);
-        ld4(gd, sm.gd + r * CW + 4 * w.q);
-        const long long to = (row0 + r) * a.D + w.c;
+        if ((S > TT || !full) && r >= rows) continue;  // (S above TT: lanes without a row)
+        f32x2 d[2], u[2], y[2], gx[2], gd[2];
+        const float* place = reinterpret_cast<const float*>(sm.h[r / 2]) + r % 2 * LD + at;
+        load_pairs(d, sm.delta + r * LD + at);
+        load_pairs(u, sm.u + r * LD + at);
+        load_pairs(y, sm.dy + r * LD + at);
+        load_pairs(gx, sm.du + r * LD + at);
+        load_pairs(gd, place);
+        const long long off = to + p * S * a.D;
         if (a.z) {
-          float z[4], ch[4], dz[4];
-          quad_floats(row_quad<WIDE, T>(a.z, row0 + r, a.z_ts, w.c, w.n), z);
-          ld4(ch, sm.dy + r * CW + 4 * w.q);
+          f32x2 dz[2], ch[2];
+          load_pairs(dz, sm.dz + r * LD + at);
+          load_pairs(ch, place + 2 * LD);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float s = sigmoid(z[e]);
-            dz[e] = y[e] * fmaf(skip[e], u[e], ch[e]) * fmaf(z[e] * s, 1.f - s, s);
-            y[e] *= z[e] * s;
-          }
-          store_quad<WIDE>(static_cast<T*>(a.dz) + to, dz, w.n);
+          for (int e = 0; e < 2; ++e) dz[e] = mul2(dz[e], fma2(skip[e], u[e], ch[e]));
+          store_quad<WIDE>(static_cast<T*>(a.dz) + off, dz, w.n);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          du[e] = fmaf(gx[e], d[e], y[e] * skip[e]);
-          ddt[e] = fmaf(gx[e], u[e], gd[e] * 0.693147180559945309f);
-          if (a.softplus) ddt[e] *= sigmoid(raw[e] + bias[e]);
-          dskip[e] = fmaf(y[e], u[e], dskip[e]);
-          dbias[e] += ddt[e];
+        for (int e = 0; e < 2; ++e) {
+          gd[e] = fma2(gx[e], u[e], mul2(gd[e], both(0.693147180559945309f)));
+          gx[e] = fma2(gx[e], d[e], mul2(y[e], skip[e]));
+          dskip[e] = fma2(y[e], u[e], dskip[e]);
         }
-        store_quad<WIDE>(static_cast<T*>(a.du) + to, du, w.n);
-        store_quad<WIDE>(static_cast<T*>(a.ddt) + to, ddt, w.n);
+        if (a.softplus) {
+          f32x2 s[2];
+          load_pairs(s, sm.slope + r * LD + at);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) gd[e] = mul2(gd[e], s[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) dbias[e] = add2(dbias[e], gd[e]);
+        store_quad<WIDE>(static_cast<T*>(a.du) + off, gx, w.n);
+        store_quad<WIDE>(static_cast<T*>(a.ddt) + off, gd, w.n);
       }
       __syncthreads();  // the sums over channels have been read
+      pu.p -= pu.tile;
+      pd.p -= pd.tile;
+      py.p -= py.tile;
+      pz.p -= pz.tile;
+      to -= TT * a.D;
+      pb.p -= pb.tile;
+      pc.p -= pc.tile;
+      kept -= row;
+      mix_to -= TT * 2 * NS;
     }
-    if (k.j == 0 && a.dh0) store_states<Shape>(a.dh0 + k.b * row, w, G);
+    if (k.j == 0 && a.dh0) store_columns<Shape>(a.dh0 + k.b * row, w, flip_c, flip_n, G);
   }
-  store_states<Shape>(parts.dA + number * row, w, dA);
+  store_columns<Shape>(parts.dA + number * row, w, flip_c, flip_n, dA);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int m = 0; m < 2; ++m) {
+    const float2 v0 = split2(m ? dbias[0] : dskip[0]), v1 = split2(m ? dbias[1] : dskip[1]);
+    float v[4] = {v0.x, v0.y, v1.x, v1.y};
 #pragma unroll
-    for (int d = 1; d < S; d *= 2) {
-      dskip[i] += __shfl_xor_sync(0xffffffffu, dskip[i], d);
-      dbias[i] += __shfl_xor_sync(0xffffffffu, dbias[i], d);
-    }
-    if (w.s == 0 && i < w.n) {
-      parts.vec[(2 * number) * a.D + w.c + i] = dskip[i];
-      parts.vec[(2 * number + 1) * a.D + w.c + i] = dbias[i];
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int d = 1; d < S; d *= 2) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+      if (w.s == 0 && i < w.n) parts.vec[(2 * number + m) * a.D + w.c + i] = v[i];
     }
   }
 }
@@ -573,22 +658,22 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   if (blocks > 0x7fffffff || join_blocks > 0x7fffffff) return cudaErrorNotSupported;
   cudaError_t e;
   if (parts.start) {
-    const int tiles = scan_tiles(a.D, a.G, NS);
-    const long long warps = p.numbers * tiles, sum_blocks = (warps + WARPS - 1) / WARPS;
+    const int tiles = scan_tiles(a.D, a.G, NS, SUM_STATES);
+    const long long warps = p.halves * tiles, sum_blocks = (warps + WARPS - 1) / WARPS;
     if (sum_blocks > 0x7fffffff) return cudaErrorNotSupported;
     prof_mark(K_SSCAN_RSUM, s, true);
-    e = launch_pdl(selective_scan_bwd_sum_kernel<T, NS, WIDE>, dim3((unsigned)sum_blocks), dim3(32 * WARPS), 0, s, a, p.L, tiles,
+    e = launch_pdl(selective_scan_bwd_sum_kernel<T, NS, WIDE>, dim3((unsigned)sum_blocks), dim3(32 * WARPS), 0, s, a, p.half, tiles,
                    warps, parts.start, parts.sums);
     prof_mark(K_SSCAN_RSUM, s, false);
     if (e != cudaSuccess) return e;
     const long long threads = (long long)a.q.B * a.D * NS;
     prof_mark(K_SCAN_CARRY, s, true);
-    e = launch_pdl(selective_scan_bwd_carry_kernel, dim3((unsigned)((threads + 127) / 128)), dim3(128), 0, s, a, p.L, parts.start,
+    e = launch_pdl(selective_scan_bwd_carry_kernel, dim3((unsigned)((threads + 127) / 128)), dim3(128), 0, s, a, p.half, parts.start,
                    (const float*)parts.sums);
     prof_mark(K_SCAN_CARRY, s, false);
     if (e != cudaSuccess) return e;
   }
-  const int bytes = (int)sizeof(BwdShared<ScanShape<NS>>) * WARPS;
+  const int bytes = (int)sizeof(BwdShared<ScanShape<NS, 4>>) * WARPS;
   e = allow_shared(reinterpret_cast<const void*>(selective_scan_bwd_kernel<T, NS, WIDE>), bytes, &done);
   if (e != cudaSuccess) return e;
   prof_mark(K_SSCAN_BWD, s, true);
