@@ -161,7 +161,7 @@ int gdn_causal_conv_bwd(const gdn_conv_dims* d, const gdn_packed* q, const gdn_r
 size_t gdn_selective_scan_residual_bytes(const gdn_scan_dims* d, const gdn_packed* q) {
   if (check_scan(d) != GDN_OK || check_packed(q, true) != GDN_OK || nothing(q)) return 0;
   const ScanArgs a = scan_args(d, q, 1);
-  return (size_t)packed_numbers(a.q, SCAN_KEEP) * d->D * d->S * sizeof(float);
+  return (size_t)packed_numbers(a.q, SCAN_KEEP) * scan_quads(d->D, d->G) * 4 * d->S * sizeof(float);
 }
 
 size_t gdn_selective_scan_workspace_bytes(const gdn_scan_dims* d, const gdn_packed* q, int max_q) {

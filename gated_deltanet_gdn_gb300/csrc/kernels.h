@@ -327,7 +327,7 @@ struct ScanArgs {
   const float *A, *skip, *bias, *h0;
   void* y;
   float* h_final;
-  float* kept;  // states before every SCAN_KEEP tokens, or NULL
+  float* kept;  // [scan_quads * 4 * NS] before every SCAN_KEEP tokens, or NULL
   int max_q;
   // backward
   const float* dh_final;
@@ -335,8 +335,13 @@ struct ScanArgs {
   float *dA, *dskip, *dbias, *dh0;
   void* ws;
 };
-// Tokens between two kept states.
+// Tokens between two kept states, and the floats of one: quads of channels, whole ones for every group.
 constexpr int SCAN_KEEP = 8;
+inline
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+int scan_quads(int D, int G) { return G * ((D / G + 3) / 4); }
 
 // Plan of a serving step (page_plan.cu).
 constexpr int PLAN_MAX_REQUESTS = 8192;

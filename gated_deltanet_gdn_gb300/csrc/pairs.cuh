@@ -60,6 +60,11 @@ __device__ __forceinline__ f32x2 ex2_2(f32x2 x) {
   const float2 f = split2(x);
   return pack2(ex2(f.x), ex2(f.y));
 }
+// 2^x of two factors' exponents s a <= 0 that are multiplied up over many steps. The hardware's result is low on average,
+// by 2e-8 of the value between 2^-8 and 1 and by less below, which a slow decay sums up; EX2_SHIFT, added in the same instruction, takes
+// most of that (all of it would leave exponents below 2^-9 high): states and gradients came out half as far off.
+constexpr float EX2_SHIFT = 2.0e-8f;
+__device__ __forceinline__ f32x2 decay2(f32x2 s, f32x2 a) { return ex2_2(fma2(s, a, both(EX2_SHIFT))); }
 __device__ __forceinline__ f32x2 rcp_2(f32x2 x) {
   const float2 f = split2(x);
   return pack2(rcp(f.x), rcp(f.y));

@@ -6,27 +6,52 @@ namespace gdn {
 namespace {
 
 constexpr int WARPS = 4;
-constexpr int STATES = 8, CTAS = 3;  // states of a lane, CTAs of an SM
+// States of a lane and CTAs of an SM. (16 states need more registers than there are: 249 against 141 us at B8 T4096 D768,
+// 16 states; 4 states: 144 us, and the chunks' ends 91 against 85 us.)
+constexpr int STATES = 8, CTAS = 3;
+
+// Stores the first n of a lane's OWN channels.
+template <bool WIDE, int OWN, class T>
+__device__ __forceinline__ void put_own(T* p, const float (&x)[4], int n) {
+  if constexpr (WIDE && OWN == 4) {
+    if (n > 0) st4(p, x);
+  } else if constexpr (WIDE && OWN == 2) {
+    if (n > 0) store2(p, x[0], x[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < OWN; ++i)
+      if (i < n) p[i] = from_f32<T>(x[i]);
+  }
+}
+
+constexpr int TILE = 4;  // tokens
 
 template <class Shape>
-struct WarpShared {
-  float delta[Shape::TT * Shape::LD], du[Shape::TT * Shape::LD], y[Shape::TT * Shape::LD];
+struct WarpTile {
+  float delta[Shape::TT * Shape::LD], du[Shape::TT * Shape::LD];
+  float skip[Shape::TT * Shape::LD], gate[Shape::TT * Shape::LD];  // D u and silu(z)
   float B[Shape::TT * Shape::NS], C[Shape::TT * Shape::NS];
+};
+template <class Shape>
+struct SumTile {
+  float delta[Shape::TT * Shape::LD], du[Shape::TT * Shape::LD], B[Shape::TT * Shape::NS];
 };
 
 // SUM: what a chunk adds to the state (from zeros) and the sum of its delta, no outputs.
 // start: [chunks][D][NS] states at the chunks' starts (SUM: written as the chunks' own ends), sums: [chunks][D].
 template <class T, int NS, bool WIDE, bool SUM>
 __global__ void __launch_bounds__(32 * WARPS, CTAS) selective_scan_kernel(ScanArgs a, int L, int tiles, long long warps, float* start,
-                                                                       float* sums) {
-  using Shape = ScanShape<NS, STATES>;
+                                                                          float* sums) {
+  using Shape = ScanShape<NS, STATES, TILE>;
   constexpr int S = Shape::S, P = Shape::P, LD = Shape::LD, TT = Shape::TT, N = STATES / 2;
-  __shared__ __align__(16) WarpShared<Shape> shared[WARPS];
+  constexpr int OWN = S == 1 ? 4 : S == 2 ? 2 : 1;  // channels whose sums a lane ends with
+  using Tile = std::conditional_t<SUM, SumTile<Shape>, WarpTile<Shape>>;
+  __shared__ __align__(16) Tile shared[WARPS][2];
   pdl_wait();
   pdl_trigger();
   const long long at = (long long)blockIdx.x * WARPS + threadIdx.x / 32;
   if (at >= warps) return;
-  WarpShared<Shape>& sm = shared[threadIdx.x / 32];
+  Tile(&sm)[2] = shared[threadIdx.x / 32];
   const long long number = at / tiles;
   const ScanPlace<Shape> w(a, (int)(at - number * tiles));
   Chunk k;
@@ -61,127 +86,150 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) selective_scan_kernel(ScanAr
   load_channels(a.bias, w, bias);
   load_channels(SUM ? nullptr : a.skip, w, skip);
   float* kept = nullptr;
-  if (!SUM && a.kept) kept = a.kept + (packed_number(a.q, k.b, k.first, SCAN_KEEP) + t0 / SCAN_KEEP) * row;
+  long long kept_channel = 0, kept_row = 0;
+  if (!SUM && a.kept) {
+    kept_channel = kept_step<NS>(a);
+    kept_row = kept_channel * 8;
+    kept = a.kept + (packed_number(a.q, k.b, k.first, SCAN_KEEP) + t0 / SCAN_KEEP) * kept_row + kept_place(a, w, 2 * w.s);
+  }
+  // the lane's channels of the sums, and how many of them there are
+  const int own = S == 1 ? 0 : S == 2 ? 2 * w.s : w.s % 4, own_n = S > 4 && w.s >= 4 ? 0 : w.n - own;
+  T* y = static_cast<T*>(a.y) + (k.first + (long long)t0) * a.y_ts + w.c + own;
 
   ScanRows<Shape, WIDE, T> ru, rd, rz;
   ScanMix<Shape, WIDE, T> rb, rc;
-  RowPtr<T> pu, pd, pz, py;
+  RowPtr<T> pu, pd, pz;
   MixPtr<T> pb, pc;
   {
     const long long row0 = k.first + (long long)t0;
     pu.set(a.u, row0, a.u_ts, w);
     pd.set(a.dt, row0, a.dt_ts, w);
+    pz.set(a.z, row0, a.z_ts, w);
     pb.set(a.B, row0, a.b_ts, a.b_gs, w);
     pc.set(a.C, row0, a.c_ts, a.c_gs, w);
-    pz.set(a.z, row0, a.z_ts, w);
-    py.set(a.y, row0, a.y_ts, w);
   }
   const bool whole = __all_sync(0xffffffffu, w.n == 4);  // every lane has its channels
+  // The next tile's loads; no rows are left behind the last one.
   auto fetch = [&](int rows) {
     if (whole && rows >= TT) {
       ru.template load<true>(pu, rows, w);
       rd.template load<true>(pd, rows, w);
       rb.template load<true>(pb, rows, w);
-      if (!SUM) rc.template load<true>(pc, rows, w);
+      if constexpr (!SUM) {
+        if (a.z) rz.template load<true>(pz, rows, w);
+        rc.template load<true>(pc, rows, w);
+      }
     } else {
       ru.template load<false>(pu, rows, w);
       rd.template load<false>(pd, rows, w);
       rb.template load<false>(pb, rows, w);
-      if (!SUM) rc.template load<false>(pc, rows, w);
+      if constexpr (!SUM) {
+        rz.template load<false>(pz, a.z ? rows : 0, w);
+        rc.template load<false>(pc, rows, w);
+      }
     }
     pu.p += pu.tile;
     pd.p += pd.tile;
     pb.p += pb.tile;
-    pc.p += pc.tile;
+    if constexpr (!SUM) {
+      pz.p += pz.tile;
+      pc.p += pc.tile;
+    }
   };
-  fetch(t1 - t0);
-  for (int t = t0; t < t1; t += TT) {
-    const int rows = t1 - t < TT ? t1 - t : TT;
-    const bool full = whole && rows == TT;
-    const ScanRows<Shape, WIDE, T> cu = ru;
-    __syncwarp();
+  // What was loaded, as the values that the steps read.
+  auto form = [&](Tile& to, int rows) {
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int r = p * S + w.s;
-      f32x2 d[2], u[2];
+      f32x2 d[2], u[2], z[2], x[2];
       quad_pairs(rd.v[p], d);
-      quad_pairs(cu.v[p], u);
+      quad_pairs(ru.v[p], u);
+      if constexpr (!SUM) quad_pairs(rz.v[p], z);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         d[i] = add2(d[i], bias[i]);
         if (a.softplus) d[i] = softplus2(d[i]);
-        if (!full && r >= rows) d[i] = both(0.f);  // leaves the state as it is
-        if (SUM) total[i] = add2(total[i], d[i]);
-        u[i] = mul2(u[i], d[i]);
-      }
-      store_pairs(sm.delta + r * LD + 4 * w.q, d);
-      store_pairs(sm.du + r * LD + 4 * w.q, u);
-    }
-    rb.store(sm.B, w);
-    if (!SUM) rc.store(sm.C, w);
-    __syncwarp();
-    if (kept && (t - t0) % SCAN_KEEP == 0) {
-      store_states<Shape>(kept, w, h);
-      kept += row;
-    }
-    if (!SUM) {
-      if (full && a.z) rz.template load<true>(pz, rows, w);
-      else rz.template load<false>(pz, a.z ? rows : 0, w);
-      pz.p += pz.tile;
-    }
-    fetch(t1 - t - TT);  // no rows are left behind the last tile
-    for (int r0 = 0; r0 < rows; r0 += 4) {
-      float out[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r0 + i;
-        const float4 dq = *reinterpret_cast<const float4*>(sm.delta + r * LD + 4 * w.q);
-        const float4 xq = *reinterpret_cast<const float4*>(sm.du + r * LD + 4 * w.q);
-        const float d[4] = {dq.x, dq.y, dq.z, dq.w}, x[4] = {xq.x, xq.y, xq.z, xq.w};
-        f32x2 b[N], c[N];
-        load_row(b, sm.B + r * NS + STATES * w.s);
-        if constexpr (!SUM) load_row(c, sm.C + r * NS + STATES * w.s);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f32x2 y;
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            h[e][n] = fma2(ex2_2(scale2(d[e], A[e][n])), h[e][n], scale2(x[e], b[n]));
-            if constexpr (!SUM) y = n == 0 ? mul2(h[e][n], c[n]) : fma2(h[e][n], c[n], y);
-          }
-          if constexpr (!SUM) {
-            const float2 f = split2(y);
-            out[i][e] = f.x + f.y;
-          }
+        if (r >= rows) d[i] = both(0.f);  // leaves the state as it is
+        x[i] = mul2(u[i], d[i]);
+        if constexpr (SUM) {
+          if (S <= TT || r < TT) total[i] = add2(total[i], d[i]);
+        } else {
+          u[i] = mul2(u[i], skip[i]);
+          z[i] = a.z ? mul2(z[i], sigmoid2(z[i])) : both(1.f);
         }
-        if constexpr (!SUM) sum_quad<S>(out[i], w.s);
+      }
+      if (S <= TT || r < TT) {
+        store_pairs(to.delta + r * LD + 4 * w.q, d);
+        store_pairs(to.du + r * LD + 4 * w.q, x);
+        if constexpr (!SUM) {
+          store_pairs(to.skip + r * LD + 4 * w.q, u);
+          store_pairs(to.gate + r * LD + 4 * w.q, z);
+        }
+      }
+    }
+    rb.store(to.B, w);
+    if constexpr (!SUM) rc.store(to.C, w);
+  };
+  auto steps = [&](const Tile& tile, int rows) {
+#pragma unroll
+    for (int r = 0; r < TT; ++r) {
+      const float4 dq = *reinterpret_cast<const float4*>(tile.delta + r * LD + 4 * w.q);
+      const float4 xq = *reinterpret_cast<const float4*>(tile.du + r * LD + 4 * w.q);
+      const float d[4] = {dq.x, dq.y, dq.z, dq.w}, x[4] = {xq.x, xq.y, xq.z, xq.w};
+      f32x2 b[N], c[N];
+      float out[4];
+      load_row(b, tile.B + r * NS + STATES * w.s);
+      if constexpr (!SUM) load_row(c, tile.C + r * NS + STATES * w.s);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f32x2 v;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          h[e][n] = fma2(decay2(both(d[e]), A[e][n]), h[e][n], scale2(x[e], b[n]));
+          if constexpr (!SUM) v = n == 0 ? mul2(h[e][n], c[n]) : fma2(h[e][n], c[n], v);
+        }
+        if constexpr (!SUM) {
+          const float2 f = split2(v);
+          out[e] = f.x + f.y;
+        }
       }
       if constexpr (!SUM) {
+        sum_quad<S>(out, w.s);
+        float more[OWN], gate[OWN];
+        memcpy(more, __builtin_assume_aligned(tile.skip + r * LD + 4 * w.q + own, 4 * OWN), 4 * OWN);
+        memcpy(gate, __builtin_assume_aligned(tile.gate + r * LD + 4 * w.q + own, 4 * OWN), 4 * OWN);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) put_quad<S>(sm.y + (r0 + i) * LD + 4 * w.q, w.s, out[i]);
+        for (int e = 0; e < OWN; ++e) out[e] = (out[e] + more[e]) * gate[e];
+        put_own<WIDE, OWN>(y, out, r < rows ? own_n : 0);
+        y += a.y_ts;
       }
     }
-    if constexpr (!SUM) {
-      __syncwarp();
+  };
+  auto keep = [&](int t) {
+    if (!SUM && kept && t < t1 && w.n > 0) {
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int r = p * S + w.s;
-        if (!full && r >= rows) continue;
-        f32x2 y[2], u[2];
-        load_pairs(y, sm.y + r * LD + 4 * w.q);
-        quad_pairs(cu.v[p], u);
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) y[i] = fma2(skip[i], u[i], y[i]);
-        if (a.z) {
-          f32x2 z[2];
-          quad_pairs(rz.v[p], z);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) y[i] = mul2(y[i], mul2(z[i], sigmoid2(z[i])));
-        }
-        store_quad<WIDE>(const_cast<T*>(py.p) + p * py.step, y, w.n);
-      }
-      py.p += py.tile;
+        for (int n = 0; n < 2; ++n)
+          *reinterpret_cast<ulonglong2*>(kept + c * kept_channel + n * 4 * kept_channel) = make_ulonglong2(h[c][2 * n], h[c][2 * n + 1]);
+      kept += kept_row;
     }
+  };
+  static_assert(SCAN_KEEP == 2 * TT, "a kept state for every two tiles");
+  fetch(t1 - t0);
+  form(sm[0], t1 - t0);
+  fetch(t1 - t0 - TT);
+  for (int t = t0; t < t1; t += 2 * TT) {  // two tiles, so that their places are known when the steps are scheduled
+    const int rows = t1 - t;
+    keep(t);
+    __syncwarp();
+    steps(sm[0], rows);
+    form(sm[1], rows - TT);
+    fetch(rows - 2 * TT);
+    __syncwarp();
+    steps(sm[1], rows - TT);
+    form(sm[0], rows - 2 * TT);
+    fetch(rows - 3 * TT);
   }
   if constexpr (SUM) {
     store_states<Shape>(start + number * row, w, h);
@@ -198,13 +246,13 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) selective_scan_kernel(ScanAr
   }
 }
 
-// The states at the chunks' starts, in place of what each chunk adds: a thread per sequence, channel and state. The
+// The states at the chunks' starts, in place of what each chunk adds: a thread per sequence, channel and four states. The
 // loads of CARRY chunks are in flight while the chain waits for them.
 constexpr int CARRY = 8;
 __global__ void __launch_bounds__(128) selective_scan_carry_kernel(ScanArgs a, int L, float* start, const float* sums) {
   pdl_wait();
   pdl_trigger();
-  const long long row = (long long)a.D * a.NS, at = (long long)blockIdx.x * 128 + threadIdx.x;
+  const long long row = (long long)a.D * a.NS, at = ((long long)blockIdx.x * 128 + threadIdx.x) * 4;
   if (at >= a.q.B * row) return;
   const int b = (int)(at / row), i = (int)(at - b * row), c = i / a.NS;
   int first, len;
@@ -212,22 +260,25 @@ __global__ void __launch_bounds__(128) selective_scan_carry_kernel(ScanArgs a, i
   const int chunks = packed_per(len, L);
   const long long number = packed_number(a.q, b, first, L);
   const int slot = packed_slot(a.q, b);
-  const float rate = a.A[i] * LOG2E;
-  float h = slot >= 0 && a.h0 && packed_goes_on(a.q, b, len) ? a.h0[slot * row + i] : 0.f;
+  float rate[4], h[4] = {};
+  ld4(rate, a.A + i);
+  if (slot >= 0 && a.h0 && packed_goes_on(a.q, b, len)) ld4(h, a.h0 + slot * row + i);
   float* p = start + number * row + i;
   const float* d = sums + number * a.D + c;
   for (int j = 0; j < chunks; j += CARRY) {
-    float own[CARRY], sum[CARRY];
+    float own[CARRY][4], sum[CARRY];
 #pragma unroll
     for (int e = 0; e < CARRY; ++e)
       if (j + e < chunks - 1) {
-        own[e] = p[(j + e) * row];
-        sum[e] = d[(long long)(j + e) * a.D];
+        ld4(own[e], p + (j + e) * row);
+        sum[e] = d[(long long)(j + e) * a.D] * LOG2E;
       }
 #pragma unroll
     for (int e = 0; e < CARRY; ++e) {
-      if (j + e < chunks) p[(j + e) * row] = h;
-      if (j + e < chunks - 1) h = fmaf(ex2(rate * sum[e]), h, own[e]);
+      if (j + e < chunks) st4(p + (j + e) * row, h);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (j + e < chunks - 1) h[n] = fmaf(ex2(rate[n] * sum[e]), h[n], own[e][n]);
     }
   }
 }
@@ -237,7 +288,7 @@ __global__ void __launch_bounds__(128) selective_scan_carry_kernel(ScanArgs a, i
 // many warps, and everything a token needs is on its way before the first result is used.
 template <class T, int NS, bool WIDE>
 __global__ void __launch_bounds__(32 * WARPS, 5) selective_step_kernel(ScanArgs a, int tiles, int warps) {
-  using Shape = ScanShape<NS, 4>;
+  using Shape = ScanShape<NS, 4, TILE>;
   constexpr int S = Shape::S;
   pdl_wait();
   pdl_trigger();
@@ -287,7 +338,7 @@ __global__ void __launch_bounds__(32 * WARPS, 5) selective_step_kernel(ScanArgs 
         const float de = j ? df.y : df.x, xe = j ? xf.y : xf.x;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
-          h[e][n] = fma2(ex2_2(mul2(scale2(de, A[e][n]), both(LOG2E))), h[e][n], scale2(xe, bn[n]));
+          h[e][n] = fma2(decay2(both(de), mul2(A[e][n], both(LOG2E))), h[e][n], scale2(xe, bn[n]));
         const float2 f = split2(fma2(h[e][1], cn[1], mul2(h[e][0], cn[0])));
         v[e] = f.x + f.y;
       }
@@ -311,7 +362,10 @@ __global__ void __launch_bounds__(32 * WARPS, 5) selective_step_kernel(ScanArgs 
 }
 constexpr int FEW = 2;  // tokens of a sequence up to which the step kernel is taken
 
-int split_of(const ScanArgs& a) { return scan_split(a, ScanCost{190, 260, 120, 4 * CTAS, STATES}); }
+int split_of(const ScanArgs& a) {
+  const int warps = scan_tiles(a.D, a.G, a.NS, STATES);
+  return scan_split(a, warps, ScanCost{400, 670, 250, CTAS, (warps + WARPS - 1) / WARPS, 16});
+}
 
 template <class T, int NS, bool WIDE>
 cudaError_t run(const ScanArgs& a, cudaStream_t s) {
@@ -337,7 +391,7 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
     cudaError_t e = launch_pdl(selective_scan_kernel<T, NS, WIDE, true>, grid, block, 0, s, a, L, tiles, warps, start, sums);
     prof_mark(K_SCAN_SUM, s, false);
     if (e != cudaSuccess) return e;
-    const long long threads = (long long)a.q.B * a.D * NS;
+    const long long threads = (long long)a.q.B * a.D * NS / 4;
     prof_mark(K_SCAN_CARRY, s, true);
     e = launch_pdl(selective_scan_carry_kernel, dim3((unsigned)((threads + 127) / 128)), dim3(128), 0, s, a, L, start,
                    (const float*)sums);

@@ -12,8 +12,9 @@
 //    products with the area: with 4 x 4 the reads alone took as long as the exponentials;
 //  * what is per token and channel only (softplus, delta u, the gate, conversions) is done once for a tile of
 //    TT tokens, spread over all lanes, and passed through shared memory;
-//  * a warp owns its tile and its shared memory: no barrier of a CTA in the forward, loads of the next
-//    tile are in flight during the steps;
+//  * a warp owns its tile and its shared memory: no barrier of a CTA in the forward. It forms the next tile's values
+//    between the steps of this one (their chains of latency are as long as a step), with the loads of the one
+//    after that in flight;
 //  * two values go through each fp32 instruction (fma.rn.f32x2), which halves the issue slots.
 //
 // Few channels and long sequences do not fill the SMs: a chunk per warp then, in three launches. The first
@@ -28,10 +29,9 @@
 
 namespace gdn {
 
-template <int NS_, int SP_>
+template <int NS_, int SP_, int TT_>
 struct ScanShape {
-  static constexpr int NS = NS_, SP = SP_, S = NS / SP, Q = 32 / S, CW = 4 * Q, TT = 4 * S < SCAN_KEEP ? 4 * S : SCAN_KEEP,
-                       P = TT > S ? TT / S : 1;
+  static constexpr int NS = NS_, SP = SP_, S = NS / SP, Q = 32 / S, CW = 4 * Q, TT = TT_, P = TT > S ? TT / S : 1;
   static constexpr int BV = (TT * NS / 4 + 31) / 32;  // quads of B (and of C) a lane loads for a tile
   // Row length of a tile in shared memory: eight lanes' vectors, of 8 / S quads and S rows, on different banks.
   static constexpr int LD = CW + (S == 1 ? 0 : S < 8 ? 32 / S : 4);
@@ -46,23 +46,35 @@ inline int scan_tiles(int D, int G, int NS, int SP) {
 
 constexpr int SCAN_WHOLE = 0x40000000;  // chunk length where sequences are not split
 
-// Clocks of a warp's step that weigh a split against whole sequences: in a full SM sub-partition; of a warp with no
-// other beside it; in the launch before that gives the chunks' ends (forward); the warps an SM holds; and the states of a lane.
+// Clocks of a warp's step that weigh a split against whole sequences, as measured: in a full SM sub-partition; of a warp
+// with no other beside it; and in the launch before that gives the chunks' ends. CTAs that an SM holds, CTAs for the channels
+// of a chunk, and the multiple of tokens that a chunk has.
 struct ScanCost {
-  int full, alone, ends, resident, states;
+  int full, alone, ends, resident, ctas, unit;
 };
-// Chunk length, a multiple of 32: SCAN_WHOLE, or as many chunks as fill the SMs once.
-inline int scan_split(const ScanArgs& a, ScanCost cost) {
-  const long long tiles = scan_tiles(a.D, a.G, a.NS, cost.states), steps = a.q.N * tiles, parts = 152 * 4;
+// Chunk length: SCAN_WHOLE, or as many chunks as fill the SMs one to four times, whichever ends first (a CTA's start counts
+// as START tokens; sequences of unknown lengths end in the middle of a chunk).
+inline int scan_split(const ScanArgs& a, int warps, ScanCost cost) {
+  constexpr int START = 12;
+  const long long steps = (long long)a.q.N * warps, parts = 152 * 4;
   const long long busy = steps * cost.full / parts, one = (long long)a.max_q * cost.alone;
   const long long whole = busy > one ? busy : one;
   const long long split = steps * (cost.full + cost.ends) / parts + 12000;  // and two more launches
   if (split >= whole) return SCAN_WHOLE;
-  // sequences of max_q tokens, were they all as long
-  const long long warps = (long long)152 * cost.resident * a.max_q, each = steps > 0 ? warps / steps : 0;
-  if (each < 2) return SCAN_WHOLE;
-  const int L = (int)((a.max_q + each - 1) / each);
-  return L < 64 ? 64 : (L + 31) / 32 * 32;
+  long long best = 0, length = SCAN_WHOLE;
+  for (int waves = 1; waves <= 4; ++waves) {
+    const long long room = (long long)waves * 152 * cost.resident / cost.ctas;  // chunks
+    const long long each = a.q.cu ? room - a.q.B / 2 : room / a.q.B, tokens = a.q.cu ? a.q.N : a.q.T;
+    if (each < 1) continue;
+    long long L = ((tokens + each - 1) / each + cost.unit - 1) / cost.unit * cost.unit;
+    if (L < 64) L = 64;
+    const long long time = waves * (L + START);
+    if (best == 0 || time < best) {
+      best = time;
+      length = L;
+    }
+  }
+  return length >= a.max_q ? SCAN_WHOLE : (int)length;
 }
 
 // A warp's place: its channels and the chunk it works on.
@@ -105,6 +117,18 @@ __device__ __forceinline__ void store_states(float* p, const ScanPlace<Shape>& w
             make_ulonglong2(x[i][2 * n], x[i][2 * n + 1]);
     }
 }
+// Kept states: 16-byte vectors of four states, [parity of the vector][channel of the quad][quad][vector / 2], so that the
+// forward's stores (two vectors a lane) and the backward's loads (one) both run over consecutive addresses.
+template <class Shape>
+__device__ __forceinline__ long long kept_place(const ScanArgs& a, const ScanPlace<Shape>& w, int vector) {
+  const int dg = a.D / a.G, quad = w.g * ((dg + 3) / 4) + (w.c - w.g * dg) / 4;
+  return ((long long)(vector % 2) * 4 * scan_quads(a.D, a.G) + quad) * (Shape::NS / 2) + vector / 2 * 4;
+}
+// Floats between two channels of a quad there.
+template <int NS>
+__device__ __forceinline__ long long kept_step(const ScanArgs& a) {
+  return (long long)scan_quads(a.D, a.G) * (NS / 2);
+}
 // SP consecutive floats as pairs.
 template <int N>
 __device__ __forceinline__ void load_row(f32x2 (&x)[N], const float* p) {
@@ -118,9 +142,9 @@ __device__ __forceinline__ void load_row(f32x2 (&x)[N], const float* p) {
 // The other way about, for four states a lane: x[e][i] holds channels 2 e' and 2 e' + 1, e' = e ^ flip_c, of state
 // i' = i ^ 2 flip_n. (Lanes that take their channels or states in another order exchange sums without selecting.)
 template <class Shape>
-__device__ __forceinline__ void load_columns(const float* p, const ScanPlace<Shape>& w, int flip_c, int flip_n, f32x2 (&x)[2][4]) {
+__device__ __forceinline__ void load_columns(const float* p, long long channel, const ScanPlace<Shape>& w, int flip_c, int flip_n,
+                                             f32x2 (&x)[2][4]) {
   static_assert(Shape::SP == 4, "four states a lane");
-  p += (long long)w.c * Shape::NS + 4 * w.s;
   float2 f[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -128,7 +152,7 @@ __device__ __forceinline__ void load_columns(const float* p, const ScanPlace<Sha
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       f[i][n] = make_float2(0.f, 0.f);
-      if (c < w.n) f[i][n] = *reinterpret_cast<const float2*>(p + c * Shape::NS + 2 * (n ^ flip_n));
+      if (c < w.n) f[i][n] = *reinterpret_cast<const float2*>(p + c * channel + 2 * (n ^ flip_n));
     }
   }
 #pragma unroll
@@ -138,6 +162,10 @@ __device__ __forceinline__ void load_columns(const float* p, const ScanPlace<Sha
       x[e][2 * n] = pack2(f[2 * e][n].x, f[2 * e + 1][n].x);
       x[e][2 * n + 1] = pack2(f[2 * e][n].y, f[2 * e + 1][n].y);
     }
+}
+template <class Shape>
+__device__ __forceinline__ void load_columns(const float* p, const ScanPlace<Shape>& w, int flip_c, int flip_n, f32x2 (&x)[2][4]) {
+  load_columns<Shape>(p + (long long)w.c * Shape::NS + 4 * w.s, Shape::NS, w, flip_c, flip_n, x);
 }
 template <class Shape>
 __device__ __forceinline__ void store_columns(float* p, const ScanPlace<Shape>& w, int flip_c, int flip_n, const f32x2 (&x)[2][4]) {
@@ -177,12 +205,12 @@ struct RowPtr {
     tile = Shape::TT * ts;
   }
 };
-// Rows p S + s of a tile, as loaded. FULL: all rows and the warp's channels are real; else rows [0, rows) are, and the
-// others become zeros. (S above TT: some lanes have no row.)
+// Rows p S + s of a tile, as loaded: rows [0, rows) are real, the others become zeros. (S above TT: some lanes have no
+// row.) FULL: all of them are, and the warp's channels too.
 template <class Shape, bool WIDE, class T>
 struct ScanRows {
   Quad<T> v[Shape::P];
-  template <bool FULL>
+  template <bool FULL = false>
   __device__ __forceinline__ void load(const RowPtr<T>& from, int rows, const ScanPlace<Shape>& w) {
 #pragma unroll
     for (int p = 0; p < Shape::P; ++p) {
@@ -208,13 +236,14 @@ template <class Shape, bool WIDE, class T>
 struct ScanMix {
   static constexpr int QUADS = Shape::TT * Shape::NS / 4;
   Quad<T> v[Shape::BV];
-  template <bool FULL>
+  template <bool FULL = false>
   __device__ __forceinline__ void load(const MixPtr<T>& from, int rows, const ScanPlace<Shape>& w) {
 #pragma unroll
     for (int i = 0; i < Shape::BV; ++i) {
+      const int k = w.lane + 32 * i;
       const T* at = from.p + i * from.step;
       if constexpr (FULL && QUADS % 32 == 0) v[i] = load_quad<WIDE>(at);
-      else v[i] = load_quad<WIDE>(at, (w.lane + 32 * i) / (Shape::NS / 4) < rows && w.lane + 32 * i < QUADS ? 4 : 0);
+      else v[i] = load_quad<WIDE>(at, k / (Shape::NS / 4) < rows && k < QUADS ? 4 : 0);
     }
   }
   __device__ __forceinline__ void store(float* sm, const ScanPlace<Shape>& w) const {
@@ -246,12 +275,4 @@ __device__ __forceinline__ void sum_quad(float (&v)[4], int s) {
     for (int d = 4; d < S; d *= 2) v[0] += __shfl_xor_sync(ALL, v[0], d);
   }
 }
-// Stores sum_quad's result in the quad's place of a row.
-template <int S>
-__device__ __forceinline__ void put_quad(float* at, int s, const float (&v)[4]) {
-  if constexpr (S == 1) *reinterpret_cast<float4*>(at) = make_float4(v[0], v[1], v[2], v[3]);
-  else if constexpr (S == 2) *reinterpret_cast<float2*>(at + 2 * s) = make_float2(v[0], v[1]);
-  else if (S == 4 || s < 4) at[s % 4] = v[0];
-}
-
 }  // namespace gdn

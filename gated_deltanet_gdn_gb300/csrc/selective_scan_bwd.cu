@@ -11,7 +11,7 @@
 // the state before every second token in shared memory, then pair by pair from the last: the state between a pair's
 // tokens is formed again, and a token's factors where they are used. So three states and one token's factors
 // are in registers at a time, 12 warps fit an SM, and the arithmetic's latency is hidden. (Four tokens' states and factors,
-// 255 registers and 8 warps: 607 against TIME_BWD us at B8 T4096 D768, 16 states.)
+// 255 registers and 8 warps: 607 against 480 us at B8 T4096 D768, 16 states.)
 //
 // A CTA's warps work on the same tokens of neighbouring channels, so their sums over channels (dB, dC) are added in
 // shared memory before they leave the SM; what is left per CTA, and the sums over the tokens
@@ -61,8 +61,8 @@ int cta_tiles(const ScanArgs& a) {
 }
 BwdPlan plan_of(const ScanArgs& a) {
   BwdPlan p;
-  p.L = scan_split(a, ScanCost{420, 900, 60, 12, 4});
   p.tiles = cta_tiles(a);
+  p.L = scan_split(a, p.tiles * WARPS, ScanCost{710, 1600, 130, 3, p.tiles, 32});
   p.half = p.L / 2;
   p.numbers = packed_numbers(a.q, p.L);
   p.halves = packed_numbers(a.q, p.half);
@@ -83,7 +83,7 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 template <class T, int NS, bool WIDE>
 __global__ void __launch_bounds__(32 * WARPS, SUM_CTAS) selective_scan_bwd_sum_kernel(ScanArgs a, int L, int tiles, long long warps,
                                                                                float* start, float* sums) {
-  using Shape = ScanShape<NS, SUM_STATES>;
+  using Shape = ScanShape<NS, SUM_STATES, SCAN_KEEP>;
   constexpr int S = Shape::S, P = Shape::P, LD = Shape::LD, TT = Shape::TT, N = Shape::SP / 2;
   struct Mine {
     float delta[TT * LD], dy[TT * LD], C[TT * NS];
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(32 * WARPS, SUM_CTAS) selective_scan_bwd_sum_k
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int n = 0; n < N; ++n) G[e][n] = mul2(ex2_2(scale2(d[e], A[e][n])), fma_by(y[e], c[n], G[e][n]));
+        for (int n = 0; n < N; ++n) G[e][n] = mul2(decay2(both(d[e]), A[e][n]), fma_by(y[e], c[n], G[e][n]));
     }
   }
   store_states<Shape>(start + number * a.D * NS, w, G);
@@ -189,34 +189,38 @@ __global__ void __launch_bounds__(32 * WARPS, SUM_CTAS) selective_scan_bwd_sum_k
   }
 }
 
-// The adjoints that enter the chunks from behind, in place of what each hands on.
+// The adjoints that enter the chunks from behind, in place of what each hands on: a thread per sequence, channel and four
+// states.
 constexpr int CARRY = 8;
 __global__ void __launch_bounds__(128) selective_scan_bwd_carry_kernel(ScanArgs a, int L, float* start, const float* sums) {
   pdl_wait();
   pdl_trigger();
-  const long long row = (long long)a.D * a.NS, at = (long long)blockIdx.x * 128 + threadIdx.x;
+  const long long row = (long long)a.D * a.NS, at = ((long long)blockIdx.x * 128 + threadIdx.x) * 4;
   if (at >= a.q.B * row) return;
   const int b = (int)(at / row), i = (int)(at - b * row), c = i / a.NS;
   int first, len;
   packed_bounds(a.q, b, &first, &len);
   const int chunks = packed_per(len, L);
   const long long number = packed_number(a.q, b, first, L);
-  const float rate = a.A[i] * LOG2E;
-  float g = a.dh_final ? a.dh_final[at] : 0.f;
+  float rate[4], g[4] = {};
+  ld4(rate, a.A + i);
+  if (a.dh_final) ld4(g, a.dh_final + at);
   float* p = start + number * row + i;
   const float* d = sums + number * a.D + c;
   for (int j = chunks - 1; j >= 0; j -= CARRY) {
-    float own[CARRY], sum[CARRY];
+    float own[CARRY][4], sum[CARRY];
 #pragma unroll
     for (int e = 0; e < CARRY; ++e)
       if (j - e > 0) {
-        own[e] = p[(j - e) * row];
-        sum[e] = d[(long long)(j - e) * a.D];
+        ld4(own[e], p + (j - e) * row);
+        sum[e] = d[(long long)(j - e) * a.D] * LOG2E;
       }
 #pragma unroll
     for (int e = 0; e < CARRY; ++e) {
-      if (j - e >= 0) p[(j - e) * row] = g;
-      if (j - e > 0) g = fmaf(ex2(rate * sum[e]), g, own[e]);
+      if (j - e >= 0) st4(p + (j - e) * row, g);
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        if (j - e > 0) g[n] = fmaf(ex2(rate[n] * sum[e]), g[n], own[e][n]);
     }
   }
 }
@@ -280,7 +284,7 @@ __device__ __forceinline__ int mix_place(const ScanPlace<Shape>& w) {
 
 template <class T, int NS, bool WIDE>
 __global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanArgs a, int L, int tiles, BwdParts parts) {
-  using Shape = ScanShape<NS, 4>;
+  using Shape = ScanShape<NS, 4, SCAN_KEEP>;
   using Shared = BwdShared<Shape>;
   constexpr int S = Shape::S, P = Shape::P, CW = Shape::CW, LD = Shape::LD, TT = Shape::TT;
   static_assert(TT == SCAN_KEEP, "a kept state for every tile");
@@ -332,7 +336,8 @@ __global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanA
     load_channels(a.bias, w, bias);
     load_channels(a.skip, w, skip);
     const int last = t1 > t0 ? t0 + (t1 - 1 - t0) / TT * TT : t0 - TT;
-    const float* kept = a.kept + (packed_number(a.q, k.b, k.first, TT) + last / TT) * row;
+    const long long kept_channel = kept_step<NS>(a), kept_row = 8 * kept_channel;
+    const float* kept = a.kept + (packed_number(a.q, k.b, k.first, TT) + last / TT) * kept_row + kept_place(a, w, w.s);
     RowPtr<T> pu, pd, py, pz;
     MixPtr<T> pb, pc;
     {
@@ -367,7 +372,7 @@ __global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanA
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) after[e][n] = fma2(ex2_2(mul2(d[e], A[e][n])), before[e][n], scale2(bn[n], x[e]));
+        for (int e = 0; e < 2; ++e) after[e][n] = fma2(decay2(d[e], A[e][n]), before[e][n], scale2(bn[n], x[e]));
     };
     // and backwards, its factors formed again: own gets the lane's part of the quad's d(delta u), sum_n (G a h) A log2 e and
     // C.h, summed over the lanes
@@ -389,7 +394,7 @@ __global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanA
           db = e ? fma2(G[e][n], x[e], db) : mul2(G[e][n], x[e]);
           sums[0][e] = n ? fma_by(bn[n], G[e][n], sums[0][e]) : scale2(bn[n], G[e][n]);
           sums[2][e] = n ? fma_by(cn[n], after[e][n], sums[2][e]) : scale2(cn[n], after[e][n]);
-          G[e][n] = mul2(G[e][n], ex2_2(mul2(d[e], A[e][n])));
+          G[e][n] = mul2(G[e][n], decay2(d[e], A[e][n]));
           const f32x2 ga = mul2(G[e][n], before[e][n]);
           sums[1][e] = n ? fma2(ga, A[e][n], sums[1][e]) : mul2(ga, A[e][n]);
           dA[e][n] = fma2(ga, d[e], dA[e][n]);
@@ -415,22 +420,13 @@ __global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanA
       {
         ScanRows<Shape, WIDE, T> ru, rd, ry, rz;
         ScanMix<Shape, WIDE, T> rb, rc;
-        if (full) {
-          rd.template load<true>(pd, rows, w);
-          ru.template load<true>(pu, rows, w);
-          ry.template load<true>(py, rows, w);
-          if (a.z) rz.template load<true>(pz, rows, w);
-          rb.template load<true>(pb, rows, w);
-          rc.template load<true>(pc, rows, w);
-        } else {
-          rd.template load<false>(pd, rows, w);
-          ru.template load<false>(pu, rows, w);
-          ry.template load<false>(py, rows, w);
-          if (a.z) rz.template load<false>(pz, rows, w);
-          rb.template load<false>(pb, rows, w);
-          rc.template load<false>(pc, rows, w);
-        }
-        load_columns<Shape>(kept, w, flip_c, flip_n, h);
+        rd.load(pd, rows, w);
+        ru.load(pu, rows, w);
+        ry.load(py, rows, w);
+        rz.load(pz, a.z ? rows : 0, w);
+        rb.load(pb, rows, w);
+        rc.load(pc, rows, w);
+        load_columns<Shape>(kept, kept_channel, w, flip_c, flip_n, h);
         if (full && t > t0) {  // the next tile's rows and state to L2
 #pragma unroll
           for (int p = 0; p < P; ++p) {
@@ -439,7 +435,8 @@ __global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanA
             prefetch_l2(py.p - py.tile + p * py.step);
             if (a.z) prefetch_l2(pz.p - pz.tile + p * pz.step);
           }
-          prefetch_l2(kept - row + (long long)(w.c + w.s % 4) * NS);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) prefetch_l2(kept - kept_row + c * kept_channel);
         }
         __syncwarp();
 #pragma unroll
@@ -570,7 +567,7 @@ __global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanA
       to -= TT * a.D;
       pb.p -= pb.tile;
       pc.p -= pc.tile;
-      kept -= row;
+      kept -= kept_row;
       mix_to -= TT * 2 * NS;
     }
     if (k.j == 0 && a.dh0) store_columns<Shape>(a.dh0 + k.b * row, w, flip_c, flip_n, G);
@@ -589,24 +586,24 @@ __global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanA
   }
 }
 
-// Adds the partial sums: CTAs of 256 threads take dB and dC (a thread four values of a row), then 32 columns of dA, dskip
-// and ddt_bias each (8 warps over every eighth chunk).
+// Adds the partial sums: CTAs of 256 threads take 32 columns of dA, dskip and ddt_bias each (8 warps over every eighth
+// chunk), then dB and dC (a thread four values of a row).
 template <class T>
 __global__ void __launch_bounds__(256) selective_scan_join_kernel(ScanArgs a, BwdParts parts, int tiles, long long numbers,
-                                                                  int mix_blocks) {
+                                                                  int sum_blocks) {
   __shared__ float sum[8][32];
   pdl_wait();
   pdl_trigger();
-  if ((int)blockIdx.x < mix_blocks) {
+  if ((int)blockIdx.x >= sum_blocks) {
     const int vecs = a.NS / 2;  // of a row and group, dB and dC
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, per = (long long)a.G * vecs, r = i / per;
+    const long long i = (long long)(blockIdx.x - sum_blocks) * 256 + threadIdx.x, per = (long long)a.G * vecs, r = i / per;
     if (r >= a.q.N) return;
     const int left = (int)(i - r * per), g = left / vecs, n = left % vecs * 4, each = tiles / a.G;
     const int end = packed_start(a.q, a.q.B);
     float v[4] = {};
     if (!a.q.cu || r < end) {
       const float* p = parts.mix + ((long long)g * each * a.q.N + r) * 2 * a.NS + n;
-#pragma unroll 4
+#pragma unroll 8
       for (int t = 0; t < each; ++t) {
         float x[4];
         ld4(x, p + (long long)t * a.q.N * 2 * a.NS);
@@ -620,13 +617,13 @@ __global__ void __launch_bounds__(256) selective_scan_join_kernel(ScanArgs a, Bw
     return;
   }
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const long long row = (long long)a.D * a.NS, col = ((long long)blockIdx.x - mix_blocks) * 32 + lane;
+  const long long row = (long long)a.D * a.NS, col = (long long)blockIdx.x * 32 + lane;
   const bool in = col < row + 2 * a.D;
   float s = 0.f;
   if (in) {
     const float* p = col < row ? parts.dA + col : parts.vec + (col - row);
     const long long step = col < row ? row : 2 * (long long)a.D;
-#pragma unroll 4
+#pragma unroll 8
     for (long long j = warp; j < numbers; j += 8) s += p[j * step];
   }
   sum[warp][lane] = s;
@@ -654,7 +651,7 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   parts.vec = reinterpret_cast<float*>(ws + p.vec);
   const long long blocks = p.numbers * p.tiles;
   const long long per = (long long)a.G * (a.NS / 2), mix_blocks = (a.q.N * per + 255) / 256;
-  const long long join_blocks = mix_blocks + ((long long)a.D * (a.NS + 2) + 31) / 32;
+  const long long column_blocks = ((long long)a.D * (a.NS + 2) + 31) / 32, join_blocks = mix_blocks + column_blocks;
   if (blocks > 0x7fffffff || join_blocks > 0x7fffffff) return cudaErrorNotSupported;
   cudaError_t e;
   if (parts.start) {
@@ -666,14 +663,14 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
                    warps, parts.start, parts.sums);
     prof_mark(K_SSCAN_RSUM, s, false);
     if (e != cudaSuccess) return e;
-    const long long threads = (long long)a.q.B * a.D * NS;
+    const long long threads = (long long)a.q.B * a.D * NS / 4;
     prof_mark(K_SCAN_CARRY, s, true);
     e = launch_pdl(selective_scan_bwd_carry_kernel, dim3((unsigned)((threads + 127) / 128)), dim3(128), 0, s, a, p.half, parts.start,
                    (const float*)parts.sums);
     prof_mark(K_SCAN_CARRY, s, false);
     if (e != cudaSuccess) return e;
   }
-  const int bytes = (int)sizeof(BwdShared<ScanShape<NS, 4>>) * WARPS;
+  const int bytes = (int)sizeof(BwdShared<ScanShape<NS, 4, SCAN_KEEP>>) * WARPS;
   e = allow_shared(reinterpret_cast<const void*>(selective_scan_bwd_kernel<T, NS, WIDE>), bytes, &done);
   if (e != cudaSuccess) return e;
   prof_mark(K_SSCAN_BWD, s, true);
@@ -682,7 +679,7 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   prof_mark(K_SSCAN_JOIN, s, true);
   e = launch_pdl(selective_scan_join_kernel<T>, dim3((unsigned)join_blocks), dim3(256), 0, s, a, parts, p.tiles, p.numbers,
-                 (int)mix_blocks);
+                 (int)column_blocks);
   prof_mark(K_SSCAN_JOIN, s, false);
   return e;
 }

@@ -284,6 +284,91 @@ def test_wide_steps():
     within("h", h[0], *ref["h"])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,G,S", [(768, 1, 16), (50, 2, 8), (37, 1, 16), (96, 1, 64), (24, 1, 32)])
+def test_single_tokens(D, G, S, dtype):
+    """No token, one or two a sequence, some without a state; and the same call whose bound says fewer than there are."""
+    gen = torch.Generator(device="cuda").manual_seed(D + S)
+    lens = [1, 0, 2, 1, 2, 0]
+    cu = torch.tensor([sum(lens[:b]) for b in range(7)], dtype=torch.int32, device="cuda")
+    s = _inputs(gen, (sum(lens) + 2,), D, G, S, dtype, True, True)
+    states, slots = _normal(gen, 9, D, S), torch.tensor([3, 5, -1, 0, 8, 2], dtype=torch.int32, device="cuda")
+    kv = torch.tensor([v + p for v, p in zip(lens, [4, 4, 4, 0, 4, 0])], dtype=torch.int32, device="cuda")
+    for bound in (2, 1):
+        after = torch.full_like(states, 3.0)
+        y, _, _ = gdn.gdn_selective_scan_fwd(**s, h0=states, h_final=after, slots=slots, cu_seqlens=cu, kv_lens=kv, max_q=bound, flags=SOFT)
+        for b in range(6):
+            slot, r = int(slots[b]), slice(int(cu[b]), int(cu[b + 1]))
+            ref = scan_seq(**_rows(s, r, h0=states[slot] if slot >= 0 and b not in (3, 5) else None))
+            within("y", y[r], *ref["y"])
+            if slot >= 0:
+                within("h", after[slot], *ref["h"])
+        assert not bool(y[sum(lens):].any()) and bool((after[[1, 4, 6, 7]] == 3).all())
+
+
+def test_bounds_choose_no_result():
+    """max_q below, at and far above the longest sequence: the same within float32."""
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    lens = [700, 3, 0, 90]
+    cu = torch.tensor([sum(lens[:b]) for b in range(5)], dtype=torch.int32, device="cuda")
+    s = _inputs(gen, (sum(lens),), 32, 1, 16, torch.float32, True, True)
+    dy = _normal(gen, sum(lens), 32)
+    for bound in (1, 5, 700, None, 2 ** 31 - 1):
+        y, h, kept = gdn.gdn_selective_scan_fwd(**s, cu_seqlens=cu, max_q=bound, flags=SOFT, save=True)
+        g = gdn.gdn_selective_scan_bwd(s["u"], s["dt"], s["A"], s["B"], s["C"], dy, kept, D=s["D"], z=s["z"], dt_bias=s["dt_bias"],
+                                       cu_seqlens=cu, max_q=bound, flags=SOFT)
+        for b in range(4):
+            r = slice(int(cu[b]), int(cu[b + 1]))
+            ref = scan_seq(**_rows(s, r, dy=dy[r]))
+            for name, t in (("y", y[r]), ("h", h[b]), ("du", g["du"][r]), ("ddt", g["ddt"][r]), ("dz", g["dz"][r])):
+                within(name, t, *ref[name])
+
+
+def test_strides_beyond_32_bits():
+    """Rows more than 2^31 elements apart."""
+    gen = torch.Generator(device="cuda").manual_seed(22)
+    s = _inputs(gen, (1, 3), 8, 1, 16, torch.bfloat16, True, True)
+    far = torch.empty(2 * (2 ** 31 + 64) + 64, dtype=torch.bfloat16, device="cuda")
+    u = far.as_strided((1, 3, 8), (3 * (2 ** 31 + 64), 2 ** 31 + 64, 1))
+    u.copy_(s["u"])
+    dy = _normal(gen, 1, 3, 8, dtype=torch.bfloat16)
+    res = []
+    for x in (s["u"], u):
+        y, h, kept = gdn.gdn_selective_scan_fwd(**dict(s, u=x), flags=SOFT, save=True)
+        g = gdn.gdn_selective_scan_bwd(x, s["dt"], s["A"], s["B"], s["C"], dy, kept, D=s["D"], z=s["z"], dt_bias=s["dt_bias"], flags=SOFT)
+        w = torch.ones(8, 4, dtype=torch.bfloat16, device="cuda")
+        c, _ = gdn.gdn_causal_conv_fwd(x, w)
+        res.append([y, h, c, gdn.gdn_causal_conv_bwd(x, w, None, dy)["dweight"]] + [t for t in g.values() if t is not None])
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams with workspaces of their own give what they give one after the other."""
+    gen = torch.Generator(device="cuda").manual_seed(23)
+    sets = [_inputs(gen, (1, 2000), 64, 1, 16, torch.float32, True, True) for _ in range(2)]
+    dys = [_normal(gen, 1, 2000, 64) for _ in range(2)]
+
+    def step(s, dy):
+        y, h, kept = gdn.gdn_selective_scan_fwd(**s, flags=SOFT, save=True)
+        g = gdn.gdn_selective_scan_bwd(s["u"], s["dt"], s["A"], s["B"], s["C"], dy, kept, D=s["D"], z=s["z"], dt_bias=s["dt_bias"], flags=SOFT)
+        return [y, h] + [t for t in g.values() if t is not None]
+
+    alone = [step(s, dy) for s, dy in zip(sets, dys)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    together = [[], []]
+    for _ in range(3):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                together[i].append(step(sets[i], dys[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for got in together[i]:
+            for a, b in zip(alone[i], got):
+                assert torch.equal(a, b)
+
+
 def test_refusals():
     gen = torch.Generator(device="cuda").manual_seed(12)
     s = _inputs(gen, (2, 4), 8, 1, 16, torch.float32, True, True)
