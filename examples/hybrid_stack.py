@@ -1,9 +1,10 @@
-"""A hybrid stack: gated delta rule layers with a softmax attention layer between them, run
-as a server does: a prompt in chunks, then token by token.
+"""A hybrid stack: gated delta rule layers with a softmax attention layer between them, and state space
+layers if wanted, run as a server does: a prompt in chunks, then token by token.
 
 Every block is  norm -> projections -> mixer -> per-head gated norm -> projection -> scaled
 residual,  and the step between two blocks (scaled residual and the next block's norm) is
-one call. Rule layers carry a state, attention layers a paged cache. The weights are random;
+one call. Rule layers carry a state, attention layers a paged cache, state space layers a state and the last
+inputs of their convolution. The weights are random;
 the check at the end is that the same tokens give the same activations however they are
 split into calls.
 
@@ -21,10 +22,11 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import gated_deltanet_gdn_gb300 as gdn  # noqa: E402
 
 PAGE = 64
+STATES, TAPS = 16, 4  # of a state space layer
 
 
 class HybridStack:
-    """`layers` names each layer's mixer: "r" (gated delta rule) or "a" (attention)."""
+    """`layers` names each layer's mixer: "r" (gated delta rule), "a" (attention) or "s" (convolution and selective scan)."""
 
     def __init__(self, layers: str = "rrra", heads: int = 6, kv_heads: int = 2, width: int = 128, batch: int = 2,
                  max_tokens: int = 1024, seed: int = 0, device: str = "cuda"):
@@ -39,12 +41,17 @@ class HybridStack:
 
         self.weights: List[Dict[str, torch.Tensor]] = []
         for kind in layers:
-            qkv = (3 * heads if kind == "r" else heads + 2 * kv_heads) * width
+            qkv = {"r": 3 * heads, "a": heads + 2 * kv_heads, "s": heads}[kind] * width
             w = {"qkv": normal(self.model, qkv), "gate": normal(self.model, self.model), "out": normal(self.model, self.model),
                  "pre": 1 + normal(self.model, std=0.1), "post": 1 + normal(width, std=0.1),
                  "scale": 0.5 + normal(self.model, std=0.1)}
             if kind == "r":
                 w["g"], w["beta"] = normal(self.model, heads), normal(self.model, heads)
+            elif kind == "s":
+                w["conv"], w["bc"] = normal(self.model, TAPS, std=TAPS ** -0.5), normal(self.model, 2 * STATES)
+                w["dt"], w["dt_bias"] = normal(self.model, self.model), torch.full((self.model,), -4.0, device=device)
+                w["A"] = -torch.arange(1.0, STATES + 1, device=device).repeat(self.model, 1)
+                w["D"] = torch.ones(self.model, device=device)
             self.weights.append(w)
         self.last_norm = 1 + normal(self.model, std=0.1)
         rate = 10000.0 ** (-torch.arange(width // 2, device=device, dtype=torch.float64) * 2 / width)
@@ -56,7 +63,10 @@ class HybridStack:
     def reset(self) -> None:
         """Empty states and caches (cache rows hold nothing until they are appended)."""
         B, H, D = self.B, self.H, self.D
-        self.states = [torch.zeros(B, H, D, D, device=self.device) if k == "r" else None for k in self.layers]
+        self.states = [torch.zeros(B, H, D, D, device=self.device) if k == "r" else
+                       torch.zeros(B, self.model, STATES, device=self.device) if k == "s" else None for k in self.layers]
+        self.inputs = [torch.zeros(B, TAPS - 1, self.model, dtype=self.dtype, device=self.device) if k == "s" else None
+                       for k in self.layers]
         shape = (B * self.pages, self.Hk, PAGE, D)
         self.caches = [[torch.empty(shape, dtype=self.dtype, device=self.device) for _ in range(2)] if k == "a" else None
                        for k in self.layers]
@@ -83,6 +93,15 @@ class HybridStack:
         q = gdn.gdn_kv_append(k, v, *where, q=q, cos=self.cos, sin=self.sin)
         return gdn.gdn_paged_attn(q, *where, max_q=T, max_kv=self.length).view(B, T, self.H, self.D)
 
+    def _state_space(self, i: int, y: torch.Tensor, w) -> torch.Tensor:
+        B, T = y.shape[:2]
+        u, _ = gdn.gdn_causal_conv_fwd(y @ w["qkv"], w["conv"], state0=self.inputs[i], state_final=self.inputs[i],
+                                       flags=gdn.GDN_FLAG_CONV_SILU)
+        Bm, Cm = (t.unflatten(-1, (1, STATES)) for t in (u @ w["bc"]).split(STATES, -1))
+        out, _, _ = gdn.gdn_selective_scan_fwd(u, u @ w["dt"], w["A"], Bm, Cm, D=w["D"], dt_bias=w["dt_bias"], h0=self.states[i],
+                                               h_final=self.states[i], flags=gdn.GDN_FLAG_DT_SOFTPLUS)
+        return out.view(B, T, self.H, self.D)
+
     def step(self, x: torch.Tensor) -> torch.Tensor:
         """Next T tokens' activations x [B, T, model] -> the stack's normed output, same shape."""
         B, T = x.shape[:2]
@@ -92,7 +111,7 @@ class HybridStack:
         h, y, _ = gdn.gdn_block_norm_fwd(x.reshape(B * T, self.model), w_pre=self.weights[0]["pre"])
         for i, w in enumerate(self.weights):
             y = y.view(B, T, self.model)
-            mixed = self._rule(i, y, w) if self.layers[i] == "r" else self._attention(i, y, w)
+            mixed = {"r": self._rule, "a": self._attention, "s": self._state_space}[self.layers[i]](i, y, w)
             gate = (y @ w["gate"]).view(B, T, self.H, self.D)
             o, _, _ = gdn.gdn_block_norm_fwd(mixed, gate=gate, w_post=w["post"])
             block = o.view(B * T, self.model) @ w["out"]

@@ -372,22 +372,19 @@ void bwd_plan(ConvArgs* a, int vecs, int* parts, long long* numbers) {
   *numbers = packed_numbers(a->q, a->run);
   *parts = (int)(*numbers < most ? *numbers : most);
 }
-template <class T>
-constexpr int fwd_vec() {
-  return 16 / (int)sizeof(T);
-}
+// A sequence's new tokens up to which a run is a sequence, with 16-byte vectors and one token's loads at a time (32 tokens of
+// 18,432 channels 5.5 us); longer runs take vectors of four channels and sixteen tokens' loads, of float32 eight (32,768 tokens of 2,304
+// channels 53 us, with 16-byte vectors and eight tokens 58 us).
+constexpr int FEW = 8;
 
-template <class T, int V, int K, bool SILU>
+template <class T, int V, int K, bool SILU, int BATCH>
 cudaError_t fwd(ConvArgs a, cudaStream_t s) {
   const int vecs = a.C / V;
-  constexpr int FEW = 8;
-  const bool few = a.max_q <= FEW;  // a run for every sequence: the loads of four tokens suffice
-  a.run = few ? FEW : run_of(a, vecs);
+  a.run = a.max_q <= FEW ? FEW : run_of(a, vecs);
   const long long blocks = (packed_numbers(a.q, a.run) * vecs + THREADS - 1) / THREADS;
   if (blocks > 0x7fffffff) return cudaErrorNotSupported;
   prof_mark(K_CONV_FWD, s, true);
-  const cudaError_t e = few ? launch_pdl(causal_conv_fwd_kernel<T, V, K, SILU, 1>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a)
-                            : launch_pdl(causal_conv_fwd_kernel<T, V, K, SILU, 8>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a);
+  const cudaError_t e = launch_pdl(causal_conv_fwd_kernel<T, V, K, SILU, BATCH>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a);
   prof_mark(K_CONV_FWD, s, false);
   return e;
 }
@@ -408,11 +405,12 @@ cudaError_t bwd(ConvArgs a, cudaStream_t s) {
   return e;
 }
 
-template <class T, int V, bool BWD>
+// BATCH: tokens of a forward batch, 0 for the backward.
+template <class T, int V, int BATCH>
 cudaError_t pick(const ConvArgs& a, cudaStream_t s) {
   auto go = [&](auto k, auto act) {
-    if constexpr (BWD) return bwd<T, V, decltype(k)::value, decltype(act)::value>(a, s);
-    else return fwd<T, V, decltype(k)::value, decltype(act)::value>(a, s);
+    if constexpr (BATCH == 0) return bwd<T, V, decltype(k)::value, decltype(act)::value>(a, s);
+    else return fwd<T, V, decltype(k)::value, decltype(act)::value, BATCH>(a, s);
   };
   auto with = [&](auto act) {
     if (a.taps == 2) return go(std::integral_constant<int, 2>(), act);
@@ -425,12 +423,16 @@ cudaError_t pick(const ConvArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_causal_conv(const ConvArgs& a, bool wide, cudaStream_t s) {
-  if (a.bf16) return wide ? pick<bf16, fwd_vec<bf16>(), false>(a, s) : pick<bf16, 1, false>(a, s);
-  return wide ? pick<float, fwd_vec<float>(), false>(a, s) : pick<float, 1, false>(a, s);
+  if (a.max_q <= FEW) {
+    if (a.bf16) return wide ? pick<bf16, 8, 1>(a, s) : pick<bf16, 1, 1>(a, s);
+    return wide ? pick<float, 4, 1>(a, s) : pick<float, 1, 1>(a, s);
+  }
+  if (a.bf16) return wide ? pick<bf16, 4, 16>(a, s) : pick<bf16, 1, 16>(a, s);
+  return wide ? pick<float, 4, 8>(a, s) : pick<float, 1, 16>(a, s);
 }
 cudaError_t launch_causal_conv_bwd(const ConvArgs& a, bool wide, cudaStream_t s) {
-  if (a.bf16) return wide ? pick<bf16, 4, true>(a, s) : pick<bf16, 1, true>(a, s);
-  return wide ? pick<float, 4, true>(a, s) : pick<float, 1, true>(a, s);
+  if (a.bf16) return wide ? pick<bf16, 4, 0>(a, s) : pick<bf16, 1, 0>(a, s);
+  return wide ? pick<float, 4, 0>(a, s) : pick<float, 1, 0>(a, s);
 }
 size_t causal_conv_workspace(const ConvArgs& a0) {
   ConvArgs a = a0;

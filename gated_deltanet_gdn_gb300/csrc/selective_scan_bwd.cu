@@ -11,7 +11,7 @@
 // the state before every second token in shared memory, then pair by pair from the last: the state between a pair's
 // tokens is formed again, and a token's factors where they are used. So three states and one token's factors
 // are in registers at a time, 12 warps fit an SM, and the arithmetic's latency is hidden. (Four tokens' states and factors,
-// 255 registers and 8 warps: 607 against 480 us at B8 T4096 D768, 16 states.)
+// 255 registers and 8 warps: 607 against 463 us at B8 T4096 D768, 16 states.)
 //
 // A CTA's warps work on the same tokens of neighbouring channels, so their sums over channels (dB, dC) are added in
 // shared memory before they leave the SM; what is left per CTA, and the sums over the tokens
@@ -480,7 +480,9 @@ __global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanA
       }
       // forward through the tile: the state before every second token is kept, the last one stays in registers
       const int pairs = (rows + 1) / 2;
-      for (int i = 0; i < pairs; ++i) {
+#pragma unroll
+      for (int i = 0; i < TT / 2; ++i) {
+        if (i >= pairs) break;
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -489,6 +491,7 @@ __global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanA
 #pragma unroll
         for (int r0 = 0; r0 < 2; ++r0) step(2 * i + r0, h, h);
       }
+#pragma unroll 2
       for (int i = pairs - 1; i >= 0; --i) {
         f32x2 h0[2][4], h1[2][4], own[2][3];  // states before the pair and between its tokens
 #pragma unroll
