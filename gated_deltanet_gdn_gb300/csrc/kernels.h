@@ -337,11 +337,7 @@ struct ScanArgs {
 };
 // Tokens between two kept states, and the floats of one: quads of channels, whole ones for every group.
 constexpr int SCAN_KEEP = 8;
-inline
-#ifdef __CUDACC__
-__host__ __device__
-#endif
-int scan_quads(int D, int G) { return G * ((D / G + 3) / 4); }
+__host__ __device__ inline int scan_quads(int D, int G) { return G * ((D / G + 3) / 4); }
 
 // Plan of a serving step (page_plan.cu).
 constexpr int PLAN_MAX_REQUESTS = 8192;

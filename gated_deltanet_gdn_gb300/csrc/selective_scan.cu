@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(128) selective_scan_carry_kernel(ScanArgs a, i
       if (j + e < chunks) st4(p + (j + e) * row, h);
 #pragma unroll
       for (int n = 0; n < 4; ++n)
-        if (j + e < chunks - 1) h[n] = fmaf(ex2(rate[n] * sum[e]), h[n], own[e][n]);
+        if (j + e < chunks - 1) h[n] = carried(rate[n], sum[e], h[n], own[e][n]);
     }
   }
 }

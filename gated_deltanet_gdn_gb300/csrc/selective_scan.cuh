@@ -60,7 +60,7 @@ inline int scan_split(const ScanArgs& a, int warps, ScanCost cost) {
   const long long busy = steps * cost.full / parts, one = (long long)a.max_q * cost.alone;
   const long long whole = busy > one ? busy : one;
   const long long split = steps * (cost.full + cost.ends) / parts + 12000;  // and two more launches
-  if (split >= whole) return SCAN_WHOLE;
+  if (a.q.B == 0 || split >= whole) return SCAN_WHOLE;
   long long best = 0, length = SCAN_WHOLE;
   for (int waves = 1; waves <= 4; ++waves) {
     const long long room = (long long)waves * 152 * cost.resident / cost.ctas;  // chunks
@@ -75,6 +75,12 @@ inline int scan_split(const ScanArgs& a, int warps, ScanCost cost) {
     }
   }
   return length >= a.max_q ? SCAN_WHOLE : (int)length;
+}
+
+// A state carried over a chunk whose delta sum to `sum` (in units of 1 / log2 e). A zero stays zero where the factor overflows,
+// as it does step by step.
+__device__ __forceinline__ float carried(float rate, float sum, float state, float own) {
+  return state == 0.f ? own : fmaf(ex2(rate * sum), state, own);
 }
 
 // A warp's place: its channels and the chunk it works on.

@@ -51,7 +51,7 @@ struct BwdParts {
 };
 struct BwdPlan {
   int L, tiles;             // chunk length; CTAs' channel tiles of all groups
-  int half;                 // of it: the launches before the chunks' own work on twice as many (130 against 92 us)
+  int half;                 // of it: the launches before the chunks' own work on twice as many (130 against 88 us)
   long long numbers, halves;
   size_t start, sums, mix, dA, vec, total;  // bytes
 };
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(128) selective_scan_bwd_carry_kernel(ScanArgs 
       if (j - e >= 0) st4(p + (j - e) * row, g);
 #pragma unroll
       for (int n = 0; n < 4; ++n)
-        if (j - e > 0) g[n] = fmaf(ex2(rate[n] * sum[e]), g[n], own[e][n]);
+        if (j - e > 0) g[n] = carried(rate[n], sum[e], g[n], own[e][n]);
     }
   }
 }
@@ -330,8 +330,9 @@ __global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanA
     if (parts.start) {
       const long long behind = packed_number(a.q, k.b, k.first, L / 2) + min(2 * k.j + 1, packed_per(k.len, L / 2) - 1);
       load_columns<Shape>(parts.start + behind * row, w, flip_c, flip_n, G);
+    } else if (a.dh_final) {
+      load_columns<Shape>(a.dh_final + k.b * row, w, flip_c, flip_n, G);
     }
-    else if (a.dh_final) load_columns<Shape>(a.dh_final + k.b * row, w, flip_c, flip_n, G);
     f32x2 bias[2], skip[2];
     load_channels(a.bias, w, bias);
     load_channels(a.skip, w, skip);

@@ -343,6 +343,28 @@ def test_strides_beyond_32_bits():
         assert torch.equal(a, b)
 
 
+def test_only_padding():
+    """No sequences at all, and rows of padding enough for a split."""
+    gen = torch.Generator(device="cuda").manual_seed(24)
+    s = _inputs(gen, (5000,), 32, 1, 16, torch.float32, True, True)
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y, h, kept = gdn.gdn_selective_scan_fwd(**s, cu_seqlens=cu, flags=SOFT, save=True)
+    g = gdn.gdn_selective_scan_bwd(s["u"], s["dt"], s["A"], s["B"], s["C"], s["u"], kept, D=s["D"], z=s["z"], dt_bias=s["dt_bias"], cu_seqlens=cu, flags=SOFT)
+    assert h.shape == (0, 32, 16) and not bool(y.any()) and not any(bool(t.any()) for t in g.values() if t is not None)
+
+
+def test_growing_states_without_inputs():
+    """A above zero: factors over a chunk overflow, and a channel without inputs stays zero all the same."""
+    gen = torch.Generator(device="cuda").manual_seed(25)
+    s = _inputs(gen, (1, 4000), 32, 1, 16, torch.float32, False, False)
+    s["A"], s["dt"] = torch.full_like(s["A"], 0.5), torch.full_like(s["dt"], 1.0)
+    s["u"].zero_()
+    y, h, kept = gdn.gdn_selective_scan_fwd(**s, flags=SOFT, save=True)
+    assert not bool(y.any()) and not bool(h.any())
+    g = gdn.gdn_selective_scan_bwd(s["u"], s["dt"], s["A"], s["B"], s["C"], torch.zeros_like(y), kept, flags=SOFT)
+    assert not any(bool(t.any()) for t in g.values() if t is not None)
+
+
 def test_two_calls_at_once():
     """Calls on two streams with workspaces of their own give what they give one after the other."""
     gen = torch.Generator(device="cuda").manual_seed(23)
