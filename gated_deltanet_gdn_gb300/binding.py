@@ -552,8 +552,8 @@ def gdn_page_plan(page_table, kv_lens, new_tokens, free_pages, free_count, *, pa
     on and popped off the stack free_pages[:free_count], page_table and free_pages change in place, and requests that
     do not fit the free pages or max_tokens have no tokens in the step. The results feed gdn_kv_append,
     gdn_paged_attn, gdn_causal_conv_fwd and gdn_selective_scan_fwd; nothing is read back to the host."""
-    return PagePlan(*(_ext or _compiled()).page_plan(page_table, kv_lens, new_tokens, free_pages, free_count, page_size,
-                                                     max_tokens))
+    return tuple.__new__(PagePlan, (_ext or _compiled()).page_plan(page_table, kv_lens, new_tokens, free_pages, free_count,
+                                                                   page_size, max_tokens))
 
 
 def gdn_selftest_wait_timeout(max_tries: int = 1024, device: Optional[torch.device] = None,

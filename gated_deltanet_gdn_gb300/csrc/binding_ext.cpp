@@ -168,10 +168,19 @@ const float* rope_table(const Tensor& t, const Tensor& like, c10::Device dev, co
   return t.data_ptr<float>();
 }
 
-// New memory comes from PyTorch's allocator without its dispatcher, which took a third of a
-// short call's host time (one token of attention: 6.5 us, through the dispatcher 9.8).
-Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, c10::Device dev) {
-  return Tensor(at::detail::empty_cuda(sizes, type, dev, std::nullopt));
+// New memory of the current device, which the callers have set to `dev`. It comes from PyTorch's allocator without its
+// dispatcher, which took a third of a short call's host time (one token of attention: 6.5 us, through the dispatcher
+// 9.8), and without the checks of its empty() (0.4 us).
+Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, c10::Device) {
+  int64_t n = 1;
+  for (int64_t v : sizes) n *= v;
+  c10::Allocator* const allocator = c10::cuda::CUDACachingAllocator::get();
+  const size_t bytes = (size_t)n * c10::elementSize(type);
+  c10::Storage storage(c10::Storage::use_byte_size_t(), bytes, allocator->allocate(bytes), allocator, true);
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(std::move(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                      c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+  return t;
 }
 
 // A contiguous vector of n elements, `at` bytes into memory that it shares (at a multiple of their size).

@@ -124,6 +124,8 @@ __global__ void __launch_bounds__(THREADS) causal_conv_fwd_kernel(ConvArgs a) {
   const long long number = item / vecs;
   const int c = (int)(item - number * vecs) * V;
   if (number >= packed_numbers(a.q, a.run)) return;
+  f32x2 w[K][NP], bias[NP], win[K][NP];  // win[K - 1]: the current input
+  if constexpr (BATCH == 1) load_weights<T, V, K>(a, c, w, bias);  // on their way during the look-up
   Chunk k;
   if (!packed_chunk(a.q, number, a.run, &k)) return;
   const int t0 = k.j * a.run, t1 = min(k.len, t0 + a.run);
@@ -153,10 +155,9 @@ __global__ void __launch_bounds__(THREADS) causal_conv_fwd_kernel(ConvArgs a) {
     if (slot >= 0 && a.state0 && packed_goes_on(a.q, k.b, k.len)) state = static_cast<const T*>(a.state0) + at;
     if (slot >= 0 && a.state_final) next = static_cast<T*>(a.state_final) + at;
   }
-  f32x2 w[K][NP], bias[NP], win[K][NP];  // win[K - 1]: the current input
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) load_past<T, V, K>(a, k, t0 - (K - 1) + i, state, c, win[i]);
-  load_weights<T, V, K>(a, c, w, bias);
+  if constexpr (BATCH != 1) load_weights<T, V, K>(a, c, w, bias);
   // The last K - 1 of the state's inputs and the sequence's: all that this thread reads of the state is
   // read by now, whatever it writes.
   if (next) {
@@ -380,7 +381,7 @@ constexpr int FEW = 8;
 template <class T, int V, int K, bool SILU, int BATCH>
 cudaError_t fwd(ConvArgs a, cudaStream_t s) {
   const int vecs = a.C / V;
-  a.run = a.max_q <= FEW ? FEW : run_of(a, vecs);
+  a.run = a.max_q <= FEW ? PACKED_WHOLE : run_of(a, vecs);
   const long long blocks = (packed_numbers(a.q, a.run) * vecs + THREADS - 1) / THREADS;
   if (blocks > 0x7fffffff) return cudaErrorNotSupported;
   prof_mark(K_CONV_FWD, s, true);

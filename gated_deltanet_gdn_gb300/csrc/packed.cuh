@@ -14,6 +14,8 @@
 
 namespace gdn {
 
+constexpr int PACKED_WHOLE = 0x40000000;  // chunk length where sequences are not cut
+
 // Chunks of a sequence of T tokens; one, without tokens, where T is 0.
 __host__ __device__ __forceinline__ int packed_per(int T, int L) { return T > L ? (T - 1) / L + 1 : 1; }
 
@@ -57,6 +59,10 @@ __device__ __forceinline__ bool packed_chunk(const PackedArgs& q, long long numb
     return c->b < q.B;
   }
   int lo = 0, hi = q.B + 1;  // the last b with number(b) <= number; number(0) is 0
+  if (L > q.N) {  // a chunk for every sequence: nothing to search
+    lo = (int)number;
+    hi = 0;
+  }
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (packed_start(q, mid) / L + mid <= number) lo = mid;

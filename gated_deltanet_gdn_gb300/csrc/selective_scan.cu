@@ -286,16 +286,21 @@ __global__ void __launch_bounds__(128) selective_scan_carry_kernel(ScanArgs a, i
 // One token a sequence, or few: a warp per sequence and 512 / NS channels, nothing staged. Bound by the states, which are
 // read and written once (32 sequences x 6144 channels x 16 states: 25 MB), so registers are kept low for
 // many warps, and everything a token needs is on its way before the first result is used.
+constexpr int STEP_WARPS = 1, STEP_CTAS = 21;  // as many as fit with 96 registers (7.4 us; four warps a CTA 7.6; fewer registers 8.7)
 template <class T, int NS, bool WIDE>
-__global__ void __launch_bounds__(32 * WARPS, 5) selective_step_kernel(ScanArgs a, int tiles, int warps) {
+__global__ void __launch_bounds__(32 * STEP_WARPS, STEP_CTAS) selective_step_kernel(ScanArgs a, int tiles, int warps) {
   using Shape = ScanShape<NS, 4, TILE>;
   constexpr int S = Shape::S;
   pdl_wait();
   pdl_trigger();
-  const int at = blockIdx.x * WARPS + threadIdx.x / 32;
+  const int at = blockIdx.x * STEP_WARPS + threadIdx.x / 32;
   if (at >= warps) return;
   const int b = at / tiles;
   const ScanPlace<Shape> w(a, at - b * tiles);
+  f32x2 A[4][2], h[4][2], bias[2], skip[2];
+  load_states<Shape>(a.A, w, A);
+  load_channels(a.bias, w, bias);
+  load_channels(a.skip, w, skip);
   int first, len;
   packed_bounds(a.q, b, &first, &len);
   if (b == a.q.B) {  // rows behind the last sequence
@@ -307,13 +312,9 @@ __global__ void __launch_bounds__(32 * WARPS, 5) selective_step_kernel(ScanArgs 
   }
   const int slot = packed_slot(a.q, b);
   const long long row = (long long)a.D * NS;
-  f32x2 A[4][2], h[4][2], bias[2], skip[2];
 #pragma unroll
   for (int e = 0; e < 4; ++e) h[e][0] = h[e][1] = both(0.f);
   if (slot >= 0 && a.h0 && packed_goes_on(a.q, b, len)) load_states<Shape>(a.h0 + slot * row, w, h);
-  load_states<Shape>(a.A, w, A);
-  load_channels(a.bias, w, bias);
-  load_channels(a.skip, w, skip);
   for (int t = 0; t < len; ++t) {
     const long long r = first + (long long)t;
     const Quad<T> qu = load_quad<WIDE>(static_cast<const T*>(a.u) + r * a.u_ts + w.c, w.n);
@@ -371,11 +372,11 @@ template <class T, int NS, bool WIDE>
 cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   if (a.max_q <= FEW && !a.kept) {
     const int tiles = scan_tiles(a.D, a.G, NS, 4);
-    const long long warps = packed_numbers(a.q, SCAN_WHOLE) * tiles;
+    const long long warps = packed_numbers(a.q, PACKED_WHOLE) * tiles;
     if (warps > 0x7fffffff) return cudaErrorNotSupported;
     prof_mark(K_SSTEP, s, true);
-    const cudaError_t e = launch_pdl(selective_step_kernel<T, NS, WIDE>, dim3((unsigned)((warps + WARPS - 1) / WARPS)),
-                                     dim3(32 * WARPS), 0, s, a, tiles, (int)warps);
+    const cudaError_t e = launch_pdl(selective_step_kernel<T, NS, WIDE>, dim3((unsigned)((warps + STEP_WARPS - 1) / STEP_WARPS)),
+                                     dim3(32 * STEP_WARPS), 0, s, a, tiles, (int)warps);
     prof_mark(K_SSTEP, s, false);
     return e;
   }
@@ -384,7 +385,7 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   if (blocks > 0x7fffffff) return cudaErrorNotSupported;
   const dim3 grid((unsigned)blocks), block(32 * WARPS);
   float* start = nullptr;
-  if (L != SCAN_WHOLE) {
+  if (L != PACKED_WHOLE) {
     start = static_cast<float*>(a.ws);
     float* sums = start + numbers * a.D * NS;
     prof_mark(K_SCAN_SUM, s, true);
@@ -418,7 +419,7 @@ cudaError_t pick(const ScanArgs& a, cudaStream_t s) {
 
 size_t selective_scan_workspace(const ScanArgs& a) {  // that of the split, which few tokens never need
   const int L = split_of(a);
-  if (L == SCAN_WHOLE) return 0;
+  if (L == PACKED_WHOLE) return 0;
   return (size_t)packed_numbers(a.q, L) * a.D * (a.NS + 1) * sizeof(float);
 }
 cudaError_t launch_selective_scan(const ScanArgs& a, bool wide, cudaStream_t s) {

@@ -44,15 +44,13 @@ inline int scan_tiles(int D, int G, int NS, int SP) {
   return G * ((dg + cw - 1) / cw);
 }
 
-constexpr int SCAN_WHOLE = 0x40000000;  // chunk length where sequences are not split
-
 // Clocks of a warp's step that weigh a split against whole sequences, as measured: in a full SM sub-partition; of a warp
 // with no other beside it; and in the launch before that gives the chunks' ends. CTAs that an SM holds, CTAs for the channels
 // of a chunk, and the multiple of tokens that a chunk has.
 struct ScanCost {
   int full, alone, ends, resident, ctas, unit;
 };
-// Chunk length: SCAN_WHOLE, or as many chunks as fill the SMs one to four times, whichever ends first (a CTA's start counts
+// Chunk length: PACKED_WHOLE, or as many chunks as fill the SMs one to four times, whichever ends first (a CTA's start counts
 // as START tokens; sequences of unknown lengths end in the middle of a chunk).
 inline int scan_split(const ScanArgs& a, int warps, ScanCost cost) {
   constexpr int START = 12;
@@ -60,8 +58,8 @@ inline int scan_split(const ScanArgs& a, int warps, ScanCost cost) {
   const long long busy = steps * cost.full / parts, one = (long long)a.max_q * cost.alone;
   const long long whole = busy > one ? busy : one;
   const long long split = steps * (cost.full + cost.ends) / parts + 12000;  // and two more launches
-  if (a.q.B == 0 || split >= whole) return SCAN_WHOLE;
-  long long best = 0, length = SCAN_WHOLE;
+  if (a.q.B == 0 || split >= whole) return PACKED_WHOLE;
+  long long best = 0, length = PACKED_WHOLE;
   for (int waves = 1; waves <= 4; ++waves) {
     const long long room = (long long)waves * 152 * cost.resident / cost.ctas;  // chunks
     const long long each = a.q.cu ? room - a.q.B / 2 : room / a.q.B, tokens = a.q.cu ? a.q.N : a.q.T;
@@ -74,7 +72,7 @@ inline int scan_split(const ScanArgs& a, int warps, ScanCost cost) {
       length = L;
     }
   }
-  return length >= a.max_q ? SCAN_WHOLE : (int)length;
+  return length >= a.max_q ? PACKED_WHOLE : (int)length;
 }
 
 // A state carried over a chunk whose delta sum to `sum` (in units of 1 / log2 e). A zero stays zero where the factor overflows,

@@ -69,8 +69,8 @@ BwdPlan plan_of(const ScanArgs& a) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   const size_t states = up((size_t)p.numbers * a.D * a.NS * sizeof(float)), rows = up((size_t)p.numbers * a.D * sizeof(float));
   p.start = 0;
-  p.sums = p.start + (p.L == SCAN_WHOLE ? 0 : up((size_t)p.halves * a.D * a.NS * sizeof(float)));
-  p.mix = p.sums + (p.L == SCAN_WHOLE ? 0 : up((size_t)p.halves * a.D * sizeof(float)));
+  p.sums = p.start + (p.L == PACKED_WHOLE ? 0 : up((size_t)p.halves * a.D * a.NS * sizeof(float)));
+  p.mix = p.sums + (p.L == PACKED_WHOLE ? 0 : up((size_t)p.halves * a.D * sizeof(float)));
   p.dA = p.mix + up((size_t)p.tiles * a.q.N * 2 * a.NS * sizeof(float));
   p.vec = p.dA + states;
   p.total = p.vec + 2 * rows;
@@ -648,7 +648,7 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   const BwdPlan p = plan_of(a);
   char* const ws = static_cast<char*>(a.ws);
   BwdParts parts;
-  parts.start = p.L == SCAN_WHOLE ? nullptr : reinterpret_cast<float*>(ws + p.start);
+  parts.start = p.L == PACKED_WHOLE ? nullptr : reinterpret_cast<float*>(ws + p.start);
   parts.sums = reinterpret_cast<float*>(ws + p.sums);
   parts.mix = reinterpret_cast<float*>(ws + p.mix);
   parts.dA = reinterpret_cast<float*>(ws + p.dA);
