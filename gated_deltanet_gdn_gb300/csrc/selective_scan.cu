@@ -6,9 +6,9 @@ namespace gdn {
 namespace {
 
 constexpr int WARPS = 4;
-// States of a lane and CTAs of an SM. (16 states need more registers than there are: 249 against 141 us at B8 T4096 D768,
+// States of a lane. (16 states need more registers than there are: 249 against 141 us at B8 T4096 D768,
 // 16 states; 4 states: 144 us, and the chunks' ends 91 against 85 us.)
-constexpr int STATES = 8, CTAS = 3;
+constexpr int STATES = 8;
 
 // Stores the first n of a lane's OWN channels.
 template <bool WIDE, int OWN, class T>
@@ -40,8 +40,8 @@ struct SumTile {
 // SUM: what a chunk adds to the state (from zeros) and the sum of its delta, no outputs.
 // start: [chunks][D][NS] states at the chunks' starts (SUM: written as the chunks' own ends), sums: [chunks][D].
 template <class T, int NS, bool WIDE, bool SUM>
-__global__ void __launch_bounds__(32 * WARPS, CTAS) selective_scan_kernel(ScanArgs a, int L, int tiles, long long warps, float* start,
-                                                                          float* sums) {
+__global__ void __launch_bounds__(32 * WARPS, SUM ? 3 : ctas_of(sizeof(T) == 4, NS))
+    selective_scan_kernel(ScanArgs a, int L, int tiles, long long warps, float* start, float* sums) {
   using Shape = ScanShape<NS, STATES, TILE>;
   constexpr int S = Shape::S, P = Shape::P, LD = Shape::LD, TT = Shape::TT, N = STATES / 2;
   constexpr int OWN = S == 1 ? 4 : S == 2 ? 2 : 1;  // channels whose sums a lane ends with
@@ -246,41 +246,11 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) selective_scan_kernel(ScanAr
   }
 }
 
-// The states at the chunks' starts, in place of what each chunk adds: a thread per sequence, channel and four states. The
-// loads of CARRY chunks are in flight while the chain waits for them.
-constexpr int CARRY = 8;
-__global__ void __launch_bounds__(128) selective_scan_carry_kernel(ScanArgs a, int L, float* start, const float* sums) {
+template <int SEG>
+__global__ void __launch_bounds__(32 * CARRY_WARPS) selective_scan_carry_kernel(ScanArgs a, int L, float* start, const float* sums) {
   pdl_wait();
   pdl_trigger();
-  const long long row = (long long)a.D * a.NS, at = ((long long)blockIdx.x * 128 + threadIdx.x) * 4;
-  if (at >= a.q.B * row) return;
-  const int b = (int)(at / row), i = (int)(at - b * row), c = i / a.NS;
-  int first, len;
-  packed_bounds(a.q, b, &first, &len);
-  const int chunks = packed_per(len, L);
-  const long long number = packed_number(a.q, b, first, L);
-  const int slot = packed_slot(a.q, b);
-  float rate[4], h[4] = {};
-  ld4(rate, a.A + i);
-  if (slot >= 0 && a.h0 && packed_goes_on(a.q, b, len)) ld4(h, a.h0 + slot * row + i);
-  float* p = start + number * row + i;
-  const float* d = sums + number * a.D + c;
-  for (int j = 0; j < chunks; j += CARRY) {
-    float own[CARRY][4], sum[CARRY];
-#pragma unroll
-    for (int e = 0; e < CARRY; ++e)
-      if (j + e < chunks - 1) {
-        ld4(own[e], p + (j + e) * row);
-        sum[e] = d[(long long)(j + e) * a.D] * LOG2E;
-      }
-#pragma unroll
-    for (int e = 0; e < CARRY; ++e) {
-      if (j + e < chunks) st4(p + (j + e) * row, h);
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        if (j + e < chunks - 1) h[n] = carried(rate[n], sum[e], h[n], own[e][n]);
-    }
-  }
+  scan_carry<false, SEG>(a, L, start, sums);
 }
 
 // One token a sequence, or few: a warp per sequence and 512 / NS channels, nothing staged. Bound by the states, which are
@@ -365,7 +335,7 @@ constexpr int FEW = 2;  // tokens of a sequence up to which the step kernel is t
 
 int split_of(const ScanArgs& a) {
   const int warps = scan_tiles(a.D, a.G, a.NS, STATES);
-  return scan_split(a, warps, ScanCost{400, 670, 250, CTAS, (warps + WARPS - 1) / WARPS, 16});
+  return scan_split(a, warps, ScanCost{400, 670, 250, 70, ctas_of(!a.bf16, a.NS), 8});
 }
 
 template <class T, int NS, bool WIDE>
@@ -392,10 +362,10 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
     cudaError_t e = launch_pdl(selective_scan_kernel<T, NS, WIDE, true>, grid, block, 0, s, a, L, tiles, warps, start, sums);
     prof_mark(K_SCAN_SUM, s, false);
     if (e != cudaSuccess) return e;
-    const long long threads = (long long)a.q.B * a.D * NS / 4;
+    const bool shared = carry_shared(a, L);
     prof_mark(K_SCAN_CARRY, s, true);
-    e = launch_pdl(selective_scan_carry_kernel, dim3((unsigned)((threads + 127) / 128)), dim3(128), 0, s, a, L, start,
-                   (const float*)sums);
+    e = launch_pdl(shared ? selective_scan_carry_kernel<CARRY_WARPS> : selective_scan_carry_kernel<1>, dim3(carry_blocks(a, shared)),
+                   dim3(32 * CARRY_WARPS), 0, s, a, L, start, (const float*)sums);
     prof_mark(K_SCAN_CARRY, s, false);
     if (e != cudaSuccess) return e;
   }

@@ -38,6 +38,11 @@ struct ScanShape {
   static_assert(P * S >= TT && SCAN_KEEP % TT == 0, "whole tiles between kept states");
 };
 
+// CTAs of four warps that an SM holds: three, with 168 registers. Eight states in fp32 (a lane loads all of a tile's rows
+// then) would spill a third of them: B4 T4096 D2048 forward 156 against 122 us, B8 T4096 D768 backward 466 against 334 us;
+// in bf16 the third CTA gives more (117 against 127 us).
+constexpr int ctas_of(bool f32, int ns) { return f32 && ns == 8 ? 2 : 3; }
+
 // Warps for the channels of all groups (a warp's channels belong to one group).
 inline int scan_tiles(int D, int G, int NS, int SP) {
   const int cw = 128 * SP / NS, dg = D / G;
@@ -45,34 +50,44 @@ inline int scan_tiles(int D, int G, int NS, int SP) {
 }
 
 // Clocks of a warp's step that weigh a split against whole sequences, as measured: in a full SM sub-partition; of a warp
-// with no other beside it; and in the launch before that gives the chunks' ends. CTAs that an SM holds, CTAs for the channels
-// of a chunk, and the multiple of tokens that a chunk has.
+// with no other beside it; and (beside a full one) in the launch before that gives the chunks' ends; then clocks to carry a
+// state over a chunk. CTAs of four warps that an SM holds, and the multiple of tokens that a chunk has.
 struct ScanCost {
-  int full, alone, ends, resident, ctas, unit;
+  int full, alone, ends, carry, resident, unit;
 };
-// Chunk length: PACKED_WHOLE, or as many chunks as fill the SMs one to four times, whichever ends first (a CTA's start counts
-// as START tokens; sequences of unknown lengths end in the middle of a chunk).
+// Chunk length: PACKED_WHOLE, or the length of the least time by these clocks, among those whose chunks fill the SMs one to
+// four times and their shorter and longer multiples of two (a warp's start counts as START tokens; sequences of unknown
+// lengths end in the middle of a chunk). warps: of one chunk.
 inline int scan_split(const ScanArgs& a, int warps, ScanCost cost) {
-  constexpr int START = 12;
-  const long long steps = (long long)a.q.N * warps, parts = 152 * 4;
-  const long long busy = steps * cost.full / parts, one = (long long)a.max_q * cost.alone;
-  const long long whole = busy > one ? busy : one;
-  const long long split = steps * (cost.full + cost.ends) / parts + 12000;  // and two more launches
-  if (a.q.B == 0 || split >= whole) return PACKED_WHOLE;
-  long long best = 0, length = PACKED_WHOLE;
-  for (int waves = 1; waves <= 4; ++waves) {
-    const long long room = (long long)waves * 152 * cost.resident / cost.ctas;  // chunks
-    const long long each = a.q.cu ? room - a.q.B / 2 : room / a.q.B, tokens = a.q.cu ? a.q.N : a.q.T;
-    if (each < 1) continue;
-    long long L = ((tokens + each - 1) / each + cost.unit - 1) / cost.unit * cost.unit;
-    if (L < 64) L = 64;
-    const long long time = waves * (L + START);
-    if (best == 0 || time < best) {
+  constexpr int START = 12, LAUNCHES = 12000;  // clocks of two more launches
+  const long long parts = 152 * 4, tokens = a.q.cu ? a.q.N : a.q.T;
+  if (a.q.B == 0) return PACKED_WHOLE;
+  auto step = [&](long long n) {  // clocks of a token where every SM sub-partition has n warps
+    return n * cost.full > cost.alone ? n * cost.full : (long long)cost.alone;
+  };
+  const long long busy = (long long)a.q.N * warps * cost.full / parts, one = (long long)a.max_q * cost.alone;
+  long long best = busy > one ? busy : one;
+  int length = PACKED_WHOLE;
+  auto weigh = [&](long long L) {
+    if (L < cost.unit) L = cost.unit;
+    if (L >= a.max_q) return;
+    const long long chunks = a.q.cu ? (tokens + L - 1) / L + a.q.B / 2 : (tokens + L - 1) / L * a.q.B;
+    const long long each = (chunks * warps + parts - 1) / parts;  // warps of a sub-partition
+    const long long waves = (each + cost.resident - 1) / cost.resident;
+    const long long clocks = step(waves > 1 ? cost.resident : each) * (cost.full + cost.ends) / cost.full;
+    const long long time = waves * (L + START) * clocks + (a.max_q + L - 1) / L * cost.carry + LAUNCHES;
+    if (time < best) {
       best = time;
-      length = L;
+      length = (int)L;
     }
+  };
+  for (int waves = 1; waves <= 4; ++waves) {
+    const long long room = waves * parts * cost.resident / warps;  // chunks
+    const long long each = a.q.cu ? room - a.q.B / 2 : room / a.q.B;
+    if (each >= 1) weigh(((tokens + each - 1) / each + cost.unit - 1) / cost.unit * cost.unit);
   }
-  return length >= a.max_q ? PACKED_WHOLE : (int)length;
+  for (int L = cost.unit; L <= 1024; L *= 2) weigh(L);
+  return length;
 }
 
 // A state carried over a chunk whose delta sum to `sum` (in units of 1 / log2 e). A zero stays zero where the factor overflows,
@@ -279,4 +294,100 @@ __device__ __forceinline__ void sum_quad(float (&v)[4], int s) {
     for (int d = 4; d < S; d *= 2) v[0] += __shfl_xor_sync(ALL, v[0], d);
   }
 }
+// The states at the chunks' starts, in place of what each chunk adds (BACK: the adjoints that enter them from behind, in place
+// of what each hands on). A lane has four states of a sequence's channel and takes CARRY chunks at once, whose loads are in flight
+// together. SEG warps share a long sequence, each with the CARRY chunks behind the warp before it: it adds up its own from zeros,
+// and what the warps before it give is carried over them.
+constexpr int CARRY = 8, CARRY_WARPS = 8;
+template <bool BACK, int SEG>
+__device__ __forceinline__ void scan_carry(const ScanArgs& a, int L, float* start, const float* sums) {
+  constexpr int LANES = 32 * CARRY_WARPS / SEG;
+  static_assert(SEG == 1 || SEG == CARRY_WARPS, "a CTA's warps share their lanes' sequences, or none does");
+  __shared__ float4 ends[SEG == 1 ? 1 : 2][SEG][32];
+  __shared__ float spans[SEG == 1 ? 1 : 2][SEG][32];
+  const int part = SEG == 1 ? 0 : threadIdx.x / 32, lane = SEG == 1 ? threadIdx.x : threadIdx.x % 32;
+  const long long row = (long long)a.D * a.NS, at = ((long long)blockIdx.x * LANES + lane) * 4;
+  const bool live = at < a.q.B * row;
+  const int b = live ? (int)(at / row) : 0, i = live ? (int)(at - b * row) : 0;
+  int first, len;
+  packed_bounds(a.q, b, &first, &len);
+  const int chunks = live ? packed_per(len, L) : 0;
+  float rate[4], h[4] = {};
+  ld4(rate, a.A + i);
+  if constexpr (BACK) {
+    if (live && a.dh_final) ld4(h, a.dh_final + at);
+  } else {
+    const int slot = live ? packed_slot(a.q, b) : -1;
+    if (slot >= 0 && a.h0 && packed_goes_on(a.q, b, len)) ld4(h, a.h0 + slot * row + i);
+  }
+  const long long number = packed_number(a.q, b, first, L) + (BACK ? chunks - 1 : 0);
+  const long long step = BACK ? -row : row, down = BACK ? -a.D : a.D;
+  float* p = start + number * row + i;
+  const float* d = sums + number * a.D + i / a.NS;
+  const int last = chunks > 0 ? chunks - 1 : 0;
+  const int most = SEG == 1 ? chunks : __reduce_max_sync(0xffffffffu, chunks);
+  for (int j = 0, side = 0; j < most; j += SEG * CARRY, side ^= 1) {
+    const int j0 = j + part * CARRY;
+    // Loads without a condition (of a place that is there), so that they are on their way together.
+    float own[CARRY][4], sum[CARRY];
+#pragma unroll
+    for (int e = 0; e < CARRY; ++e) {
+      const int at = j0 + e < last ? j0 + e : last;
+      ld4(own[e], p + at * step);
+      sum[e] = d[at * down];
+    }
+    auto pass = [&](int e, float (&g)[4]) {  // chunk j0 + e, if another comes after it
+      const bool on = j0 + e < chunks - 1;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float x = carried(rate[n], sum[e] * LOG2E, g[n], own[e][n]);
+        g[n] = on ? x : g[n];
+      }
+    };
+    float g[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) g[n] = h[n];
+    if constexpr (SEG > 1) {
+      float end[4] = {}, span = 0.f;
+#pragma unroll
+      for (int e = 0; e < CARRY; ++e) {
+        span += j0 + e < chunks - 1 ? sum[e] : 0.f;
+        pass(e, end);
+      }
+      ends[side][part][lane] = make_float4(end[0], end[1], end[2], end[3]);
+      spans[side][part][lane] = span * LOG2E;
+      __syncthreads();  // one a round: the other side is written next
+#pragma unroll
+      for (int v = 0; v < SEG; ++v) {
+        const float4 o = ends[side][v][lane];
+        const float x[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          g[n] = v == part ? h[n] : g[n];
+          h[n] = carried(rate[n], spans[side][v][lane], h[n], x[n]);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < CARRY; ++e) {
+      if (j0 + e < chunks) st4(p + (j0 + e) * step, g);
+      pass(e, g);
+    }
+    if constexpr (SEG == 1) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) h[n] = g[n];
+    }
+  }
+}
+// Whether the warps of a CTA share sequences: from half a round of them on (64 channels x 16 states, 398 chunks: 20 against
+// 57 us; 1024 x 16, 13 chunks: 8 both, but the two launches of a training step of 2 x 200 tokens take 80 against 58 us), and
+// where there are SMs to spare (6144 channels x 16 states of six sequences: 62 against 13 us).
+inline bool carry_shared(const ScanArgs& a, int L) {
+  return a.max_q > CARRY * CARRY_WARPS / 2 * L && (long long)a.q.B * a.D * a.NS <= 1 << 16;
+}
+inline unsigned carry_blocks(const ScanArgs& a, bool shared) {
+  const int lanes = shared ? 32 : 32 * CARRY_WARPS;
+  return (unsigned)(((long long)a.q.B * a.D * a.NS / 4 + lanes - 1) / lanes);
+}
+
 }  // namespace gdn

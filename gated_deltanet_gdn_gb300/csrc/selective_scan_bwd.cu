@@ -22,7 +22,7 @@ namespace gdn {
 namespace {
 
 constexpr int WARPS = 4;
-constexpr int SUM_STATES = 8, SUM_CTAS = 3;
+constexpr int SUM_STATES = 8;
 
 template <class Shape>
 struct BwdShared {
@@ -62,7 +62,7 @@ int cta_tiles(const ScanArgs& a) {
 BwdPlan plan_of(const ScanArgs& a) {
   BwdPlan p;
   p.tiles = cta_tiles(a);
-  p.L = scan_split(a, p.tiles * WARPS, ScanCost{710, 1600, 130, 3, p.tiles, 32});
+  p.L = scan_split(a, p.tiles * WARPS, ScanCost{710, 1600, 130, 140, ctas_of(!a.bf16, a.NS), 16});
   p.half = p.L / 2;
   p.numbers = packed_numbers(a.q, p.L);
   p.halves = packed_numbers(a.q, p.half);
@@ -81,8 +81,8 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 
 // What a chunk hands to the one before it when nothing comes in from behind, and the sum of its delta.
 template <class T, int NS, bool WIDE>
-__global__ void __launch_bounds__(32 * WARPS, SUM_CTAS) selective_scan_bwd_sum_kernel(ScanArgs a, int L, int tiles, long long warps,
-                                                                               float* start, float* sums) {
+__global__ void __launch_bounds__(32 * WARPS, ctas_of(sizeof(T) == 4, NS))
+    selective_scan_bwd_sum_kernel(ScanArgs a, int L, int tiles, long long warps, float* start, float* sums) {
   using Shape = ScanShape<NS, SUM_STATES, SCAN_KEEP>;
   constexpr int S = Shape::S, P = Shape::P, LD = Shape::LD, TT = Shape::TT, N = Shape::SP / 2;
   struct Mine {
@@ -189,40 +189,11 @@ __global__ void __launch_bounds__(32 * WARPS, SUM_CTAS) selective_scan_bwd_sum_k
   }
 }
 
-// The adjoints that enter the chunks from behind, in place of what each hands on: a thread per sequence, channel and four
-// states.
-constexpr int CARRY = 8;
-__global__ void __launch_bounds__(128) selective_scan_bwd_carry_kernel(ScanArgs a, int L, float* start, const float* sums) {
+template <int SEG>
+__global__ void __launch_bounds__(32 * CARRY_WARPS) selective_scan_bwd_carry_kernel(ScanArgs a, int L, float* start, const float* sums) {
   pdl_wait();
   pdl_trigger();
-  const long long row = (long long)a.D * a.NS, at = ((long long)blockIdx.x * 128 + threadIdx.x) * 4;
-  if (at >= a.q.B * row) return;
-  const int b = (int)(at / row), i = (int)(at - b * row), c = i / a.NS;
-  int first, len;
-  packed_bounds(a.q, b, &first, &len);
-  const int chunks = packed_per(len, L);
-  const long long number = packed_number(a.q, b, first, L);
-  float rate[4], g[4] = {};
-  ld4(rate, a.A + i);
-  if (a.dh_final) ld4(g, a.dh_final + at);
-  float* p = start + number * row + i;
-  const float* d = sums + number * a.D + c;
-  for (int j = chunks - 1; j >= 0; j -= CARRY) {
-    float own[CARRY][4], sum[CARRY];
-#pragma unroll
-    for (int e = 0; e < CARRY; ++e)
-      if (j - e > 0) {
-        ld4(own[e], p + (j - e) * row);
-        sum[e] = d[(long long)(j - e) * a.D] * LOG2E;
-      }
-#pragma unroll
-    for (int e = 0; e < CARRY; ++e) {
-      if (j - e >= 0) st4(p + (j - e) * row, g);
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        if (j - e > 0) g[n] = carried(rate[n], sum[e], g[n], own[e][n]);
-    }
-  }
+  scan_carry<true, SEG>(a, L, start, sums);
 }
 
 // Whether lane s of a quad takes the channels' second pair first: the one whose sums it ends with.
@@ -283,7 +254,7 @@ __device__ __forceinline__ int mix_place(const ScanPlace<Shape>& w) {
 }
 
 template <class T, int NS, bool WIDE>
-__global__ void __launch_bounds__(32 * WARPS, 3) selective_scan_bwd_kernel(ScanArgs a, int L, int tiles, BwdParts parts) {
+__global__ void __launch_bounds__(32 * WARPS, ctas_of(sizeof(T) == 4, NS)) selective_scan_bwd_kernel(ScanArgs a, int L, int tiles, BwdParts parts) {
   using Shape = ScanShape<NS, 4, SCAN_KEEP>;
   using Shared = BwdShared<Shape>;
   constexpr int S = Shape::S, P = Shape::P, CW = Shape::CW, LD = Shape::LD, TT = Shape::TT;
@@ -667,10 +638,10 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
                    warps, parts.start, parts.sums);
     prof_mark(K_SSCAN_RSUM, s, false);
     if (e != cudaSuccess) return e;
-    const long long threads = (long long)a.q.B * a.D * NS / 4;
+    const bool shared = carry_shared(a, p.half);
     prof_mark(K_SCAN_CARRY, s, true);
-    e = launch_pdl(selective_scan_bwd_carry_kernel, dim3((unsigned)((threads + 127) / 128)), dim3(128), 0, s, a, p.half, parts.start,
-                   (const float*)parts.sums);
+    e = launch_pdl(shared ? selective_scan_bwd_carry_kernel<CARRY_WARPS> : selective_scan_bwd_carry_kernel<1>,
+                   dim3(carry_blocks(a, shared)), dim3(32 * CARRY_WARPS), 0, s, a, p.half, parts.start, (const float*)parts.sums);
     prof_mark(K_SCAN_CARRY, s, false);
     if (e != cudaSuccess) return e;
   }

@@ -202,6 +202,31 @@ def test_differences():
         assert abs(got - want) <= 2e-5 * float((g["d" + k].double().abs() * v.abs()).sum()) + 1e-6, k
 
 
+@pytest.mark.parametrize("S,D,dtype", [(16, 20, torch.float32), (8, 36, torch.bfloat16), (64, 12, torch.bfloat16)])
+def test_states_in_a_pool_over_many_chunks(S, D, dtype):
+    """Hundreds of short chunks a sequence beside empty and short ones; states read and written in place."""
+    gen = torch.Generator(device="cuda").manual_seed(40 + S)
+    lens, past, slots = [1700, 0, 40, 1, 521], [3, 5, 0, 2, 0], [4, 0, 6, 2, -1]
+    rows = sum(lens)
+    cu = torch.tensor([sum(lens[:b]) for b in range(6)], dtype=torch.int32, device="cuda")
+    kv = torch.tensor([p + n for p, n in zip(past, lens)], dtype=torch.int32, device="cuda")
+    s = _inputs(gen, (rows,), D, 1, S, dtype, True, True)
+    s["dt_bias"] -= 2.0  # states that outlive chunks
+    states = _normal(gen, 7, D, S)
+    own = states.clone()
+    y, _, _ = gdn.gdn_selective_scan_fwd(**s, h0=own, h_final=own, slots=torch.tensor(slots, dtype=torch.int32, device="cuda"),
+                                         cu_seqlens=cu, kv_lens=kv, max_q=1700, flags=SOFT)
+    for b, slot in enumerate(slots):
+        r = slice(int(cu[b]), int(cu[b + 1]))
+        ref = scan_seq(**_rows(s, r, h0=states[slot] if slot >= 0 and past[b] else None))
+        within("y", y[r], *ref["y"])
+        if slot >= 0:
+            within("h", own[slot], *ref["h"])
+    for slot in set(range(7)) - set(slots):
+        assert torch.equal(own[slot], states[slot])
+    assert gdn.gdn_check_device_error() == 0
+
+
 def test_split_calls_carry_the_state():
     gen = torch.Generator(device="cuda").manual_seed(6)
     s = _inputs(gen, (2, 60), 40, 1, 16, torch.float32, True, True)
