@@ -326,25 +326,27 @@ __global__ void __launch_bounds__(THREADS, 4) causal_conv_bwd_kernel(ConvArgs a,
     }
 }
 
-// Adds the partial weight gradients: 8 warps take every eighth part of 32 channels, then add up in order.
+// Adds the partial weight gradients of 32 channels: a CTA's warps take the parts in turn, then add up in order. About 16
+// parts a warp: with 8 warps always, the 1216 parts of 512 fp32 channels took 17 us in place of 10, with 32 always the 102 parts
+// of 6144 channels 14 in place of 9.
 template <class T>
-__global__ void __launch_bounds__(256) causal_conv_wgrad_kernel(ConvArgs a, int parts) {
-  __shared__ float sum[8][32];
+__global__ void __launch_bounds__(1024) causal_conv_wgrad_kernel(ConvArgs a, int parts) {
+  __shared__ float sum[32][32];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, j = blockIdx.y;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32, j = blockIdx.y;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < a.C) {
     const float* p = a.partial + (long long)j * a.C + c;
     const long long step = (long long)(a.taps + 1) * a.C;
-#pragma unroll 4
-    for (int i = warp; i < parts; i += 8) s += p[i * step];
+#pragma unroll 8
+    for (int i = warp; i < parts; i += warps) s += p[i * step];
   }
   sum[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || c >= a.C) return;
-  for (int i = 1; i < 8; ++i) s += sum[i][lane];
+  for (int i = 1; i < warps; ++i) s += sum[i][lane];
   if (j < a.taps) static_cast<T*>(a.dw)[(long long)c * a.taps + j] = from_f32<T>(s);
   else if (a.dbias) static_cast<T*>(a.dbias)[c] = from_f32<T>(s);
 }
@@ -401,7 +403,8 @@ cudaError_t bwd(ConvArgs a, cudaStream_t s) {
   prof_mark(K_CONV_BWD, s, false);
   if (e != cudaSuccess) return e;
   prof_mark(K_CONV_WGRAD, s, true);
-  e = launch_pdl(causal_conv_wgrad_kernel<T>, dim3((a.C + 31) / 32, K + 1), dim3(256), 0, s, a, parts);
+  const int warps = parts < 128 ? 8 : parts < 512 ? parts / 16 : 32;
+  e = launch_pdl(causal_conv_wgrad_kernel<T>, dim3((a.C + 31) / 32, K + 1), dim3(32 * warps), 0, s, a, parts);
   prof_mark(K_CONV_WGRAD, s, false);
   return e;
 }

@@ -562,36 +562,51 @@ __global__ void __launch_bounds__(32 * WARPS, ctas_of(sizeof(T) == 4, NS)) selec
 }
 
 // Adds the partial sums: CTAs of 256 threads take 32 columns of dA, dskip and ddt_bias each (8 warps over every eighth
-// chunk), then dB and dC (a thread four values of a row).
+// chunk), then dB and dC: four values of a row a thread, or, where a group has JOIN_TILES CTAs' sums or more, 8 threads of
+// different warps (1024 tokens, 4096 channels, 64 states, 128 sums: 55 against 25 us; 16 sums: 1 to 2 us either way).
+constexpr int JOIN_TILES = 32;
 template <class T>
 __global__ void __launch_bounds__(256) selective_scan_join_kernel(ScanArgs a, BwdParts parts, int tiles, long long numbers,
                                                                   int sum_blocks) {
-  __shared__ float sum[8][32];
+  __shared__ float4 sum4[8][32];
+  float(*const sum)[32] = reinterpret_cast<float(*)[32]>(sum4);
   pdl_wait();
   pdl_trigger();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   if ((int)blockIdx.x >= sum_blocks) {
-    const int vecs = a.NS / 2;  // of a row and group, dB and dC
-    const long long i = (long long)(blockIdx.x - sum_blocks) * 256 + threadIdx.x, per = (long long)a.G * vecs, r = i / per;
-    if (r >= a.q.N) return;
-    const int left = (int)(i - r * per), g = left / vecs, n = left % vecs * 4, each = tiles / a.G;
+    const int vecs = a.NS / 2, each = tiles / a.G;  // of a row and group, dB and dC
+    const bool shared = each >= JOIN_TILES;
+    const long long block = blockIdx.x - sum_blocks, i = shared ? block * 32 + lane : block * 256 + threadIdx.x;
+    const long long per = (long long)a.G * vecs, r = i / per;
+    const int left = (int)(i - r * per), g = left / vecs, n = left % vecs * 4;
     const int end = packed_start(a.q, a.q.B);
     float v[4] = {};
-    if (!a.q.cu || r < end) {
+    if (r < a.q.N && (!a.q.cu || r < end)) {
       const float* p = parts.mix + ((long long)g * each * a.q.N + r) * 2 * a.NS + n;
+      const int step = shared ? 8 : 1;
 #pragma unroll 8
-      for (int t = 0; t < each; ++t) {
+      for (int t = shared ? warp : 0; t < each; t += step) {
         float x[4];
         ld4(x, p + (long long)t * a.q.N * 2 * a.NS);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += x[e];
       }
     }
+    if (shared) {
+      sum4[warp][lane] = make_float4(v[0], v[1], v[2], v[3]);
+      __syncthreads();
+      if (warp != 0) return;
+      for (int w = 1; w < 8; ++w) {
+        const float4 x = sum4[w][lane];
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+      }
+    }
+    if (r >= a.q.N) return;
     T* const out = static_cast<T*>(n < a.NS ? a.dB : a.dC) + (r * a.G + g) * a.NS + (n < a.NS ? n : n - a.NS);
 #pragma unroll
     for (int e = 0; e < 4; ++e) out[e] = from_f32<T>(v[e]);
     return;
   }
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const long long row = (long long)a.D * a.NS, col = (long long)blockIdx.x * 32 + lane;
   const bool in = col < row + 2 * a.D;
   float s = 0.f;
@@ -625,7 +640,8 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   parts.dA = reinterpret_cast<float*>(ws + p.dA);
   parts.vec = reinterpret_cast<float*>(ws + p.vec);
   const long long blocks = p.numbers * p.tiles;
-  const long long per = (long long)a.G * (a.NS / 2), mix_blocks = (a.q.N * per + 255) / 256;
+  const long long per = (long long)a.G * (a.NS / 2), items = p.tiles / a.G >= JOIN_TILES ? 32 : 256;
+  const long long mix_blocks = (a.q.N * per + items - 1) / items;
   const long long column_blocks = ((long long)a.D * (a.NS + 2) + 31) / 32, join_blocks = mix_blocks + column_blocks;
   if (blocks > 0x7fffffff || join_blocks > 0x7fffffff) return cudaErrorNotSupported;
   cudaError_t e;

@@ -71,7 +71,7 @@ def test_packed_forward(lens, pad, C, taps, silu, with_bias, with_state, dtype):
 # sequences, tokens, channels, taps, silu, bias, state, gradient of the state
 TRAIN = [(2, 40, 768, 4, True, False, False, False), (3, 17, 37, 3, True, True, True, True), (1, 1, 64, 4, True, True, True, True),
          (2, 2, 12, 4, False, True, True, True), (1, 700, 24, 2, True, False, True, False), (4, 129, 101, 4, False, True, False, True),
-         (5, 3, 8, 4, True, True, True, True)]
+         (5, 3, 8, 4, True, True, True, True), (1, 9001, 20, 3, True, True, True, True), (3, 1000, 136, 4, False, True, False, False)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
