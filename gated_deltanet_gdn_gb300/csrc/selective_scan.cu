@@ -253,83 +253,106 @@ __global__ void __launch_bounds__(32 * CARRY_WARPS) selective_scan_carry_kernel(
   scan_carry<false, SEG>(a, L, start, sums);
 }
 
-// One token a sequence, or few: a warp per sequence and 512 / NS channels, nothing staged. Bound by the states, which are
-// read and written once (32 sequences x 6144 channels x 16 states: 25 MB), so registers are kept low for
-// many warps, and everything a token needs is on its way before the first result is used.
-constexpr int STEP_WARPS = 1, STEP_CTAS = 21;  // as many as fit with 96 registers (7.4 us; four warps a CTA 7.6; fewer registers 8.7)
-template <class T, int NS, bool WIDE>
-__global__ void __launch_bounds__(32 * STEP_WARPS, STEP_CTAS) selective_step_kernel(ScanArgs a, int tiles, int warps) {
+// One token a sequence, or few: a warp per 512 / NS channels of SEQS sequences, nothing staged. Bound by the states, which are
+// read and written once (32 sequences x 6144 channels x 16 states: 25 MB), so registers are kept low for many warps, and
+// everything that the first tokens need is on its way before the first result is used. Two sequences a warp read A once for
+// both: 32 sequences 6.8 against 7.5 us, 64 11.0 against 13.7; where there are not STEP_ALONE warps one is faster (16
+// sequences 4.6 against 4.8), and with more tokens than one (32 sequences of two: 9.1 against 9.3). CTAs an SM: 96 and 128 registers;
+// four and two more spill (7.5 and 8.4 us).
+constexpr int STEP_CTAS[2] = {20, 16};
+constexpr long long STEP_ALONE = 152 * 20;
+template <class T, int NS, bool WIDE, int SEQS>
+__global__ void __launch_bounds__(32, STEP_CTAS[SEQS - 1]) selective_step_kernel(ScanArgs a, int tiles) {
   using Shape = ScanShape<NS, 4, TILE>;
   constexpr int S = Shape::S;
   pdl_wait();
   pdl_trigger();
-  const int at = blockIdx.x * STEP_WARPS + threadIdx.x / 32;
-  if (at >= warps) return;
-  const int b = at / tiles;
-  const ScanPlace<Shape> w(a, at - b * tiles);
-  f32x2 A[4][2], h[4][2], bias[2], skip[2];
+  const int at = blockIdx.x / tiles * SEQS;  // the first sequence
+  const ScanPlace<Shape> w(a, blockIdx.x % tiles);
+  f32x2 A[4][2], h[SEQS][4][2], bias[2], skip[2];
   load_states<Shape>(a.A, w, A);
   load_channels(a.bias, w, bias);
   load_channels(a.skip, w, skip);
-  int first, len;
-  packed_bounds(a.q, b, &first, &len);
-  if (b == a.q.B) {  // rows behind the last sequence
-    const float none[4] = {};
-    if (a.q.zero_tail)
-      for (int t = w.s; t < len; t += S)
-        store_quad<WIDE>(static_cast<T*>(a.y) + (first + (long long)t) * a.y_ts + w.c, none, w.n);
-    return;
-  }
-  const int slot = packed_slot(a.q, b);
+  int first[SEQS], len[SEQS], slot[SEQS];
   const long long row = (long long)a.D * NS;
+  struct Token {
+    Quad<T> u, d, z, B, C;
+  } token[SEQS];
+  auto load = [&](Token& q, long long r, bool on) {
+    const int n = on ? w.n : 0;
+    q.u = load_quad<WIDE>(static_cast<const T*>(a.u) + r * a.u_ts + w.c, n);
+    q.d = load_quad<WIDE>(static_cast<const T*>(a.dt) + r * a.dt_ts + w.c, n);
+    q.z = load_quad<WIDE>(static_cast<const T*>(a.z) + r * a.z_ts + w.c, a.z ? n : 0);
+    q.B = load_quad<WIDE>(static_cast<const T*>(a.B) + r * a.b_ts + w.g * a.b_gs + 4 * w.s, on ? 4 : 0);
+    q.C = load_quad<WIDE>(static_cast<const T*>(a.C) + r * a.c_ts + w.g * a.c_gs + 4 * w.s, on ? 4 : 0);
+  };
 #pragma unroll
-  for (int e = 0; e < 4; ++e) h[e][0] = h[e][1] = both(0.f);
-  if (slot >= 0 && a.h0 && packed_goes_on(a.q, b, len)) load_states<Shape>(a.h0 + slot * row, w, h);
-  for (int t = 0; t < len; ++t) {
-    const long long r = first + (long long)t;
-    const Quad<T> qu = load_quad<WIDE>(static_cast<const T*>(a.u) + r * a.u_ts + w.c, w.n);
-    const Quad<T> qd = load_quad<WIDE>(static_cast<const T*>(a.dt) + r * a.dt_ts + w.c, w.n);
-    const Quad<T> qz = load_quad<WIDE>(static_cast<const T*>(a.z) + r * a.z_ts + w.c, a.z ? w.n : 0);
-    const Quad<T> qb = load_quad<WIDE>(static_cast<const T*>(a.B) + r * a.b_ts + w.g * a.b_gs + 4 * w.s, 4);
-    const Quad<T> qc = load_quad<WIDE>(static_cast<const T*>(a.C) + r * a.c_ts + w.g * a.c_gs + 4 * w.s, 4);
-    f32x2 d[2], u[2], bn[2], cn[2];
-    float v[4];
-    quad_pairs(qd, d);
-    quad_pairs(qu, u);
-    quad_pairs(qb, bn);
-    quad_pairs(qc, cn);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      d[i] = add2(d[i], bias[i]);
-      if (a.softplus) d[i] = softplus2(d[i]);
-      const float2 df = split2(d[i]), xf = split2(mul2(d[i], u[i]));
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int e = 2 * i + j;
-        const float de = j ? df.y : df.x, xe = j ? xf.y : xf.x;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-          h[e][n] = fma2(decay2(both(de), mul2(A[e][n], both(LOG2E))), h[e][n], scale2(xe, bn[n]));
-        const float2 f = split2(fma2(h[e][1], cn[1], mul2(h[e][0], cn[0])));
-        v[e] = f.x + f.y;
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-#pragma unroll
-      for (int f = 1; f < S; f *= 2) v[e] += __shfl_xor_sync(0xffffffffu, v[e], f);
-    if (w.s == 0) {
-      f32x2 y[2] = {fma2(skip[0], u[0], pack2(v[0], v[1])), fma2(skip[1], u[1], pack2(v[2], v[3]))};
-      if (a.z) {
-        f32x2 z[2];
-        quad_pairs(qz, z);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) y[i] = mul2(y[i], mul2(z[i], sigmoid2(z[i])));
-      }
-      store_quad<WIDE>(static_cast<T*>(a.y) + r * a.y_ts + w.c, y, w.n);
+  for (int i = 0; i < SEQS; ++i) {
+    const int b = at + i;
+    slot[i] = -1;
+    first[i] = len[i] = 0;
+    if (b < a.q.B) {
+      packed_bounds(a.q, b, &first[i], &len[i]);
+      slot[i] = packed_slot(a.q, b);
+    } else if (b == a.q.B && a.q.cu && a.q.zero_tail) {  // rows behind the last sequence
+      int from, n;
+      packed_bounds(a.q, b, &from, &n);
+      const float none[4] = {};
+      for (int t = w.s; t < n; t += S)
+        store_quad<WIDE>(static_cast<T*>(a.y) + (from + (long long)t) * a.y_ts + w.c, none, w.n);
     }
   }
-  if (slot >= 0 && a.h_final) store_states<Shape>(a.h_final + slot * row, w, h);
+#pragma unroll
+  for (int i = 0; i < SEQS; ++i) {
+    load(token[i], first[i], len[i] > 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[i][e][0] = h[i][e][1] = both(0.f);
+    if (slot[i] >= 0 && a.h0 && packed_goes_on(a.q, at + i, len[i])) load_states<Shape>(a.h0 + slot[i] * row, w, h[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < SEQS; ++i) {
+    for (int t = 0; t < len[i]; ++t) {
+      const long long r = first[i] + (long long)t;
+      if (t > 0) load(token[i], r, true);
+      f32x2 d[2], u[2], bn[2], cn[2];
+      float v[4];
+      quad_pairs(token[i].d, d);
+      quad_pairs(token[i].u, u);
+      quad_pairs(token[i].B, bn);
+      quad_pairs(token[i].C, cn);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        d[m] = add2(d[m], bias[m]);
+        if (a.softplus) d[m] = softplus2(d[m]);
+        const float2 df = split2(d[m]), xf = split2(mul2(d[m], u[m]));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int e = 2 * m + j;
+          const float de = j ? df.y : df.x, xe = j ? xf.y : xf.x;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            h[i][e][n] = fma2(decay2(both(de), mul2(A[e][n], both(LOG2E))), h[i][e][n], scale2(xe, bn[n]));
+          const float2 f = split2(fma2(h[i][e][1], cn[1], mul2(h[i][e][0], cn[0])));
+          v[e] = f.x + f.y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int f = 1; f < S; f *= 2) v[e] += __shfl_xor_sync(0xffffffffu, v[e], f);
+      if (w.s == 0) {
+        f32x2 y[2] = {fma2(skip[0], u[0], pack2(v[0], v[1])), fma2(skip[1], u[1], pack2(v[2], v[3]))};
+        if (a.z) {
+          f32x2 z[2];
+          quad_pairs(token[i].z, z);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) y[m] = mul2(y[m], mul2(z[m], sigmoid2(z[m])));
+        }
+        store_quad<WIDE>(static_cast<T*>(a.y) + r * a.y_ts + w.c, y, w.n);
+      }
+    }
+    if (slot[i] >= 0 && a.h_final) store_states<Shape>(a.h_final + slot[i] * row, w, h[i]);
+  }
 }
 constexpr int FEW = 2;  // tokens of a sequence up to which the step kernel is taken
 
@@ -342,11 +365,13 @@ template <class T, int NS, bool WIDE>
 cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   if (a.max_q <= FEW && !a.kept) {
     const int tiles = scan_tiles(a.D, a.G, NS, 4);
-    const long long warps = packed_numbers(a.q, PACKED_WHOLE) * tiles;
-    if (warps > 0x7fffffff) return cudaErrorNotSupported;
+    const long long numbers = packed_numbers(a.q, PACKED_WHOLE), pairs = (numbers + 1) / 2;
+    const bool two = a.max_q == 1 && numbers * tiles > STEP_ALONE;
+    const long long blocks = (two ? pairs : numbers) * tiles;
+    if (blocks > 0x7fffffff) return cudaErrorNotSupported;
     prof_mark(K_SSTEP, s, true);
-    const cudaError_t e = launch_pdl(selective_step_kernel<T, NS, WIDE>, dim3((unsigned)((warps + STEP_WARPS - 1) / STEP_WARPS)),
-                                     dim3(32 * STEP_WARPS), 0, s, a, tiles, (int)warps);
+    const cudaError_t e = launch_pdl(two ? selective_step_kernel<T, NS, WIDE, 2> : selective_step_kernel<T, NS, WIDE, 1>,
+                                     dim3((unsigned)blocks), dim3(32), 0, s, a, tiles);
     prof_mark(K_SSTEP, s, false);
     return e;
   }

@@ -33,7 +33,8 @@ def _rows(s, r, **more):
 PACKED = [([1] * 4, 0, 768, 1, 16, True, True, True), ([1, 2, 3, 4, 5], 3, 64, 1, 16, True, True, True),
           ([0, 7, 0, 1, 0], 9, 40, 2, 8, False, True, True), ([33, 129, 1], 70, 37, 1, 16, True, False, True),
           ([300, 17], 1, 100, 4, 32, True, True, True), ([1], 0, 1, 1, 16, True, True, True), ([64, 16, 65], 0, 30, 3, 64, False, True, True),
-          ([], 20, 16, 1, 16, True, True, True), ([15, 16, 17], 40, 132, 1, 16, True, True, True), ([9, 8, 7], 2, 72, 1, 8, True, True, True)]
+          ([], 20, 16, 1, 16, True, True, True), ([15, 16, 17], 40, 132, 1, 16, True, True, True), ([9, 8, 7], 2, 72, 1, 8, True, True, True),
+          ([1, 0, 1, 1, 1] * 13, 3, 404, 1, 64, True, True, True), ([1] * 66, 0, 410, 2, 64, False, False, True)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -226,6 +227,20 @@ def test_states_in_a_pool_over_many_chunks(S, D, dtype):
     for slot in set(range(7)) - set(slots):
         assert torch.equal(own[slot], states[slot])
     assert gdn.gdn_check_device_error() == 0
+
+
+@pytest.mark.parametrize("n", [70, 71])
+def test_single_tokens_of_a_batch(n):
+    """More channels and sequences than one of each a warp would fit; an odd and an even number of them."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    s = _inputs(gen, (n, 1), 400, 1, 64, torch.bfloat16, True, True)
+    h0 = _normal(gen, n, 400, 64)
+    own = h0.clone()
+    y, h, _ = gdn.gdn_selective_scan_fwd(**s, h0=own, h_final=own, flags=SOFT)
+    for b in range(n):
+        ref = scan_seq(**_rows(s, b, h0=h0[b]))
+        within("y", y[b], *ref["y"])
+        within("h", h[b], *ref["h"])
 
 
 def test_split_calls_carry_the_state():
