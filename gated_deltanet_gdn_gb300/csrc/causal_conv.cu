@@ -376,7 +376,7 @@ void bwd_plan(ConvArgs* a, int vecs, int* parts, long long* numbers) {
   *parts = (int)(*numbers < most ? *numbers : most);
 }
 // A sequence's new tokens up to which a run is a sequence, with 16-byte vectors and one token's loads at a time (32 tokens of
-// 18,432 channels 5.5 us); longer runs take vectors of four channels and sixteen tokens' loads, of float32 eight (32,768 tokens of 2,304
+// 18,432 channels 4.0 us); longer runs take vectors of four channels and sixteen tokens' loads, of float32 eight (32,768 tokens of 2,304
 // channels 53 us, with 16-byte vectors and eight tokens 58 us).
 constexpr int FEW = 8;
 
