@@ -320,11 +320,12 @@ __device__ __forceinline__ void scan_carry(const ScanArgs& a, int L, float* star
     const int slot = live ? packed_slot(a.q, b) : -1;
     if (slot >= 0 && a.h0 && packed_goes_on(a.q, b, len)) ld4(h, a.h0 + slot * row + i);
   }
-  const long long number = packed_number(a.q, b, first, L) + (BACK ? chunks - 1 : 0);
+  // A lane behind the last state loads chunk 0 of the first sequence with the others of its warp, and stores nothing.
+  const int last = chunks > 0 ? chunks - 1 : 0;
+  const long long number = packed_number(a.q, b, first, L) + (BACK ? last : 0);
   const long long step = BACK ? -row : row, down = BACK ? -a.D : a.D;
   float* p = start + number * row + i;
   const float* d = sums + number * a.D + i / a.NS;
-  const int last = chunks > 0 ? chunks - 1 : 0;
   const int most = SEG == 1 ? chunks : __reduce_max_sync(0xffffffffu, chunks);
   for (int j = 0, side = 0; j < most; j += SEG * CARRY, side ^= 1) {
     const int j0 = j + part * CARRY;
@@ -383,7 +384,7 @@ __device__ __forceinline__ void scan_carry(const ScanArgs& a, int L, float* star
 // 57 us; 1024 x 16, 13 chunks: 8 both, but the two launches of a training step of 2 x 200 tokens take 80 against 58 us), and
 // where there are SMs to spare (6144 channels x 16 states of six sequences: 62 against 13 us).
 inline bool carry_shared(const ScanArgs& a, int L) {
-  return a.max_q > CARRY * CARRY_WARPS / 2 * L && (long long)a.q.B * a.D * a.NS <= 1 << 16;
+  return a.max_q > (long long)CARRY * CARRY_WARPS / 2 * L && (long long)a.q.B * a.D * a.NS <= 1 << 16;
 }
 inline unsigned carry_blocks(const ScanArgs& a, bool shared) {
   const int lanes = shared ? 32 : 32 * CARRY_WARPS;

@@ -80,7 +80,8 @@ TRAIN = [(2, 40, 96, 1, 16, True, True, True, False, False), (3, 17, 37, 1, 16, 
          (1, 1, 64, 1, 16, True, True, True, True, True), (2, 33, 30, 3, 8, False, True, True, True, False),
          (1, 700, 24, 1, 16, True, True, True, True, True), (2, 50, 72, 2, 64, True, True, True, False, True),
          (2, 21, 136, 1, 32, False, False, True, True, True), (1, 19, 260, 1, 16, True, True, False, True, True),
-         (1, 9, 1040, 1, 64, True, True, True, True, True), (2, 5, 2052, 2, 64, False, True, True, False, False)]
+         (1, 9, 1040, 1, 64, True, True, True, True, True), (2, 5, 2052, 2, 64, False, True, True, False, False),
+         (3, 900, 5, 1, 8, True, True, True, True, True)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
