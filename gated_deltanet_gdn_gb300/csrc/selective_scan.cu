@@ -254,15 +254,15 @@ __global__ void __launch_bounds__(32 * CARRY_WARPS) selective_scan_carry_kernel(
 }
 
 // One token a sequence, or few: a warp per 512 / NS channels of SEQS sequences, nothing staged. Bound by the states, which are
-// read and written once (32 sequences x 6144 channels x 16 states: 25 MB), so registers are kept low for many warps, and
-// everything that the first tokens need is on its way before the first result is used. Two sequences a warp read A once for
-// both: 32 sequences 6.8 against 7.5 us, 64 11.0 against 13.7; where there are not STEP_ALONE warps one is faster (16
-// sequences 4.6 against 4.8), and with more tokens than one (32 sequences of two: 9.1 against 9.3). CTAs an SM: 96 and 128 registers;
-// four and two more spill (7.5 and 8.4 us).
-constexpr int STEP_CTAS[2] = {20, 16};
-constexpr long long STEP_ALONE = 152 * 20;
+// read and written once (32 sequences x 6144 channels x 16 states: 25 MB), and by latency: everything that the first tokens
+// need is on its way before the first result is used, and a sequence's next token while one is worked on. Where there is one
+// token each and more than STEP_FULL warps, a warp takes two sequences and reads A once for both: 32 sequences 6.8 against 7.5 us,
+// 64 11.0 against 13.7 (16: 4.8 against 4.6). STEP_CTAS an SM leave 128 registers: with 96 and the next token's loads, 8 sequences
+// of 4 tokens x 2048 channels take 4.3 in place of 3.7 us; with 112, two sequences a warp spill (8.4 us).
+constexpr int STEP_CTAS = 16;
+constexpr long long STEP_FULL = 152 * STEP_CTAS;
 template <class T, int NS, bool WIDE, int SEQS>
-__global__ void __launch_bounds__(32, STEP_CTAS[SEQS - 1]) selective_step_kernel(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(32, STEP_CTAS) selective_step_kernel(ScanArgs a, int tiles) {
   using Shape = ScanShape<NS, 4, TILE>;
   constexpr int S = Shape::S;
   pdl_wait();
@@ -313,13 +313,15 @@ __global__ void __launch_bounds__(32, STEP_CTAS[SEQS - 1]) selective_step_kernel
   for (int i = 0; i < SEQS; ++i) {
     for (int t = 0; t < len[i]; ++t) {
       const long long r = first[i] + (long long)t;
-      if (t > 0) load(token[i], r, true);
+      if (SEQS > 1 && t > 0) load(token[i], r, true);
+      const Token now = token[i];
+      if (SEQS == 1) load(token[i], r + 1, t + 1 < len[i]);  // on its way while this one is worked on
       f32x2 d[2], u[2], bn[2], cn[2];
       float v[4];
-      quad_pairs(token[i].d, d);
-      quad_pairs(token[i].u, u);
-      quad_pairs(token[i].B, bn);
-      quad_pairs(token[i].C, cn);
+      quad_pairs(now.d, d);
+      quad_pairs(now.u, u);
+      quad_pairs(now.B, bn);
+      quad_pairs(now.C, cn);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         d[m] = add2(d[m], bias[m]);
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(32, STEP_CTAS[SEQS - 1]) selective_step_kernel
         f32x2 y[2] = {fma2(skip[0], u[0], pack2(v[0], v[1])), fma2(skip[1], u[1], pack2(v[2], v[3]))};
         if (a.z) {
           f32x2 z[2];
-          quad_pairs(token[i].z, z);
+          quad_pairs(now.z, z);
 #pragma unroll
           for (int m = 0; m < 2; ++m) y[m] = mul2(y[m], mul2(z[m], sigmoid2(z[m])));
         }
@@ -354,7 +356,10 @@ __global__ void __launch_bounds__(32, STEP_CTAS[SEQS - 1]) selective_step_kernel
     if (slot[i] >= 0 && a.h_final) store_states<Shape>(a.h_final + slot[i] * row, w, h[i]);
   }
 }
-constexpr int FEW = 2;  // tokens of a sequence up to which the step kernel is taken
+// Whether it is taken: it goes token by token where the other kernel's tiles of eight cost the same for one as for eight. In us,
+// it against the other: 32 sequences x 6144 channels, of 4 tokens 12.5 and 18.2, of 6 16.1 and 18.4, of 8 19.7 and 18.5; of at most
+// STEP_FULL warps also more tokens: 12 x 6144, of 8 8.4 and 10.7, of 16 14.2 and 14.6; 2 x 6144 of 16 7.6 and 10.5.
+bool few(int tokens, long long warps) { return tokens <= 6 || (tokens <= 16 && warps <= STEP_FULL); }
 
 int split_of(const ScanArgs& a) {
   const int warps = scan_tiles(a.D, a.G, a.NS, STATES);
@@ -363,15 +368,15 @@ int split_of(const ScanArgs& a) {
 
 template <class T, int NS, bool WIDE>
 cudaError_t run(const ScanArgs& a, cudaStream_t s) {
-  if (a.max_q <= FEW && !a.kept) {
-    const int tiles = scan_tiles(a.D, a.G, NS, 4);
-    const long long numbers = packed_numbers(a.q, PACKED_WHOLE), pairs = (numbers + 1) / 2;
-    const bool two = a.max_q == 1 && numbers * tiles > STEP_ALONE;
-    const long long blocks = (two ? pairs : numbers) * tiles;
+  const int step_tiles = scan_tiles(a.D, a.G, NS, 4);
+  const long long sequences = packed_numbers(a.q, PACKED_WHOLE);
+  if (!a.kept && few(a.max_q, sequences * step_tiles)) {
+    const bool two = a.max_q == 1 && sequences * step_tiles > STEP_FULL;
+    const long long blocks = (two ? (sequences + 1) / 2 : sequences) * step_tiles;
     if (blocks > 0x7fffffff) return cudaErrorNotSupported;
     prof_mark(K_SSTEP, s, true);
     const cudaError_t e = launch_pdl(two ? selective_step_kernel<T, NS, WIDE, 2> : selective_step_kernel<T, NS, WIDE, 1>,
-                                     dim3((unsigned)blocks), dim3(32), 0, s, a, tiles);
+                                     dim3((unsigned)blocks), dim3(32), 0, s, a, step_tiles);
     prof_mark(K_SSTEP, s, false);
     return e;
   }
