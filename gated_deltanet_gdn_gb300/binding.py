@@ -500,8 +500,8 @@ def gdn_causal_conv_fwd(x, weight, bias=None, *, state0=None, state_final=None, 
     GDN_FLAG_CONV_SILU. x is [B, T, C], or packed [N, C] with cu_seqlens [B + 1]; states are the last taps - 1 inputs,
     [B, taps - 1, C], or rows `slots` [B] of pools (state_final may be state0: in place; a negative slot
     has no state). With kv_lens (cached tokens with the new ones) a sequence without earlier tokens starts from
-    zeros. max_q: the caller's bound on one sequence's new tokens. Returns (y, state_final). Packed rows behind the
-    last sequence are zeros, or in a given `out` left as they were. For gradients: causal_conv."""
+    zeros. max_q: the caller's bound on one sequence's new tokens. Returns (y, state_final). Packed rows before
+    the first sequence and behind the last are zeros, or in a given `out` left as they were. For gradients: causal_conv."""
     return (_ext or _compiled()).causal_conv_fwd(x, weight, bias, state0, state_final, slots, cu_seqlens, kv_lens, max_q,
                                                  flags, out)
 

@@ -114,11 +114,27 @@ __device__ __forceinline__ void load_past(const ConvArgs& a, const Chunk& k, int
   r.pairs(past);
 }
 
+// Zeros in the padding's rows of y or dx.
+template <class T, int V>
+__device__ __forceinline__ void zero_padding(const ConvArgs& a, unsigned from, void* p, long long ts) {
+  packed_padding(a.q, from, [&](long long r) {
+    f32x2 none[Raw<T, V>::NP];
+#pragma unroll
+    for (int e = 0; e < Raw<T, V>::NP; ++e) none[e] = both(0.f);
+    for (int c = threadIdx.x * V; c < a.C; c += THREADS * V) store_v<T, V>(static_cast<T*>(p) + r * ts + c, none);
+  });
+}
+constexpr int PAD_BYTES = 32768;  // of a CTA
+
 template <class T, int V, int K, bool SILU, int BATCH>
-__global__ void __launch_bounds__(THREADS) causal_conv_fwd_kernel(ConvArgs a) {
+__global__ void __launch_bounds__(THREADS) causal_conv_fwd_kernel(ConvArgs a, unsigned ctas) {
   constexpr int NP = Raw<T, V>::NP;
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x >= ctas) {
+    zero_padding<T, V>(a, ctas, a.y, a.y_ts);
+    return;
+  }
   const int vecs = a.C / V;
   const long long item = (long long)blockIdx.x * THREADS + threadIdx.x;
   const long long number = item / vecs;
@@ -195,10 +211,14 @@ __global__ void __launch_bounds__(THREADS) causal_conv_fwd_kernel(ConvArgs a) {
 
 // Gradients. Token indexes run from -(K - 1), the state's inputs, to len - 1.
 template <class T, int V, int K, bool SILU>
-__global__ void __launch_bounds__(THREADS, 4) causal_conv_bwd_kernel(ConvArgs a, int parts, long long numbers) {
+__global__ void __launch_bounds__(THREADS, 4) causal_conv_bwd_kernel(ConvArgs a, int parts, long long numbers, unsigned ctas) {
   constexpr int NP = Raw<T, V>::NP, BATCH = 4;
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x >= ctas) {
+    zero_padding<T, V>(a, ctas, a.dx, a.C);
+    return;
+  }
   const int vecs = a.C / V;
   const long long item = (long long)blockIdx.x * THREADS + threadIdx.x;
   const int part = (int)(item / vecs);
@@ -385,9 +405,11 @@ cudaError_t fwd(ConvArgs a, cudaStream_t s) {
   const int vecs = a.C / V;
   a.run = a.max_q <= FEW ? PACKED_WHOLE : run_of(a, vecs);
   const long long blocks = (packed_numbers(a.q, a.run) * vecs + THREADS - 1) / THREADS;
-  if (blocks > 0x7fffffff) return cudaErrorNotSupported;
+  const unsigned pad = packed_pad_ctas(a.q, a.q.zero_tail, (long long)a.C * sizeof(T), PAD_BYTES);
+  if (blocks + pad > 0x7fffffff) return cudaErrorNotSupported;
   prof_mark(K_CONV_FWD, s, true);
-  const cudaError_t e = launch_pdl(causal_conv_fwd_kernel<T, V, K, SILU, BATCH>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a);
+  const cudaError_t e = launch_pdl(causal_conv_fwd_kernel<T, V, K, SILU, BATCH>, dim3((unsigned)blocks + pad), dim3(THREADS), 0, s, a,
+                                   (unsigned)blocks);
   prof_mark(K_CONV_FWD, s, false);
   return e;
 }
@@ -398,8 +420,10 @@ cudaError_t bwd(ConvArgs a, cudaStream_t s) {
   long long numbers;
   bwd_plan(&a, vecs, &parts, &numbers);
   const long long blocks = ((long long)parts * vecs + THREADS - 1) / THREADS;
+  const unsigned pad = packed_pad_ctas(a.q, true, (long long)a.C * sizeof(T), PAD_BYTES);
   prof_mark(K_CONV_BWD, s, true);
-  cudaError_t e = launch_pdl(causal_conv_bwd_kernel<T, V, K, SILU>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a, parts, numbers);
+  cudaError_t e = launch_pdl(causal_conv_bwd_kernel<T, V, K, SILU>, dim3((unsigned)blocks + pad), dim3(THREADS), 0, s, a, parts, numbers,
+                             (unsigned)blocks);
   prof_mark(K_CONV_BWD, s, false);
   if (e != cudaSuccess) return e;
   prof_mark(K_CONV_WGRAD, s, true);

@@ -300,7 +300,7 @@ struct PackedArgs {
   const int* lens;   // [B] cached tokens with the new ones, or NULL: every sequence goes on from its state
   const int* slots;  // [B] rows of the state pools, or NULL: row b
   int pool;          // rows of the pools
-  int zero_tail;     // rows behind the last sequence become zeros (else they are left alone)
+  int zero_tail;     // rows of no sequence become zeros (else they are left alone)
   unsigned* err;
 };
 

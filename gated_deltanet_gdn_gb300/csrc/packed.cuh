@@ -7,7 +7,8 @@
 // floor(cu[b] / L) + b + j. Its first number never reaches the one before's last, since
 // floor(e / L) + 1 >= floor(s / L) + ceil((e - s) / L); so floor(N / L) + B + 1 numbers hold
 // every chunk, and those of the rows behind the last sequence, which count as sequence B. Some numbers stay
-// unused. (Without cu a sequence's chunks are numbered one after the other, none unused.)
+// unused, those below floor(cu[0] / L) among them. (Without cu a sequence's chunks are numbered one after the other, none
+// unused.)
 #pragma once
 
 #include "kernels.h"
@@ -71,7 +72,22 @@ __device__ __forceinline__ bool packed_chunk(const PackedArgs& q, long long numb
   c->b = lo;
   packed_bounds(q, lo, &c->first, &c->len);
   c->j = (int)(number - (c->first / L + lo));
+  if (c->j < 0) return false;  // below the first sequence's first number
   return (long long)c->j * L < c->len || (c->j == 0 && lo < q.B);
+}
+// The rows before the first sequence belong to none. Where they are to become zeros, a grid has CTAs for them behind
+// its own: one for every `each` bytes that its padding can have, up to one an SM. (By the CTAs of the sequences themselves,
+// after their work: other registers and spills in most of the kernels.)
+inline unsigned packed_pad_ctas(const PackedArgs& q, bool wanted, long long row_bytes, int each) {
+  if (!q.cu || !wanted) return 0;
+  const long long n = (q.N * row_bytes + each - 1) / each;
+  return n > 152 ? 152 : (unsigned)n;
+}
+// body(row) of these rows, a CTA a row; from: the first of the CTAs.
+template <class F>
+__device__ __forceinline__ void packed_padding(const PackedArgs& q, unsigned from, F body) {
+  const int front = packed_start(q, 0);
+  for (long long r = blockIdx.x - from; r < front; r += gridDim.x - from) body(r);
 }
 // Row of the pool with sequence b's state, -1 for none.
 __device__ __forceinline__ int packed_slot(const PackedArgs& q, int b) {

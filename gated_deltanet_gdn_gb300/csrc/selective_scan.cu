@@ -41,7 +41,7 @@ struct SumTile {
 // start: [chunks][D][NS] states at the chunks' starts (SUM: written as the chunks' own ends), sums: [chunks][D].
 template <class T, int NS, bool WIDE, bool SUM>
 __global__ void __launch_bounds__(32 * WARPS, SUM ? 3 : ctas_of(sizeof(T) == 4, NS))
-    selective_scan_kernel(ScanArgs a, int L, int tiles, long long warps, float* start, float* sums) {
+    selective_scan_kernel(ScanArgs a, int L, int tiles, long long warps, float* start, float* sums, unsigned ctas) {
   using Shape = ScanShape<NS, STATES, TILE>;
   constexpr int S = Shape::S, P = Shape::P, LD = Shape::LD, TT = Shape::TT, N = STATES / 2;
   constexpr int OWN = S == 1 ? 4 : S == 2 ? 2 : 1;  // channels whose sums a lane ends with
@@ -49,6 +49,12 @@ __global__ void __launch_bounds__(32 * WARPS, SUM ? 3 : ctas_of(sizeof(T) == 4, 
   __shared__ __align__(16) Tile shared[WARPS][2];
   pdl_wait();
   pdl_trigger();
+  if constexpr (!SUM) {
+    if (blockIdx.x >= ctas) {
+      zero_padding<WIDE, 32 * WARPS, T>(a, ctas, a.y, a.y_ts);
+      return;
+    }
+  }
   const long long at = (long long)blockIdx.x * WARPS + threadIdx.x / 32;
   if (at >= warps) return;
   Tile(&sm)[2] = shared[threadIdx.x / 32];
@@ -262,11 +268,15 @@ __global__ void __launch_bounds__(32 * CARRY_WARPS) selective_scan_carry_kernel(
 constexpr int STEP_CTAS = 16;
 constexpr long long STEP_FULL = 152 * STEP_CTAS;
 template <class T, int NS, bool WIDE, int SEQS>
-__global__ void __launch_bounds__(32, STEP_CTAS) selective_step_kernel(ScanArgs a, int tiles) {
+__global__ void __launch_bounds__(32, STEP_CTAS) selective_step_kernel(ScanArgs a, int tiles, unsigned ctas) {
   using Shape = ScanShape<NS, 4, TILE>;
   constexpr int S = Shape::S;
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x >= ctas) {
+    zero_padding<WIDE, 32, T>(a, ctas, a.y, a.y_ts);
+    return;
+  }
   const int at = blockIdx.x / tiles * SEQS;  // the first sequence
   const ScanPlace<Shape> w(a, blockIdx.x % tiles);
   f32x2 A[4][2], h[SEQS][4][2], bias[2], skip[2];
@@ -373,23 +383,25 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   if (!a.kept && few(a.max_q, sequences * step_tiles)) {
     const bool two = a.max_q == 1 && sequences * step_tiles > STEP_FULL;
     const long long blocks = (two ? (sequences + 1) / 2 : sequences) * step_tiles;
-    if (blocks > 0x7fffffff) return cudaErrorNotSupported;
+    const unsigned pad = packed_pad_ctas(a.q, a.q.zero_tail, (long long)a.D * sizeof(T), PAD_BYTES * 32);
+    if (blocks + pad > 0x7fffffff) return cudaErrorNotSupported;
     prof_mark(K_SSTEP, s, true);
     const cudaError_t e = launch_pdl(two ? selective_step_kernel<T, NS, WIDE, 2> : selective_step_kernel<T, NS, WIDE, 1>,
-                                     dim3((unsigned)blocks), dim3(32), 0, s, a, step_tiles);
+                                     dim3((unsigned)blocks + pad), dim3(32), 0, s, a, step_tiles, (unsigned)blocks);
     prof_mark(K_SSTEP, s, false);
     return e;
   }
   const int L = split_of(a), tiles = scan_tiles(a.D, a.G, NS, STATES);
   const long long numbers = packed_numbers(a.q, L), warps = numbers * tiles, blocks = (warps + WARPS - 1) / WARPS;
-  if (blocks > 0x7fffffff) return cudaErrorNotSupported;
-  const dim3 grid((unsigned)blocks), block(32 * WARPS);
+  const unsigned pad = packed_pad_ctas(a.q, a.q.zero_tail, (long long)a.D * sizeof(T), PAD_BYTES * 32 * WARPS), own = (unsigned)blocks;
+  if (blocks + pad > 0x7fffffff) return cudaErrorNotSupported;
+  const dim3 grid(own), block(32 * WARPS);
   float* start = nullptr;
   if (L != PACKED_WHOLE) {
     start = static_cast<float*>(a.ws);
     float* sums = start + numbers * a.D * NS;
     prof_mark(K_SCAN_SUM, s, true);
-    cudaError_t e = launch_pdl(selective_scan_kernel<T, NS, WIDE, true>, grid, block, 0, s, a, L, tiles, warps, start, sums);
+    cudaError_t e = launch_pdl(selective_scan_kernel<T, NS, WIDE, true>, grid, block, 0, s, a, L, tiles, warps, start, sums, own);
     prof_mark(K_SCAN_SUM, s, false);
     if (e != cudaSuccess) return e;
     const bool shared = carry_shared(a, L);
@@ -401,7 +413,7 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   }
   prof_mark(K_SSCAN, s, true);
   const cudaError_t e =
-      launch_pdl(selective_scan_kernel<T, NS, WIDE, false>, grid, block, 0, s, a, L, tiles, warps, start, (float*)nullptr);
+      launch_pdl(selective_scan_kernel<T, NS, WIDE, false>, dim3(own + pad), block, 0, s, a, L, tiles, warps, start, (float*)nullptr, own);
   prof_mark(K_SSCAN, s, false);
   return e;
 }

@@ -275,6 +275,16 @@ struct ScanMix {
   }
 };
 
+// Zeros in the padding's rows of y or a gradient, by CTAs of THREADS; PAD_BYTES of a thread.
+constexpr int PAD_BYTES = 256;
+template <bool WIDE, int THREADS, class T>
+__device__ __forceinline__ void zero_padding(const ScanArgs& a, unsigned from, void* p, long long ts) {
+  packed_padding(a.q, from, [&](long long r) {
+    const float none[4] = {};
+    for (int c = 4 * threadIdx.x; c < a.D; c += 4 * THREADS) store_quad<WIDE>(static_cast<T*>(p) + r * ts + c, none, a.D - c);
+  });
+}
+
 // Sums of four values (channels of the quad) over its S lanes: every lane ends with channels 4 s / S .. of them in front
 // (S = 1 all, S = 2 two; from 4 on channel s % 4).
 template <int S>

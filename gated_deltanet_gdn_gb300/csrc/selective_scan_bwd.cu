@@ -254,7 +254,7 @@ __device__ __forceinline__ int mix_place(const ScanPlace<Shape>& w) {
 }
 
 template <class T, int NS, bool WIDE>
-__global__ void __launch_bounds__(32 * WARPS, ctas_of(sizeof(T) == 4, NS)) selective_scan_bwd_kernel(ScanArgs a, int L, int tiles, BwdParts parts) {
+__global__ void __launch_bounds__(32 * WARPS, ctas_of(sizeof(T) == 4, NS)) selective_scan_bwd_kernel(ScanArgs a, int L, int tiles, BwdParts parts, unsigned ctas) {
   using Shape = ScanShape<NS, 4, SCAN_KEEP>;
   using Shared = BwdShared<Shape>;
   constexpr int S = Shape::S, P = Shape::P, CW = Shape::CW, LD = Shape::LD, TT = Shape::TT;
@@ -263,6 +263,12 @@ __global__ void __launch_bounds__(32 * WARPS, ctas_of(sizeof(T) == 4, NS)) selec
   Shared* const all = reinterpret_cast<Shared*>(raw_shared);
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x >= ctas) {
+    zero_padding<WIDE, 32 * WARPS, T>(a, ctas, a.du, a.D);
+    zero_padding<WIDE, 32 * WARPS, T>(a, ctas, a.ddt, a.D);
+    if (a.dz) zero_padding<WIDE, 32 * WARPS, T>(a, ctas, a.dz, a.D);
+    return;
+  }
   Shared& sm = all[threadIdx.x / 32];
   const long long number = blockIdx.x / tiles;
   const int tile = (int)(blockIdx.x - number * tiles);
@@ -579,9 +585,9 @@ __global__ void __launch_bounds__(256) selective_scan_join_kernel(ScanArgs a, Bw
     const long long block = blockIdx.x - sum_blocks, i = shared ? block * 32 + lane : block * 256 + threadIdx.x;
     const long long per = (long long)a.G * vecs, r = i / per;
     const int left = (int)(i - r * per), g = left / vecs, n = left % vecs * 4;
-    const int end = packed_start(a.q, a.q.B);
+    const int first = packed_start(a.q, 0), end = packed_start(a.q, a.q.B);
     float v[4] = {};
-    if (r < a.q.N && (!a.q.cu || r < end)) {
+    if (r < a.q.N && (!a.q.cu || (r >= first && r < end))) {
       const float* p = parts.mix + ((long long)g * each * a.q.N + r) * 2 * a.NS + n;
       const int step = shared ? 8 : 1;
 #pragma unroll 8
@@ -643,7 +649,8 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   const long long per = (long long)a.G * (a.NS / 2), items = p.tiles / a.G >= JOIN_TILES ? 32 : 256;
   const long long mix_blocks = (a.q.N * per + items - 1) / items;
   const long long column_blocks = ((long long)a.D * (a.NS + 2) + 31) / 32, join_blocks = mix_blocks + column_blocks;
-  if (blocks > 0x7fffffff || join_blocks > 0x7fffffff) return cudaErrorNotSupported;
+  const unsigned pad = packed_pad_ctas(a.q, true, (long long)a.D * sizeof(T), PAD_BYTES * 32 * WARPS);
+  if (blocks + pad > 0x7fffffff || join_blocks > 0x7fffffff) return cudaErrorNotSupported;
   cudaError_t e;
   if (parts.start) {
     const int tiles = scan_tiles(a.D, a.G, NS, SUM_STATES);
@@ -665,7 +672,8 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   e = allow_shared(reinterpret_cast<const void*>(selective_scan_bwd_kernel<T, NS, WIDE>), bytes, &done);
   if (e != cudaSuccess) return e;
   prof_mark(K_SSCAN_BWD, s, true);
-  e = launch_pdl(selective_scan_bwd_kernel<T, NS, WIDE>, dim3((unsigned)blocks), dim3(32 * WARPS), bytes, s, a, p.L, p.tiles, parts);
+  e = launch_pdl(selective_scan_bwd_kernel<T, NS, WIDE>, dim3((unsigned)blocks + pad), dim3(32 * WARPS), bytes, s, a, p.L, p.tiles, parts,
+                 (unsigned)blocks);
   prof_mark(K_SSCAN_BWD, s, false);
   if (e != cudaSuccess) return e;
   prof_mark(K_SSCAN_JOIN, s, true);

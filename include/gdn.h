@@ -431,7 +431,8 @@ int gdn_block_norm_bwd(const gdn_norm_dims* dims, const gdn_norm_parts* parts, c
  * Sequences. gdn_packed says which rows of [N, ...] tensors belong to which
  * sequence: with cu_seqlens rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 (the
  * arrays of the paged calls above serve here too; a sequence may be empty), without
- * it sequence b has the N / B rows from b N / B on. Rows from cu_seqlens[B] on are padding:
+ * it sequence b has the N / B rows from b N / B on. cu_seqlens does not decrease; it need not begin at zero (part
+ * of a batch: cu_seqlens + k). Rows before cu_seqlens[0] and from cu_seqlens[B] on are padding:
  * their values are not used; outputs there are left as they were, or become zero with
  * GDN_FLAG_ZERO_PADDING; gradients there are zero.
  * States lie in pools of `pool` rows; sequence b's is row slots[b] (row b without
