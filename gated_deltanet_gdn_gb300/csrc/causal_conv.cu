@@ -117,14 +117,13 @@ __device__ __forceinline__ void load_past(const ConvArgs& a, const Chunk& k, int
 // Zeros in the padding's rows of y or dx.
 template <class T, int V>
 __device__ __forceinline__ void zero_padding(const ConvArgs& a, unsigned from, void* p, long long ts) {
-  packed_padding(a.q, from, [&](long long r) {
+  packed_padding<THREADS>(a.q, from, a.C / V, [&](long long r, int v) {
     f32x2 none[Raw<T, V>::NP];
 #pragma unroll
     for (int e = 0; e < Raw<T, V>::NP; ++e) none[e] = both(0.f);
-    for (int c = threadIdx.x * V; c < a.C; c += THREADS * V) store_v<T, V>(static_cast<T*>(p) + r * ts + c, none);
+    store_v<T, V>(static_cast<T*>(p) + r * ts + v * V, none);
   });
 }
-constexpr int PAD_BYTES = 32768;  // of a CTA
 
 template <class T, int V, int K, bool SILU, int BATCH>
 __global__ void __launch_bounds__(THREADS) causal_conv_fwd_kernel(ConvArgs a, unsigned ctas) {
@@ -146,14 +145,6 @@ __global__ void __launch_bounds__(THREADS) causal_conv_fwd_kernel(ConvArgs a, un
   if (!packed_chunk(a.q, number, a.run, &k)) return;
   const int t0 = k.j * a.run, t1 = min(k.len, t0 + a.run);
   T* y = static_cast<T*>(a.y) + (k.first + (long long)t0) * a.y_ts + c;
-  if (k.b == a.q.B) {
-    f32x2 none[NP];
-#pragma unroll
-    for (int e = 0; e < NP; ++e) none[e] = both(0.f);
-    if (a.q.zero_tail)
-      for (int t = t0; t < t1; ++t, y += a.y_ts) store_v<T, V>(y, none);
-    return;
-  }
   const T* x = static_cast<const T*>(a.x) + (k.first + (long long)t0) * a.x_ts + c;
   Raw<T, V> raw[BATCH];
   auto fetch = [&](int t) {
@@ -237,13 +228,6 @@ __global__ void __launch_bounds__(THREADS, 4) causal_conv_bwd_kernel(ConvArgs a,
     if (!packed_chunk(a.q, number, a.run, &k)) continue;
     const int t0 = k.j * a.run, t1 = min(k.len, t0 + a.run);
     T* dx = static_cast<T*>(a.dx) + (k.first + (long long)t0) * a.C + c;  // of token t0, moving on with the tokens
-    if (k.b == a.q.B) {
-      f32x2 none[NP];
-#pragma unroll
-      for (int e = 0; e < NP; ++e) none[e] = both(0.f);
-      for (int t = t0; t < t1; ++t, dx += a.C) store_v<T, V>(dx, none);
-      continue;
-    }
     const long long held = (long long)k.b * (K - 1) * a.C + c;
     const T* state = a.state0 ? static_cast<const T*>(a.state0) + held - c : nullptr;
     const T* dstate = a.dstate ? static_cast<const T*>(a.dstate) + held : nullptr;
@@ -405,7 +389,7 @@ cudaError_t fwd(ConvArgs a, cudaStream_t s) {
   const int vecs = a.C / V;
   a.run = a.max_q <= FEW ? PACKED_WHOLE : run_of(a, vecs);
   const long long blocks = (packed_numbers(a.q, a.run) * vecs + THREADS - 1) / THREADS;
-  const unsigned pad = packed_pad_ctas(a.q, a.q.zero_tail, (long long)a.C * sizeof(T), PAD_BYTES);
+  const unsigned pad = packed_pad_ctas(a.q, a.q.zero_tail, vecs, THREADS);
   if (blocks + pad > 0x7fffffff) return cudaErrorNotSupported;
   prof_mark(K_CONV_FWD, s, true);
   const cudaError_t e = launch_pdl(causal_conv_fwd_kernel<T, V, K, SILU, BATCH>, dim3((unsigned)blocks + pad), dim3(THREADS), 0, s, a,
@@ -420,7 +404,7 @@ cudaError_t bwd(ConvArgs a, cudaStream_t s) {
   long long numbers;
   bwd_plan(&a, vecs, &parts, &numbers);
   const long long blocks = ((long long)parts * vecs + THREADS - 1) / THREADS;
-  const unsigned pad = packed_pad_ctas(a.q, true, (long long)a.C * sizeof(T), PAD_BYTES);
+  const unsigned pad = packed_pad_ctas(a.q, true, vecs, THREADS);
   prof_mark(K_CONV_BWD, s, true);
   cudaError_t e = launch_pdl(causal_conv_bwd_kernel<T, V, K, SILU>, dim3((unsigned)blocks + pad), dim3(THREADS), 0, s, a, parts, numbers,
                              (unsigned)blocks);

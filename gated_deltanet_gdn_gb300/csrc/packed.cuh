@@ -6,9 +6,8 @@
 // sequences are numbered without a prefix sum: sequence b's chunk j has number
 // floor(cu[b] / L) + b + j. Its first number never reaches the one before's last, since
 // floor(e / L) + 1 >= floor(s / L) + ceil((e - s) / L); so floor(N / L) + B + 1 numbers hold
-// every chunk, and those of the rows behind the last sequence, which count as sequence B. Some numbers stay
-// unused, those below floor(cu[0] / L) among them. (Without cu a sequence's chunks are numbered one after the other, none
-// unused.)
+// every chunk. Some numbers stay unused, those below floor(cu[0] / L) and from the last sequence's end on among them.
+// (Without cu a sequence's chunks are numbered one after the other, none unused.)
 #pragma once
 
 #include "kernels.h"
@@ -21,7 +20,7 @@ constexpr int PACKED_WHOLE = 0x40000000;  // chunk length where sequences are no
 __host__ __device__ __forceinline__ int packed_per(int T, int L) { return T > L ? (T - 1) / L + 1 : 1; }
 
 struct Chunk {
-  int b;       // sequence; B: the rows behind the last one
+  int b;       // sequence
   int first;   // row of the sequence's first token
   int len;     // its tokens
   int j;       // chunk of the sequence
@@ -72,22 +71,31 @@ __device__ __forceinline__ bool packed_chunk(const PackedArgs& q, long long numb
   c->b = lo;
   packed_bounds(q, lo, &c->first, &c->len);
   c->j = (int)(number - (c->first / L + lo));
-  if (c->j < 0) return false;  // below the first sequence's first number
-  return (long long)c->j * L < c->len || (c->j == 0 && lo < q.B);
+  if (c->j < 0 || lo == q.B) return false;  // below the first sequence's first number, or behind the last one's
+  return (long long)c->j * L < c->len || c->j == 0;
 }
-// The rows before the first sequence belong to none. Where they are to become zeros, a grid has CTAs for them behind
-// its own: one for every `each` bytes that its padding can have, up to one an SM. (By the CTAs of the sequences themselves,
-// after their work: other registers and spills in most of the kernels.)
-inline unsigned packed_pad_ctas(const PackedArgs& q, bool wanted, long long row_bytes, int each) {
+// The rows before the first sequence and behind the last belong to none. Where they are to become zeros, a grid has CTAs for
+// them behind its own: one for every PAD_VECS vectors a thread that there can be, up to sixteen warps an SM. (By the CTAs of
+// the sequences themselves, after their work: other registers and spills in most of the kernels. As chunks like a sequence's,
+// which were rows one after the other for a single token's step: 1 token in 8,192 rows x 6,144 channels took 256 us,
+// now 16; 4 in its own row.)
+constexpr int PAD_VECS = 8;
+inline unsigned packed_pad_ctas(const PackedArgs& q, bool wanted, int vecs, int threads) {
   if (!q.cu || !wanted) return 0;
-  const long long n = (q.N * row_bytes + each - 1) / each;
-  return n > 152 ? 152 : (unsigned)n;
+  const long long n = ((long long)q.N * vecs + PAD_VECS * threads - 1) / (PAD_VECS * threads), most = 152 * 512 / threads;
+  return (unsigned)(n < most ? n : most);
 }
-// body(row) of these rows, a CTA a row; from: the first of the CTAs.
-template <class F>
-__device__ __forceinline__ void packed_padding(const PackedArgs& q, unsigned from, F body) {
-  const int front = packed_start(q, 0);
-  for (long long r = blockIdx.x - from; r < front; r += gridDim.x - from) body(r);
+// body(row, vector) of these rows, each of so many vectors; from: the first of the CTAs.
+template <int THREADS, class F>
+__device__ __forceinline__ void packed_padding(const PackedArgs& q, unsigned from, int vecs, F body) {
+  const int front = packed_start(q, 0), end = packed_start(q, q.B);
+  const int wide = vecs < THREADS ? vecs : THREADS, each = THREADS / wide, mine = threadIdx.x / wide, v0 = threadIdx.x % wide;
+  if (mine >= each) return;
+  const long long rows = (long long)front + q.N - end, step = (long long)(gridDim.x - from) * each;
+#pragma unroll 1
+  for (long long r = (long long)(blockIdx.x - from) * each + mine; r < rows; r += step)
+#pragma unroll 1
+    for (int v = v0; v < vecs; v += wide) body(r < front ? r : end + r - front, v);
 }
 // Row of the pool with sequence b's state, -1 for none.
 __device__ __forceinline__ int packed_slot(const PackedArgs& q, int b) {

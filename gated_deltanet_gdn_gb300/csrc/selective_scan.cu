@@ -63,14 +63,6 @@ __global__ void __launch_bounds__(32 * WARPS, SUM ? 3 : ctas_of(sizeof(T) == 4, 
   Chunk k;
   if (!packed_chunk(a.q, number, L, &k)) return;
   const int t0 = k.j * L, t1 = k.len - t0 < L ? k.len : t0 + L;
-  if (k.b == a.q.B) {  // rows behind the last sequence
-    if (!SUM && a.q.zero_tail) {
-      const float none[4] = {};
-      for (int t = t0 + w.s; t < t1; t += S)
-        store_quad<WIDE>(static_cast<T*>(a.y) + (k.first + (long long)t) * a.y_ts + w.c, none, w.n);
-    }
-    return;
-  }
   if (SUM && t1 == k.len) return;  // nothing comes after it
 
   f32x2 A[4][N], h[4][N];
@@ -304,12 +296,6 @@ __global__ void __launch_bounds__(32, STEP_CTAS) selective_step_kernel(ScanArgs 
     if (b < a.q.B) {
       packed_bounds(a.q, b, &first[i], &len[i]);
       slot[i] = packed_slot(a.q, b);
-    } else if (b == a.q.B && a.q.cu && a.q.zero_tail) {  // rows behind the last sequence
-      int from, n;
-      packed_bounds(a.q, b, &from, &n);
-      const float none[4] = {};
-      for (int t = w.s; t < n; t += S)
-        store_quad<WIDE>(static_cast<T*>(a.y) + (from + (long long)t) * a.y_ts + w.c, none, w.n);
     }
   }
 #pragma unroll
@@ -379,12 +365,13 @@ int split_of(const ScanArgs& a) {
 template <class T, int NS, bool WIDE>
 cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   const int step_tiles = scan_tiles(a.D, a.G, NS, 4);
-  const long long sequences = packed_numbers(a.q, PACKED_WHOLE);
+  const long long sequences = a.q.B;
   if (!a.kept && few(a.max_q, sequences * step_tiles)) {
     const bool two = a.max_q == 1 && sequences * step_tiles > STEP_FULL;
     const long long blocks = (two ? (sequences + 1) / 2 : sequences) * step_tiles;
-    const unsigned pad = packed_pad_ctas(a.q, a.q.zero_tail, (long long)a.D * sizeof(T), PAD_BYTES * 32);
+    const unsigned pad = packed_pad_ctas(a.q, a.q.zero_tail, (a.D + 3) / 4, 32);
     if (blocks + pad > 0x7fffffff) return cudaErrorNotSupported;
+    if (blocks + pad == 0) return cudaSuccess;  // rows of no sequence, left alone
     prof_mark(K_SSTEP, s, true);
     const cudaError_t e = launch_pdl(two ? selective_step_kernel<T, NS, WIDE, 2> : selective_step_kernel<T, NS, WIDE, 1>,
                                      dim3((unsigned)blocks + pad), dim3(32), 0, s, a, step_tiles, (unsigned)blocks);
@@ -393,7 +380,7 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   }
   const int L = split_of(a), tiles = scan_tiles(a.D, a.G, NS, STATES);
   const long long numbers = packed_numbers(a.q, L), warps = numbers * tiles, blocks = (warps + WARPS - 1) / WARPS;
-  const unsigned pad = packed_pad_ctas(a.q, a.q.zero_tail, (long long)a.D * sizeof(T), PAD_BYTES * 32 * WARPS), own = (unsigned)blocks;
+  const unsigned pad = packed_pad_ctas(a.q, a.q.zero_tail, (a.D + 3) / 4, 32 * WARPS), own = (unsigned)blocks;
   if (blocks + pad > 0x7fffffff) return cudaErrorNotSupported;
   const dim3 grid(own), block(32 * WARPS);
   float* start = nullptr;

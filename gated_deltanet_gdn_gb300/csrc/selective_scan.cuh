@@ -275,13 +275,12 @@ struct ScanMix {
   }
 };
 
-// Zeros in the padding's rows of y or a gradient, by CTAs of THREADS; PAD_BYTES of a thread.
-constexpr int PAD_BYTES = 256;
+// Zeros in the padding's rows of y or a gradient, by CTAs of THREADS.
 template <bool WIDE, int THREADS, class T>
 __device__ __forceinline__ void zero_padding(const ScanArgs& a, unsigned from, void* p, long long ts) {
-  packed_padding(a.q, from, [&](long long r) {
+  packed_padding<THREADS>(a.q, from, (a.D + 3) / 4, [&](long long r, int v) {
     const float none[4] = {};
-    for (int c = 4 * threadIdx.x; c < a.D; c += 4 * THREADS) store_quad<WIDE>(static_cast<T*>(p) + r * ts + c, none, a.D - c);
+    store_quad<WIDE>(static_cast<T*>(p) + r * ts + 4 * v, none, a.D - 4 * v);
   });
 }
 

@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(32 * WARPS, ctas_of(sizeof(T) == 4, NS))
   const long long number = at / tiles;
   const ScanPlace<Shape> w(a, (int)(at - number * tiles));
   Chunk k;
-  if (!packed_chunk(a.q, number, L, &k) || k.b == a.q.B || k.j == 0) return;
+  if (!packed_chunk(a.q, number, L, &k) || k.j == 0) return;
   const int t0 = k.j * L, t1 = k.len - t0 < L ? k.len : t0 + L;
   f32x2 A[4][N], G[4][N];
   load_states<Shape>(a.A, w, A);
@@ -286,17 +286,7 @@ __global__ void __launch_bounds__(32 * WARPS, ctas_of(sizeof(T) == 4, NS)) selec
   f32x2 dskip[2] = {both(0.f), both(0.f)}, dbias[2] = {both(0.f), both(0.f)};
 
   Chunk k;
-  const bool used = packed_chunk(a.q, number, L, &k);
-  if (used && k.b == a.q.B) {  // rows behind the last sequence
-    const int t0 = k.j * L, t1 = k.len - t0 < L ? k.len : t0 + L;
-    const float none[4] = {};
-    for (int t = t0 + w.s; t < t1; t += S) {
-      const long long to = (k.first + (long long)t) * a.D + w.c;
-      store_quad<WIDE>(static_cast<T*>(a.du) + to, none, w.n);
-      store_quad<WIDE>(static_cast<T*>(a.ddt) + to, none, w.n);
-      if (a.dz) store_quad<WIDE>(static_cast<T*>(a.dz) + to, none, w.n);
-    }
-  } else if (used) {
+  if (packed_chunk(a.q, number, L, &k)) {
     const int t0 = k.j * L, t1 = k.len - t0 < L ? k.len : t0 + L;
     load_columns<Shape>(a.A, w, flip_c, flip_n, A);
 #pragma unroll
@@ -649,7 +639,7 @@ cudaError_t run(const ScanArgs& a, cudaStream_t s) {
   const long long per = (long long)a.G * (a.NS / 2), items = p.tiles / a.G >= JOIN_TILES ? 32 : 256;
   const long long mix_blocks = (a.q.N * per + items - 1) / items;
   const long long column_blocks = ((long long)a.D * (a.NS + 2) + 31) / 32, join_blocks = mix_blocks + column_blocks;
-  const unsigned pad = packed_pad_ctas(a.q, true, (long long)a.D * sizeof(T), PAD_BYTES * 32 * WARPS);
+  const unsigned pad = packed_pad_ctas(a.q, true, (a.D + 3) / 4, 32 * WARPS);
   if (blocks + pad > 0x7fffffff || join_blocks > 0x7fffffff) return cudaErrorNotSupported;
   cudaError_t e;
   if (parts.start) {
