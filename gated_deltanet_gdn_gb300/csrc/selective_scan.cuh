@@ -90,10 +90,14 @@ inline int scan_split(const ScanArgs& a, int warps, ScanCost cost) {
   return length;
 }
 
-// A state carried over a chunk whose delta sum to `sum` (in units of 1 / log2 e). A zero stays zero where the factor overflows,
-// as it does step by step.
+// A state carried over a chunk whose delta sum to `sum` (in units of 1 / log2 e). Where the factor leaves float32's range the
+// carried state need not (1e-20 that grows by 1e39), so half of the exponent goes into the state and half comes after it. A zero
+// stays zero where even that overflows, as it does step by step.
 __device__ __forceinline__ float carried(float rate, float sum, float state, float own) {
-  return state == 0.f ? own : fmaf(ex2(rate * sum), state, own);
+  const float x = rate * sum;
+  const bool far = fabsf(x) > 126.f;
+  const float f = ex2(far ? 0.5f * x : x);
+  return state == 0.f ? own : fmaf(f, far ? f * state : state, own);
 }
 
 // A warp's place: its channels and the chunk it works on.
