@@ -710,5 +710,9 @@ class SelectiveScan(torch.autograd.Function):
 
 def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, cu_seqlens=None,
                    max_q: Optional[int] = None, flags: int = 0):
-    """(y, h_final) of gdn_selective_scan_fwd, differentiable once through autograd."""
+    """(y, h_final) of gdn_selective_scan_fwd, differentiable once through autograd. Without gradients (torch.no_grad(),
+    torch.inference_mode()) nothing is kept for a backward."""
+    if not torch.is_grad_enabled():  # needs_input_grad asks the inputs alone
+        return gdn_selective_scan_fwd(u, dt, A, B, C, D=D, z=z, dt_bias=dt_bias, h0=h0, cu_seqlens=cu_seqlens, max_q=max_q,
+                                      flags=int(flags))[:2]
     return SelectiveScan.apply(u, dt, A, B, C, D, z, dt_bias, h0, cu_seqlens, max_q, int(flags))
