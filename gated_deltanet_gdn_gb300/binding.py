@@ -519,8 +519,8 @@ def gdn_selective_scan_fwd(u, dt, A, B, C, *, D=None, z=None, dt_bias=None, h0=N
                            out=None, workspace=None):
     """Selective state space scan: h_t = exp(delta_t A) h_{t-1} + delta_t u_t B_t, y_t = (C_t . h_t + D u_t) silu(z_t),
     delta = dt + dt_bias or, with GDN_FLAG_DT_SOFTPLUS, its softplus. u, dt, z are [B, T, D], or packed [N, D] with
-    cu_seqlens; B, C [..., groups, S] (S 8, 16, 32 or 64); A [D, S], D and dt_bias [D] and the states [B, D, S] float32.
-    States, slots, kv_lens and max_q as in gdn_causal_conv_fwd. Returns (y, h_final, residuals): the
+    cu_seqlens; B, C [..., groups, S] (S 8, 16, 32 or 64); A [D, S], D and dt_bias [D] and the states [B, D, S] float32,
+    16-byte aligned. States, slots, kv_lens and max_q as in gdn_causal_conv_fwd. Returns (y, h_final, residuals): the
     residuals (with save) are the backward's. For gradients: selective_scan."""
     return (_ext or _compiled()).selective_scan_fwd(u, dt, A, B, C, D, z, dt_bias, h0, h_final, slots, cu_seqlens, kv_lens,
                                                     max_q, flags, save, out, workspace)
@@ -702,8 +702,11 @@ class SelectiveScan(torch.autograd.Function):
             return (None,) * 12
         u, dt, A, B, C, D, z, dt_bias, cu_seqlens, kept = ctx.saved_tensors
         dy = torch.zeros_like(u) if dy is None else dy.contiguous()
-        g = gdn_selective_scan_bwd(u, dt, A, B, C, dy, kept, D=D, z=z, dt_bias=dt_bias,
-                                   dh_final=None if dh is None else dh.contiguous(), need_dh0=ctx.needs_input_grad[8],
+        if dh is not None:
+            dh = dh.contiguous()
+            if dh.data_ptr() % 16:  # a part of a larger gradient: of a concatenation, say
+                dh = dh.clone()
+        g = gdn_selective_scan_bwd(u, dt, A, B, C, dy, kept, D=D, z=z, dt_bias=dt_bias, dh_final=dh, need_dh0=ctx.needs_input_grad[8],
                                    cu_seqlens=cu_seqlens, max_q=ctx.max_q, flags=ctx.flags)
         return (g["du"], g["ddt"], g["dA"], g["dB"], g["dC"], g["dD"], g["dz"], g["ddt_bias"], g["dh0"], None, None, None)
 

@@ -46,3 +46,27 @@ def test_scan_without_gradients_keeps_nothing(mode):
     # with gradients on they are kept, and go through
     y, _ = gdn.selective_scan(u, dt, A, B, C, skip, None, bias, flags=gdn.GDN_FLAG_DT_SOFTPLUS)
     assert y.requires_grad and bool(torch.isfinite(torch.autograd.grad(y.float().sum(), A)[0]).all())
+
+
+def test_gradients_of_states_from_the_middle_of_a_tensor():
+    """A loss over states concatenated with other values: their gradient begins at any element of a larger one."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    D, S = 20, 16
+    A, skip, bias = _model(gen, D, S)
+    u, dt, B, C = _inputs(gen, 9, D, S, torch.float32)
+    w = torch.nn.Parameter(torch.randn(D, 4, generator=gen, device="cuda"))
+    weights = torch.randn(1 + D * S, generator=gen, device="cuda")
+
+    def grads(join):
+        x, state = gdn.causal_conv(u, w)
+        y, h = gdn.selective_scan(x, dt, A, B, C, skip, None, bias, flags=gdn.GDN_FLAG_DT_SOFTPLUS)
+        if join:
+            loss = (torch.cat((y.sum().view(1), h.reshape(-1))) * weights).sum()
+            loss = loss + (torch.cat((y.sum().view(1), state.reshape(-1))) * weights[:1 + 3 * D]).sum()
+        else:
+            loss = y.sum() * weights[0] + (h.reshape(-1) * weights[1:]).sum()
+            loss = loss + y.sum() * weights[0] + (state.reshape(-1) * weights[1:1 + 3 * D]).sum()
+        return torch.autograd.grad(loss, (A, skip, bias, w))
+
+    for a, b in zip(grads(True), grads(False)):
+        assert torch.equal(a, b)
