@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(32 * WARPS, SUM ? 3 : ctas_of(sizeof(T) == 4, 
 
   f32x2 A[4][N], h[4][N];
   load_states<Shape>(a.A, w, A);
+  finite_rates(A);
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -273,6 +274,7 @@ __global__ void __launch_bounds__(32, STEP_CTAS) selective_step_kernel(ScanArgs 
   const ScanPlace<Shape> w(a, blockIdx.x % tiles);
   f32x2 A[4][2], h[SEQS][4][2], bias[2], skip[2];
   load_states<Shape>(a.A, w, A);
+  finite_rates(A);
   load_channels(a.bias, w, bias);
   load_channels(a.skip, w, skip);
   int first[SEQS], len[SEQS], slot[SEQS];

@@ -129,6 +129,19 @@ __device__ __forceinline__ void load_states(const float* p, const ScanPlace<Shap
       x[i][2 * n + 1] = v.y;
     }
 }
+// Rates A, where -infinity becomes a finite value whose products with a step decay to zero all the same: the tokens that fill
+// up a tile have steps of zero and are to leave the states as they are. NaN stays NaN.
+__device__ __forceinline__ float finite_rate(float a) { return a < -2e38f ? -2e38f : a; }
+template <int N, int M>
+__device__ __forceinline__ void finite_rates(f32x2 (&A)[N][M]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int n = 0; n < M; ++n) {
+      const float2 f = split2(A[i][n]);
+      A[i][n] = pack2(finite_rate(f.x), finite_rate(f.y));
+    }
+}
 template <class Shape>
 __device__ __forceinline__ void store_states(float* p, const ScanPlace<Shape>& w, const f32x2 (&x)[4][Shape::SP / 2]) {
 #pragma unroll
@@ -327,6 +340,8 @@ __device__ __forceinline__ void scan_carry(const ScanArgs& a, int L, float* star
   const int chunks = live ? packed_per(len, L) : 0;
   float rate[4], h[4] = {};
   ld4(rate, a.A + i);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) rate[n] = finite_rate(rate[n]);
   if constexpr (BACK) {
     if (live && a.dh_final) ld4(h, a.dh_final + at);
   } else {

@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(32 * WARPS, ctas_of(sizeof(T) == 4, NS))
   const int t0 = k.j * L, t1 = k.len - t0 < L ? k.len : t0 + L;
   f32x2 A[4][N], G[4][N];
   load_states<Shape>(a.A, w, A);
+  finite_rates(A);
 #pragma unroll
   for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -289,6 +290,7 @@ __global__ void __launch_bounds__(32 * WARPS, ctas_of(sizeof(T) == 4, NS)) selec
   if (packed_chunk(a.q, number, L, &k)) {
     const int t0 = k.j * L, t1 = k.len - t0 < L ? k.len : t0 + L;
     load_columns<Shape>(a.A, w, flip_c, flip_n, A);
+    finite_rates(A);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       A[0][i] = mul2(A[0][i], both(LOG2E));

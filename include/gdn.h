@@ -497,7 +497,7 @@ int gdn_causal_conv_bwd(const gdn_conv_dims* dims, const gdn_packed* seqs, const
  * (else GDN_ERR_UNSUPPORTED, GDN_ERR_INVALID_ARG). States and sums are float32, outputs
  * rounded once; exp, softplus and silu take the hardware's approximate functions (relative
  * error of a few 2^-23). Values are not clipped: A of any sign (a state that stays within float32's range
- * token by token does so however the call is split).
+ * token by token does so however the call is split), -infinity too (a step above zero forgets the state).
  * residuals: NULL, or gdn_selective_scan_residual_bytes for the backward (the states before every 8 tokens,
  * float32). workspace: gdn_selective_scan_workspace_bytes (may be 0, then NULL), 256-byte aligned.
  * The backward takes the forward's inputs and residuals, dy and dh_final ([B, D, S] or NULL) and writes

@@ -1,9 +1,11 @@
-"""Selective scan where a chunk's decay leaves float32's range while the states do not."""
+"""Selective scan where a chunk's decay leaves float32's range while the states do not, and where A is -infinity."""
+import math
+
 import pytest
 import torch
 
 import gated_deltanet_gdn_gb300 as gdn
-from tests.mixer_reference import UNIT, within
+from tests.mixer_reference import UNIT, scan_seq, within
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +44,28 @@ def test_states_grow_and_decay_beyond_the_factors_range(sign, T, D, bound):
     within("dA", g["dA"], want, 3 * off * want)
     ddt = (sign * rate * dh.double() * h0.double() * factor)[0].sum(-1)
     within("ddt", g["ddt"][at:at + 8], ddt.expand(8, D), 3 * off * ddt.abs())
+
+
+@pytest.mark.parametrize("bound", [None, 1])
+@pytest.mark.parametrize("T", [1, 13, 1605])
+def test_a_rate_of_minus_infinity_forgets_at_once(T, bound):
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    D, S = 24, 16
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    u, dy = (torch.randn(T, D, generator=gen, device="cuda") for _ in range(2))
+    dt = 1 + torch.rand(T, D, generator=gen, device="cuda")
+    A = -torch.rand(D, S, generator=gen, device="cuda")
+    A[3:, 2:5] = -200.0  # e^-200 is zero too
+    B, C = (torch.randn(T, 1, S, generator=gen, device="cuda") for _ in range(2))
+    h0, dh = (torch.randn(1, D, S, generator=gen, device="cuda") for _ in range(2))
+    ref = scan_seq(u, dt, A, B, C, softplus=False, h0=h0[0], dy=dy, dh=dh[0])
+    A[3:, 2:5] = -math.inf
+    y, h, kept = gdn.gdn_selective_scan_fwd(u, dt, A, B, C, h0=h0, cu_seqlens=cu, max_q=bound, save=bound is None)
+    within("y", y, *ref["y"])
+    within("h", h[0], *ref["h"])
+    if bound is None:
+        g = gdn.gdn_selective_scan_bwd(u, dt, A, B, C, dy, kept, dh_final=dh, need_dh0=True, cu_seqlens=cu)
+        within("du", g["du"], *ref["du"])
+        within("dh0", g["dh0"][0], *ref["dh0"])
+        within("dA", g["dA"], *ref["dA"])
+        within("ddt", g["ddt"], *ref["ddt"])
