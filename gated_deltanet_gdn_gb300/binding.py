@@ -501,7 +501,8 @@ def gdn_causal_conv_fwd(x, weight, bias=None, *, state0=None, state_final=None, 
     [B, taps - 1, C], or rows `slots` [B] of pools (state_final may be state0: in place; a negative slot
     has no state). With kv_lens (cached tokens with the new ones) a sequence without earlier tokens starts from
     zeros. max_q: the caller's bound on one sequence's new tokens. Returns (y, state_final). Packed rows before
-    the first sequence and behind the last are zeros, or in a given `out` left as they were. For gradients: causal_conv."""
+    the first sequence and behind the last are zeros, or in a given `out` left as they were; `out` shares no
+    memory with the inputs. For gradients: causal_conv."""
     return (_ext or _compiled()).causal_conv_fwd(x, weight, bias, state0, state_final, slots, cu_seqlens, kv_lens, max_q,
                                                  flags, out)
 
@@ -520,8 +521,8 @@ def gdn_selective_scan_fwd(u, dt, A, B, C, *, D=None, z=None, dt_bias=None, h0=N
     """Selective state space scan: h_t = exp(delta_t A) h_{t-1} + delta_t u_t B_t, y_t = (C_t . h_t + D u_t) silu(z_t),
     delta = dt + dt_bias or, with GDN_FLAG_DT_SOFTPLUS, its softplus. u, dt, z are [B, T, D], or packed [N, D] with
     cu_seqlens; B, C [..., groups, S] (S 8, 16, 32 or 64); A [D, S], D and dt_bias [D] and the states [B, D, S] float32,
-    16-byte aligned. States, slots, kv_lens and max_q as in gdn_causal_conv_fwd. Returns (y, h_final, residuals): the
-    residuals (with save) are the backward's. For gradients: selective_scan."""
+    16-byte aligned. States, slots, kv_lens and max_q as in gdn_causal_conv_fwd; `out` may be u, dt or z itself.
+    Returns (y, h_final, residuals): the residuals (with save) are the backward's. For gradients: selective_scan."""
     return (_ext or _compiled()).selective_scan_fwd(u, dt, A, B, C, D, z, dt_bias, h0, h_final, slots, cu_seqlens, kv_lens,
                                                     max_q, flags, save, out, workspace)
 

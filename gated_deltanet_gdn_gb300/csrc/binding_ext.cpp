@@ -433,6 +433,42 @@ PyObject* block_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Bytes that a call reads or writes: rows of `width`, `step` apart.
+struct Span {
+  const char* name;
+  uintptr_t at;
+  int64_t rows, step, width;
+};
+Span span(const Tensor* t, const char* name) {  // contiguous
+  if (!t) return Span{name, 0, 0, 0, 0};
+  return Span{name, reinterpret_cast<uintptr_t>(t->data_ptr()), t->numel() > 0, 0, (int64_t)t->nbytes()};
+}
+Span span(const gdn_rows& r, int64_t n, int64_t groups, int64_t width, int64_t es, const char* name) {
+  return Span{name, reinterpret_cast<uintptr_t>(r.p), r.p && width > 0 ? n : 0, r.row_stride * es,
+              ((groups - 1) * r.group_stride + width) * es};
+}
+// Whether two share a byte. Rows as far apart as the other's may lie between those (columns of one buffer); of other rows,
+// ranges that meet count as shared.
+bool meet(const Span& a, const Span& b) {
+  if (a.rows == 0 || b.rows == 0) return false;
+  const int64_t along_a = (a.rows - 1) * a.step, along_b = (b.rows - 1) * b.step;
+  if (a.at + along_a + a.width <= b.at || b.at + along_b + b.width <= a.at) return false;
+  if (along_a && along_b && a.step != b.step) return true;
+  const int64_t step = along_a ? a.step : b.step;
+  if (!along_a && !along_b) return true;
+  int64_t d = (int64_t)(a.at - b.at) % step;
+  if (d < 0) d += step;
+  return d < b.width || d + a.width > step;
+}
+// Refuses an output on the memory of what the call reads; `same`: spans that it may be.
+void apart(const Span& out, std::initializer_list<Span> reads, std::initializer_list<Span> same = {}) {
+  for (const Span& r : reads)
+    if (meet(out, r)) refuse(out.name, std::string(out.name) + " shares memory with " + r.name);
+  for (const Span& r : same)
+    if ((out.at != r.at || out.step != r.step) && meet(out, r))
+      refuse(out.name, std::string(out.name) + " shares memory with " + r.name + " and is not the same");
+}
+
 // The sequences of a convolution or scan call: [B, T, ...] tensors, or [N, ...] with cu_seqlens.
 struct Seqs {
   gdn_packed q{};
@@ -557,6 +593,10 @@ PyObject* causal_conv_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (slots && !state_final) refuse("state_final", "with slots give state_final (it may be state0)");
     gdn_rows yr{};
     if (out) yr = s.out_rows(*out, c.d.C, "out");
+    const Span xs = span(xr, s.q.N, 1, c.d.C, x.element_size(), "x"), ws = span(&weight, "weight"), bs = span(bias, "bias"),
+               fs = span(state_final, "state_final"), is = span(state0, "state0");
+    if (out) apart(span(yr, s.q.N, 1, c.d.C, x.element_size(), "out"), {xs, ws, bs, is, fs});
+    if (state_final) apart(fs, {xs, ws, bs}, {is});
     Tensor y, sfo;
     {
       const NoGil nogil;
@@ -657,6 +697,15 @@ PyObject* selective_scan_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (slots && !h_final) refuse("h_final", "with slots give h_final (it may be h0)");
     gdn_rows yr{};
     if (out) yr = s.out_rows(*out, c.d.D, "out");
+    if (out || h_final) {
+      const int64_t es = u.element_size();
+      const Span us = span(c.p.u, s.q.N, 1, c.d.D, es, "u"), ds = span(c.p.dt, s.q.N, 1, c.d.D, es, "dt"),
+                 zs = span(c.p.z, s.q.N, 1, c.d.D, es, "z"), bs = span(c.p.B, s.q.N, c.d.G, c.d.S, es, "B"),
+                 cs = span(c.p.C, s.q.N, c.d.G, c.d.S, es, "C"), as = span(c.part[2], "A"), ss = span(c.part[5], "D"),
+                 ts = span(c.part[7], "dt_bias"), fs = span(h_final, "h_final"), is = span(h0, "h0");
+      if (out) apart(span(yr, s.q.N, 1, c.d.D, es, "out"), {bs, cs, as, ss, ts, is, fs}, {us, ds, zs});
+      if (h_final) apart(fs, {us, ds, zs, bs, cs, as, ss, ts}, {is});
+    }
     Tensor y, hfo, kept;
     {
       const NoGil nogil;

@@ -441,7 +441,9 @@ int gdn_block_norm_bwd(const gdn_norm_dims* dims, const gdn_norm_parts* parts, c
  * and sets bit 8 of the device error word. Two sequences of a call must not have
  * the same slot. With kv_lens (cached tokens with the new ones) a sequence whose
  * new tokens are its first starts from zeros whatever its slot holds. Initial and
- * final states may be the same memory (in-place carry). A sequence without tokens
+ * final states may be the same memory (in-place carry), and the scan's y the rows of
+ * u, dt or z; else nothing that a call writes shares memory with what it reads (y's
+ * rows may lie between x's: columns of one buffer). A sequence without tokens
  * hands its initial state on. Rows of the pools that no sequence has are left alone.
  * The arrays are device memory, read by the kernels only: a captured graph replays
  * with other lengths. max_q (> 0) bounds the tokens of one sequence; it chooses the
