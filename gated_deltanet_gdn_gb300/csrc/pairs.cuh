@@ -168,14 +168,5 @@ __device__ __forceinline__ void store_quad(T* p, const f32x2 (&x)[2], int n) {
   const float f[4] = {a.x, a.y, b.x, b.y};
   store_quad<WIDE>(p, f, n);
 }
-__device__ __forceinline__ void quad_floats(const Quad<bf16>& q, float (&x)[4]) {
-  x[0] = __uint_as_float(q.v.x << 16);
-  x[1] = __uint_as_float(q.v.x & 0xffff0000u);
-  x[2] = __uint_as_float(q.v.y << 16);
-  x[3] = __uint_as_float(q.v.y & 0xffff0000u);
-}
-__device__ __forceinline__ void quad_floats(const Quad<float>& q, float (&x)[4]) {
-  x[0] = q.v.x; x[1] = q.v.y; x[2] = q.v.z; x[3] = q.v.w;
-}
 
 }  // namespace gdn
