@@ -538,7 +538,8 @@ def gdn_selective_scan_bwd(u, dt, A, B, C, dy, residuals, *, D=None, z=None, dt_
 
 
 class PagePlan(NamedTuple):
-    """What gdn_page_plan returns, all on the device."""
+    """What gdn_page_plan returns, all on the device and in one allocation: a part that is kept keeps all (clone it where
+    max_tokens is large)."""
 
     cu_seqlens: torch.Tensor  # [B + 1] packed offsets of the granted new tokens
     kv_lens: torch.Tensor  # [B] cached tokens after the step
@@ -551,7 +552,7 @@ class PagePlan(NamedTuple):
 def gdn_page_plan(page_table, kv_lens, new_tokens, free_pages, free_count, *, page_size: int, max_tokens: int) -> PagePlan:
     """Plan a serving step from kv_lens [B] and new_tokens [B] (negative: tokens given back): pages are pushed
     on and popped off the stack free_pages[:free_count], page_table and free_pages change in place, and requests that
-    do not fit the free pages or max_tokens have no tokens in the step. The results feed gdn_kv_append,
+    do not fit the free pages or max_tokens, counted with all that is asked for before them, have no tokens in the step. The results feed gdn_kv_append,
     gdn_paged_attn, gdn_causal_conv_fwd and gdn_selective_scan_fwd; nothing is read back to the host."""
     return tuple.__new__(PagePlan, (_ext or _compiled()).page_plan(page_table, kv_lens, new_tokens, free_pages, free_count,
                                                                    page_size, max_tokens))

@@ -501,7 +501,7 @@ int gdn_causal_conv_bwd(const gdn_conv_dims* dims, const gdn_packed* seqs, const
  * error of a few 2^-23). Values are not clipped: A of any sign (a state that stays within float32's range
  * token by token does so however the call is split), -infinity too (a step above zero forgets the state).
  * residuals: NULL, or gdn_selective_scan_residual_bytes for the backward (the states before every 8 tokens,
- * float32). workspace: gdn_selective_scan_workspace_bytes (may be 0, then NULL), 256-byte aligned.
+ * float32: S / 2 bytes a token and channel). workspace: gdn_selective_scan_workspace_bytes (may be 0, then NULL), 256-byte aligned.
  * The backward takes the forward's inputs and residuals, dy and dh_final ([B, D, S] or NULL) and writes
  * the gradients, contiguous, du, ddt, dB, dC and dz of dims.dtype, dA, dskip, ddt_bias and dh0 ([B, D, S])
  * float32; dz, dskip, ddt_bias and dh0 may be NULL, and must be for absent parts (dh0 excepted: it may
