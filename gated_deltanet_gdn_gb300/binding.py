@@ -552,8 +552,9 @@ class PagePlan(NamedTuple):
 def gdn_page_plan(page_table, kv_lens, new_tokens, free_pages, free_count, *, page_size: int, max_tokens: int) -> PagePlan:
     """Plan a serving step from kv_lens [B] and new_tokens [B] (negative: tokens given back): pages are pushed
     on and popped off the stack free_pages[:free_count], page_table and free_pages change in place, and requests that
-    do not fit the free pages or max_tokens, counted with all that is asked for before them, have no tokens in the step. The results feed gdn_kv_append,
-    gdn_paged_attn, gdn_causal_conv_fwd and gdn_selective_scan_fwd; nothing is read back to the host."""
+    do not fit the free pages or max_tokens, counted with all that is asked for before them, have no tokens in the
+    step. The results feed gdn_kv_append, gdn_paged_attn, gdn_causal_conv_fwd and gdn_selective_scan_fwd; nothing is
+    read back to the host."""
     return tuple.__new__(PagePlan, (_ext or _compiled()).page_plan(page_table, kv_lens, new_tokens, free_pages, free_count,
                                                                    page_size, max_tokens))
 
